@@ -9,6 +9,9 @@ the FP8 output of section "Blackwell support"):
     h = RN_in(x + residual);  residual_out = h
     y = (weight + weight_offset) * h * rsqrt(mean(h^2) + eps) + bias
     out = RN_out(y)   or   FP8-E4M3 codes of y * 448 / max|y| with scale max|y| / 448
+
+The attention path around the QK norm (``qk_norm_rope``, ``kv_cache_append_``,
+``kv_cache_attention``) has the C ABI of ``include/rmsnorm_attn.h``.
 """
 from __future__ import annotations
 
@@ -24,3 +27,8 @@ from ._lib import (  # noqa: F401
     rmsnorm_read_status, rmsnorm_set_wait_limit, status_string)
 from .api import (block_format_configs, check_row_args, fused_add_rmsnorm, fused_add_rmsnorm_blockscaled,  # noqa: F401
                   fused_add_rmsnorm_host, make_flags, qk_norm_)
+from ._attn_lib import (  # noqa: F401
+    EXPORTED_ATTN, RMSATTN_BAD_PAGE, RMSATTN_BLOCK, RMSATTN_INTERLEAVED, RMSATTN_MAX_QUERIES,
+    RMSATTN_NORM, RMSATTN_POS_I64, attn_library_path, load_attn, rmsattn_read_status)
+from .attn import (KVCache, RopeTable, kv_cache_append_, kv_cache_attention, qk_norm_rope,  # noqa: F401
+                   rope_table)

@@ -4,6 +4,9 @@ Each kernel translation unit is compiled by its own nvcc process in parallel,
 then linked with the C-ABI unit into one shared library that exports only
 the ``rmsnorm_*`` symbols of ``include/rmsnorm.h``.  The CUDA runtime is
 linked statically, so the library needs nothing but the driver at run time.
+The attention-path operators (``csrc/attn``) are built the same way into a
+library of their own (``_build/librmsnorm_attn_gb300.so``, the ``rmsattn_*``
+symbols of ``include/rmsnorm_attn.h``).
 
 ``build(checked=True)`` makes the bounds-checked debug library
 (``_build/librmsnorm_gb300_checked.so``, compiled with -DRMSNORM_BOUNDS_CHECK):
@@ -29,6 +32,9 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "librmsnorm_gb300.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 CHECKED_PATH = os.path.join(BUILD_DIR, "librmsnorm_gb300_checked.so")
+# the attention-path operators, a library of their own
+ATTN_CSRC = os.path.join(CSRC, "attn")
+ATTN_PATH = os.path.join(BUILD_DIR, "librmsnorm_attn_gb300.so")
 # the bench's C timing harness (not part of the library)
 HOSTCOST_SRC = os.path.join(PKG, "bench_src", "host_cost.cu")
 HOSTCOST_PATH = os.path.join(BUILD_DIR, "librmsn_hostcost.so")
@@ -49,14 +55,19 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def attn_sources() -> list[str]:
+    return sorted(glob.glob(os.path.join(ATTN_CSRC, "*.cu")))
+
+
 def _inputs() -> list[str]:
-    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
+    return (sources() + attn_sources() + glob.glob(os.path.join(ATTN_CSRC, "*.cuh"))
+            + glob.glob(os.path.join(ATTN_CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
             + glob.glob(os.path.join(CSRC, "*.inc")) + glob.glob(os.path.join(INCLUDE, "*.h"))
             + [os.path.abspath(__file__)])
 
 
 def up_to_date(checked: bool = False) -> bool:
-    outs = [CHECKED_PATH] if checked else [LIB_PATH, HOSTCOST_PATH]
+    outs = [CHECKED_PATH] if checked else [LIB_PATH, ATTN_PATH, HOSTCOST_PATH]
     if not all(os.path.exists(o) for o in outs):
         return False
     t = min(os.path.getmtime(o) for o in outs)
@@ -65,15 +76,15 @@ def up_to_date(checked: bool = False) -> bool:
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None,
           checked: bool = False) -> str:
-    """Compile and link the library (the bounds-checked one with ``checked``)
-    if a source is newer than it; return its path."""
+    """Compile and link the libraries (the bounds-checked row-norm one with
+    ``checked``) if a source is newer; return the row-norm library's path."""
     out = CHECKED_PATH if checked else LIB_PATH
     if not force and up_to_date(checked):
         return out
     obj_dir = os.path.join(BUILD_DIR, "checked") if checked else BUILD_DIR
     os.makedirs(obj_dir, exist_ok=True)
     cc = nvcc()
-    srcs = sources()
+    srcs = sources() + ([] if checked else attn_sources())
     objs = [os.path.join(obj_dir, os.path.basename(s)[:-3] + ".o") for s in srcs]
     extra = ["-DRMSNORM_BOUNDS_CHECK"] if checked else []
 
@@ -93,12 +104,14 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None,
     if verbose:
         for src, log in zip(srcs, logs):
             sys.stderr.write(f"== {os.path.basename(src)}\n{log}")
-    tmp = out + f".tmp{os.getpid()}"
-    link = [cc, *ARCH, "-shared", "-cudart", "static", *objs, "-o", tmp]
-    r = subprocess.run(link, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, out)
+    n_norm = len(sources())
+    for lib, part in [(out, objs[:n_norm])] + ([] if checked else [(ATTN_PATH, objs[n_norm:])]):
+        tmp = lib + f".tmp{os.getpid()}"
+        link = [cc, *ARCH, "-shared", "-cudart", "static", *part, "-o", tmp]
+        r = subprocess.run(link, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, lib)
     if checked:
         return out
     # the C timing harness, linked against the library it times

@@ -1,0 +1,324 @@
+// C ABI of the attention-path operators (include/rmsnorm_attn.h): argument
+// checks, launch shapes and launches.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <mutex>
+
+#include "../../../include/rmsnorm_attn.h"
+#include "attn_args.h"
+
+#define RMSATTN_API extern "C" __attribute__((visibility("default")))
+
+namespace rmsattn {
+namespace {
+
+constexpr int kMaxDevices = 64;
+constexpr int64_t kMaxTokens = int64_t(1) << 30;  // positions fit 31 bits with room for windows
+
+// Status word of the kernels on each device.
+__device__ uint32_t g_status;
+
+struct DeviceInfo {
+    std::once_flag once;
+    int num_sms = 0;
+    uint32_t* status = nullptr;
+    cudaError_t err = cudaSuccess;
+};
+DeviceInfo g_dev[kMaxDevices];
+
+DeviceInfo* device_info() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return nullptr;
+    DeviceInfo& d = g_dev[dev];
+    std::call_once(d.once, [&] {
+        d.err = cudaDeviceGetAttribute(&d.num_sms, cudaDevAttrMultiProcessorCount, dev);
+        if (d.err == cudaSuccess) d.err = cudaGetSymbolAddress((void**)&d.status, g_status);
+    });
+    return d.err == cudaSuccess ? &d : nullptr;
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+// RMSN_IN_* of flags, or -1; `bytes`: its element size.
+int dtype_of(uint32_t flags, int64_t* bytes) {
+    const uint32_t in = flags & RMSN_IN_MASK;
+    if (in != RMSN_IN_F32 && in != RMSN_IN_BF16 && in != RMSN_IN_F16) return -1;
+    *bytes = in == RMSN_IN_F32 ? 4 : 2;
+    return (int)in;
+}
+
+// a * b without overflow for sizes (>= 0), saturating far above any memory.
+int64_t times(int64_t a, int64_t b) {
+    if (a != 0 && b > (INT64_MAX / 64) / a) return INT64_MAX / 64;
+    return a * b;
+}
+bool too_big(int64_t n) { return n >= INT64_MAX / 64; }
+
+int launch(const void* fn, dim3 grid, int threads, size_t smem, void* args, bool pdl,
+           cudaStream_t stream) {
+    void* list[] = {args};
+    if (!pdl)
+        return cudaLaunchKernel(fn, grid, dim3(threads), list, smem, stream) == cudaSuccess
+                   ? RMSN_OK
+                   : RMSN_ECUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = grid;
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = stream;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    return cudaLaunchKernelExC(&lc, fn, list) == cudaSuccess ? RMSN_OK : RMSN_ECUDA;
+}
+
+// The cache's shape and pointers; fills the kernels' form of it.
+int check_cache(const rmsattn_cache* c, Cache* out) {
+    if (!c || c->reserved != 0) return RMSN_EINVAL;
+    if (c->n_pages < 0 || c->n_pages > INT32_MAX || c->n_kv_heads < 1 || c->n_kv_heads > 4096)
+        return RMSN_EINVAL;
+    if (c->page_size < kBlock || c->page_size > 65536 || c->page_size % kBlock) return RMSN_EINVAL;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return RMSN_EUNSUPPORTED;
+    const int64_t codes = (int64_t)c->n_kv_heads * c->page_size * c->head_dim;
+    const int64_t scales = (int64_t)c->n_kv_heads * (c->page_size / kBlock);
+    if (c->page_stride < codes || c->page_stride % 16 || c->scale_stride < scales)
+        return RMSN_EINVAL;
+    if (too_big(times(c->n_pages, c->page_stride)) || too_big(times(c->n_pages, c->scale_stride)))
+        return RMSN_EINVAL;
+    if (c->n_pages > 0 && (!c->k || !c->v || !c->k_scale || !c->v_scale)) return RMSN_EINVAL;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
+        !aligned(c->v_scale, 4))
+        return RMSN_EALIGN;
+    out->k = (uint8_t*)c->k;
+    out->v = (uint8_t*)c->v;
+    out->ks = c->k_scale;
+    out->vs = c->v_scale;
+    out->n_pages = c->n_pages;
+    out->page_stride = c->page_stride;
+    out->scale_stride = c->scale_stride;
+    out->H = c->n_kv_heads;
+    out->page = c->page_size;
+    out->D = c->head_dim;
+    return RMSN_OK;
+}
+
+// Block table of n_seqs rows: positions have to fit 30 bits.
+int check_table(const int32_t* table, int64_t stride, int64_t width, int64_t n_seqs, int page) {
+    if (width < 0 || stride < width || times(width, page) > kMaxTokens) return RMSN_EINVAL;
+    if (too_big(times(n_seqs, stride))) return RMSN_EINVAL;
+    if (n_seqs > 0 && width > 0 && !table) return RMSN_EINVAL;
+    return aligned(table, 4) ? RMSN_OK : RMSN_EALIGN;
+}
+
+}  // namespace
+}  // namespace rmsattn
+
+using namespace rmsattn;
+
+RMSATTN_API int rmsattn_qk_rope_fwd(const void* q, const void* k, const void* q_weight,
+                                    const void* k_weight, void* q_out, void* k_out,
+                                    const void* positions, int64_t pos_stride,
+                                    const uint64_t* turns, const int32_t* axis, int64_t n_tokens,
+                                    int64_t n_q_heads, int64_t n_k_heads, int64_t head_dim,
+                                    int64_t rot_dim, int64_t n_axes, int64_t q_stride,
+                                    int64_t k_stride, int64_t q_out_stride, int64_t k_out_stride,
+                                    float eps, float weight_offset, uint32_t flags,
+                                    cudaStream_t stream) {
+    if (flags & ~(RMSN_IN_MASK | RMSN_PDL | RMSATTN_NORM | RMSATTN_INTERLEAVED | RMSATTN_POS_I64))
+        return RMSN_EINVAL;
+    int64_t bytes = 0;
+    const int dt = dtype_of(flags, &bytes);
+    if (dt < 0) return RMSN_EINVAL;
+    if (n_tokens < 0 || n_q_heads < 0 || n_k_heads < 0 || head_dim < 1 || head_dim > 4096)
+        return RMSN_EINVAL;
+    if (n_q_heads > (1 << 20) || n_k_heads > (1 << 20)) return RMSN_EINVAL;
+    if (rot_dim < 0 || rot_dim > head_dim || rot_dim % 2 || n_axes < 0 || n_axes > 64)
+        return RMSN_EINVAL;
+    if (!(eps >= 0.f) || !isfinite(eps) || !isfinite(weight_offset)) return RMSN_EINVAL;
+    if (n_q_heads && (q_stride < n_q_heads * head_dim || q_out_stride < n_q_heads * head_dim))
+        return RMSN_EINVAL;
+    if (n_k_heads && (k_stride < n_k_heads * head_dim || k_out_stride < n_k_heads * head_dim))
+        return RMSN_EINVAL;
+    const int64_t strides[] = {n_q_heads ? q_stride : 0, n_q_heads ? q_out_stride : 0,
+                               n_k_heads ? k_stride : 0, n_k_heads ? k_out_stride : 0};
+    for (int64_t s : strides)
+        if (too_big(times(n_tokens, times(s, 4)))) return RMSN_EINVAL;
+    if (rot_dim && (n_axes < 1 || pos_stride < 0 || too_big(times(n_axes, times(pos_stride, 8)))))
+        return RMSN_EINVAL;
+    if (n_axes > 1 && pos_stride < n_tokens) return RMSN_EINVAL;
+    if (n_tokens == 0 || n_q_heads + n_k_heads == 0) return RMSN_OK;
+    if ((n_q_heads && (!q || !q_out)) || (n_k_heads && (!k || !k_out))) return RMSN_EINVAL;
+    if (rot_dim && (!positions || !turns || !axis)) return RMSN_EINVAL;
+    const void* ptrs[] = {q, k, q_weight, k_weight, q_out, k_out};
+    for (const void* p : ptrs)
+        if (!aligned(p, (uintptr_t)bytes)) return RMSN_EALIGN;
+    if (rot_dim && (!aligned(positions, flags & RMSATTN_POS_I64 ? 8 : 4) || !aligned(turns, 8) ||
+                    !aligned(axis, 4)))
+        return RMSN_EALIGN;
+    DeviceInfo* d = device_info();
+    if (!d) return RMSN_ECUDA;
+    RopeArgs a;
+    memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k = k;
+    a.qw = q_weight;
+    a.kw = k_weight;
+    a.qo = q_out;
+    a.ko = k_out;
+    a.pos = positions;
+    a.turns = turns;
+    a.axis = axis;
+    a.T = n_tokens;
+    a.pos_stride = pos_stride;
+    a.qs = q_stride;
+    a.ks = k_stride;
+    a.qos = q_out_stride;
+    a.kos = k_out_stride;
+    a.Hq = (int32_t)n_q_heads;
+    a.Hk = (int32_t)n_k_heads;
+    a.D = (int32_t)head_dim;
+    a.R = (int32_t)rot_dim;
+    a.n_axes = (int32_t)n_axes;
+    a.norm = (flags & RMSATTN_NORM) ? 1 : 0;
+    a.interleaved = (flags & RMSATTN_INTERLEAVED) ? 1 : 0;
+    a.pos64 = (flags & RMSATTN_POS_I64) ? 1 : 0;
+    a.pdl = (flags & RMSN_PDL) ? 1 : 0;
+    a.eps = eps;
+    a.woff = weight_offset;
+    int64_t blocks = (n_tokens * (n_q_heads + n_k_heads) + 7) / 8;
+    if (blocks > (1 << 30)) blocks = 1 << 30;
+    return launch(rope_generic_kernel(dt), dim3((unsigned)blocks), 256, 0, &a, a.pdl, stream);
+}
+
+RMSATTN_API int rmsattn_kv_append(const rmsattn_cache* cache, const void* k, const void* v,
+                                  int64_t k_stride, int64_t v_stride, const int32_t* block_table,
+                                  int64_t table_stride, int64_t table_width,
+                                  const int32_t* lengths, const int32_t* cu_seqlens,
+                                  int64_t n_tokens, int64_t n_seqs, uint32_t flags,
+                                  cudaStream_t stream) {
+    if (flags & ~(RMSN_IN_MASK | RMSN_PDL)) return RMSN_EINVAL;
+    int64_t bytes = 0;
+    const int dt = dtype_of(flags, &bytes);
+    if (dt < 0) return RMSN_EINVAL;
+    AppendArgs a;
+    memset(&a, 0, sizeof(a));
+    int st = check_cache(cache, &a.c);
+    if (st != RMSN_OK) return st;
+    if (n_tokens < 0 || n_seqs < 0 || n_tokens > kMaxTokens || n_seqs > (1 << 24))
+        return RMSN_EINVAL;
+    if (!cu_seqlens && n_tokens != n_seqs) return RMSN_EINVAL;
+    const int64_t width = (int64_t)a.c.H * a.c.D;
+    if (k_stride < width || v_stride < width || too_big(times(n_tokens, times(k_stride, 4))) ||
+        too_big(times(n_tokens, times(v_stride, 4))))
+        return RMSN_EINVAL;
+    st = check_table(block_table, table_stride, table_width, n_seqs, a.c.page);
+    if (st != RMSN_OK) return st;
+    if (n_tokens == 0 || n_seqs == 0) return RMSN_OK;
+    if (!k || !v || !lengths) return RMSN_EINVAL;
+    if (!aligned(k, (uintptr_t)bytes) || !aligned(v, (uintptr_t)bytes) || !aligned(lengths, 4) ||
+        !aligned(cu_seqlens, 4))
+        return RMSN_EALIGN;
+    DeviceInfo* d = device_info();
+    if (!d) return RMSN_ECUDA;
+    a.k = k;
+    a.v = v;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.table_width = table_width;
+    a.lengths = lengths;
+    a.cu = cu_seqlens;
+    a.T = n_tokens;
+    a.B = n_seqs;
+    a.pdl = (flags & RMSN_PDL) ? 1 : 0;
+    a.status = d->status;
+    const int64_t units = cu_seqlens ? n_tokens / kBlock + 2 * n_seqs : n_seqs;
+    return launch(append_simple_kernel(dt), dim3((unsigned)units, 2 * (unsigned)a.c.H), 128, 0, &a,
+                  a.pdl, stream);
+}
+
+RMSATTN_API int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_queries,
+                                                   int64_t n_q_heads, int64_t n_kv_heads,
+                                                   int64_t head_dim) {
+    if (n_seqs < 0 || n_seqs > (1 << 24) || n_queries < 1 || n_queries > RMSATTN_MAX_QUERIES ||
+        n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads || n_q_heads > 4096)
+        return RMSN_EINVAL;
+    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return RMSN_EUNSUPPORTED;
+    return 0;
+}
+
+RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
+                                     const int32_t* block_table, int64_t table_stride,
+                                     int64_t table_width, const int32_t* lengths, void* out,
+                                     int64_t q_stride, int64_t out_stride, int64_t n_seqs,
+                                     int64_t n_queries, int64_t n_q_heads, float scale,
+                                     int64_t window, int64_t sinks, void* workspace,
+                                     int64_t workspace_bytes, uint32_t flags,
+                                     cudaStream_t stream) {
+    if (flags & ~(RMSN_IN_MASK | RMSN_PDL)) return RMSN_EINVAL;
+    int64_t bytes = 0;
+    const int dt = dtype_of(flags, &bytes);
+    if (dt < 0) return RMSN_EINVAL;
+    if (dt == RMSN_IN_F32) return RMSN_EUNSUPPORTED;
+    AttendArgs a;
+    memset(&a, 0, sizeof(a));
+    int st = check_cache(cache, &a.c);
+    if (st != RMSN_OK) return st;
+    const int64_t need =
+        rmsattn_kv_attention_workspace(n_seqs, n_queries, n_q_heads, a.c.H, a.c.D);
+    if (need < 0) return (int)need;
+    if (!isfinite(scale) || window < 0 || sinks < 0) return RMSN_EINVAL;
+    const int64_t width = n_q_heads * a.c.D;
+    if (q_stride < width || out_stride < width || (q_stride * bytes) % 16 ||
+        (out_stride * bytes) % 16)
+        return RMSN_EINVAL;
+    if (too_big(times(n_seqs * n_queries, times(q_stride, 2))) ||
+        too_big(times(n_seqs * n_queries, times(out_stride, 2))))
+        return RMSN_EINVAL;
+    st = check_table(block_table, table_stride, table_width, n_seqs, a.c.page);
+    if (st != RMSN_OK) return st;
+    if (n_seqs == 0) return RMSN_OK;
+    if (!q || !out || !lengths || (need > 0 && !workspace) || workspace_bytes < need)
+        return RMSN_EINVAL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(workspace, 16))
+        return RMSN_EALIGN;
+    DeviceInfo* d = device_info();
+    if (!d) return RMSN_ECUDA;
+    a.q = q;
+    a.out = out;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.table_width = table_width;
+    a.lengths = lengths;
+    a.B = n_seqs;
+    a.n = (int32_t)n_queries;
+    a.Hq = (int32_t)n_q_heads;
+    a.scale = scale;
+    // wider than any position: every earlier token
+    a.window = window >= kMaxTokens ? 0 : (int32_t)window;
+    a.sinks = (int32_t)(sinks > kMaxTokens ? kMaxTokens : sinks);
+    a.pdl = (flags & RMSN_PDL) ? 1 : 0;
+    a.status = d->status;
+    const int64_t warps = n_seqs * n_queries * n_q_heads;
+    return launch(attend_simple_kernel(dt), dim3((unsigned)((warps + 3) / 4)), 128, 0, &a, a.pdl,
+                  stream);
+}
+
+RMSATTN_API int rmsattn_read_status(uint32_t* status, int clear) {
+    if (!status) return RMSN_EINVAL;
+    DeviceInfo* d = device_info();
+    if (!d) return RMSN_ECUDA;
+    if (cudaMemcpy(status, d->status, sizeof(uint32_t), cudaMemcpyDeviceToHost) != cudaSuccess)
+        return RMSN_ECUDA;
+    if (clear && *status && cudaMemset(d->status, 0, sizeof(uint32_t)) != cudaSuccess)
+        return RMSN_ECUDA;
+    return RMSN_OK;
+}

@@ -1,0 +1,74 @@
+// Kernel arguments and tables of the attention-path operators, shared by the
+// kernels' units and the C-ABI layer.
+#pragma once
+
+#include <stdint.h>
+
+namespace rmsattn {
+
+constexpr int kBlock = 16;          // tokens that share a cache scale
+constexpr uint32_t kBadPage = 4u;   // status bit: a page or token outside the cache
+
+// q / k: first element of token 0's first head; strides in elements.
+struct RopeArgs {
+    const void* q;
+    const void* k;
+    const void* qw;
+    const void* kw;
+    void* qo;
+    void* ko;
+    const void* pos;
+    const uint64_t* turns;
+    const int32_t* axis;
+    int64_t T, pos_stride, qs, ks, qos, kos;
+    int32_t Hq, Hk, D, R;
+    int32_t n_axes;
+    int32_t norm, interleaved, pos64, pdl;
+    float eps, woff;
+};
+
+struct Cache {
+    uint8_t* k;
+    uint8_t* v;
+    float* ks;
+    float* vs;
+    int64_t n_pages, page_stride, scale_stride;
+    int32_t H, page, D;
+};
+
+struct AppendArgs {
+    Cache c;
+    const void* k;
+    const void* v;
+    int64_t k_stride, v_stride;
+    const int32_t* table;
+    int64_t table_stride, table_width;
+    const int32_t* lengths;
+    const int32_t* cu;  // NULL: one token per sequence
+    int64_t T, B;
+    int32_t pdl;
+    uint32_t* status;
+};
+
+struct AttendArgs {
+    Cache c;
+    const void* q;
+    void* out;
+    int64_t q_stride, out_stride;
+    const int32_t* table;
+    int64_t table_stride, table_width;
+    const int32_t* lengths;
+    int64_t B;
+    int32_t n, Hq;
+    float scale;
+    int32_t window, sinks;  // window 0: every earlier token
+    int32_t pdl;
+    uint32_t* status;
+};
+
+// dt: 0 fp32, 1 bf16, 2 fp16 (the RMSN_IN_* values)
+const void* rope_generic_kernel(int dt);
+const void* append_simple_kernel(int dt);
+const void* attend_simple_kernel(int dt);
+
+}  // namespace rmsattn

@@ -4,7 +4,7 @@ Each kernel translation unit is compiled by its own nvcc process in parallel,
 then linked with the C-ABI unit into one shared library that exports only
 the ``rmsnorm_*`` symbols of ``include/rmsnorm.h``.  The CUDA runtime is
 linked statically, so the library needs nothing but the driver at run time.
-The attention-path operators (``csrc/attn``) are built the same way into a
+The attention-path operators (``csrc_attn``) are built the same way into a
 library of their own (``_build/librmsnorm_attn_gb300.so``, the ``rmsattn_*``
 symbols of ``include/rmsnorm_attn.h``).
 
@@ -33,7 +33,7 @@ LIB_NAME = "librmsnorm_gb300.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 CHECKED_PATH = os.path.join(BUILD_DIR, "librmsnorm_gb300_checked.so")
 # the attention-path operators, a library of their own
-ATTN_CSRC = os.path.join(CSRC, "attn")
+ATTN_CSRC = os.path.join(PKG, "csrc_attn")
 ATTN_PATH = os.path.join(BUILD_DIR, "librmsnorm_attn_gb300.so")
 # the bench's C timing harness (not part of the library)
 HOSTCOST_SRC = os.path.join(PKG, "bench_src", "host_cost.cu")

@@ -7,7 +7,7 @@
 
 #include <mutex>
 
-#include "../../../include/rmsnorm_attn.h"
+#include "../../include/rmsnorm_attn.h"
 #include "attn_args.h"
 
 #define RMSATTN_API extern "C" __attribute__((visibility("default")))

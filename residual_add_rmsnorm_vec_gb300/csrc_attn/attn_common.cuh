@@ -1,7 +1,7 @@
 // Device helpers of the attention-path kernels.
 #pragma once
 
-#include "../rmsn_kernels.cuh"
+#include "../csrc/rmsn_kernels.cuh"
 #include "attn_args.h"
 
 namespace rmsattn {

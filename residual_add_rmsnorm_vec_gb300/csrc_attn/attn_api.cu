@@ -6,6 +6,8 @@
 #include <string.h>
 
 #include <mutex>
+#include <utility>
+#include <vector>
 
 #include "../../include/rmsnorm_attn.h"
 #include "attn_args.h"
@@ -26,6 +28,8 @@ struct DeviceInfo {
     int num_sms = 0;
     uint32_t* status = nullptr;
     cudaError_t err = cudaSuccess;
+    std::mutex mu;
+    std::vector<std::pair<const void*, int64_t>> resident;  // attention kernel -> resident blocks
 };
 DeviceInfo g_dev[kMaxDevices];
 
@@ -243,14 +247,62 @@ RMSATTN_API int rmsattn_kv_append(const rmsattn_cache* cache, const void* k, con
                   a.pdl, stream);
 }
 
+namespace {
+
+// Sizes of an attention call, before any device is asked.
+int check_attend(int64_t n_seqs, int64_t n_queries, int64_t n_q_heads, int64_t n_kv_heads,
+                 int64_t head_dim) {
+    if (n_seqs < 0 || n_seqs > (1 << 24) || n_queries < 1 || n_queries > RMSATTN_MAX_QUERIES ||
+        n_kv_heads < 1 || n_q_heads < 1 || n_q_heads > 4096 || n_q_heads % n_kv_heads)
+        return RMSN_EINVAL;
+    return head_dim == 64 || head_dim == 128 || head_dim == 256 ? RMSN_OK : RMSN_EUNSUPPORTED;
+}
+
+const AttendEntry* attend_entry_of(int dt, int64_t D, int64_t cols) {
+    int n = 0;
+    const AttendEntry* t = D == 64 ? attend_kernels_64(&n)
+                                   : (D == 128 ? attend_kernels_128(&n) : attend_kernels_256(&n));
+    // the fewest column tiles that hold all columns, or the most there are
+    const AttendEntry* best = nullptr;
+    for (int i = 0; i < n; ++i) {
+        if (t[i].dt != dt) continue;
+        if (!best || best->NT * 8 < cols) best = &t[i];
+    }
+    return best;
+}
+
+// Resident blocks of an entry on the device (its grid), or 0.
+int64_t attend_blocks(DeviceInfo* d, const AttendEntry* e) {
+    std::lock_guard<std::mutex> lock(d->mu);
+    for (const auto& f : d->resident)
+        if (f.first == e->fn) return f.second;
+    int bps = 0;
+    if (cudaFuncSetAttribute(e->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, e->smem) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&bps, e->fn, e->threads, e->smem) !=
+            cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    const int64_t n = (int64_t)bps * d->num_sms;
+    if (n > 0) d->resident.emplace_back(e->fn, n);
+    return n;
+}
+
+}  // namespace
+
 RMSATTN_API int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_queries,
                                                    int64_t n_q_heads, int64_t n_kv_heads,
                                                    int64_t head_dim) {
-    if (n_seqs < 0 || n_seqs > (1 << 24) || n_queries < 1 || n_queries > RMSATTN_MAX_QUERIES ||
-        n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads || n_q_heads > 4096)
-        return RMSN_EINVAL;
-    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return RMSN_EUNSUPPORTED;
-    return 0;
+    const int st = check_attend(n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim);
+    if (st != RMSN_OK) return st;
+    if (n_seqs == 0) return 0;
+    DeviceInfo* d = device_info();
+    if (!d) return RMSN_ECUDA;
+    const AttendEntry* e =
+        attend_entry_of(RMSN_IN_BF16, head_dim, n_q_heads / n_kv_heads * n_queries);
+    const int64_t blocks = attend_blocks(d, e);
+    return blocks > 0 ? blocks * 2 * e->part * 4 : RMSN_ECUDA;
 }
 
 RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
@@ -270,9 +322,8 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     memset(&a, 0, sizeof(a));
     int st = check_cache(cache, &a.c);
     if (st != RMSN_OK) return st;
-    const int64_t need =
-        rmsattn_kv_attention_workspace(n_seqs, n_queries, n_q_heads, a.c.H, a.c.D);
-    if (need < 0) return (int)need;
+    st = check_attend(n_seqs, n_queries, n_q_heads, a.c.H, a.c.D);
+    if (st != RMSN_OK) return st;
     if (!isfinite(scale) || window < 0 || sinks < 0) return RMSN_EINVAL;
     const int64_t width = n_q_heads * a.c.D;
     if (q_stride < width || out_stride < width || (q_stride * bytes) % 16 ||
@@ -284,12 +335,16 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     st = check_table(block_table, table_stride, table_width, n_seqs, a.c.page);
     if (st != RMSN_OK) return st;
     if (n_seqs == 0) return RMSN_OK;
-    if (!q || !out || !lengths || (need > 0 && !workspace) || workspace_bytes < need)
-        return RMSN_EINVAL;
+    if (!q || !out || !lengths) return RMSN_EINVAL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(workspace, 16))
         return RMSN_EALIGN;
     DeviceInfo* d = device_info();
     if (!d) return RMSN_ECUDA;
+    const int64_t cols = n_q_heads / a.c.H * n_queries;
+    const AttendEntry* e = attend_entry_of(dt, a.c.D, cols);
+    const int64_t resident = attend_blocks(d, e);
+    if (resident < 1) return RMSN_ECUDA;
+    if (!workspace || workspace_bytes < resident * 2 * e->part * 4) return RMSN_EINVAL;
     a.q = q;
     a.out = out;
     a.q_stride = q_stride;
@@ -307,8 +362,20 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     a.sinks = (int32_t)(sinks > kMaxTokens ? kMaxTokens : sinks);
     a.pdl = (flags & RMSN_PDL) ? 1 : 0;
     a.status = d->status;
-    const int64_t warps = n_seqs * n_queries * n_q_heads;
-    return launch(attend_simple_kernel(dt), dim3((unsigned)((warps + 3) / 4)), 128, 0, &a, a.pdl,
+    a.groups = (int32_t)((cols + 8 * e->NT - 1) / (8 * e->NT));
+    a.ws = static_cast<float*>(workspace);
+    // a block takes at least two steps for each of its warps; no more blocks
+    // than the longest sequences that the table holds would fill
+    a.min_chunk = 2 * (e->threads / 32);
+    const int64_t most = (table_width * a.c.page + e->tok - 1) / e->tok;
+    const int64_t steps = times(times(n_seqs, (int64_t)a.c.H * a.groups), most < 1 ? 1 : most);
+    const int64_t full = (steps + a.min_chunk - 1) / a.min_chunk;
+    a.blocks = full < resident ? full : resident;
+    st = launch(e->fn, dim3((unsigned)a.blocks), e->threads, (size_t)e->smem, &a, a.pdl, stream);
+    if (st != RMSN_OK || a.blocks == 1) return st;
+    // always behind the stream's own kernel: a programmatic dependent of it
+    const int64_t used = cols < 8 * e->NT ? cols : 8 * e->NT;
+    return launch(e->join, dim3((unsigned)(a.blocks - 1), (unsigned)used), 128, 0, &a, true,
                   stream);
 }
 

@@ -64,11 +64,26 @@ struct AttendArgs {
     int32_t window, sinks;  // window 0: every earlier token
     int32_t pdl;
     uint32_t* status;
+    // how the line of all steps is shared out
+    int32_t groups;     // column groups of a key head
+    int64_t blocks;     // blocks of the grid
+    int64_t min_chunk;  // steps of a block, at least
+    float* ws;          // two parts for every block
 };
+
+// One compiled attention kernel and the join of its parts.
+struct AttendEntry {
+    int32_t dt, D, NT, tok, threads, smem;
+    int32_t part;  // floats of one part
+    const void* fn;
+    const void* join;
+};
+const AttendEntry* attend_kernels_64(int* n);
+const AttendEntry* attend_kernels_128(int* n);
+const AttendEntry* attend_kernels_256(int* n);
 
 // dt: 0 fp32, 1 bf16, 2 fp16 (the RMSN_IN_* values)
 const void* rope_generic_kernel(int dt);
 const void* append_simple_kernel(int dt);
-const void* attend_simple_kernel(int dt);
 
 }  // namespace rmsattn

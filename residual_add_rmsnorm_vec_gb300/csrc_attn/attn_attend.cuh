@@ -1,0 +1,868 @@
+// Attention over the paged E4M3 cache: the kernels.
+//
+//   s_j = scale q . k_j,  m = max s_j,  out = sum exp(s_j - m) v_j / sum exp(s_j - m)
+//
+// in one pass over the tokens: m, the sum l and the weighted sum O are carried
+// along, and multiplied by exp(m_old - m_new) where the maximum grows.
+//
+// What bounds it.  A decode step reads 2 D + 1/2 bytes per token and key head
+// and does 4 D products for each of the G query heads that share it: DRAM, as
+// long as the G n columns (query head x query token) of a row stay few.  So
+// the work is laid out around the reads:
+//
+// * Columns are the narrow side of mma.m16n8k16: S^T = K Q^T with 16 tokens
+//   as its rows, O^T = V^T P^T with 16 dims as its rows.  The codes are
+//   widened to fp16 (exact) on their way from shared memory into the operand
+//   registers; tcgen05 would need 16-bit copies of the codes in shared memory
+//   first, twice their traffic, for matrices of 8 columns.
+// * A dot product may take its dims in any order, so a lane's 16-byte vector
+//   of K covers four k-steps, and its 16-byte vectors of V (one for each of
+//   its four tokens) cover all of its dims: only vector loads, and the swizzle
+//   of the stage makes them free of bank conflicts.
+// * P^T is turned from S^T's accumulator layout into the second product's
+//   operand layout by movmatrix: no shared memory, and no exchange between
+//   warps before a row ends.
+// * Each warp streams its own steps (16 or 32 tokens) through its own ring of
+//   cp.async stages, pages and scales included, across row borders: no block
+//   barrier in the stream.
+// * The steps of all rows (sequence x key head x column group) form one line
+//   that the blocks of a resident grid share evenly, whatever the lengths.  A
+//   row inside one block is finished there; the parts of a row that a border
+//   cuts go to the workspace in fp32 and are joined, in block order, by a
+//   second launch: results do not depend on timing.
+#pragma once
+
+#include "attn_common.cuh"
+
+namespace rmsattn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTinyScale = 1.17549435e-38f;
+// weights are exp2 of at most 0, times 2^14 before they are rounded to fp16:
+// its subnormals then begin at 2^-38 of a row's largest weight, so that what
+// 2^17 tokens lose at most (2^-39 each) stays below an fp32 rounding
+constexpr float kLift = 16384.f;
+
+// ---------------------------------------------------------------- instructions
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+                 "r"(on ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float exp2a(float x) {  // two ulp; exp2(-inf) = 0
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements held one row to four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float max_over_rows(float v) {  // over lanes of equal lane % 4
+    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+    v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+    return fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+}
+__device__ __forceinline__ float sum_over_rows(float v) {
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+    return v + __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+}
+// High bit of each byte that holds an E4M3 NaN (0x7F or 0xFF).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+// ---------------------------------------------------------------- shape
+
+// D head dim; NT column tiles of 8; KT tiles of 16 tokens in a step; W warps;
+// S ring stages.
+template <int D_, int NT_, int KT_, int W_, int S_>
+struct Shape {
+    static constexpr int D = D_, NT = NT_, KT = KT_, W = W_, S = S_;
+    static constexpr int kTok = 16 * KT;            // tokens of a step
+    static constexpr int kCols = 8 * NT;            // columns of a row
+    static constexpr int kTile = 16 * D;            // bytes of 16 tokens' K
+    static constexpr int kStage = 2 * KT * kTile;   // K tiles, then V tiles
+    static constexpr int kMeta = 16 * KT;           // per stage: K scale, V scale, valid, -
+    static constexpr int kQPitch = 2 * D + 16;      // fp16 query row; + 16: no bank conflicts
+    static constexpr int kJPitch = D + 4;           // fp32 join row
+    static constexpr int kRing = W * S * kStage;
+    static constexpr int kMetaAll = W * S * kMeta;
+    static constexpr int kQ = kCols * kQPitch;
+    static constexpr int kJoin = W * 8 * kJPitch * 4;
+    static constexpr int kSmem = kRing + kMetaAll + kQ + kJoin;
+};
+
+// ---------------------------------------------------------------- rows and steps
+
+// What a sequence's rows see, in tokens and steps of TOK tokens.
+template <int TOK>
+struct Span {
+    int L;      // tokens of the sequence
+    int end;    // tokens within the table: [0, end)
+    int lo;     // first token that any query's window reaches (0 without a window)
+    int sink;   // tokens [0, sink) stay visible
+    int n_sink; // steps before the gap (those of the sinks), or all of them
+    int jump;   // step numbers from n_sink on are this much higher
+    int ns;     // steps, at least 1
+
+    __device__ __forceinline__ void of(const AttendArgs& a, int len) {
+        L = len < 0 ? 0 : len;
+        const int room = (int)(a.table_width * a.c.page);
+        end = L < room ? L : room;
+        lo = 0;
+        sink = a.sinks < end ? a.sinks : end;
+        const int all = (end + TOK - 1) / TOK;
+        n_sink = all;
+        jump = 0;
+        ns = all;
+        if (a.window > 0) {
+            lo = L - a.n - a.window + 1;
+            if (lo < 0) lo = 0;
+            const int s = (sink + TOK - 1) / TOK, w = (lo < end ? lo : end) / TOK;
+            if (w > s) {
+                n_sink = s;
+                jump = w - s;
+                ns = all - jump;
+            }
+        }
+        if (ns < 1) ns = 1;
+    }
+    __device__ __forceinline__ int first_token(int step) const {
+        return (step < n_sink ? step : step + jump) * TOK;
+    }
+};
+
+// A place on the line of all steps: row (b, hc), its first step's place, and
+// the row's steps.
+struct Place {
+    int64_t b;
+    int64_t first;  // place of the row's first step
+    int hc;
+};
+
+// Steps of all rows on the line, each block's share of them, and the row that
+// holds place share * chunk (share = the caller's block).
+struct Line {
+    int64_t total, chunk, at;  // at >= total: nothing there
+    Place row;
+};
+
+__device__ __forceinline__ int64_t chunk_of(const AttendArgs& a, int64_t total) {
+    const int64_t c = (total + a.blocks - 1) / a.blocks;
+    return c < a.min_chunk ? a.min_chunk : c;
+}
+
+// Every thread of the block calls this.  Sequences are scanned THREADS at a
+// time; up to THREADS of them (any usual batch) are scanned once.
+template <int TOK, int THREADS>
+__device__ __forceinline__ void find_share(const AttendArgs& a, int64_t share, Line* line) {
+    __shared__ int64_t sums[THREADS / 32], found[3];
+    constexpr int NW = THREADS / 32;
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const int64_t HC = (int64_t)a.c.H * a.groups;
+    const bool once = a.B <= THREADS;
+    line->at = INT64_MAX;
+    for (int pass = 0; pass < 2; ++pass) {
+        int64_t carry = 0;  // steps of a key head and column group, of the sequences so far
+        for (int64_t b0 = 0; b0 < a.B; b0 += THREADS) {
+            const int64_t b = b0 + threadIdx.x;
+            int64_t ns = 0;
+            if (b < a.B) {
+                Span<TOK> s;
+                s.of(a, a.lengths[b]);
+                ns = s.ns;
+            }
+            int64_t inc = ns;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (lane == 31) sums[wp] = inc;
+            __syncthreads();
+            int64_t before = carry;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const int64_t v = sums[w];
+                if (w < wp) before += v;
+                carry += v;
+            }
+            __syncthreads();
+            if (once) {
+                line->total = carry * HC;
+                line->chunk = chunk_of(a, line->total);
+                line->at = share * line->chunk;
+            }
+            const int64_t p0 = (before + inc - ns) * HC, p1 = (before + inc) * HC;
+            if (b < a.B && line->at >= p0 && line->at < p1) {
+                const int64_t hc = (line->at - p0) / ns;
+                found[0] = b;
+                found[1] = hc;
+                found[2] = p0 + hc * ns;
+            }
+        }
+        if (once) break;
+        line->total = carry * HC;
+        line->chunk = chunk_of(a, line->total);
+        line->at = share * line->chunk;
+        if (line->at >= line->total) break;
+    }
+    __syncthreads();
+    line->row.b = found[0];
+    line->row.hc = (int)found[1];
+    line->row.first = found[2];
+}
+
+// ---------------------------------------------------------------- one row's results
+
+// Column c (0 .. kCols - 1) of column group cg: its query token and head.
+struct Col {
+    int qi, head;
+    bool on;
+};
+__device__ __forceinline__ Col column(const AttendArgs& a, int hk, int cg, int c, int cols) {
+    const int G = a.Hq / a.c.H, cc = cg * cols + c;
+    Col r;
+    r.on = cc < G * a.n;
+    r.qi = cc / G;
+    r.head = hk * G + cc % G;
+    return r;
+}
+
+template <class T>
+__device__ __forceinline__ void store8(const AttendArgs& a, int64_t b, const Col& c, int d,
+                                       const float (&y)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = rmsn::pack2<T>(y[2 * i], y[2 * i + 1]);
+    uint16_t* o = static_cast<uint16_t*>(a.out) + (b * a.n + c.qi) * a.out_stride +
+                  (int64_t)c.head * a.c.D + d;
+    *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Partial results of block `blk`'s first (0) or last (1) row in the workspace.
+template <class C>
+__device__ __forceinline__ float* part_of(const AttendArgs& a, int64_t blk, int which) {
+    return a.ws + (blk * 2 + which) * (int64_t)(C::kCols * (C::D + 2));
+}
+
+// ---------------------------------------------------------------- the stream
+
+template <class T, class C>
+__global__ void __launch_bounds__(C::W * 32) attend_kernel(const AttendArgs a) {
+    constexpr int D = C::D, NT = C::NT, KT = C::KT, W = C::W, S = C::S;
+    constexpr int CH = D / 16;                 // 16-byte chunks of a token
+    constexpr int MT = D / 16;                 // tiles of 16 dims
+    constexpr bool kQRegs = NT == 1 && D <= 128;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ float q_scale[C::kCols];
+    __shared__ float j_m[W][8], j_l[W][8];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    rmsn::pdl_wait(a.pdl);
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+
+    Line line;
+    find_share<C::kTok, W * 32>(a, blockIdx.x, &line);
+    const int64_t begin = line.at;
+    if (begin >= line.total) return;
+    const int64_t stop = begin + line.chunk < line.total ? begin + line.chunk : line.total;
+    const Place at = line.row;
+
+    unsigned char* ring = smem + wp * (S * C::kStage);
+    unsigned char* meta = smem + C::kRing + wp * (S * C::kMeta);
+    unsigned char* qrows = smem + C::kRing + C::kMetaAll;
+    float* join = reinterpret_cast<float*>(smem + C::kRing + C::kMetaAll + C::kQ);
+    const uint32_t ring_s = smem_addr(ring), meta_s = smem_addr(meta);
+
+    // ---- producer: this warp's steps begin + wp, begin + wp + W, ...
+    int64_t p_at = begin + wp, p_b = at.b, p_first = at.first;
+    int p_hc = at.hc;
+    Span<C::kTok> p_span;
+    p_span.of(a, a.lengths[p_b]);
+    int p_len_next = p_b + 1 < a.B ? a.lengths[p_b + 1] : 0;
+    bool p_on = false;
+    int p_t0 = 0, p_in[KT], p_hk = 0;
+    int32_t p_page[KT];  // -1: nothing to load, else the table's entry
+
+    // the next step's row and pages (loaded here, used one step later)
+    auto locate = [&]() {
+        p_on = p_at < stop;
+        if (!p_on) return;
+        while (p_at >= p_first + p_span.ns) {
+            p_first += p_span.ns;
+            if (++p_hc == a.c.H * a.groups) {
+                p_hc = 0;
+                ++p_b;
+                p_span.of(a, p_len_next);
+                p_len_next = p_b + 1 < a.B ? a.lengths[p_b + 1] : 0;
+            }
+        }
+        p_hk = p_hc / a.groups;
+        p_t0 = p_span.first_token((int)(p_at - p_first));
+        const int32_t* row = a.table + p_b * a.table_stride;
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            const int j = p_t0 + 16 * k;
+            p_page[k] = -1;
+            p_in[k] = 0;
+            if (j < p_span.end) {  // within the table's width
+                const int slot = j / a.c.page;
+                p_in[k] = j - slot * a.c.page;
+                p_page[k] = row[slot];
+            }
+        }
+        p_at += W;
+    };
+    // copies of the located step into stage `slot`
+    auto issue = [&](int slot) {
+        if (p_on) {
+            const uint32_t st = ring_s + slot * C::kStage, me = meta_s + slot * C::kMeta;
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                const int j0 = p_t0 + 16 * k;
+                // a tile of which no query sees a token brings nothing in, its scales neither
+                const bool any = j0 < p_span.end && (j0 + 15 >= p_span.lo || j0 < p_span.sink);
+                const bool ok = any && p_page[k] >= 0 && p_page[k] < a.c.n_pages;
+                const int64_t pg = ok ? p_page[k] : 0;
+                const int64_t at8 = pg * a.c.page_stride + ((int64_t)p_hk * a.c.page + p_in[k]) * D;
+                const uint8_t *kp = a.c.k + at8, *vp = a.c.v + at8;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const int e = lane + 32 * i, r = e / CH, c = e % CH, j = j0 + r;
+                    const bool on = ok && j < p_span.end && (j >= p_span.lo || j < p_span.sink);
+                    const uint32_t kd = D == 64 ? e * 16 : (r * CH + (c ^ ((r & 1) * 4))) * 16;
+                    const uint32_t vx = ((r >> 1) & 3) * 2;
+                    const uint32_t vd = (D == 64 ? (e & ~7) + ((e & 7) ^ vx) : r * CH + (c ^ vx)) * 16;
+                    cp16(st + k * C::kTile + kd, kp + r * D + c * 16, on);
+                    cp16(st + (KT + k) * C::kTile + vd, vp + r * D + c * 16, on);
+                }
+                if (lane < 2) {
+                    const int64_t sc = pg * a.c.scale_stride +
+                                       (int64_t)p_hk * (a.c.page / kBlock) + p_in[k] / kBlock;
+                    cp4(me + k * 16 + lane * 4, (lane ? a.c.vs : a.c.ks) + sc, ok);
+                } else if (lane == 2) {
+                    *reinterpret_cast<int*>(meta + slot * C::kMeta + k * 16 + 8) = ok;
+                    if (!ok && any) atomicOr(a.status, kBadPage);
+                }
+            }
+        }
+        cp_commit();
+    };
+
+    locate();
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) {
+        issue(s);
+        locate();
+    }
+
+    // ---- consumer: rows one after another, this warp's steps of each
+    int slot = 0;
+    int64_t cur = begin;  // the row's first place within this block
+    int64_t mine = begin + wp;
+    int64_t c_b = at.b, c_first = at.first;
+    int c_hc = at.hc;
+    Span<C::kTok> span;
+    span.of(a, a.lengths[c_b]);
+    while (cur < stop) {
+        const int64_t row_end = c_first + span.ns;
+        const int64_t seg_end = row_end < stop ? row_end : stop;
+        const int hk = c_hc / a.groups, cg = c_hc % a.groups;
+        if (span.L > span.end && threadIdx.x == 0) atomicOr(a.status, kBadPage);
+
+        // queries in fp16, each scaled by a power of two to at most 2^8 (so
+        // that fp16 holds any bf16 row: what is below 2^-32 of the row's
+        // largest value loses bits); q_scale undoes it, times scale * log2(e)
+        for (int c = wp; c < C::kCols; c += W) {
+            const Col col = column(a, hk, cg, c, C::kCols);
+            float x[D / 32];
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                uint32_t u = 0;
+                if (col.on)
+                    u = *reinterpret_cast<const uint32_t*>(
+                        static_cast<const uint16_t*>(a.q) + (c_b * a.n + col.qi) * a.q_stride +
+                        (int64_t)col.head * D + 64 * i + 2 * lane);
+                x[2 * i] = rmsn::lo2<T>(u);
+                x[2 * i + 1] = rmsn::hi2<T>(u);
+                m = fmaxf(m, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+            }
+            m = rmsn::warp_max(m);
+            int e = (int)(__float_as_uint(m) >> 23) - 127 - 7;  // 2^e <= m / 128 < 2^(e + 1)
+            e = e < -126 ? -126 : (e > 126 ? 126 : e);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            if (lane == 0) q_scale[c] = up * (a.scale * kLog2e);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i)
+                *reinterpret_cast<uint32_t*>(qrows + c * C::kQPitch + (64 * i + 2 * lane) * 2) =
+                    rmsn::pack_f16x2(x[2 * i] * down, x[2 * i + 1] * down);
+        }
+        __syncthreads();
+        float cs[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            cs[nt][0] = q_scale[nt * 8 + 2 * t];
+            cs[nt][1] = q_scale[nt * 8 + 2 * t + 1];
+        }
+        const uint32_t q_s = smem_addr(qrows) + g * C::kQPitch + t * 32;
+        uint4 qf[kQRegs ? CH / 2 : 1];
+        if constexpr (kQRegs) {
+#pragma unroll
+            for (int i = 0; i < CH / 2; ++i) qf[i] = lds16(q_s + (i / 2) * 128 + (i & 1) * 16);
+        }
+        float o[MT][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[i][nt][k] = 0.f;
+        }
+        float vref = kTinyScale;  // O is in units of vref / kLift
+
+        for (; mine < seg_end; mine += W) {
+            cp_wait<S - 2>();
+            __syncwarp();
+            issue(slot == 0 ? S - 1 : slot - 1);
+            locate();
+            const uint32_t st = ring_s + slot * C::kStage;
+            const float* me = reinterpret_cast<const float*>(meta + slot * C::kMeta);
+            float ks[KT], vs[KT];
+            bool ok[KT];
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                ks[k] = me[4 * k];
+                vs[k] = me[4 * k + 1];
+                ok[k] = reinterpret_cast<const int*>(me)[4 * k + 2] != 0;
+            }
+
+            // S^T = K Q^T
+            float s[KT][NT][4];
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s[k][nt][x] = 0.f;
+#pragma unroll
+            for (int j = 0; j < CH / 4; ++j) {
+                uint4 qa[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if constexpr (kQRegs) qa[nt][h] = qf[2 * j + h];
+                        else qa[nt][h] = lds16(q_s + nt * 8 * C::kQPitch + j * 128 + h * 16);
+                    }
+#pragma unroll
+                for (int k = 0; k < KT; ++k) {
+                    const int c = D == 64 ? t : ((t + 4 * j) ^ ((g & 1) * 4));
+                    const uint4 k0 = lds16(st + k * C::kTile + (g * CH + c) * 16);
+                    const uint4 k1 = lds16(st + k * C::kTile + ((g + 8) * CH + c) * 16);
+                    const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t a0 = e4m3x2_to_f16x2(w0[u]), a2 = e4m3x2_to_f16x2(w0[u] >> 16);
+                        const uint32_t a1 = e4m3x2_to_f16x2(w1[u]), a3 = e4m3x2_to_f16x2(w1[u] >> 16);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint4 q = qa[nt][u >> 1];
+                            mma16816(s[k][nt], a0, a1, a2, a3, (u & 1) ? q.z : q.x, (u & 1) ? q.w : q.y);
+                        }
+                    }
+                }
+            }
+
+            // scores in units of log2, masked where a column does not see the token
+            const int t0 = span.first_token((int)(mine - c_first));
+            bool all_ok = true;
+#pragma unroll
+            for (int k = 0; k < KT; ++k) all_ok = all_ok && ok[k];
+            const bool open = all_ok && t0 + C::kTok - 1 <= span.L - a.n &&
+                              (a.window == 0 || t0 > span.L - 1 - a.window || t0 + C::kTok <= span.sink);
+            uint32_t see[KT];  // bit 4 nt + x: this lane's element is visible
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                see[k] = 0xFFFFFFFFu;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) s[k][nt][x] *= ks[k] * cs[nt][x & 1];
+            }
+            if (!open) {
+                const int G = a.Hq / a.c.H;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int pos = span.L - a.n + (cg * C::kCols + nt * 8 + 2 * t + x) / G;
+#pragma unroll
+                        for (int k = 0; k < KT; ++k)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int j = t0 + 16 * k + g + 8 * h;
+                                const bool on = ok[k] && j <= pos && j < span.end &&
+                                                (a.window == 0 || j > pos - a.window || j < a.sinks);
+                                if (!on) {
+                                    s[k][nt][2 * h + x] = -INFINITY;
+                                    see[k] &= ~(1u << (4 * nt + 2 * h + x));
+                                }
+                            }
+                    }
+            }
+
+            // running maximum; what was summed so far follows it
+            bool grew = false;
+            float mm[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float v = fmaxf(s[0][nt][x], s[0][nt][2 + x]);
+#pragma unroll
+                    for (int k = 1; k < KT; ++k) v = fmaxf(v, fmaxf(s[k][nt][x], s[k][nt][2 + x]));
+                    v = fmaxf(max_over_rows(v), m[nt][x]);
+                    grew = grew || v > m[nt][x];
+                    mm[nt][x] = v;
+                }
+            float vmax = vref;
+#pragma unroll
+            for (int k = 0; k < KT; ++k) vmax = fmaxf(vmax, vs[k]);
+            if (__any_sync(0xFFFFFFFFu, grew) || vmax > vref) {
+                const float vr = vref / vmax;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float keep[2];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        keep[x] = mm[nt][x] == -INFINITY ? 1.f : exp2a(m[nt][x] - mm[nt][x]);
+                        l[nt][x] *= keep[x];
+                        m[nt][x] = mm[nt][x];
+                        keep[x] *= vr;
+                    }
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) o[i][nt][x] *= keep[x & 1];
+                }
+                vref = vmax;
+            }
+
+            // weights; P^T as the second product's operand
+            uint32_t pb[KT][NT][2];
+            const float rv = 1.f / vref;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+                const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+                for (int k = 0; k < KT; ++k) {
+                    const float f = vs[k] * rv * kLift;
+                    float p[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        p[x] = exp2a(s[k][nt][x] - ((x & 1) ? m1 : m0));
+                        l[nt][x & 1] += p[x];
+                    }
+                    pb[k][nt][0] = transpose8(rmsn::pack_f16x2(p[0] * f, p[1] * f));
+                    pb[k][nt][1] = transpose8(rmsn::pack_f16x2(p[2] * f, p[3] * f));
+                }
+            }
+
+            // O^T += V^T P^T
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                const uint32_t vt = st + (KT + k) * C::kTile;
+#pragma unroll
+                for (int cj = 0; cj < (D == 256 ? 2 : 1); ++cj) {
+                    constexpr int WD = D == 64 ? 2 : 4;  // words of dims a lane holds per token
+                    uint32_t w[4][WD];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int r = 2 * t + (x & 1) + 8 * (x >> 1);
+                        if constexpr (D == 64) {
+                            const int e = r * 4 + (g >> 1);
+                            const uint2 v = lds8(vt + ((e & ~7) + ((e & 7) ^ (2 * t))) * 16 + (g & 1) * 8);
+                            w[x][0] = v.x;
+                            w[x][1] = v.y;
+                        } else {
+                            const uint4 v = lds16(vt + (r * CH + ((g + 8 * cj) ^ (2 * t))) * 16);
+                            w[x][0] = v.x;
+                            w[x][1] = v.y;
+                            w[x][2] = v.z;
+                            w[x][3] = v.w;
+                        }
+                    }
+                    // A token that some columns see and others do not may hold
+                    // NaN codes, which 0 weights would carry into the others'
+                    // sums: here they count as 0, and a product of "is NaN"
+                    // with "sees it" finds the sums that become NaN.
+                    uint32_t nan[4][WD];
+                    bool any_nan = false;
+                    if (!open && a.n > 1) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int i = 0; i < WD; ++i) {
+                                nan[x][i] = nan_bytes(w[x][i]) >> 7;
+                                any_nan = any_nan || nan[x][i];
+                                w[x][i] &= ~(nan[x][i] * 0xFFu);
+                                nan[x][i] *= 0x38u;  // 1.0
+                            }
+                        any_nan = __any_sync(0xFFFFFFFFu, any_nan);
+                    }
+#pragma unroll
+                    for (int i = 0; i < WD; ++i) {
+                        const uint32_t lo01 = __byte_perm(w[0][i], w[1][i], 0x5140);
+                        const uint32_t hi01 = __byte_perm(w[0][i], w[1][i], 0x7362);
+                        const uint32_t lo23 = __byte_perm(w[2][i], w[3][i], 0x5140);
+                        const uint32_t hi23 = __byte_perm(w[2][i], w[3][i], 0x7362);
+                        const uint32_t a0 = e4m3x2_to_f16x2(lo01), a1 = e4m3x2_to_f16x2(lo01 >> 16);
+                        const uint32_t a2 = e4m3x2_to_f16x2(lo23), a3 = e4m3x2_to_f16x2(lo23 >> 16);
+                        const uint32_t b0 = e4m3x2_to_f16x2(hi01), b1 = e4m3x2_to_f16x2(hi01 >> 16);
+                        const uint32_t b2 = e4m3x2_to_f16x2(hi23), b3 = e4m3x2_to_f16x2(hi23 >> 16);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816(o[cj * 8 + 2 * i][nt], a0, a1, a2, a3, pb[k][nt][0], pb[k][nt][1]);
+                            mma16816(o[cj * 8 + 2 * i + 1][nt], b0, b1, b2, b3, pb[k][nt][0], pb[k][nt][1]);
+                        }
+                    }
+                    if (any_nan) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint32_t e = see[k] >> (4 * nt);
+                            const uint32_t v0 = transpose8(((e & 1) ? 0x3C00u : 0) | ((e & 2) ? 0x3C000000u : 0));
+                            const uint32_t v1 = transpose8(((e & 4) ? 0x3C00u : 0) | ((e & 8) ? 0x3C000000u : 0));
+#pragma unroll
+                            for (int i = 0; i < WD; ++i)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    const int sel = h ? 0x7362 : 0x5140;
+                                    const uint32_t n01 = __byte_perm(nan[0][i], nan[1][i], sel);
+                                    const uint32_t n23 = __byte_perm(nan[2][i], nan[3][i], sel);
+                                    float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma16816(hit, e4m3x2_to_f16x2(n01), e4m3x2_to_f16x2(n01 >> 16),
+                                             e4m3x2_to_f16x2(n23), e4m3x2_to_f16x2(n23 >> 16), v0, v1);
+#pragma unroll
+                                    for (int x = 0; x < 4; ++x)
+                                        if (hit[x] > 0.f) o[cj * 8 + 2 * i + h][nt][x] = NAN;
+                                }
+                        }
+                    }
+                }
+            }
+            slot = slot == S - 1 ? 0 : slot + 1;
+        }
+
+        // the row's (or the part's) results: join the warps, eight columns at a time
+        const bool whole = cur == c_first && seg_end == row_end;
+        const float unit = vref / kLift;
+        float* part = part_of<C>(a, blockIdx.x, cur == begin ? 0 : 1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (nt > 0) __syncthreads();
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const float ls = sum_over_rows(l[nt][x]);
+                const int c = 2 * t + x;
+                if (g == 0) {
+                    j_m[wp][c] = m[nt][x];
+                    j_l[wp][c] = ls;
+                }
+                if (m[nt][x] != -INFINITY || ls != 0.f) {
+                    float* jr = join + (wp * 8 + c) * C::kJPitch;
+#pragma unroll
+                    for (int i = 0; i < MT; i += 2) {
+                        const int d = D == 64 ? g * 8 + 2 * i : (g + 8 * (i / 8)) * 16 + 2 * (i % 8);
+                        *reinterpret_cast<float4*>(jr + d) =
+                            make_float4(o[i][nt][x] * unit, o[i][nt][2 + x] * unit,
+                                        o[i + 1][nt][x] * unit, o[i + 1][nt][2 + x] * unit);
+                    }
+                }
+            }
+            __syncthreads();
+            for (int e = threadIdx.x; e < D; e += W * 32) {  // 8 columns x D / 8 vectors
+                const int c = e / (D / 8), d = e % (D / 8) * 8;
+                const Col col = column(a, hk, cg, nt * 8 + c, C::kCols);
+                if (!col.on) continue;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < W; ++w) mx = fmaxf(mx, j_m[w][c]);
+                const float ms = mx == -INFINITY ? 0.f : mx;
+                float ls = 0.f, y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = 0.f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float lw = j_l[w][c];
+                    if (j_m[w][c] == -INFINITY && lw == 0.f) continue;  // no token of this warp is seen
+                    const float f = exp2a(j_m[w][c] - ms);
+                    ls += lw * f;
+                    const float4* jr = reinterpret_cast<const float4*>(join + (w * 8 + c) * C::kJPitch + d);
+                    const float4 u = jr[0], v = jr[1];
+                    y[0] += u.x * f;
+                    y[1] += u.y * f;
+                    y[2] += u.z * f;
+                    y[3] += u.w * f;
+                    y[4] += v.x * f;
+                    y[5] += v.y * f;
+                    y[6] += v.z * f;
+                    y[7] += v.w * f;
+                }
+                if (whole) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = ls == 0.f ? 0.f : y[k] / ls;
+                    store8<T>(a, c_b, col, d, y);
+                } else {
+                    const int cc = nt * 8 + c;
+                    float4* dst = reinterpret_cast<float4*>(part + cc * D + d);
+                    dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                    dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                    if (d == 0)
+                        *reinterpret_cast<float2*>(part + C::kCols * D + cc * 2) = make_float2(mx, ls);
+                }
+            }
+        }
+        __syncthreads();  // the join rows and statistics are read before they are written again
+
+        cur = seg_end;
+        if (cur < stop) {
+            c_first = row_end;
+            if (++c_hc == a.c.H * a.groups) {
+                c_hc = 0;
+                ++c_b;
+                span.of(a, a.lengths[c_b]);
+            }
+        }
+    }
+    cp_wait<0>();
+}
+
+// Joins the parts of the rows that a block border cuts.  Block (i, c): border
+// i + 1, column c; the row's first border does the work.
+template <class T, class C>
+__global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a) {
+    constexpr int D = C::D, TD = D / 4, NG = 128 / TD;  // threads per part, parts at a time
+    __shared__ float4 sum[NG][TD];
+    __shared__ float sum_l[NG], sum_m[NG];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Line line;
+    find_share<C::kTok, 128>(a, blockIdx.x + 1, &line);
+    const int64_t border = line.at, chunk = line.chunk;
+    if (border >= line.total) return;
+    const Place at = line.row;
+    if (at.first == border || at.first < border - chunk) return;
+    Span<C::kTok> span;
+    span.of(a, a.lengths[at.b]);
+    const int64_t c0 = blockIdx.x, c1 = (at.first + span.ns - 1) / chunk;
+    const int c = blockIdx.y;
+    const Col col = column(a, at.hc / a.groups, at.hc % a.groups, c, C::kCols);
+    if (!col.on) return;
+    const int grp = threadIdx.x / TD, d = threadIdx.x % TD * 4;
+    float m = -INFINITY, l = 0.f;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int64_t i = c0 + grp; i <= c1; i += NG) {
+        const float* part = part_of<C>(a, i, i == c0 && at.first != c0 * chunk ? 1 : 0);
+        const float2 ml = *reinterpret_cast<const float2*>(part + C::kCols * D + c * 2);
+        const float4 v = *reinterpret_cast<const float4*>(part + c * D + d);
+        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing of this part is seen
+        const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
+        const float f0 = exp2a(m - ms), f1 = exp2a(ml.x - ms);
+        m = mn;
+        l = l * f0 + ml.y * f1;
+        y.x = y.x * f0 + v.x * f1;
+        y.y = y.y * f0 + v.y * f1;
+        y.z = y.z * f0 + v.z * f1;
+        y.w = y.w * f0 + v.w * f1;
+    }
+    sum[grp][threadIdx.x % TD] = y;
+    if (threadIdx.x % TD == 0) {
+        sum_l[grp] = l;
+        sum_m[grp] = m;
+    }
+    __syncthreads();
+    if (threadIdx.x >= D / 8) return;
+    float mx = -INFINITY;
+    for (int k = 0; k < NG; ++k) mx = fmaxf(mx, sum_m[k]);
+    const float ms = mx == -INFINITY ? 0.f : mx;
+    float ls = 0.f, r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < NG; ++k) {
+        if (sum_m[k] == -INFINITY && sum_l[k] == 0.f) continue;
+        const float f = exp2a(sum_m[k] - ms);
+        ls += sum_l[k] * f;
+        const float4 u = sum[k][2 * threadIdx.x], v = sum[k][2 * threadIdx.x + 1];
+        r[0] += u.x * f;
+        r[1] += u.y * f;
+        r[2] += u.z * f;
+        r[3] += u.w * f;
+        r[4] += v.x * f;
+        r[5] += v.y * f;
+        r[6] += v.z * f;
+        r[7] += v.w * f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = ls == 0.f ? 0.f : r[k] / ls;
+    store8<T>(a, at.b, col, threadIdx.x * 8, r);
+}
+
+template <class C>
+AttendEntry attend_entry(int dt) {
+    AttendEntry e;
+    e.dt = dt;
+    e.D = C::D;
+    e.NT = C::NT;
+    e.tok = C::kTok;
+    e.threads = C::W * 32;
+    e.smem = C::kSmem;
+    e.part = C::kCols * (C::D + 2);
+    e.fn = dt == 1 ? (const void*)&attend_kernel<BF16, C> : (const void*)&attend_kernel<F16, C>;
+    e.join = dt == 1 ? (const void*)&attend_join_kernel<BF16, C>
+                     : (const void*)&attend_join_kernel<F16, C>;
+    return e;
+}
+
+}  // namespace rmsattn

@@ -194,6 +194,36 @@ RMSATTN_API int rmsattn_qk_rope_fwd(const void* q, const void* k, const void* q_
     a.pdl = (flags & RMSN_PDL) ? 1 : 0;
     a.eps = eps;
     a.woff = weight_offset;
+    a.rcp_d = (head_dim & (head_dim - 1)) == 0 ? 1.0f / (float)head_dim : 0.f;
+
+    // 16-byte vectors: whole chunk pairs in the head and in its turned part,
+    // every head of every operand on a 16-byte boundary
+    const int64_t pair = 32 / bytes;  // elements of a lane's two chunks
+    bool vec = head_dim % pair == 0 && rot_dim % pair == 0 && head_dim / pair <= 32 &&
+               n_tokens < (int64_t(1) << 30);
+    for (const void* p : ptrs) vec = vec && aligned(p, 16);
+    for (int64_t s : strides) vec = vec && (s * bytes) % 16 == 0;
+    if (vec) {
+        int tph = 1;
+        while (tph * pair < head_dim) tph *= 2;
+        // two tokens a block put twice the bytes in flight per lane once
+        // there are blocks enough for every SM
+        const int u = n_tokens >= 4 * (int64_t)d->num_sms ? 2 : 1;
+        int n = 0;
+        const RopeEntry* table = rope_kernels(&n);
+        const RopeEntry* e = nullptr;
+        for (int i = 0; i < n; ++i)
+            if (table[i].dt == dt && table[i].tph == tph && table[i].u == u &&
+                table[i].interleaved == a.interleaved)
+                e = &table[i];
+        // W <= 16 warps of 32 / tph heads, groups of them split evenly
+        const int64_t nh = 32 / tph, warps = (n_q_heads + n_k_heads + nh - 1) / nh;
+        const int64_t gy = (warps + 15) / 16;
+        if (e && gy <= 65535)
+            return launch(e->fn, dim3((unsigned)((n_tokens + u - 1) / u), (unsigned)gy),
+                          (int)((warps + gy - 1) / gy) * 32, (size_t)(u * rot_dim / 2) * 8, &a,
+                          a.pdl, stream);
+    }
     int64_t blocks = (n_tokens * (n_q_heads + n_k_heads) + 7) / 8;
     if (blocks > (1 << 30)) blocks = 1 << 30;
     return launch(rope_generic_kernel(dt), dim3((unsigned)blocks), 256, 0, &a, a.pdl, stream);
@@ -243,8 +273,13 @@ RMSATTN_API int rmsattn_kv_append(const rmsattn_cache* cache, const void* k, con
     a.pdl = (flags & RMSN_PDL) ? 1 : 0;
     a.status = d->status;
     const int64_t units = cu_seqlens ? n_tokens / kBlock + 2 * n_seqs : n_seqs;
-    return launch(append_simple_kernel(dt), dim3((unsigned)units, 2 * (unsigned)a.c.H), 128, 0, &a,
-                  a.pdl, stream);
+    const bool vec = aligned(k, 16) && aligned(v, 16) && (k_stride * bytes) % 16 == 0 &&
+                     (v_stride * bytes) % 16 == 0;
+    // a warp for each head and side of a unit, eight of them a block
+    const int sides = 2 * a.c.H, warps = sides < 8 ? sides : 8;
+    return launch(append_kernel_of(dt, a.c.D, vec),
+                  dim3((unsigned)units, (unsigned)((sides + warps - 1) / warps)), warps * 32, 0,
+                  &a, a.pdl, stream);
 }
 
 namespace {

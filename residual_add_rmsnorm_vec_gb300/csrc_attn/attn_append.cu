@@ -15,10 +15,11 @@ namespace rmsattn {
 struct Unit {
     int64_t b;       // sequence, or -1: none
     int64_t lo;      // position of the block's first token
-    int64_t r0, r1;  // rows of the block that get new tokens: [r0, r1)
-    int64_t src;     // row of k / v that goes to row r0
+    int r0, r1;      // rows of the block that get new tokens: [r0, r1)
+    int64_t src;     // row of k / v that would go to row 0
 };
 
+// The warp's lanes search together, 32 sequences a step.
 __device__ __forceinline__ Unit unit_of(const AppendArgs& a, int64_t u) {
     Unit w;
     w.b = -1;
@@ -28,14 +29,16 @@ __device__ __forceinline__ Unit unit_of(const AppendArgs& a, int64_t u) {
         c0 = u;
         c1 = u + 1;
         base = u;
-        if (b >= a.B) return w;
     } else {
         // the last sequence whose base is at most u
-        int64_t lo = 0, hi = a.B;  // base(lo) <= u < base(hi)
-        while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) / 2;
-            if (((int64_t)a.cu[mid] >> 4) + 2 * mid <= u) lo = mid;
-            else hi = mid;
+        int64_t lo = 0, n = a.B;
+        while (n > 1) {
+            const int64_t step = (n + 31) / 32, i = (threadIdx.x & 31) * step;
+            const bool in = i < n && ((int64_t)a.cu[lo + i] >> 4) + 2 * (lo + i) <= u;
+            const uint32_t hit = __ballot_sync(0xFFFFFFFFu, in) | 1u;
+            const int64_t k = 31 - __clz(hit);
+            lo += k * step;
+            n = n - k * step < step ? n - k * step : step;
         }
         b = lo;
         c0 = a.cu[b];
@@ -43,15 +46,15 @@ __device__ __forceinline__ Unit unit_of(const AppendArgs& a, int64_t u) {
         base = (c0 >> 4) + 2 * b;
     }
     const int64_t len = a.lengths[b];
-    if (len < 0 || c0 < 0 || c1 <= c0 || c1 > a.T) return w;
+    if (len < 0 || c0 < 0 || c1 <= c0 || c1 > a.T || u < base) return w;
     const int64_t n = c1 - c0;
     const int64_t blk = (len >> 4) + (u - base);
-    if (blk < 0 || blk * kBlock >= len + n) return w;
+    if (blk * kBlock >= len + n) return w;
     w.b = b;
     w.lo = blk * kBlock;
-    w.r0 = len > w.lo ? len - w.lo : 0;
-    w.r1 = len + n - w.lo < kBlock ? len + n - w.lo : kBlock;
-    w.src = c0 + w.lo + w.r0 - len;
+    w.r0 = len > w.lo ? (int)(len - w.lo) : 0;
+    w.r1 = len + n - w.lo < kBlock ? (int)(len + n - w.lo) : kBlock;
+    w.src = c0 + w.lo - len;
     return w;
 }
 
@@ -63,54 +66,119 @@ __device__ __forceinline__ float next_scale(float before, float a) {
     return s;
 }
 
-// One block of 128 threads per unit, head and side, element by element.
-template <class T>
-__global__ void __launch_bounds__(128) append_simple(const AppendArgs a) {
-    __shared__ float part[4];
+// One warp per unit, head and side.  D / 8 lanes hold a token, eight elements
+// each, 32 / (D / 8) tokens at a time, so the whole block of 16 tokens is read
+// in one go (4 KB in bf16 at head_dim 128: enough bytes in flight without a
+// ring), stays in registers while the warp finds its largest magnitude, and is
+// written once.  VEC: 16-byte loads; else element by element.
+template <class T, int D, bool VEC>
+__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
+    constexpr int LPR = D / 8, RPS = 32 / LPR, N = kBlock / RPS;
+    constexpr int NW = T::kBytes * 2;  // words of eight elements
     rmsn::pdl_launch_dependents(a.pdl);
     rmsn::pdl_wait(a.pdl);
+    const int hs = (int)blockIdx.y * (int)(blockDim.x >> 5) + (int)(threadIdx.x >> 5);
+    if (hs >= 2 * a.c.H) return;
     const Unit w = unit_of(a, blockIdx.x);
     if (w.b < 0) return;
-    const int h = (int)blockIdx.y >> 1;
-    const bool is_v = blockIdx.y & 1;
-    const int64_t pg = page_of(a.c, a.table + w.b * a.table_stride, a.table_width, w.lo);
-    if (pg < 0) {
-        if (threadIdx.x == 0) atomicOr(a.status, kBadPage);
-        return;
-    }
-    const int D = a.c.D;
-    const int64_t in_page = w.lo % a.c.page;
-    uint8_t* codes = (is_v ? a.c.v : a.c.k) + pg * a.c.page_stride +
-                     ((int64_t)h * a.c.page + in_page) * D;
-    float* scale = (is_v ? a.c.vs : a.c.ks) + pg * a.c.scale_stride +
-                   (int64_t)h * (a.c.page / kBlock) + in_page / kBlock;
+    const int h = hs >> 1, lane = threadIdx.x & 31, r = lane / LPR, d = lane % LPR * 8;
+    const bool is_v = hs & 1;
     const void* x = is_v ? a.v : a.k;
     const int64_t xs = is_v ? a.v_stride : a.k_stride;
-    const int n = (int)(w.r1 - w.r0) * D;
-    float m = 0.f;
-    for (int e = threadIdx.x; e < n; e += 128)
-        m = fmaxf(m, fabsf(load1<T>(x, (w.src + e / D) * xs + (int64_t)h * D + e % D)));
-    m = rmsn::warp_max(m);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
-    const float before = w.r0 > 0 ? *scale : 0.f;
-    __syncthreads();
-    const float s = next_scale(before, fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])));
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-    if (threadIdx.x == 0) *scale = s;
-    if (s > before) {
-        const float ratio = before * r;
-        for (int e = threadIdx.x; e < (int)w.r0 * D; e += 128)
-            codes[e] = (uint8_t)pack_e4m3x2(rmsn::e4m3_value(codes[e]) * ratio, 0.f);
+    uint32_t u[N][NW];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int row = i * RPS + r;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) u[i][k] = 0;
+        if (row < w.r0 || row >= w.r1) continue;
+        const int64_t e = (w.src + row) * xs + (int64_t)h * D + d;
+        if constexpr (VEC) {
+            const char* p = static_cast<const char*>(x) + e * T::kBytes;
+#pragma unroll
+            for (int k = 0; k < NW; k += 4) {
+                const uint4 v = rmsn::ld_stream16(p + 4 * k);
+                u[i][k] = v.x;
+                u[i][k + 1] = v.y;
+                u[i][k + 2] = v.z;
+                u[i][k + 3] = v.w;
+            }
+        } else if constexpr (T::kBytes == 4) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) u[i][k] = static_cast<const uint32_t*>(x)[e + k];
+        } else {
+            const uint16_t* p = static_cast<const uint16_t*>(x) + e;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[i][k] = (uint32_t)p[2 * k] | ((uint32_t)p[2 * k + 1] << 16);
+        }
     }
-    for (int e = threadIdx.x; e < n; e += 128) {
-        const float v = load1<T>(x, (w.src + e / D) * xs + (int64_t)h * D + e % D);
-        codes[w.r0 * D + e] = (uint8_t)pack_e4m3x2(v * r, 0.f);
+    const int64_t pg = page_of(a.c, a.table + w.b * a.table_stride, a.table_width, w.lo);
+    if (pg < 0) {
+        if (lane == 0) atomicOr(a.status, kBadPage);
+        return;
+    }
+    const int in_page = (int)(w.lo % a.c.page);
+    uint8_t* codes = (is_v ? a.c.v : a.c.k) + pg * a.c.page_stride +
+                     ((int64_t)h * a.c.page + in_page) * D + d;
+    float* scale = (is_v ? a.c.vs : a.c.ks) + pg * a.c.scale_stride +
+                   (int64_t)h * (a.c.page / kBlock) + in_page / kBlock;
+    const float before = w.r0 > 0 ? *scale : 0.f;
+    auto value = [&](int i, int k) {  // element k of row i
+        if constexpr (T::kBytes == 4) return __uint_as_float(u[i][k]);
+        else return (k & 1) ? rmsn::hi2<T>(u[i][k >> 1]) : rmsn::lo2<T>(u[i][k >> 1]);
+    };
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; k += 2) m = rmsn::absmax3(m, value(i, k), value(i, k + 1));
+    m = rmsn::warp_max(m);
+    const float s = next_scale(before, m);
+    const float f = s > 0.f ? __frcp_rn(s) : 0.f;
+    __syncwarp();  // every lane has read the scale before
+    if (lane == 0) *scale = s;
+    if (s > before && w.r0 > 0) {  // the older codes follow the scale
+        const float ratio = before * f;
+#pragma unroll 4
+        for (int i = 0; i < N; ++i) {
+            const int row = i * RPS + r;
+            if (row >= w.r0) continue;
+            uint2 c = *reinterpret_cast<const uint2*>(codes + row * D);
+            uint32_t out[2];
+            const uint32_t in[2] = {c.x, c.y};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t lo = e4m3x2_to_f16x2(in[k]), hi = e4m3x2_to_f16x2(in[k] >> 16);
+                out[k] = rmsn::pack_e4m3x4(rmsn::lo2<F16>(lo) * ratio, rmsn::hi2<F16>(lo) * ratio,
+                                           rmsn::lo2<F16>(hi) * ratio, rmsn::hi2<F16>(hi) * ratio);
+            }
+            *reinterpret_cast<uint2*>(codes + row * D) = make_uint2(out[0], out[1]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int row = i * RPS + r;
+        if (row < w.r0 || row >= w.r1) continue;
+        uint32_t out[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            out[k] = rmsn::pack_e4m3x4(value(i, 4 * k) * f, value(i, 4 * k + 1) * f,
+                                       value(i, 4 * k + 2) * f, value(i, 4 * k + 3) * f);
+        *reinterpret_cast<uint2*>(codes + row * D) = make_uint2(out[0], out[1]);
     }
 }
 
-const void* append_simple_kernel(int dt) {
-    return dt == 0 ? (const void*)&append_simple<F32>
-                   : (dt == 1 ? (const void*)&append_simple<BF16> : (const void*)&append_simple<F16>);
+template <int D, bool VEC>
+const void* append_of(int dt) {
+    return dt == 0 ? (const void*)&append_kernel<F32, D, VEC>
+                   : (dt == 1 ? (const void*)&append_kernel<BF16, D, VEC>
+                              : (const void*)&append_kernel<F16, D, VEC>);
+}
+
+const void* append_kernel_of(int dt, int D, bool vec) {
+    if (D == 64) return vec ? append_of<64, true>(dt) : append_of<64, false>(dt);
+    if (D == 128) return vec ? append_of<128, true>(dt) : append_of<128, false>(dt);
+    return vec ? append_of<256, true>(dt) : append_of<256, false>(dt);
 }
 
 }  // namespace rmsattn

@@ -25,7 +25,15 @@ struct RopeArgs {
     int32_t n_axes;
     int32_t norm, interleaved, pos64, pdl;
     float eps, woff;
+    float rcp_d;  // 1 / head_dim when that is exact, else 0
 };
+
+// One compiled 16-byte-vector rotary kernel: tph lanes a head, u tokens a block.
+struct RopeEntry {
+    int32_t dt, tph, u, interleaved;
+    const void* fn;
+};
+const RopeEntry* rope_kernels(int* n);
 
 struct Cache {
     uint8_t* k;
@@ -84,6 +92,6 @@ const AttendEntry* attend_kernels_256(int* n);
 
 // dt: 0 fp32, 1 bf16, 2 fp16 (the RMSN_IN_* values)
 const void* rope_generic_kernel(int dt);
-const void* append_simple_kernel(int dt);
+const void* append_kernel_of(int dt, int D, bool vec);
 
 }  // namespace rmsattn

@@ -18,7 +18,7 @@ namespace rmsattn {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int64_t kMaxTokens = int64_t(1) << 30;  // positions fit 31 bits with room for windows
+constexpr int64_t kMaxTokens = int64_t(1) << 29;  // tokens that a table's row may hold
 
 // Status word of the kernels on each device.
 __device__ uint32_t g_status;
@@ -111,7 +111,7 @@ int check_cache(const rmsattn_cache* c, Cache* out) {
     return RMSN_OK;
 }
 
-// Block table of n_seqs rows: positions have to fit 30 bits.
+// Block table of n_seqs rows.
 int check_table(const int32_t* table, int64_t stride, int64_t width, int64_t n_seqs, int page) {
     if (width < 0 || stride < width || times(width, page) > kMaxTokens) return RMSN_EINVAL;
     if (too_big(times(n_seqs, stride))) return RMSN_EINVAL;
@@ -398,6 +398,8 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     a.pdl = (flags & RMSN_PDL) ? 1 : 0;
     a.status = d->status;
     a.groups = (int32_t)((cols + 8 * e->NT - 1) / (8 * e->NT));
+    a.cols = (int32_t)cols;
+    a.page_rcp = ((uint64_t(1) << 37) + a.c.page / kBlock - 1) / (a.c.page / kBlock);
     a.ws = static_cast<float*>(workspace);
     // a block takes at least two steps for each of its warps; no more blocks
     // than the longest sequences that the table holds would fill
@@ -406,6 +408,7 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     const int64_t steps = times(times(n_seqs, (int64_t)a.c.H * a.groups), most < 1 ? 1 : most);
     const int64_t full = (steps + a.min_chunk - 1) / a.min_chunk;
     a.blocks = full < resident ? full : resident;
+    if (steps / a.blocks > (1 << 30)) return RMSN_EUNSUPPORTED;  // a block counts its steps in 31 bits
     st = launch(e->fn, dim3((unsigned)a.blocks), e->threads, (size_t)e->smem, &a, a.pdl, stream);
     if (st != RMSN_OK || a.blocks == 1) return st;
     // always behind the stream's own kernel: a programmatic dependent of it

@@ -71,8 +71,25 @@ __device__ __forceinline__ float next_scale(float before, float a) {
 // in one go (4 KB in bf16 at head_dim 128: enough bytes in flight without a
 // ring), stays in registers while the warp finds its largest magnitude, and is
 // written once.  VEC: 16-byte loads; else element by element.
+// Held as loaded: the values are widened twice (for the maximum in the 16-bit
+// type itself), so that 64 registers do and 32 warps share an SM.
+template <class T, int D>
+struct AppendBounds {
+    static constexpr int kHeld = D / 16 * T::kBytes * 2;  // registers of a lane's elements
+    static constexpr int kBlocks = kHeld <= 32 ? 4 : (kHeld <= 64 ? 2 : 1);
+};
+// Largest magnitude of the 16-bit pairs a and b, lane by lane (the sign bits
+// of the result say nothing); NaN is left out.
+template <class T>
+__device__ __forceinline__ uint32_t absmax16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if constexpr (rmsn::IsF16<T>::value) asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 template <class T, int D, bool VEC>
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(256, AppendBounds<T, D>::kBlocks) append_kernel(const AppendArgs a) {
     constexpr int LPR = D / 8, RPS = 32 / LPR, N = kBlock / RPS;
     constexpr int NW = T::kBytes * 2;  // words of eight elements
     rmsn::pdl_launch_dependents(a.pdl);
@@ -128,10 +145,23 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
         else return (k & 1) ? rmsn::hi2<T>(u[i][k >> 1]) : rmsn::lo2<T>(u[i][k >> 1]);
     };
     float m = 0.f;
+    if constexpr (T::kBytes == 4) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-        for (int k = 0; k < 8; k += 2) m = rmsn::absmax3(m, value(i, k), value(i, k + 1));
+            for (int k = 0; k < 8; k += 2) m = rmsn::absmax3(m, value(i, k), value(i, k + 1));
+    } else {
+        uint32_t m2 = 0u;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int k = 0; k < NW; ++k) m2 = absmax16x2<T>(m2, u[i][k]);
+        m = rmsn::absmax3(0.f, rmsn::lo2<T>(m2), rmsn::hi2<T>(m2));
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int k = 0; k < NW; ++k) asm volatile("" : "+r"(u[i][k]));
+    }
     m = rmsn::warp_max(m);
     const float s = next_scale(before, m);
     const float f = s > 0.f ? __frcp_rn(s) : 0.f;
@@ -162,8 +192,13 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
         uint32_t out[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            out[k] = rmsn::pack_e4m3x4(value(i, 4 * k) * f, value(i, 4 * k + 1) * f,
-                                       value(i, 4 * k + 2) * f, value(i, 4 * k + 3) * f);
+        {
+            const rmsn::F2 f2 = rmsn::f2(f, f);
+            float x[4];
+            rmsn::f2split(rmsn::mul2(rmsn::f2(value(i, 4 * k), value(i, 4 * k + 1)), f2), x[0], x[1]);
+            rmsn::f2split(rmsn::mul2(rmsn::f2(value(i, 4 * k + 2), value(i, 4 * k + 3)), f2), x[2], x[3]);
+            out[k] = rmsn::pack_e4m3x4(x[0], x[1], x[2], x[3]);
+        }
         *reinterpret_cast<uint2*>(codes + row * D) = make_uint2(out[0], out[1]);
     }
 }

@@ -74,6 +74,8 @@ struct AttendArgs {
     uint32_t* status;
     // how the line of all steps is shared out
     int32_t groups;     // column groups of a key head
+    int32_t cols;       // columns of a key head: query heads x query tokens
+    uint64_t page_rcp;  // ceil(2^37 / (page / 16))
     int64_t blocks;     // blocks of the grid
     int64_t min_chunk;  // steps of a block, at least
     float* ws;          // two parts for every block

@@ -50,6 +50,9 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
                  "r"(on ? 16 : 0)
                  : "memory");
 }
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool on) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
                  "r"(on ? 4 : 0)
@@ -113,20 +116,20 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 
 // D head dim; NT column tiles of 8; KT tiles of 16 tokens in a step; W warps;
 // S ring stages.
-template <int D_, int NT_, int KT_, int W_, int S_>
+// M blocks share an SM.
+template <int D_, int NT_, int KT_, int W_, int S_, int M_>
 struct Shape {
-    static constexpr int D = D_, NT = NT_, KT = KT_, W = W_, S = S_;
+    static constexpr int D = D_, NT = NT_, KT = KT_, W = W_, S = S_, M = M_;
     static constexpr int kTok = 16 * KT;            // tokens of a step
     static constexpr int kCols = 8 * NT;            // columns of a row
     static constexpr int kTile = 16 * D;            // bytes of 16 tokens' K
     static constexpr int kStage = 2 * KT * kTile;   // K tiles, then V tiles
     static constexpr int kMeta = 16 * KT;           // per stage: K scale, V scale, valid, -
     static constexpr int kQPitch = 2 * D + 16;      // fp16 query row; + 16: no bank conflicts
-    static constexpr int kJPitch = D + 4;           // fp32 join row
     static constexpr int kRing = W * S * kStage;
     static constexpr int kMetaAll = W * S * kMeta;
     static constexpr int kQ = kCols * kQPitch;
-    static constexpr int kJoin = W * 8 * kJPitch * 4;
+    static constexpr int kJoin = W * 4 * D * 4;     // fp32, four columns of every warp
     static constexpr int kSmem = kRing + kMetaAll + kQ + kJoin;
 };
 
@@ -287,14 +290,14 @@ __device__ __forceinline__ float* part_of(const AttendArgs& a, int64_t blk, int 
 // ---------------------------------------------------------------- the stream
 
 template <class T, class C>
-__global__ void __launch_bounds__(C::W * 32) attend_kernel(const AttendArgs a) {
+__global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArgs a) {
     constexpr int D = C::D, NT = C::NT, KT = C::KT, W = C::W, S = C::S;
     constexpr int CH = D / 16;                 // 16-byte chunks of a token
     constexpr int MT = D / 16;                 // tiles of 16 dims
     constexpr bool kQRegs = NT == 1 && D <= 128;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ float q_scale[C::kCols];
-    __shared__ float j_m[W][8], j_l[W][8];
+    __shared__ float j_m[W][4], j_l[W][4];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     rmsn::pdl_wait(a.pdl);
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
@@ -313,44 +316,62 @@ __global__ void __launch_bounds__(C::W * 32) attend_kernel(const AttendArgs a) {
     float* join = reinterpret_cast<float*>(smem + C::kRing + C::kMetaAll + C::kQ);
     const uint32_t ring_s = smem_addr(ring), meta_s = smem_addr(meta);
 
-    // ---- producer: this warp's steps begin + wp, begin + wp + W, ...
-    int64_t p_at = begin + wp, p_b = at.b, p_first = at.first;
-    int p_hc = at.hc;
+    // ---- producer: this warp's steps wp, wp + W, ... of the block's `count`
+    const int count = (int)(stop - begin);
+    int p_at = wp, p_first = (int)(at.first - begin), p_hc = at.hc;  // places relative to begin
+    int64_t p_b = at.b;
     Span<C::kTok> p_span;
     p_span.of(a, a.lengths[p_b]);
     int p_len_next = p_b + 1 < a.B ? a.lengths[p_b + 1] : 0;
+    const int32_t* p_row = a.table + p_b * a.table_stride;
     bool p_on = false;
-    int p_t0 = 0, p_in[KT], p_hk = 0;
-    int32_t p_page[KT];  // -1: nothing to load, else the table's entry
+    int p_t0 = 0, p_in[KT], p_hk = p_hc / a.groups;
+    int32_t p_page[KT];  // the table's entry, or -1 past the sequence
 
     // the next step's row and pages (loaded here, used one step later)
     auto locate = [&]() {
-        p_on = p_at < stop;
+        p_on = p_at < count;
         if (!p_on) return;
         while (p_at >= p_first + p_span.ns) {
             p_first += p_span.ns;
             if (++p_hc == a.c.H * a.groups) {
                 p_hc = 0;
                 ++p_b;
+                p_row += a.table_stride;
                 p_span.of(a, p_len_next);
                 p_len_next = p_b + 1 < a.B ? a.lengths[p_b + 1] : 0;
             }
+            p_hk = p_hc / a.groups;
         }
-        p_hk = p_hc / a.groups;
-        p_t0 = p_span.first_token((int)(p_at - p_first));
-        const int32_t* row = a.table + p_b * a.table_stride;
+        p_t0 = p_span.first_token(p_at - p_first);
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
             const int j = p_t0 + 16 * k;
-            p_page[k] = -1;
-            p_in[k] = 0;
-            if (j < p_span.end) {  // within the table's width
-                const int slot = j / a.c.page;
-                p_in[k] = j - slot * a.c.page;
-                p_page[k] = row[slot];
-            }
+            // slot = j / page, both multiples of 16: exact for j < 2^29
+            const int slot = (int)(((uint64_t)(uint32_t)(j >> 4) * a.page_rcp) >> 37);
+            p_in[k] = j - slot * a.c.page;
+            p_page[k] = j < p_span.end ? p_row[slot] : -1;  // end lies within the table
         }
         p_at += W;
+    };
+    // Lane constants of the copies: chunk i of a tile is 512 i bytes on in
+    // memory, and in the stage too, but for V's swizzle, which flips with i.
+    const int l_row = lane / CH, l_chunk = lane % CH;
+    uint32_t k_dst, v_dst[2];
+    if constexpr (D == 64) {  // two tokens to a 128-byte line, 8 tokens a copy
+        k_dst = lane * 16;
+        v_dst[0] = v_dst[1] = ((lane & ~7) + ((lane & 7) ^ (((l_row >> 1) & 3) * 2))) * 16;
+    } else if constexpr (D == 128) {  // 4 tokens a copy
+        k_dst = (l_row * CH + (l_chunk ^ ((l_row & 1) * 4))) * 16;
+        v_dst[0] = (l_row * CH + (l_chunk ^ ((l_row >> 1) * 2))) * 16;
+        v_dst[1] = (l_row * CH + (l_chunk ^ (((l_row >> 1) * 2) ^ 4))) * 16;
+    } else {  // 2 tokens a copy
+        k_dst = (l_row * CH + (l_chunk ^ (l_row * 4))) * 16;
+        v_dst[0] = v_dst[1] = lane * 16;  // and the swizzle (i & 3) * 2, below
+    }
+    auto v_at = [&](int i) -> uint32_t {
+        if constexpr (D == 256) return v_dst[0] ^ ((i & 3) * 32);
+        else return v_dst[i & 1];
     };
     // copies of the located step into stage `slot`
     auto issue = [&](int slot) {
@@ -361,23 +382,30 @@ __global__ void __launch_bounds__(C::W * 32) attend_kernel(const AttendArgs a) {
                 const int j0 = p_t0 + 16 * k;
                 // a tile of which no query sees a token brings nothing in, its scales neither
                 const bool any = j0 < p_span.end && (j0 + 15 >= p_span.lo || j0 < p_span.sink);
-                const bool ok = any && p_page[k] >= 0 && p_page[k] < a.c.n_pages;
+                const bool ok = any && (uint32_t)p_page[k] < (uint32_t)a.c.n_pages;
                 const int64_t pg = ok ? p_page[k] : 0;
-                const int64_t at8 = pg * a.c.page_stride + ((int64_t)p_hk * a.c.page + p_in[k]) * D;
+                const int64_t at8 =
+                    pg * a.c.page_stride + (int64_t)(p_hk * a.c.page + p_in[k]) * D + lane * 16;
                 const uint8_t *kp = a.c.k + at8, *vp = a.c.v + at8;
+                const uint32_t kd = st + k * C::kTile + k_dst, vd = st + (KT + k) * C::kTile;
+                if (ok && j0 + 16 <= p_span.end && j0 >= p_span.lo) {
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const int e = lane + 32 * i, r = e / CH, c = e % CH, j = j0 + r;
-                    const bool on = ok && j < p_span.end && (j >= p_span.lo || j < p_span.sink);
-                    const uint32_t kd = D == 64 ? e * 16 : (r * CH + (c ^ ((r & 1) * 4))) * 16;
-                    const uint32_t vx = ((r >> 1) & 3) * 2;
-                    const uint32_t vd = (D == 64 ? (e & ~7) + ((e & 7) ^ vx) : r * CH + (c ^ vx)) * 16;
-                    cp16(st + k * C::kTile + kd, kp + r * D + c * 16, on);
-                    cp16(st + (KT + k) * C::kTile + vd, vp + r * D + c * 16, on);
+                    for (int i = 0; i < D / 32; ++i) {
+                        cp16(kd + i * 512, kp + i * 512);
+                        cp16(vd + v_at(i) + i * 512, vp + i * 512);
+                    }
+                } else {  // rows that no query sees are zeros
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const int j = j0 + l_row + i * (32 / CH);
+                        const bool on = ok && j < p_span.end && (j >= p_span.lo || j < p_span.sink);
+                        cp16(kd + i * 512, kp + i * 512, on);
+                        cp16(vd + v_at(i) + i * 512, vp + i * 512, on);
+                    }
                 }
                 if (lane < 2) {
-                    const int64_t sc = pg * a.c.scale_stride +
-                                       (int64_t)p_hk * (a.c.page / kBlock) + p_in[k] / kBlock;
+                    const int64_t sc = pg * a.c.scale_stride + p_hk * (a.c.page / kBlock) +
+                                       p_in[k] / kBlock;
                     cp4(me + k * 16 + lane * 4, (lane ? a.c.vs : a.c.ks) + sc, ok);
                 } else if (lane == 2) {
                     *reinterpret_cast<int*>(meta + slot * C::kMeta + k * 16 + 8) = ok;
@@ -397,15 +425,15 @@ __global__ void __launch_bounds__(C::W * 32) attend_kernel(const AttendArgs a) {
 
     // ---- consumer: rows one after another, this warp's steps of each
     int slot = 0;
-    int64_t cur = begin;  // the row's first place within this block
-    int64_t mine = begin + wp;
-    int64_t c_b = at.b, c_first = at.first;
-    int c_hc = at.hc;
+    int cur = 0;  // the row's first place within this block
+    int mine = wp;
+    int64_t c_b = at.b;
+    int c_first = (int)(at.first - begin), c_hc = at.hc;
     Span<C::kTok> span;
     span.of(a, a.lengths[c_b]);
-    while (cur < stop) {
-        const int64_t row_end = c_first + span.ns;
-        const int64_t seg_end = row_end < stop ? row_end : stop;
+    while (cur < count) {
+        const int row_end = c_first + span.ns;
+        const int seg_end = row_end < count ? row_end : count;
         const int hk = c_hc / a.groups, cg = c_hc % a.groups;
         if (span.L > span.end && threadIdx.x == 0) atomicOr(a.status, kBadPage);
 
@@ -517,7 +545,7 @@ __global__ void __launch_bounds__(C::W * 32) attend_kernel(const AttendArgs a) {
             }
 
             // scores in units of log2, masked where a column does not see the token
-            const int t0 = span.first_token((int)(mine - c_first));
+            const int t0 = span.first_token(mine - c_first);
             bool all_ok = true;
 #pragma unroll
             for (int k = 0; k < KT; ++k) all_ok = all_ok && ok[k];
@@ -697,79 +725,88 @@ __global__ void __launch_bounds__(C::W * 32) attend_kernel(const AttendArgs a) {
             slot = slot == S - 1 ? 0 : slot + 1;
         }
 
-        // the row's (or the part's) results: join the warps, eight columns at a time
+        // the row's (or the part's) results: join the warps, four columns at a
+        // time (lanes t of one parity hold four of a tile's columns)
         const bool whole = cur == c_first && seg_end == row_end;
         const float unit = vref / kLift;
-        float* part = part_of<C>(a, blockIdx.x, cur == begin ? 0 : 1);
+        float* part = part_of<C>(a, blockIdx.x, cur == 0 ? 0 : 1);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            if (nt > 0) __syncthreads();
+            float ls[2];
+            ls[0] = sum_over_rows(l[nt][0]);
+            ls[1] = sum_over_rows(l[nt][1]);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const float ls = sum_over_rows(l[nt][x]);
-                const int c = 2 * t + x;
-                if (g == 0) {
-                    j_m[wp][c] = m[nt][x];
-                    j_l[wp][c] = ls;
-                }
-                if (m[nt][x] != -INFINITY || ls != 0.f) {
-                    float* jr = join + (wp * 8 + c) * C::kJPitch;
+            for (int half = 0; half < 2; ++half) {
+                const int first = nt * 8 + half * 4;
+                if (cg * C::kCols + first >= a.cols) break;  // the same for all threads
+                if (first > 0) __syncthreads();
+                if ((t >> 1) == half) {
 #pragma unroll
-                    for (int i = 0; i < MT; i += 2) {
-                        const int d = D == 64 ? g * 8 + 2 * i : (g + 8 * (i / 8)) * 16 + 2 * (i % 8);
-                        *reinterpret_cast<float4*>(jr + d) =
-                            make_float4(o[i][nt][x] * unit, o[i][nt][2 + x] * unit,
-                                        o[i + 1][nt][x] * unit, o[i + 1][nt][2 + x] * unit);
+                    for (int x = 0; x < 2; ++x) {
+                        const int c = 2 * (t & 1) + x;
+                        if (g == 0) {
+                            j_m[wp][c] = m[nt][x];
+                            j_l[wp][c] = ls[x];
+                        }
+                        float* jr = join + (wp * 4 + c) * D;
+#pragma unroll
+                        for (int i = 0; i < MT; i += 2) {
+                            const int d = D == 64 ? g * 8 + 2 * i : (g + 8 * (i / 8)) * 16 + 2 * (i % 8);
+                            *reinterpret_cast<float4*>(jr + d) =
+                                make_float4(o[i][nt][x] * unit, o[i][nt][2 + x] * unit,
+                                            o[i + 1][nt][x] * unit, o[i + 1][nt][2 + x] * unit);
+                        }
                     }
                 }
-            }
-            __syncthreads();
-            for (int e = threadIdx.x; e < D; e += W * 32) {  // 8 columns x D / 8 vectors
-                const int c = e / (D / 8), d = e % (D / 8) * 8;
-                const Col col = column(a, hk, cg, nt * 8 + c, C::kCols);
-                if (!col.on) continue;
-                float mx = -INFINITY;
+                __syncthreads();
+                for (int e = threadIdx.x; e < D / 2; e += W * 32) {  // 4 columns x D / 8 vectors
+                    const int c = e / (D / 8), d = e % (D / 8) * 8;
+                    const Col col = column(a, hk, cg, first + c, C::kCols);
+                    if (!col.on) continue;
+                    float mx = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < W; ++w) mx = fmaxf(mx, j_m[w][c]);
-                const float ms = mx == -INFINITY ? 0.f : mx;
-                float ls = 0.f, y[8];
+                    for (int w = 0; w < W; ++w) mx = fmaxf(mx, j_m[w][c]);
+                    const float ms = mx == -INFINITY ? 0.f : mx;
+                    float lsum = 0.f, y[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = 0.f;
+                    for (int k = 0; k < 8; ++k) y[k] = 0.f;
 #pragma unroll
-                for (int w = 0; w < W; ++w) {
-                    const float lw = j_l[w][c];
-                    if (j_m[w][c] == -INFINITY && lw == 0.f) continue;  // no token of this warp is seen
-                    const float f = exp2a(j_m[w][c] - ms);
-                    ls += lw * f;
-                    const float4* jr = reinterpret_cast<const float4*>(join + (w * 8 + c) * C::kJPitch + d);
-                    const float4 u = jr[0], v = jr[1];
-                    y[0] += u.x * f;
-                    y[1] += u.y * f;
-                    y[2] += u.z * f;
-                    y[3] += u.w * f;
-                    y[4] += v.x * f;
-                    y[5] += v.y * f;
-                    y[6] += v.z * f;
-                    y[7] += v.w * f;
-                }
-                if (whole) {
+                    for (int w = 0; w < W; ++w) {
+                        const float lw = j_l[w][c];
+                        if (j_m[w][c] == -INFINITY && lw == 0.f) continue;  // it saw no token
+                        const float f = exp2a(j_m[w][c] - ms);
+                        lsum += lw * f;
+                        const float4* jr = reinterpret_cast<const float4*>(join + (w * 4 + c) * D + d);
+                        const float4 u = jr[0], v = jr[1];
+                        y[0] += u.x * f;
+                        y[1] += u.y * f;
+                        y[2] += u.z * f;
+                        y[3] += u.w * f;
+                        y[4] += v.x * f;
+                        y[5] += v.y * f;
+                        y[6] += v.z * f;
+                        y[7] += v.w * f;
+                    }
+                    if (whole) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] = ls == 0.f ? 0.f : y[k] / ls;
-                    store8<T>(a, c_b, col, d, y);
-                } else {
-                    const int cc = nt * 8 + c;
-                    float4* dst = reinterpret_cast<float4*>(part + cc * D + d);
-                    dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-                    dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-                    if (d == 0)
-                        *reinterpret_cast<float2*>(part + C::kCols * D + cc * 2) = make_float2(mx, ls);
+                        for (int k = 0; k < 8; ++k) y[k] = lsum == 0.f ? 0.f : y[k] / lsum;
+                        store8<T>(a, c_b, col, d, y);
+                    } else {
+                        const int cc = first + c;
+                        float4* dst = reinterpret_cast<float4*>(part + cc * D + d);
+                        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                        if (d == 0)
+                            *reinterpret_cast<float2*>(part + C::kCols * D + cc * 2) =
+                                make_float2(mx, lsum);
+                    }
                 }
             }
         }
         __syncthreads();  // the join rows and statistics are read before they are written again
 
         cur = seg_end;
-        if (cur < stop) {
+        if (cur < count) {
             c_first = row_end;
             if (++c_hc == a.c.H * a.groups) {
                 c_hc = 0;

@@ -92,28 +92,78 @@ struct Chunk {
     static constexpr int kElems = 16 / T::kBytes;
 };
 
+using rmsn::F2;
+
+// One 16-byte chunk as its four words, and as pairs of neighbouring elements.
+struct Words {
+    uint32_t u[4];
+};
+__device__ __forceinline__ Words words(const uint4& v) { return {{v.x, v.y, v.z, v.w}}; }
+
 template <class T>
-__device__ __forceinline__ void unpack16(const uint4& v, float (&x)[16 / T::kBytes]) {
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void widen(const Words& w, F2 (&y)[8 / T::kBytes]) {
+    if constexpr (T::kBytes == 4) {
+        y[0] = rmsn::f2(__uint_as_float(w.u[0]), __uint_as_float(w.u[1]));
+        y[1] = rmsn::f2(__uint_as_float(w.u[2]), __uint_as_float(w.u[3]));
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if constexpr (T::kBytes == 4) {
-            x[k] = __uint_as_float(u[k]);
-        } else {
-            x[2 * k] = rmsn::lo2<T>(u[k]);
-            x[2 * k + 1] = rmsn::hi2<T>(u[k]);
-        }
+        for (int k = 0; k < 4; ++k) y[k] = rmsn::widen2<T>(w.u[k]);
     }
 }
 template <class T>
-__device__ __forceinline__ uint4 pack16(const float (&x)[16 / T::kBytes]) {
-    uint32_t u[4];
+__device__ __forceinline__ float sum_squares(const Words& w, float acc) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        if constexpr (T::kBytes == 4) u[k] = __float_as_uint(x[k]);
-        else u[k] = rmsn::pack2<T>(x[2 * k], x[2 * k + 1]);
+        if constexpr (T::kBytes == 4) {
+            const float x = __uint_as_float(w.u[k]);
+            acc = fmaf(x, x, acc);
+        } else {
+            acc = rmsn::sumsq16x2<T>(w.u[k], acc);
+        }
     }
-    return make_uint4(u[0], u[1], u[2], u[3]);
+    return acc;
+}
+// y = (w + woff) * (x * inv).  Without an offset the 16-bit product x w is
+// exact in fp32 and goes into the FMA unwidened: y = RN((x w) inv).
+template <class T>
+__device__ __forceinline__ void normed(const Words& x, const Words& w, float inv, float woff,
+                                       F2 (&y)[8 / T::kBytes]) {
+    const F2 inv2 = rmsn::f2(inv, inv);
+    if constexpr (T::kBytes == 2) {
+        if (woff == 0.f) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                y[k] = rmsn::mul2(rmsn::mul16x2_exact<T>(x.u[k], w.u[k]), inv2);
+            return;
+        }
+    }
+    F2 v[8 / T::kBytes];
+    widen<T>(x, y);
+    widen<T>(w, v);
+#pragma unroll
+    for (int k = 0; k < 8 / T::kBytes; ++k)
+        y[k] = rmsn::mul2(rmsn::add2(v[k], rmsn::f2(woff, woff)), rmsn::mul2(y[k], inv2));
+}
+template <class T>
+__device__ __forceinline__ void store_chunk(char* p, const F2 (&y)[8 / T::kBytes]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int k = 0; k < 8 / T::kBytes; ++k) {
+        float lo, hi;
+        rmsn::f2split(y[k], lo, hi);
+        if constexpr (T::kBytes == 4) {
+            u[2 * k] = __float_as_uint(lo);
+            u[2 * k + 1] = __float_as_uint(hi);
+        } else {
+            u[k] = rmsn::pack2<T>(lo, hi);
+        }
+    }
+    rmsn::st_stream16(p, u);
+}
+__device__ __forceinline__ void lds_f2x2(const float* p, F2& a, F2& b) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    a = rmsn::f2(v.x, v.y);
+    b = rmsn::f2(v.z, v.w);
 }
 
 // Multi-head, U tokens a block.  Warp w of block (b, y) holds heads
@@ -121,10 +171,11 @@ __device__ __forceinline__ uint4 pack16(const float (&x)[16 / T::kBytes]) {
 template <class T, int TPH, int U, bool INTER>
 __global__ void __launch_bounds__(512) rope_vec(const RopeArgs a) {
     constexpr int VE = Chunk<T>::kElems;  // elements of a chunk
+    constexpr int NP = VE / 2;            // F2 of a chunk
     constexpr int NH = 32 / TPH;
-    // [U][R / 2] (cos, sin), element k of all lanes' chunks side by side: a
-    // warp's reads of it fall on different banks
-    extern __shared__ float2 cs_all[];
+    // per token R / 2 cosines, then as many sines, in fours: four of lane 0,
+    // four of lane 1, ...; a warp's 16-byte reads fall on different banks
+    extern __shared__ __align__(16) float cs_all[];
     rmsn::pdl_launch_dependents(a.pdl);
     const int lane = threadIdx.x & 31, sub = lane % TPH;
     const int hh = ((int)blockIdx.y * (int)(blockDim.x >> 5) + (int)(threadIdx.x >> 5)) * NH + lane / TPH;
@@ -136,100 +187,99 @@ __global__ void __launch_bounds__(512) rope_vec(const RopeArgs a) {
     const int e0 = rot ? sub * VE : a.R + (sub - turned) * 2 * VE;
     const int e1 = rot ? a.R / 2 + sub * VE : e0 + VE;
     const int h = is_q ? hh : hh - a.Hq;
-    const char* src = static_cast<const char*>(is_q ? a.q : a.k);
-    char* dst = static_cast<char*>(is_q ? a.qo : a.ko);
     const int64_t ss = is_q ? a.qs : a.ks, ds = is_q ? a.qos : a.kos;
+    const char* src = static_cast<const char*>(is_q ? a.q : a.k) + (int64_t)h * a.D * T::kBytes;
+    char* dst = static_cast<char*>(is_q ? a.qo : a.ko) + (int64_t)h * a.D * T::kBytes;
     const char* w = static_cast<const char*>(is_q ? a.qw : a.kw);
     const int P = a.R / 2;
     rmsn::pdl_wait(a.pdl);
     const int64_t t0 = (int64_t)blockIdx.x * U;
-    uint4 x0[U], x1[U], w0, w1;
+    uint4 x0[U], x1[U];
+    uint4 w0 = make_uint4(0u, 0u, 0u, 0u), w1 = w0;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
+        x0[j] = x1[j] = make_uint4(0u, 0u, 0u, 0u);
         if (on && t0 + j < a.T) {
-            const char* p = src + ((t0 + j) * ss + (int64_t)h * a.D) * T::kBytes;
+            const char* p = src + (t0 + j) * ss * T::kBytes;
             x0[j] = rmsn::ld_stream16(p + e0 * T::kBytes);
             x1[j] = rmsn::ld_stream16(p + e1 * T::kBytes);
-        } else {
-            x0[j] = x1[j] = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-    const bool weighted = a.norm && w != nullptr && on;
-    if (weighted) {
-        w0 = rmsn::ld_keep16(w + e0 * T::kBytes);
-        w1 = rmsn::ld_keep16(w + e1 * T::kBytes);
+    if (a.norm && on) {
+        if (w) {
+            w0 = rmsn::ld_keep16(w + e0 * T::kBytes);
+            w1 = rmsn::ld_keep16(w + e1 * T::kBytes);
+        } else {
+            const uint32_t one = rmsn::ones_word<T>();
+            w0 = w1 = make_uint4(one, one, one, one);
+        }
     }
     for (int i = threadIdx.x; i < U * P; i += blockDim.x) {
-        const int64_t t = t0 + i / P;
-        if (t >= a.T) continue;
-        const int p = i % P;
-        int at;
-        if constexpr (INTER) {
-            const int half = P / 2, q = p % half;
-            at = p - q + (q % (VE / 2)) * turned + q / (VE / 2);
+        const int j = i / P, p = i - j * P;
+        if (t0 + j >= a.T) continue;
+        const float2 cs = turn(a, p, t0 + j);
+        // lane and place of the pair among the lane's VE pairs
+        int s, k;
+        if constexpr (INTER) {  // NP pairs of the first chunk, NP of the second
+            const int half = P / 2, q = p < half ? p : p - half;
+            s = q / NP;
+            k = q % NP + (p < half ? 0 : NP);
         } else {
-            at = (p % VE) * turned + p / VE;
+            s = p / VE;
+            k = p % VE;
         }
-        cs_all[i - p + at] = turn(a, p, t);
+        float* c = cs_all + j * 2 * P + ((k >> 2) * turned + s) * 4 + (k & 3);
+        c[0] = cs.x;
+        c[P] = cs.y;
     }
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-        float y0[VE], y1[VE];
-        unpack16<T>(x0[j], y0);
-        unpack16<T>(x1[j], y1);
+        F2 y0[NP], y1[NP];
         if (a.norm) {
-            float acc = 0.f;
-#pragma unroll
-            for (int k = 0; k < VE; ++k) acc = fmaf(y0[k], y0[k], acc);
-#pragma unroll
-            for (int k = 0; k < VE; ++k) acc = fmaf(y1[k], y1[k], acc);
+            float acc = sum_squares<T>(words(x1[j]), sum_squares<T>(words(x0[j]), 0.f));
 #pragma unroll
             for (int o = TPH / 2; o > 0; o >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, o);
             const float inv = __frsqrt_rn(__fadd_rn(
                 a.rcp_d > 0.f ? __fmul_rn(acc, a.rcp_d) : __fdiv_rn(acc, (float)a.D), a.eps));
-            float v0[VE], v1[VE];
-            if (weighted) {
-                unpack16<T>(w0, v0);
-                unpack16<T>(w1, v1);
-            } else {
-#pragma unroll
-                for (int k = 0; k < VE; ++k) v0[k] = v1[k] = 1.f;
-            }
-#pragma unroll
-            for (int k = 0; k < VE; ++k) {
-                y0[k] = (v0[k] + a.woff) * (y0[k] * inv);
-                y1[k] = (v1[k] + a.woff) * (y1[k] * inv);
-            }
+            normed<T>(words(x0[j]), words(w0), inv, a.woff, y0);
+            normed<T>(words(x1[j]), words(w1), inv, a.woff, y1);
+        } else {
+            widen<T>(words(x0[j]), y0);
+            widen<T>(words(x1[j]), y1);
         }
         if (!on || t0 + j >= a.T) continue;
         if (rot) {
-            const float2* cs = cs_all + j * P;
-            if constexpr (INTER) {
-                // pairs e / 2 of both chunks
+            const float* cs = cs_all + j * 2 * P + sub * 4;
 #pragma unroll
-                for (int k = 0; k < VE / 2; ++k) {
-                    const float2 c0 = cs[k * turned + sub], c1 = cs[P / 2 + k * turned + sub];
-                    const float p0 = y0[2 * k], q0 = y0[2 * k + 1], p1 = y1[2 * k], q1 = y1[2 * k + 1];
-                    y0[2 * k] = p0 * c0.x - q0 * c0.y;
-                    y0[2 * k + 1] = q0 * c0.x + p0 * c0.y;
-                    y1[2 * k] = p1 * c1.x - q1 * c1.y;
-                    y1[2 * k + 1] = q1 * c1.x + p1 * c1.y;
-                }
-            } else {
+            for (int k = 0; k < VE / 4; ++k) {  // four pairs
+                F2 c[2], s[2];
+                lds_f2x2(cs + k * turned * 4, c[0], c[1]);
+                lds_f2x2(cs + P + k * turned * 4, s[0], s[1]);
+                if constexpr (INTER) {
 #pragma unroll
-                for (int k = 0; k < VE; ++k) {
-                    const float2 c = cs[k * turned + sub];
-                    const float p = y0[k], q = y1[k];
-                    y0[k] = p * c.x - q * c.y;
-                    y1[k] = q * c.x + p * c.y;
+                    for (int i = 0; i < 4; ++i) {
+                        F2& y = 4 * k + i < NP ? y0[(4 * k + i) % NP] : y1[(4 * k + i) % NP];
+                        float cl[2], sl[2], p, q;
+                        rmsn::f2split(c[i >> 1], cl[0], cl[1]);
+                        rmsn::f2split(s[i >> 1], sl[0], sl[1]);
+                        rmsn::f2split(y, p, q);
+                        y = rmsn::f2(p * cl[i & 1] - q * sl[i & 1], q * cl[i & 1] + p * sl[i & 1]);
+                    }
+                } else {
+                    const F2 neg = rmsn::f2(-1.f, -1.f);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const F2 p = y0[2 * k + i], q = y1[2 * k + i];
+                        y0[2 * k + i] = rmsn::fma2(q, rmsn::mul2(s[i], neg), rmsn::mul2(p, c[i]));
+                        y1[2 * k + i] = rmsn::fma2(p, s[i], rmsn::mul2(q, c[i]));
+                    }
                 }
             }
         }
-        char* p = dst + ((t0 + j) * ds + (int64_t)h * a.D) * T::kBytes;
-        const uint4 o0 = pack16<T>(y0), o1 = pack16<T>(y1);
-        rmsn::st_stream16(p + e0 * T::kBytes, &o0.x);
-        rmsn::st_stream16(p + e1 * T::kBytes, &o1.x);
+        char* p = dst + (t0 + j) * ds * T::kBytes;
+        store_chunk<T>(p + e0 * T::kBytes, y0);
+        store_chunk<T>(p + e1 * T::kBytes, y1);
     }
 }
 

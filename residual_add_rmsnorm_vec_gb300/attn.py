@@ -18,32 +18,24 @@ from .api import _IN, _check
 _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
-def _on(device, stream):
-    """(cudaStream_t, stream to enter or None, caller's stream) of a call on
-    `device`: outputs and workspaces are allocated, and the launch made, with
-    that device and stream current."""
+# (cudaStream_t of the current stream of a device index; no Stream object)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+@contextlib.contextmanager
+def _other(device, stream):
+    """Device and stream of a call that names a stream, or whose tensors are
+    on another device than the current one: outputs and workspaces are
+    allocated, and the launch made, with both current.  Yields (cudaStream_t,
+    keep): keep(t) holds a new output's memory back from other streams' use
+    while the caller's stream still works on it."""
     caller = torch.cuda.current_stream(device)
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return caller.cuda_stream, None, caller
         stream = caller
     elif stream.device != device:
         raise ValueError(f"stream must be on {device}, got {stream.device}")
-    return stream.cuda_stream, stream, caller
-
-
-def _enter(s):
-    return contextlib.nullcontext() if s is None else torch.cuda.stream(s)
-
-
-def _new(shape, dtype, device, s, caller):
-    """An output of a call on stream s (None: the caller's own): its memory
-    comes from that stream's pool, and is not handed on while the caller's
-    stream still works on it."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if s is not None and s != caller:
-        t.record_stream(caller)
-    return t
+    with torch.cuda.stream(stream):
+        yield stream.cuda_stream, (lambda t: t.record_stream(caller)) if stream != caller else None
 
 
 class RopeTable:
@@ -51,7 +43,7 @@ class RopeTable:
     fractions of a turn per position), ``axis`` (int32, the axis whose position
     turns the pair), both [rot_dim / 2] on the device; made by ``rope_table``."""
 
-    __slots__ = ("turns", "axis", "rot_dim", "n_axes")
+    __slots__ = ("turns", "axis", "rot_dim", "n_axes", "index", "turns_ptr", "axis_ptr")
 
     def __init__(self, turns: torch.Tensor, axis: torch.Tensor, n_axes: int):
         if turns.dim() != 1:
@@ -60,6 +52,8 @@ class RopeTable:
         _check("axis", axis, (turns.numel(),), (torch.int32,), turns.device)
         self.turns, self.axis = turns, axis
         self.rot_dim, self.n_axes = 2 * turns.numel(), int(n_axes)
+        self.index = turns.get_device()
+        self.turns_ptr, self.axis_ptr = turns.data_ptr(), axis.data_ptr()
 
 
 def rope_table(rot_dim: int, *, base: float = 10000.0, sections=None, axis=None, inv_freq=None,
@@ -105,21 +99,28 @@ def rope_table(rot_dim: int, *, base: float = 10000.0, sections=None, axis=None,
 def _heads(name, t, head_dim):
     """(heads, token stride) of [T, H * head_dim] or [T, H, head_dim] with the
     heads of a token back to back."""
-    if t.dim() == 2:
-        width = t.shape[1]
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        width = shape[1]
         if width % head_dim:
             raise ValueError(f"{name}: rows must hold whole heads of head_dim elements")
-        ok = t.stride(1) == 1 or width == 1
-    elif t.dim() == 3:
-        if t.shape[2] != head_dim:
+        ok = stride[1] == 1 or width == 1
+    elif len(shape) == 3:
+        if shape[2] != head_dim:
             raise ValueError(f"{name}: rows must hold whole heads of head_dim elements")
-        width = t.shape[1] * head_dim
-        ok = (t.stride(2) == 1 or head_dim == 1) and (t.stride(1) == head_dim or t.shape[1] <= 1)
+        width = shape[1] * head_dim
+        ok = (stride[2] == 1 or head_dim == 1) and (stride[1] == head_dim or shape[1] <= 1)
     else:
         raise ValueError(f"{name} must be [T, heads * head_dim] or [T, heads, head_dim]")
     if not ok:
         raise ValueError(f"{name}: a token's heads must lie back to back")
-    return width // head_dim, (t.stride(0) if t.shape[0] > 1 else width)
+    return width // head_dim, (stride[0] if shape[0] > 1 else width)
+
+
+def _like(name, out, x, dt, index):
+    if out.shape != x.shape or out.dtype != dt or out.get_device() != index:
+        raise ValueError(f"{name} must be like {name[0]}")
+    return out
 
 
 def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torch.Tensor,
@@ -144,72 +145,81 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
         return q_out, k_out
     if head_dim < 1:
         raise ValueError("head_dim must be positive")
-    dt, dev, T = ref.dtype, ref.device, ref.shape[0]
-    if dt not in _IN:
+    dt, index, T = ref.dtype, ref.get_device(), ref.shape[0]
+    flags = _IN.get(dt)
+    if flags is None:
         raise TypeError(f"unsupported dtype {dt}")
-    if table.rot_dim > head_dim:
-        raise ValueError(f"the table turns {table.rot_dim} elements of heads of {head_dim}")
-    hq = qs = hk = ks = 0
+    rot, n_axes = table.rot_dim, table.n_axes
+    if rot > head_dim:
+        raise ValueError(f"the table turns {rot} elements of heads of {head_dim}")
+    hq = qs = hk = ks = qos = kos = 0
     if q is not None:
         hq, qs = _heads("q", q, head_dim)
     if k is not None:
         hk, ks = _heads("k", k, head_dim)
-        if q is not None and (k.shape[0] != T or k.dtype != dt or k.device != dev):
+        if q is not None and (k.shape[0] != T or k.dtype != dt or k.get_device() != index):
             raise ValueError("q and k need the same tokens, dtype and device")
-    if positions.dim() == 1 and table.n_axes == 1:
-        positions = positions[None]
-    if tuple(positions.shape) != (table.n_axes, T):
-        raise ValueError(f"positions must be [{table.n_axes}, {T}], got {tuple(positions.shape)}")
-    if positions.dtype not in (torch.int32, torch.int64):
-        raise TypeError(f"positions must be int32 or int64, got {positions.dtype}")
-    if T > 1 and positions.stride(1) != 1:
+    shape, pstride = positions.shape, positions.stride()
+    if len(shape) == 2:
+        if shape[0] != n_axes or shape[1] != T:
+            raise ValueError(f"positions must be [{n_axes}, {T}], got {tuple(shape)}")
+    elif len(shape) != 1 or n_axes != 1 or shape[0] != T:
+        raise ValueError(f"positions must be [{n_axes}, {T}], got {tuple(shape)}")
+    pdt = positions.dtype
+    if pdt is torch.int64:
+        flags |= _al.RMSATTN_POS_I64
+    elif pdt is not torch.int32:
+        raise TypeError(f"positions must be int32 or int64, got {pdt}")
+    if T > 1 and pstride[-1] != 1:
         raise ValueError("positions of an axis must be contiguous")
-    if not ref.is_cuda:
+    if index < 0:
         raise ValueError("q / k must be CUDA tensors")
-    if positions.device != dev or table.turns.device != dev:
-        raise ValueError(f"positions and table must be on {dev}")
-    flags = _IN[dt]
+    if positions.get_device() != index or table.index != index:
+        raise ValueError(f"positions and table must be on {ref.device}")
     if eps is None:
         if q_weight is not None or k_weight is not None:
             raise ValueError("weights need the norm's eps")
+        eps = 0.0
     else:
         flags |= _al.RMSATTN_NORM
-        if q_weight is not None:
-            _check("q_weight", q_weight, (head_dim,), (dt,), dev)
-        if k_weight is not None:
-            _check("k_weight", k_weight, (head_dim,), (dt,), dev)
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None and (w.dtype != dt or w.dim() != 1 or w.shape[0] != head_dim
+                                  or w.get_device() != index or (head_dim > 1 and w.stride(0) != 1)):
+                raise ValueError(f"{name} must be a contiguous [{head_dim}] {dt} on {ref.device}")
     if interleaved:
         flags |= _al.RMSATTN_INTERLEAVED
-    if positions.dtype == torch.int64:
-        flags |= _al.RMSATTN_POS_I64
     if pdl:
         flags |= _lib.RMSN_PDL
-    handle, s, caller = _on(dev, stream)
-    with _enter(s):
-        qos = kos = 0
-        if q is not None:
-            if q_out is None:
-                q_out = _new(q.shape, dt, dev, s, caller)
-            elif q_out.shape != q.shape or q_out.dtype != dt or q_out.device != dev:
-                raise ValueError("q_out must be like q")
-            qos = _heads("q_out", q_out, head_dim)[1]
-        if k is not None:
-            if k_out is None:
-                k_out = _new(k.shape, dt, dev, s, caller)
-            elif k_out.shape != k.shape or k_out.dtype != dt or k_out.device != dev:
-                raise ValueError("k_out must be like k")
-            kos = _heads("k_out", k_out, head_dim)[1]
-        st = _al.load_attn().rmsattn_qk_rope_fwd(
-            q.data_ptr() if q is not None else None, k.data_ptr() if k is not None else None,
-            None if q_weight is None else q_weight.data_ptr(),
-            None if k_weight is None else k_weight.data_ptr(),
-            q_out.data_ptr() if q is not None else None,
-            k_out.data_ptr() if k is not None else None,
-            positions.data_ptr(), positions.stride(0) if table.n_axes > 1 else T,
-            table.turns.data_ptr(), table.axis.data_ptr(), T, hq, hk, head_dim, table.rot_dim,
-            table.n_axes, qs, ks, qos, kos, 0.0 if eps is None else eps, weight_offset, flags,
-            handle)
-    if st != _lib.RMSN_OK:
+    if stream is not None or index != torch._C._cuda_getDevice():
+        with _other(ref.device, stream) as (_, keep):
+            new_q, new_k = q is not None and q_out is None, k is not None and k_out is None
+            q_out, k_out = qk_norm_rope(q, k, positions, table, q_weight, k_weight,
+                                        head_dim=head_dim, eps=eps if flags & _al.RMSATTN_NORM else None,
+                                        weight_offset=weight_offset, interleaved=interleaved,
+                                        q_out=q_out, k_out=k_out, pdl=pdl)
+            for t in (q_out if new_q else None, k_out if new_k else None):
+                if t is not None and keep is not None:
+                    keep(t)
+        return q_out, k_out
+    if q is not None:
+        if q_out is None:
+            q_out, qos = torch.empty(q.shape, dtype=dt, device=ref.device), hq * head_dim
+        else:
+            qos = _heads("q_out", _like("q_out", q_out, q, dt, index), head_dim)[1]
+    if k is not None:
+        if k_out is None:
+            k_out, kos = torch.empty(k.shape, dtype=dt, device=ref.device), hk * head_dim
+        else:
+            kos = _heads("k_out", _like("k_out", k_out, k, dt, index), head_dim)[1]
+    st = _al.load_attn().rmsattn_qk_rope_fwd(
+        None if q is None else q.data_ptr(), None if k is None else k.data_ptr(),
+        None if q_weight is None else q_weight.data_ptr(),
+        None if k_weight is None else k_weight.data_ptr(),
+        None if q is None else q_out.data_ptr(), None if k is None else k_out.data_ptr(),
+        positions.data_ptr(), pstride[0] if n_axes > 1 else T, table.turns_ptr, table.axis_ptr, T,
+        hq, hk, head_dim, rot, n_axes, qs, ks, qos, kos, eps, weight_offset, flags,
+        _raw_stream(index))
+    if st:
         raise _lib.RmsnError(st, "rmsattn_qk_rope_fwd")
     return q_out, k_out
 
@@ -223,7 +233,7 @@ class KVCache:
     a model in one tensor), the rest of each tensor is contiguous."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "n_pages", "n_kv_heads", "page_size", "head_dim",
-                 "device", "_c")
+                 "device", "index", "_c", "_ref")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
                  v_scale: torch.Tensor):
@@ -242,17 +252,26 @@ class KVCache:
                 raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
             if t.device != k.device:
                 raise ValueError(f"{name} must be on {k.device}, got {t.device}")
-            if pages and not t[0].is_contiguous():
+            # each page contiguous; pages any stride apart
+            inner = 1
+            for size, step in zip(want[:0:-1], t.stride()[:0:-1]):
+                if size > 1 and step != inner:
+                    break
+                inner *= size
+            else:
+                continue
+            if pages:
                 raise ValueError(f"{name}: each page must be contiguous")
         if pages > 1 and (k.stride(0) != v.stride(0) or k_scale.stride(0) != v_scale.stride(0)):
             raise ValueError("k and v need the same page stride, and so do their scales")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
         self._c = _al.RmsattnCache(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
             k.stride(0) if pages > 1 else heads * page * dim,
             k_scale.stride(0) if pages > 1 else shape[1] * shape[2], heads, page, dim, 0)
+        self._ref = ctypes.byref(self._c)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int,
@@ -268,17 +287,20 @@ class KVCache:
 
 
 def _check_seqs(cache, block_table, lengths, n_seqs):
-    if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
-        raise ValueError(f"block_table must be [{n_seqs}, pages], got {tuple(block_table.shape)}")
-    if block_table.dtype != torch.int32 or lengths.dtype != torch.int32:
+    """The table's row stride and width; both tensors as the kernels read them."""
+    shape, stride = block_table.shape, block_table.stride()
+    if len(shape) != 2 or shape[0] != n_seqs:
+        raise ValueError(f"block_table must be [{n_seqs}, pages], got {tuple(shape)}")
+    if block_table.dtype is not torch.int32 or lengths.dtype is not torch.int32:
         raise TypeError("block_table and lengths must be int32")
     if lengths.dim() != 1 or lengths.shape[0] != n_seqs:
         raise ValueError(f"lengths must be [{n_seqs}], got {tuple(lengths.shape)}")
-    if ((block_table.shape[1] > 1 and block_table.stride(1) != 1)
-            or (n_seqs > 1 and lengths.stride(0) != 1)):
+    width = shape[1]
+    if (width > 1 and stride[1] != 1) or (n_seqs > 1 and lengths.stride(0) != 1):
         raise ValueError("block_table rows and lengths must be contiguous")
-    if block_table.device != cache.device or lengths.device != cache.device:
+    if block_table.get_device() != cache.index or lengths.get_device() != cache.index:
         raise ValueError(f"block_table and lengths must be on {cache.device}")
+    return (stride[0] if n_seqs > 1 else width), width
 
 
 def kv_cache_append_(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
@@ -297,32 +319,50 @@ def kv_cache_append_(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_tab
     """
     hk, ks = _heads("k", k, cache.head_dim)
     hv, vs = _heads("v", v, cache.head_dim)
-    T = k.shape[0]
-    if hk != cache.n_kv_heads or hv != cache.n_kv_heads:
+    T, dt, index = k.shape[0], k.dtype, cache.index
+    if hk != cache.n_kv_heads or hv != hk:
         raise ValueError(f"k and v must hold {cache.n_kv_heads} heads")
-    if v.shape[0] != T or k.dtype != v.dtype:
+    if v.shape[0] != T or v.dtype != dt:
         raise ValueError("k and v need the same tokens and dtype")
-    if k.dtype not in _IN:
-        raise TypeError(f"unsupported dtype {k.dtype}")
-    _check_seqs(cache, block_table, lengths, lengths.shape[0] if lengths.dim() else 0)
-    n = lengths.shape[0]
+    flags = _IN.get(dt)
+    if flags is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    n = lengths.shape[0] if lengths.dim() == 1 else 0
+    stride, width = _check_seqs(cache, block_table, lengths, n)
     if cu_seqlens is None:
         if T != n:
             raise ValueError(f"without cu_seqlens, k must have one row for each of {n} sequences")
-    else:
+    elif (cu_seqlens.dtype is not torch.int32 or cu_seqlens.dim() != 1
+          or cu_seqlens.shape[0] != n + 1 or cu_seqlens.get_device() != index
+          or (n and cu_seqlens.stride(0) != 1)):
         _check("cu_seqlens", cu_seqlens, (n + 1,), (torch.int32,), cache.device)
-    if not k.is_cuda or k.device != cache.device or v.device != cache.device:
-        raise ValueError(f"k and v must be on the cache's CUDA device {cache.device}")
-    handle, s, caller = _on(cache.device, stream)
-    with _enter(s):
-        st = _al.load_attn().rmsattn_kv_append(
-            ctypes.byref(cache._c), k.data_ptr(), v.data_ptr(), ks, vs, block_table.data_ptr(),
-            block_table.stride(0) if n > 1 else block_table.shape[1], block_table.shape[1],
-            lengths.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(), T, n,
-            _IN[k.dtype] | (_lib.RMSN_PDL if pdl else 0), handle)
-    if st != _lib.RMSN_OK:
+    if index < 0 or k.get_device() != index or v.get_device() != index:
+        raise ValueError(f"k and v must be on the cache's CUDA device, {cache.device}")
+    if stream is not None or index != torch._C._cuda_getDevice():
+        with _other(cache.device, stream):
+            return kv_cache_append_(cache, k, v, block_table, lengths, cu_seqlens, pdl=pdl)
+    st = _al.load_attn().rmsattn_kv_append(
+        cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, block_table.data_ptr(), stride, width,
+        lengths.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(), T, n,
+        flags | _lib.RMSN_PDL if pdl else flags, _raw_stream(index))
+    if st:
         raise _lib.RmsnError(st, "rmsattn_kv_append")
     return cache
+
+
+def _token_stride(name, t, n):
+    """Elements between the tokens of [n_seqs, heads, head_dim] (n = 1) or
+    [n_seqs, n, heads, head_dim], which must be evenly spaced with their heads
+    back to back."""
+    shape, stride = t.shape, t.stride()
+    H, D = shape[-2], shape[-1]
+    if stride[-1] != 1 or (H > 1 and stride[-2] != D):
+        raise ValueError(f"{name}: a token's heads must lie back to back")
+    if n > 1:
+        if shape[0] > 1 and stride[0] != n * stride[1]:
+            raise ValueError(f"{name}: the tokens must be evenly spaced")
+        return stride[1]
+    return stride[0] if shape[0] > 1 else H * D
 
 
 def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor,
@@ -341,62 +381,53 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     (length 0, a padded row) gives 0.  ``scale``: default 1 / sqrt(head_dim).
     Returns out, shaped like q.
     """
-    if q.dim() == 3:
-        q4 = q.unsqueeze(1)
-    elif q.dim() == 4:
-        q4 = q
+    shape, dt, index = q.shape, q.dtype, cache.index
+    if len(shape) == 3:
+        B, H, D = shape
+        n = 1
+    elif len(shape) == 4:
+        B, n, H, D = shape
     else:
         raise ValueError("q must be [n_seqs, heads, head_dim] or [n_seqs, n, heads, head_dim]")
-    B, n, H, D = q4.shape
-    if D != cache.head_dim or H < 1 or H % cache.n_kv_heads:
-        raise ValueError(f"q must hold a multiple of {cache.n_kv_heads} heads of {cache.head_dim}")
+    Hk = cache.n_kv_heads
+    if D != cache.head_dim or H < 1 or H % Hk:
+        raise ValueError(f"q must hold a multiple of {Hk} heads of {cache.head_dim}")
     if not 1 <= n <= _al.RMSATTN_MAX_QUERIES:
         raise ValueError(f"1 to {_al.RMSATTN_MAX_QUERIES} query tokens a sequence, got {n}")
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
+    if dt is not torch.bfloat16 and dt is not torch.float16:
+        raise TypeError(f"q must be bfloat16 or float16, got {dt}")
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
-    _check_seqs(cache, block_table, lengths, B)
-    if not q.is_cuda or q.device != cache.device:
-        raise ValueError(f"q must be on the cache's CUDA device {cache.device}")
-    qs = _token_stride("q", q4)
+    stride, width = _check_seqs(cache, block_table, lengths, B)
+    if index < 0 or q.get_device() != index:
+        raise ValueError(f"q must be on the cache's CUDA device, {cache.device}")
+    if stream is not None or index != torch._C._cuda_getDevice():
+        with _other(cache.device, stream) as (_, keep):
+            new = out is None
+            out = kv_cache_attention(q, cache, block_table, lengths, scale=scale, window=window,
+                                     sinks=sinks, out=out, pdl=pdl)
+            if new and keep is not None:
+                keep(out)
+        return out
+    qs = _token_stride("q", q, n)
     lib = _al.load_attn()
-    handle, s, caller = _on(cache.device, stream)
-    with _enter(s):
-        if out is None:
-            out = _new(q.shape, q.dtype, q.device, s, caller)
-            os = H * D
-        else:
-            if out.shape != q.shape or out.dtype != q.dtype or out.device != q.device:
-                raise ValueError("out must be like q")
-            os = _token_stride("out", out if q.dim() == 4 else out.unsqueeze(1))
-        need = lib.rmsattn_kv_attention_workspace(B, n, H, cache.n_kv_heads, D)
-        if need < 0:
-            raise _lib.RmsnError(need, "rmsattn_kv_attention_workspace")
-        # freed when this returns: the allocator hands it to later work of the
-        # same stream only, which runs behind the kernels
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        st = lib.rmsattn_kv_attention(
-            q.data_ptr(), ctypes.byref(cache._c), block_table.data_ptr(),
-            block_table.stride(0) if B > 1 else block_table.shape[1], block_table.shape[1],
-            lengths.data_ptr(), out.data_ptr(), qs, os, B, n, H,
-            1.0 / math.sqrt(D) if scale is None else scale, window, sinks,
-            None if ws is None else ws.data_ptr(), need,
-            _IN[q.dtype] | (_lib.RMSN_PDL if pdl else 0), handle)
-    if st != _lib.RMSN_OK:
+    if out is None:
+        out, os = torch.empty(shape, dtype=dt, device=cache.device), H * D
+    else:
+        if out.shape != shape or out.dtype != dt or out.get_device() != index:
+            raise ValueError("out must be like q")
+        os = _token_stride("out", out, n)
+    need = lib.rmsattn_kv_attention_workspace(B, n, H, Hk, D)
+    if need < 0:
+        raise _lib.RmsnError(need, "rmsattn_kv_attention_workspace")
+    # freed when this returns: the allocator hands it to later work of the
+    # same stream only, which runs behind the kernels
+    ws = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    flags = _IN[dt]
+    st = lib.rmsattn_kv_attention(
+        q.data_ptr(), cache._ref, block_table.data_ptr(), stride, width, lengths.data_ptr(),
+        out.data_ptr(), qs, os, B, n, H, 1.0 / math.sqrt(D) if scale is None else scale, window,
+        sinks, ws.data_ptr(), need, flags | _lib.RMSN_PDL if pdl else flags, _raw_stream(index))
+    if st:
         raise _lib.RmsnError(st, "rmsattn_kv_attention")
     return out
-
-
-def _token_stride(name, t):
-    """Elements between the tokens of [n_seqs, n, heads, head_dim], which must
-    be evenly spaced with their heads back to back."""
-    B, n, H, D = t.shape
-    if t.stride(3) != 1 or (H > 1 and t.stride(2) != D):
-        raise ValueError(f"{name}: a token's heads must lie back to back")
-    if n > 1:
-        step = t.stride(1)
-        if B > 1 and t.stride(0) != n * step:
-            raise ValueError(f"{name}: the tokens must be evenly spaced")
-        return step
-    return t.stride(0) if B > 1 else H * D

@@ -324,6 +324,10 @@ int64_t attend_blocks(DeviceInfo* d, const AttendEntry* e) {
     return n;
 }
 
+int64_t workspace_of(const AttendEntry* e, int64_t blocks) {
+    return blocks * (kCutBytes + 2 * (int64_t)e->part * 4);
+}
+
 }  // namespace
 
 RMSATTN_API int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_queries,
@@ -337,7 +341,7 @@ RMSATTN_API int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_que
     const AttendEntry* e =
         attend_entry_of(RMSN_IN_BF16, head_dim, n_q_heads / n_kv_heads * n_queries);
     const int64_t blocks = attend_blocks(d, e);
-    return blocks > 0 ? blocks * 2 * e->part * 4 : RMSN_ECUDA;
+    return blocks > 0 ? workspace_of(e, blocks) : RMSN_ECUDA;
 }
 
 RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
@@ -379,7 +383,7 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     const AttendEntry* e = attend_entry_of(dt, a.c.D, cols);
     const int64_t resident = attend_blocks(d, e);
     if (resident < 1) return RMSN_ECUDA;
-    if (!workspace || workspace_bytes < resident * 2 * e->part * 4) return RMSN_EINVAL;
+    if (!workspace || workspace_bytes < workspace_of(e, resident)) return RMSN_EINVAL;
     a.q = q;
     a.out = out;
     a.q_stride = q_stride;
@@ -400,7 +404,7 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     a.groups = (int32_t)((cols + 8 * e->NT - 1) / (8 * e->NT));
     a.cols = (int32_t)cols;
     a.page_rcp = ((uint64_t(1) << 37) + a.c.page / kBlock - 1) / (a.c.page / kBlock);
-    a.ws = static_cast<float*>(workspace);
+    a.ws = static_cast<char*>(workspace);
     // a block takes at least two steps for each of its warps; no more blocks
     // than the longest sequences that the table holds would fill
     a.min_chunk = 2 * (e->threads / 32);
@@ -413,7 +417,7 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     if (st != RMSN_OK || a.blocks == 1) return st;
     // always behind the stream's own kernel: a programmatic dependent of it
     const int64_t used = cols < 8 * e->NT ? cols : 8 * e->NT;
-    return launch(e->join, dim3((unsigned)(a.blocks - 1), (unsigned)used), 128, 0, &a, true,
+    return launch(e->join, dim3((unsigned)(a.blocks - 1), (unsigned)(used + 3) / 4), 512, 0, &a, true,
                   stream);
 }
 

@@ -78,8 +78,10 @@ struct AttendArgs {
     uint64_t page_rcp;  // ceil(2^37 / (page / 16))
     int64_t blocks;     // blocks of the grid
     int64_t min_chunk;  // steps of a block, at least
-    float* ws;          // two parts for every block
+    char* ws;           // a Cut and two parts for every block
 };
+
+constexpr int64_t kCutBytes = 32;
 
 // One compiled attention kernel and the join of its parts.
 struct AttendEntry {

@@ -130,6 +130,7 @@ struct Shape {
     static constexpr int kMetaAll = W * S * kMeta;
     static constexpr int kQ = kCols * kQPitch;
     static constexpr int kJoin = W * 4 * D * 4;     // fp32, four columns of every warp
+    static constexpr int kRingQuads = kRing / kJoin < 2 * NT ? kRing / kJoin : 2 * NT;
     static constexpr int kSmem = kRing + kMetaAll + kQ + kJoin;
 };
 
@@ -281,10 +282,27 @@ __device__ __forceinline__ void store8(const AttendArgs& a, int64_t b, const Col
     *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-// Partial results of block `blk`'s first (0) or last (1) row in the workspace.
+// The workspace: a Cut for every block, then two parts for every block.
+// Block i's Cut tells of the row that its upper border cuts, if i is the first
+// block that the row lies in: whose it is, which of block i's parts is its
+// first, and the last block it reaches.  Every block writes its Cut.
+struct __align__(16) Cut {
+    int64_t b;
+    int64_t last;
+    int32_t hc;
+    int32_t which;
+    int32_t on;
+    int32_t pad;
+};
+static_assert(sizeof(Cut) == kCutBytes, "the workspace is sized on the host");
+__device__ __forceinline__ Cut* cut_of(const AttendArgs& a, int64_t blk) {
+    return reinterpret_cast<Cut*>(a.ws) + blk;
+}
+// Partial results of block `blk`'s first (0) or last (1) row.
 template <class C>
 __device__ __forceinline__ float* part_of(const AttendArgs& a, int64_t blk, int which) {
-    return a.ws + (blk * 2 + which) * (int64_t)(C::kCols * (C::D + 2));
+    return reinterpret_cast<float*>(a.ws + a.blocks * kCutBytes) +
+           (blk * 2 + which) * (int64_t)(C::kCols * (C::D + 2));
 }
 
 // ---------------------------------------------------------------- the stream
@@ -297,23 +315,25 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     constexpr bool kQRegs = NT == 1 && D <= 128;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ float q_scale[C::kCols];
-    __shared__ float j_m[W][4], j_l[W][4];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ float j_m[W][C::kCols], j_l[W][C::kCols];
     rmsn::pdl_wait(a.pdl);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
 
     Line line;
     find_share<C::kTok, W * 32>(a, blockIdx.x, &line);
     const int64_t begin = line.at;
-    if (begin >= line.total) return;
+    if (begin >= line.total) {
+        if (threadIdx.x == 0) cut_of(a, blockIdx.x)->on = 0;
+        return;
+    }
     const int64_t stop = begin + line.chunk < line.total ? begin + line.chunk : line.total;
     const Place at = line.row;
 
     unsigned char* ring = smem + wp * (S * C::kStage);
     unsigned char* meta = smem + C::kRing + wp * (S * C::kMeta);
     unsigned char* qrows = smem + C::kRing + C::kMetaAll;
-    float* join = reinterpret_cast<float*>(smem + C::kRing + C::kMetaAll + C::kQ);
     const uint32_t ring_s = smem_addr(ring), meta_s = smem_addr(meta);
 
     // ---- producer: this warp's steps wp, wp + W, ... of the block's `count`
@@ -726,84 +746,97 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         }
 
         // the row's (or the part's) results: join the warps, four columns at a
-        // time (lanes t of one parity hold four of a tile's columns)
+        // time (lanes t of one parity hold four of a tile's columns); behind
+        // the block's last step the ring is free, and holds as many as fit
         const bool whole = cur == c_first && seg_end == row_end;
+        const bool last = seg_end == count;
         const float unit = vref / kLift;
         float* part = part_of<C>(a, blockIdx.x, cur == 0 ? 0 : 1);
+        if (threadIdx.x == 0 && last) {
+            Cut* cut = cut_of(a, blockIdx.x);
+            cut->on = row_end > count && c_first >= 0;
+            cut->b = c_b;
+            cut->hc = c_hc;
+            cut->which = cur == 0 ? 0 : 1;
+            cut->last = (begin + row_end - 1) / line.chunk;
+        }
+        int used = a.cols - cg * C::kCols;  // columns of this row
+        if (used > C::kCols) used = C::kCols;
+        const int quads = (used + 3) / 4, step = last ? C::kRingQuads : 1;
+        float ls[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float ls[2];
-            ls[0] = sum_over_rows(l[nt][0]);
-            ls[1] = sum_over_rows(l[nt][1]);
+            ls[nt][0] = sum_over_rows(l[nt][0]);
+            ls[nt][1] = sum_over_rows(l[nt][1]);
+        }
+        float* join = reinterpret_cast<float*>(last ? smem : smem + C::kRing + C::kMetaAll + C::kQ);
+        if (last) __syncthreads();  // every warp is through with its stages
+        for (int q0 = 0; q0 < quads; q0 += step) {
+            if (q0 > 0) __syncthreads();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int first = nt * 8 + half * 4;
-                if (cg * C::kCols + first >= a.cols) break;  // the same for all threads
-                if (first > 0) __syncthreads();
-                if ((t >> 1) == half) {
+            for (int q = 0; q < 2 * NT; ++q) {
+                const int nt = q >> 1;
+                if (q < q0 || q >= q0 + step || q >= quads || (t >> 1) != (q & 1)) continue;
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int c = 2 * (t & 1) + x;
-                        if (g == 0) {
-                            j_m[wp][c] = m[nt][x];
-                            j_l[wp][c] = ls[x];
-                        }
-                        float* jr = join + (wp * 4 + c) * D;
-#pragma unroll
-                        for (int i = 0; i < MT; i += 2) {
-                            const int d = D == 64 ? g * 8 + 2 * i : (g + 8 * (i / 8)) * 16 + 2 * (i % 8);
-                            *reinterpret_cast<float4*>(jr + d) =
-                                make_float4(o[i][nt][x] * unit, o[i][nt][2 + x] * unit,
-                                            o[i + 1][nt][x] * unit, o[i + 1][nt][2 + x] * unit);
-                        }
+                for (int x = 0; x < 2; ++x) {
+                    const int c = (q - q0) * 4 + 2 * (t & 1) + x;
+                    if (g == 0) {
+                        j_m[wp][q * 4 + 2 * (t & 1) + x] = m[nt][x];
+                        j_l[wp][q * 4 + 2 * (t & 1) + x] = ls[nt][x];
                     }
-                }
-                __syncthreads();
-                for (int e = threadIdx.x; e < D / 2; e += W * 32) {  // 4 columns x D / 8 vectors
-                    const int c = e / (D / 8), d = e % (D / 8) * 8;
-                    const Col col = column(a, hk, cg, first + c, C::kCols);
-                    if (!col.on) continue;
-                    float mx = -INFINITY;
+                    float* jr = join + (c * W + wp) * D;
 #pragma unroll
-                    for (int w = 0; w < W; ++w) mx = fmaxf(mx, j_m[w][c]);
-                    const float ms = mx == -INFINITY ? 0.f : mx;
-                    float lsum = 0.f, y[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] = 0.f;
-#pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        const float lw = j_l[w][c];
-                        if (j_m[w][c] == -INFINITY && lw == 0.f) continue;  // it saw no token
-                        const float f = exp2a(j_m[w][c] - ms);
-                        lsum += lw * f;
-                        const float4* jr = reinterpret_cast<const float4*>(join + (w * 4 + c) * D + d);
-                        const float4 u = jr[0], v = jr[1];
-                        y[0] += u.x * f;
-                        y[1] += u.y * f;
-                        y[2] += u.z * f;
-                        y[3] += u.w * f;
-                        y[4] += v.x * f;
-                        y[5] += v.y * f;
-                        y[6] += v.z * f;
-                        y[7] += v.w * f;
-                    }
-                    if (whole) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) y[k] = lsum == 0.f ? 0.f : y[k] / lsum;
-                        store8<T>(a, c_b, col, d, y);
-                    } else {
-                        const int cc = first + c;
-                        float4* dst = reinterpret_cast<float4*>(part + cc * D + d);
-                        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-                        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-                        if (d == 0)
-                            *reinterpret_cast<float2*>(part + C::kCols * D + cc * 2) =
-                                make_float2(mx, lsum);
+                    for (int i = 0; i < MT; i += 2) {
+                        const int d = D == 64 ? g * 8 + 2 * i : (g + 8 * (i / 8)) * 16 + 2 * (i % 8);
+                        *reinterpret_cast<float4*>(jr + d) =
+                            make_float4(o[i][nt][x] * unit, o[i][nt][2 + x] * unit,
+                                        o[i + 1][nt][x] * unit, o[i + 1][nt][2 + x] * unit);
                     }
                 }
             }
+            __syncthreads();
+            const int in = quads - q0 < step ? quads - q0 : step;
+            for (int e = threadIdx.x; e < in * (D / 2); e += W * 32) {  // columns x D / 8 vectors
+                const int c = e / (D / 8), d = e % (D / 8) * 8, cc = q0 * 4 + c;
+                const Col col = column(a, hk, cg, cc, C::kCols);
+                if (!col.on) continue;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < W; ++w) mx = fmaxf(mx, j_m[w][cc]);
+                const float ms = mx == -INFINITY ? 0.f : mx;
+                float lsum = 0.f, y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = 0.f;
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    const float f = exp2a(j_m[w][cc] - ms);
+                    lsum += j_l[w][cc] * f;
+                    const float4* jr = reinterpret_cast<const float4*>(join + (c * W + w) * D + d);
+                    const float4 u = jr[0], v = jr[1];
+                    y[0] += u.x * f;
+                    y[1] += u.y * f;
+                    y[2] += u.z * f;
+                    y[3] += u.w * f;
+                    y[4] += v.x * f;
+                    y[5] += v.y * f;
+                    y[6] += v.z * f;
+                    y[7] += v.w * f;
+                }
+                if (whole) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = lsum == 0.f ? 0.f : y[k] / lsum;
+                    store8<T>(a, c_b, col, d, y);
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(part + cc * D + d);
+                    dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                    dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                    if (d == 0)
+                        *reinterpret_cast<float2*>(part + C::kCols * D + cc * 2) =
+                            make_float2(mx, lsum);
+                }
+            }
         }
-        __syncthreads();  // the join rows and statistics are read before they are written again
+        if (!last) __syncthreads();  // the join rows and statistics are read before they are written again
 
         cur = seg_end;
         if (cur < count) {
@@ -818,72 +851,78 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     cp_wait<0>();
 }
 
-// Joins the parts of the rows that a block border cuts.  Block (i, c): border
-// i + 1, column c; the row's first border does the work.
+// Joins the parts of the rows that block borders cut, in block order.  Block
+// (i, q): the row of block i's Cut, columns 4 q to 4 q + 3; 512 / D parts at a
+// time, D threads to a part (four dims of a column each).
 template <class T, class C>
-__global__ void __launch_bounds__(128) attend_join_kernel(const AttendArgs a) {
-    constexpr int D = C::D, TD = D / 4, NG = 128 / TD;  // threads per part, parts at a time
-    __shared__ float4 sum[NG][TD];
-    __shared__ float sum_l[NG], sum_m[NG];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+__global__ void __launch_bounds__(512) attend_join_kernel(const AttendArgs a) {
+    constexpr int D = C::D, NG = 512 / D;
+    __shared__ float4 sum[NG][D];
+    __shared__ float top[4], total[4];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    Line line;
-    find_share<C::kTok, 128>(a, blockIdx.x + 1, &line);
-    const int64_t border = line.at, chunk = line.chunk;
-    if (border >= line.total) return;
-    const Place at = line.row;
-    if (at.first == border || at.first < border - chunk) return;
-    Span<C::kTok> span;
-    span.of(a, a.lengths[at.b]);
-    const int64_t c0 = blockIdx.x, c1 = (at.first + span.ns - 1) / chunk;
-    const int c = blockIdx.y;
-    const Col col = column(a, at.hc / a.groups, at.hc % a.groups, c, C::kCols);
-    if (!col.on) return;
-    const int grp = threadIdx.x / TD, d = threadIdx.x % TD * 4;
-    float m = -INFINITY, l = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int64_t i = c0 + grp; i <= c1; i += NG) {
-        const float* part = part_of<C>(a, i, i == c0 && at.first != c0 * chunk ? 1 : 0);
-        const float2 ml = *reinterpret_cast<const float2*>(part + C::kCols * D + c * 2);
-        const float4 v = *reinterpret_cast<const float4*>(part + c * D + d);
-        if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing of this part is seen
-        const float mn = fmaxf(m, ml.x), ms = mn == -INFINITY ? 0.f : mn;
-        const float f0 = exp2a(m - ms), f1 = exp2a(ml.x - ms);
-        m = mn;
-        l = l * f0 + ml.y * f1;
-        y.x = y.x * f0 + v.x * f1;
-        y.y = y.y * f0 + v.y * f1;
-        y.z = y.z * f0 + v.z * f1;
-        y.w = y.w * f0 + v.w * f1;
-    }
-    sum[grp][threadIdx.x % TD] = y;
-    if (threadIdx.x % TD == 0) {
-        sum_l[grp] = l;
-        sum_m[grp] = m;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Cut cut = *cut_of(a, blockIdx.x);
+    if (!cut.on) return;
+    const int64_t c0 = blockIdx.x;
+    const int n = (int)(cut.last - c0) + 1, q = blockIdx.y * 4;
+    const int hk = cut.hc / a.groups, cg = cut.hc % a.groups;
+    if (cg * C::kCols + q >= a.cols) return;
+    auto part = [&](int i) { return part_of<C>(a, c0 + i, i == 0 ? cut.which : 0); };
+    const int wp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (wp < 4) {  // the largest maximum of column q + wp, and the sum at it
+        float m = -INFINITY, l = 0.f;
+        for (int i = lane; i < n; i += 32)
+            m = fmaxf(m, part(i)[C::kCols * D + (q + wp) * 2]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        const float ms = m == -INFINITY ? 0.f : m;
+        for (int i = lane; i < n; i += 32) {
+            const float2 ml = *reinterpret_cast<const float2*>(part(i) + C::kCols * D + (q + wp) * 2);
+            l += ml.y * exp2a(ml.x - ms);
+        }
+        l = rmsn::warp_sum(l);
+        if (lane == 0) {
+            top[wp] = ms;
+            total[wp] = l;
+        }
     }
     __syncthreads();
-    if (threadIdx.x >= D / 8) return;
-    float mx = -INFINITY;
-    for (int k = 0; k < NG; ++k) mx = fmaxf(mx, sum_m[k]);
-    const float ms = mx == -INFINITY ? 0.f : mx;
-    float ls = 0.f, r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < NG; ++k) {
-        if (sum_m[k] == -INFINITY && sum_l[k] == 0.f) continue;
-        const float f = exp2a(sum_m[k] - ms);
-        ls += sum_l[k] * f;
-        const float4 u = sum[k][2 * threadIdx.x], v = sum[k][2 * threadIdx.x + 1];
-        r[0] += u.x * f;
-        r[1] += u.y * f;
-        r[2] += u.z * f;
-        r[3] += u.w * f;
-        r[4] += v.x * f;
-        r[5] += v.y * f;
-        r[6] += v.z * f;
-        r[7] += v.w * f;
+    const int grp = threadIdx.x / D, c = threadIdx.x % D / (D / 4), d = threadIdx.x % (D / 4) * 4;
+    const float ms = top[c];
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = grp; i < n; i += NG) {
+        const float* p = part(i);
+        const float f = exp2a(p[C::kCols * D + (q + c) * 2] - ms);
+        const float4 v = *reinterpret_cast<const float4*>(p + (q + c) * D + d);
+        y.x += v.x * f;
+        y.y += v.y * f;
+        y.z += v.z * f;
+        y.w += v.w * f;
     }
+    sum[grp][threadIdx.x % D] = y;
+    __syncthreads();
+    if (threadIdx.x >= D / 2) return;
+    const int oc = threadIdx.x / (D / 8), od = threadIdx.x % (D / 8);
+    const Col col = column(a, hk, cg, q + oc, C::kCols);
+    if (!col.on) return;
+    float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = ls == 0.f ? 0.f : r[k] / ls;
-    store8<T>(a, at.b, col, threadIdx.x * 8, r);
+    for (int k = 0; k < NG; ++k) {
+        const float4 u = sum[k][oc * (D / 4) + 2 * od], v = sum[k][oc * (D / 4) + 2 * od + 1];
+        r[0] += u.x;
+        r[1] += u.y;
+        r[2] += u.z;
+        r[3] += u.w;
+        r[4] += v.x;
+        r[5] += v.y;
+        r[6] += v.z;
+        r[7] += v.w;
+    }
+    const float l = total[oc];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = l == 0.f ? 0.f : r[k] / l;
+    store8<T>(a, cut.b, col, od * 8, r);
 }
 
 template <class C>

@@ -146,7 +146,8 @@ int rmsattn_kv_append(const rmsattn_cache* cache, const void* k, const void* v, 
  *               q_stride / out_stride elements apart, heads back to back, 16-byte
  *               aligned with strides of whole 16-byte vectors
  *   workspace   rmsattn_kv_attention_workspace(...) bytes on the device, 16-byte
- *               aligned, used by this call alone until it has finished
+ *               aligned, used by this call alone until it has finished (may be
+ *               NULL where that is 0)
  */
 #define RMSATTN_MAX_QUERIES 32
 
@@ -158,9 +159,10 @@ int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache, const int32_
                          cudaStream_t stream);
 
 /* Bytes of workspace that rmsattn_kv_attention needs for these sizes on the
- * current device (>= 0), or a negative rmsn_status. */
+ * current device (>= 0), or a negative rmsn_status.  max_tokens: what a table
+ * row holds, table_width * page_size. */
 int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_queries, int64_t n_q_heads,
-                                       int64_t n_kv_heads, int64_t head_dim);
+                                       int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens);
 
 /* Status word of this library's kernels on the current device: bit 2 (value
  * 4) is set when a block table named a page outside the cache or a token lay

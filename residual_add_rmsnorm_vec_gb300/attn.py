@@ -19,7 +19,7 @@ _CODES = (torch.uint8, torch.float8_e4m3fn)
 
 
 # (cudaStream_t of the current stream of a device index; no Stream object)
-_raw_stream = torch._C._cuda_getCurrentRawStream
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 @contextlib.contextmanager
@@ -417,17 +417,17 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
         if out.shape != shape or out.dtype != dt or out.get_device() != index:
             raise ValueError("out must be like q")
         os = _token_stride("out", out, n)
-    need = lib.rmsattn_kv_attention_workspace(B, n, H, Hk, D)
+    need = lib.rmsattn_kv_attention_workspace(B, n, H, Hk, D, width * cache.page_size)
     if need < 0:
         raise _lib.RmsnError(need, "rmsattn_kv_attention_workspace")
     # freed when this returns: the allocator hands it to later work of the
     # same stream only, which runs behind the kernels
-    ws = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    ws = torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
     flags = _IN[dt]
     st = lib.rmsattn_kv_attention(
         q.data_ptr(), cache._ref, block_table.data_ptr(), stride, width, lengths.data_ptr(),
         out.data_ptr(), qs, os, B, n, H, 1.0 / math.sqrt(D) if scale is None else scale, window,
-        sinks, ws.data_ptr(), need, flags | _lib.RMSN_PDL if pdl else flags, _raw_stream(index))
+        sinks, ws.data_ptr() if need else None, need, flags | _lib.RMSN_PDL if pdl else flags, _raw_stream(index))
     if st:
         raise _lib.RmsnError(st, "rmsattn_kv_attention")
     return out

@@ -18,6 +18,7 @@ namespace rmsattn {
 namespace {
 
 constexpr int kMaxDevices = 64;
+constexpr int64_t kRowSteps = 16;  // steps of a warp up to which a row stays in one cluster
 constexpr int64_t kMaxTokens = int64_t(1) << 29;  // tokens that a table's row may hold
 
 // Status word of the kernels on each device.
@@ -62,22 +63,31 @@ int64_t times(int64_t a, int64_t b) {
 bool too_big(int64_t n) { return n >= INT64_MAX / 64; }
 
 int launch(const void* fn, dim3 grid, int threads, size_t smem, void* args, bool pdl,
-           cudaStream_t stream) {
+           cudaStream_t stream, int cluster = 1) {
     void* list[] = {args};
-    if (!pdl)
+    if (!pdl && cluster == 1)
         return cudaLaunchKernel(fn, grid, dim3(threads), list, smem, stream) == cudaSuccess
                    ? RMSN_OK
                    : RMSN_ECUDA;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
     cudaLaunchConfig_t lc = {};
     lc.gridDim = grid;
     lc.blockDim = dim3(threads);
     lc.dynamicSmemBytes = smem;
     lc.stream = stream;
     lc.attrs = attr;
-    lc.numAttrs = 1;
+    lc.numAttrs = n;
     return cudaLaunchKernelExC(&lc, fn, list) == cudaSuccess ? RMSN_OK : RMSN_ECUDA;
 }
 
@@ -324,24 +334,66 @@ int64_t attend_blocks(DeviceInfo* d, const AttendEntry* e) {
     return n;
 }
 
-int64_t workspace_of(const AttendEntry* e, int64_t blocks) {
-    return blocks * (kCutBytes + 2 * (int64_t)e->part * 4);
+// How a call's steps are shared out.
+struct Plan {
+    const AttendEntry* e;
+    int64_t rows;    // sequences x key heads x column groups
+    int64_t steps;   // of the longest row that the table holds
+    int groups;
+    int split;       // a row to `split` blocks of a cluster; 0: one line of all steps
+    int64_t blocks;
+    int64_t min_chunk;
+    int64_t workspace;
+};
+
+int plan_attend(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_t n_q_heads,
+                int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens, Plan* p) {
+    const int64_t cols = n_q_heads / n_kv_heads * n_queries;
+    p->e = attend_entry_of(dt, head_dim, cols);
+    const int64_t resident = attend_blocks(d, p->e);
+    if (resident < 1) return RMSN_ECUDA;
+    const int warps = p->e->threads / 32;
+    p->groups = (int)((cols + 8 * p->e->NT - 1) / (8 * p->e->NT));
+    p->rows = n_seqs * n_kv_heads * p->groups;
+    p->steps = (max_tokens + p->e->tok - 1) / p->e->tok;
+    if (p->steps < 1) p->steps = 1;
+    int split = 1;
+    while (split < 8 && p->rows * split * 2 <= resident) split *= 2;
+    const int64_t per = (p->steps + split - 1) / split;  // steps of a block
+    if (per <= kRowSteps * warps && p->rows * split < (int64_t(1) << 31)) {
+        p->split = split;
+        p->blocks = p->rows * split;
+        p->min_chunk = 0;
+        p->workspace = 0;
+        return RMSN_OK;
+    }
+    p->split = 0;
+    // a block takes at least two steps for each of its warps; no more blocks
+    // than the longest rows that the table holds would fill
+    p->min_chunk = 2 * warps;
+    const int64_t total = times(p->rows, p->steps);
+    const int64_t full = (total + p->min_chunk - 1) / p->min_chunk;
+    p->blocks = full < resident ? full : resident;
+    if (total / p->blocks > (1 << 30)) return RMSN_EUNSUPPORTED;  // a block counts in 31 bits
+    p->workspace = p->blocks * (kCutBytes + 2 * (int64_t)p->e->part * 4);
+    return RMSN_OK;
 }
 
 }  // namespace
 
 RMSATTN_API int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_queries,
                                                    int64_t n_q_heads, int64_t n_kv_heads,
-                                                   int64_t head_dim) {
+                                                   int64_t head_dim, int64_t max_tokens) {
     const int st = check_attend(n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim);
     if (st != RMSN_OK) return st;
+    if (max_tokens < 0 || max_tokens > kMaxTokens) return RMSN_EINVAL;
     if (n_seqs == 0) return 0;
     DeviceInfo* d = device_info();
     if (!d) return RMSN_ECUDA;
-    const AttendEntry* e =
-        attend_entry_of(RMSN_IN_BF16, head_dim, n_q_heads / n_kv_heads * n_queries);
-    const int64_t blocks = attend_blocks(d, e);
-    return blocks > 0 ? workspace_of(e, blocks) : RMSN_ECUDA;
+    Plan p;  // both dtypes' kernels have the same shape
+    const int sp = plan_attend(d, RMSN_IN_BF16, n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim,
+                               max_tokens, &p);
+    return sp == RMSN_OK ? p.workspace : sp;
 }
 
 RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
@@ -379,11 +431,10 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
         return RMSN_EALIGN;
     DeviceInfo* d = device_info();
     if (!d) return RMSN_ECUDA;
-    const int64_t cols = n_q_heads / a.c.H * n_queries;
-    const AttendEntry* e = attend_entry_of(dt, a.c.D, cols);
-    const int64_t resident = attend_blocks(d, e);
-    if (resident < 1) return RMSN_ECUDA;
-    if (!workspace || workspace_bytes < workspace_of(e, resident)) return RMSN_EINVAL;
+    Plan p;
+    st = plan_attend(d, dt, n_seqs, n_queries, n_q_heads, a.c.H, a.c.D, table_width * a.c.page, &p);
+    if (st != RMSN_OK) return st;
+    if (p.workspace > 0 && (!workspace || workspace_bytes < p.workspace)) return RMSN_EINVAL;
     a.q = q;
     a.out = out;
     a.q_stride = q_stride;
@@ -401,24 +452,20 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     a.sinks = (int32_t)(sinks > kMaxTokens ? kMaxTokens : sinks);
     a.pdl = (flags & RMSN_PDL) ? 1 : 0;
     a.status = d->status;
-    a.groups = (int32_t)((cols + 8 * e->NT - 1) / (8 * e->NT));
-    a.cols = (int32_t)cols;
+    a.cols = (int32_t)(n_q_heads / a.c.H * n_queries);
+    a.groups = p.groups;
     a.page_rcp = ((uint64_t(1) << 37) + a.c.page / kBlock - 1) / (a.c.page / kBlock);
+    a.split = p.split;
+    a.blocks = p.blocks;
+    a.min_chunk = p.min_chunk;
     a.ws = static_cast<char*>(workspace);
-    // a block takes at least two steps for each of its warps; no more blocks
-    // than the longest sequences that the table holds would fill
-    a.min_chunk = 2 * (e->threads / 32);
-    const int64_t most = (table_width * a.c.page + e->tok - 1) / e->tok;
-    const int64_t steps = times(times(n_seqs, (int64_t)a.c.H * a.groups), most < 1 ? 1 : most);
-    const int64_t full = (steps + a.min_chunk - 1) / a.min_chunk;
-    a.blocks = full < resident ? full : resident;
-    if (steps / a.blocks > (1 << 30)) return RMSN_EUNSUPPORTED;  // a block counts its steps in 31 bits
-    st = launch(e->fn, dim3((unsigned)a.blocks), e->threads, (size_t)e->smem, &a, a.pdl, stream);
-    if (st != RMSN_OK || a.blocks == 1) return st;
+    st = launch(p.e->fn, dim3((unsigned)p.blocks), p.e->threads, (size_t)p.e->smem, &a, a.pdl,
+                stream, p.split > 1 ? p.split : 1);
+    if (st != RMSN_OK || p.split > 0 || p.blocks == 1) return st;
     // always behind the stream's own kernel: a programmatic dependent of it
-    const int64_t used = cols < 8 * e->NT ? cols : 8 * e->NT;
-    return launch(e->join, dim3((unsigned)(a.blocks - 1), (unsigned)(used + 3) / 4), 512, 0, &a, true,
-                  stream);
+    const int used = a.cols < 8 * p.e->NT ? a.cols : 8 * p.e->NT;
+    return launch(p.e->join, dim3((unsigned)(p.blocks - 1), (unsigned)(used + 3) / 4), 512, 0, &a,
+                  true, stream);
 }
 
 RMSATTN_API int rmsattn_read_status(uint32_t* status, int clear) {

@@ -72,7 +72,8 @@ struct AttendArgs {
     int32_t window, sinks;  // window 0: every earlier token
     int32_t pdl;
     uint32_t* status;
-    // how the line of all steps is shared out
+    // how the steps are shared out: 0, as one line; else a row to `split` blocks
+    int32_t split;
     int32_t groups;     // column groups of a key head
     int32_t cols;       // columns of a key head: query heads x query tokens
     uint64_t page_rcp;  // ceil(2^37 / (page / 16))

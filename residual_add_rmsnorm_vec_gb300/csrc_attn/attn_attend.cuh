@@ -25,11 +25,15 @@
 // * Each warp streams its own steps (16 or 32 tokens) through its own ring of
 //   cp.async stages, pages and scales included, across row borders: no block
 //   barrier in the stream.
-// * The steps of all rows (sequence x key head x column group) form one line
-//   that the blocks of a resident grid share evenly, whatever the lengths.  A
-//   row inside one block is finished there; the parts of a row that a border
-//   cuts go to the workspace in fp32 and are joined, in block order, by a
-//   second launch: results do not depend on timing.
+// * Long rows: the steps of all rows (sequence x key head x column group) form
+//   one line that the blocks of a resident grid share evenly, whatever the
+//   lengths.  A row inside one block is finished there; the parts of a row
+//   that a border cuts go to the workspace in fp32 and are joined, in block
+//   order, by a second launch.
+// * Short rows (a.split > 0): a cluster of a.split blocks takes one row, and
+//   joins its parts through distributed shared memory: one launch, no
+//   workspace, no scan of the lengths.
+//   Either way nothing depends on timing.
 #pragma once
 
 #include "attn_common.cuh"
@@ -130,7 +134,7 @@ struct Shape {
     static constexpr int kMetaAll = W * S * kMeta;
     static constexpr int kQ = kCols * kQPitch;
     static constexpr int kJoin = W * 4 * D * 4;     // fp32, four columns of every warp
-    static constexpr int kRingQuads = kRing / kJoin < 2 * NT ? kRing / kJoin : 2 * NT;
+    static_assert(kRing >= 2 * NT * kJoin, "the ring holds the join of all columns");
     static constexpr int kSmem = kRing + kMetaAll + kQ + kJoin;
 };
 
@@ -282,6 +286,54 @@ __device__ __forceinline__ void store8(const AttendArgs& a, int64_t b, const Col
     *reinterpret_cast<uint4*>(o) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+__device__ __forceinline__ void add8(float (&y)[8], const float4* p, float f) {
+    const float4 u = p[0], v = p[1];
+    y[0] += u.x * f;
+    y[1] += u.y * f;
+    y[2] += u.z * f;
+    y[3] += u.w * f;
+    y[4] += v.x * f;
+    y[5] += v.y * f;
+    y[6] += v.z * f;
+    y[7] += v.w * f;
+}
+// Eight dims of a row's sums over its weights' sum; nothing seen gives 0.
+template <class T>
+__device__ __forceinline__ void finish8(const AttendArgs& a, int64_t b, const Col& c, int d,
+                                        float (&y)[8], float l) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = l == 0.f ? 0.f : y[k] / l;
+    store8<T>(a, b, c, d, y);
+}
+
+// ---------------------------------------------------------------- the cluster's shared memory
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+__device__ __forceinline__ uint32_t in_block(uint32_t addr, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr, int rank) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(in_block(addr, rank))
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, int rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(in_block(addr, rank))
+                 : "memory");
+    return v;
+}
+
 // The workspace: a Cut for every block, then two parts for every block.
 // Block i's Cut tells of the row that its upper border cuts, if i is the first
 // block that the row lies in: whose it is, which of block i's parts is its
@@ -315,29 +367,92 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     constexpr bool kQRegs = NT == 1 && D <= 128;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ float q_scale[C::kCols];
+    __shared__ float2 part_ml[C::kCols];
     __shared__ float j_m[W][C::kCols], j_l[W][C::kCols];
     rmsn::pdl_wait(a.pdl);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
 
-    Line line;
-    find_share<C::kTok, W * 32>(a, blockIdx.x, &line);
-    const int64_t begin = line.at;
-    if (begin >= line.total) {
-        if (threadIdx.x == 0) cut_of(a, blockIdx.x)->on = 0;
-        return;
+    // this block's steps: `count` from place `begin`, the first of them in row
+    // `at` (whose first step lies at at.first <= begin)
+    int64_t begin, chunk = 0;
+    int count;
+    Place at;
+    if (a.split > 0) {
+        const int64_t HC = (int64_t)a.c.H * a.groups, row = blockIdx.x / (uint32_t)a.split;
+        at.b = row / HC;
+        at.hc = (int)(row % HC);
+        at.first = 0;
+        Span<C::kTok> s;
+        s.of(a, a.lengths[at.b]);
+        const int per = (s.ns + a.split - 1) / a.split;
+        begin = (int64_t)(blockIdx.x % (uint32_t)a.split) * per;
+        const int left = s.ns - (int)begin;
+        count = left < 0 ? 0 : (left < per ? left : per);
+    } else {
+        Line line;
+        find_share<C::kTok, W * 32>(a, blockIdx.x, &line);
+        begin = line.at;
+        chunk = line.chunk;
+        at = line.row;
+        if (begin >= line.total) {
+            if (threadIdx.x == 0) cut_of(a, blockIdx.x)->on = 0;
+            return;
+        }
+        count = (int)(line.total - begin < chunk ? line.total - begin : chunk);
     }
-    const int64_t stop = begin + line.chunk < line.total ? begin + line.chunk : line.total;
-    const Place at = line.row;
 
     unsigned char* ring = smem + wp * (S * C::kStage);
     unsigned char* meta = smem + C::kRing + wp * (S * C::kMeta);
     unsigned char* qrows = smem + C::kRing + C::kMetaAll;
     const uint32_t ring_s = smem_addr(ring), meta_s = smem_addr(meta);
 
+    // ---- queries: this warp's columns wp, wp + W, ... of a row, first into
+    // registers (before the wait that they can hide behind), then to shared
+    // memory in fp16, each scaled by a power of two to at most 2^8 (so that
+    // fp16 holds any bf16 row: what is below 2^-32 of the row's largest value
+    // loses bits); q_scale undoes it, times scale * log2(e)
+    constexpr int QC = (C::kCols + W - 1) / W, QW = D / 64;
+    uint32_t qreg[QC][QW];
+    auto load_q = [&](int64_t b, int hc) {
+        const int hk = hc / a.groups, cg = hc % a.groups;
+#pragma unroll
+        for (int i = 0; i < QC; ++i) {
+            const Col col = column(a, hk, cg, wp + i * W, C::kCols);
+            const uint16_t* p = static_cast<const uint16_t*>(a.q) + (b * a.n + col.qi) * a.q_stride +
+                                (int64_t)col.head * D + 2 * lane;
+#pragma unroll
+            for (int k = 0; k < QW; ++k)
+                qreg[i][k] = col.on && wp + i * W < C::kCols
+                                 ? *reinterpret_cast<const uint32_t*>(p + 64 * k)
+                                 : 0u;
+        }
+    };
+    auto store_q = [&]() {
+#pragma unroll
+        for (int i = 0; i < QC; ++i) {
+            const int c = wp + i * W;
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < QW; ++k)
+                m = rmsn::absmax3(m, rmsn::lo2<T>(qreg[i][k]), rmsn::hi2<T>(qreg[i][k]));
+            m = rmsn::warp_max(m);
+            int e = (int)(__float_as_uint(m) >> 23) - 127 - 7;  // 2^e <= m / 128 < 2^(e + 1)
+            e = e < -126 ? -126 : (e > 126 ? 126 : e);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+            if (c >= C::kCols) break;
+            if (lane == 0) q_scale[c] = up * (a.scale * kLog2e);
+#pragma unroll
+            for (int k = 0; k < QW; ++k)
+                *reinterpret_cast<uint32_t*>(qrows + c * C::kQPitch + (64 * k + 2 * lane) * 2) =
+                    rmsn::pack_f16x2(rmsn::lo2<T>(qreg[i][k]) * down, rmsn::hi2<T>(qreg[i][k]) * down);
+        }
+    };
+    load_q(at.b, at.hc);
+
     // ---- producer: this warp's steps wp, wp + W, ... of the block's `count`
-    const int count = (int)(stop - begin);
     int p_at = wp, p_first = (int)(at.first - begin), p_hc = at.hc;  // places relative to begin
     int64_t p_b = at.b;
     Span<C::kTok> p_span;
@@ -451,41 +566,15 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     int c_first = (int)(at.first - begin), c_hc = at.hc;
     Span<C::kTok> span;
     span.of(a, a.lengths[c_b]);
-    while (cur < count) {
+    int c_len_next = c_b + 1 < a.B ? a.lengths[c_b + 1] : 0;
+    do {  // once at least: a block of a cluster may have no steps
         const int row_end = c_first + span.ns;
-        const int seg_end = row_end < count ? row_end : count;
+        // (a cluster's block works on one row, and may lie behind its end)
+        const int seg_end = a.split == 0 && row_end < count ? row_end : count;
         const int hk = c_hc / a.groups, cg = c_hc % a.groups;
         if (span.L > span.end && threadIdx.x == 0) atomicOr(a.status, kBadPage);
 
-        // queries in fp16, each scaled by a power of two to at most 2^8 (so
-        // that fp16 holds any bf16 row: what is below 2^-32 of the row's
-        // largest value loses bits); q_scale undoes it, times scale * log2(e)
-        for (int c = wp; c < C::kCols; c += W) {
-            const Col col = column(a, hk, cg, c, C::kCols);
-            float x[D / 32];
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                uint32_t u = 0;
-                if (col.on)
-                    u = *reinterpret_cast<const uint32_t*>(
-                        static_cast<const uint16_t*>(a.q) + (c_b * a.n + col.qi) * a.q_stride +
-                        (int64_t)col.head * D + 64 * i + 2 * lane);
-                x[2 * i] = rmsn::lo2<T>(u);
-                x[2 * i + 1] = rmsn::hi2<T>(u);
-                m = fmaxf(m, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
-            }
-            m = rmsn::warp_max(m);
-            int e = (int)(__float_as_uint(m) >> 23) - 127 - 7;  // 2^e <= m / 128 < 2^(e + 1)
-            e = e < -126 ? -126 : (e > 126 ? 126 : e);
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-            if (lane == 0) q_scale[c] = up * (a.scale * kLog2e);
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i)
-                *reinterpret_cast<uint32_t*>(qrows + c * C::kQPitch + (64 * i + 2 * lane) * 2) =
-                    rmsn::pack_f16x2(x[2 * i] * down, x[2 * i + 1] * down);
-        }
+        store_q();
         __syncthreads();
         float cs[NT][2];
 #pragma unroll
@@ -747,22 +836,31 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 
         // the row's (or the part's) results: join the warps, four columns at a
         // time (lanes t of one parity hold four of a tile's columns); behind
-        // the block's last step the ring is free, and holds as many as fit
-        const bool whole = cur == c_first && seg_end == row_end;
-        const bool last = seg_end == count;
+        // the block's last step the ring is free, and holds all of them
+        const bool last = seg_end >= count;
+        const bool whole = a.split > 0 ? a.split == 1 : cur == c_first && seg_end == row_end;
         const float unit = vref / kLift;
         float* part = part_of<C>(a, blockIdx.x, cur == 0 ? 0 : 1);
-        if (threadIdx.x == 0 && last) {
+        if (threadIdx.x == 0 && last && a.split == 0) {
             Cut* cut = cut_of(a, blockIdx.x);
             cut->on = row_end > count && c_first >= 0;
             cut->b = c_b;
             cut->hc = c_hc;
             cut->which = cur == 0 ? 0 : 1;
-            cut->last = (begin + row_end - 1) / line.chunk;
+            cut->last = (begin + row_end - 1) / chunk;
+        }
+        // the next row's queries and length, while this one is joined
+        const int64_t row_b = c_b;
+        if (!last) {
+            if (++c_hc == a.c.H * a.groups) {
+                c_hc = 0;
+                ++c_b;
+            }
+            load_q(c_b, c_hc);
         }
         int used = a.cols - cg * C::kCols;  // columns of this row
         if (used > C::kCols) used = C::kCols;
-        const int quads = (used + 3) / 4, step = last ? C::kRingQuads : 1;
+        const int quads = (used + 3) / 4, step = last ? 2 * NT : 1;
         float ls[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -811,21 +909,15 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                 for (int w = 0; w < W; ++w) {
                     const float f = exp2a(j_m[w][cc] - ms);
                     lsum += j_l[w][cc] * f;
-                    const float4* jr = reinterpret_cast<const float4*>(join + (c * W + w) * D + d);
-                    const float4 u = jr[0], v = jr[1];
-                    y[0] += u.x * f;
-                    y[1] += u.y * f;
-                    y[2] += u.z * f;
-                    y[3] += u.w * f;
-                    y[4] += v.x * f;
-                    y[5] += v.y * f;
-                    y[6] += v.z * f;
-                    y[7] += v.w * f;
+                    add8(y, reinterpret_cast<const float4*>(join + (c * W + w) * D + d), f);
                 }
                 if (whole) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] = lsum == 0.f ? 0.f : y[k] / lsum;
-                    store8<T>(a, c_b, col, d, y);
+                    finish8<T>(a, row_b, col, d, y, lsum);
+                } else if (a.split > 0) {  // for the cluster, in the place of warp 0's
+                    float4* dst = reinterpret_cast<float4*>(join + c * W * D + d);
+                    dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                    dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                    if (d == 0) part_ml[cc] = make_float2(mx, lsum);
                 } else {
                     float4* dst = reinterpret_cast<float4*>(part + cc * D + d);
                     dst[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -836,18 +928,42 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                 }
             }
         }
-        if (!last) __syncthreads();  // the join rows and statistics are read before they are written again
-
+        if (a.split > 1) {
+            // the parts of the cluster's blocks, each block its share of the vectors
+            cluster_sync();
+            const uint32_t rank = blockIdx.x % (uint32_t)a.split;
+            for (int e = rank * (W * 32) + threadIdx.x; e < quads * (D / 2); e += a.split * (W * 32)) {
+                const int cc = e / (D / 8), d = e % (D / 8) * 8;
+                const Col col = column(a, hk, cg, cc, C::kCols);
+                if (!col.on) continue;
+                const uint32_t ml = smem_addr(&part_ml[cc]);
+                const uint32_t jr = smem_addr(join + cc * W * D + d);
+                float mx = -INFINITY;
+                for (int r = 0; r < a.split; ++r) mx = fmaxf(mx, ld_cluster2(ml, r).x);
+                const float ms = mx == -INFINITY ? 0.f : mx;
+                float lsum = 0.f, y[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = 0.f;
+                for (int r = 0; r < a.split; ++r) {
+                    const float2 p = ld_cluster2(ml, r);
+                    const float f = exp2a(p.x - ms);
+                    lsum += p.y * f;
+                    const float4 v[2] = {ld_cluster4(jr, r), ld_cluster4(jr + 16, r)};
+                    add8(y, v, f);
+                }
+                finish8<T>(a, row_b, col, d, y, lsum);
+            }
+            cluster_sync();  // no block leaves while another reads its shared memory
+        }
         cur = seg_end;
-        if (cur < count) {
+        if (!last) {
             c_first = row_end;
-            if (++c_hc == a.c.H * a.groups) {
-                c_hc = 0;
-                ++c_b;
-                span.of(a, a.lengths[c_b]);
+            if (c_b != row_b) {
+                span.of(a, c_len_next);
+                c_len_next = c_b + 1 < a.B ? a.lengths[c_b + 1] : 0;
             }
         }
-    }
+    } while (cur < count);
     cp_wait<0>();
 }
 
@@ -919,10 +1035,7 @@ __global__ void __launch_bounds__(512) attend_join_kernel(const AttendArgs a) {
         r[6] += v.z;
         r[7] += v.w;
     }
-    const float l = total[oc];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = l == 0.f ? 0.f : r[k] / l;
-    store8<T>(a, cut.b, col, od * 8, r);
+    finish8<T>(a, cut.b, col, od * 8, r, total[oc]);
 }
 
 template <class C>

@@ -5,7 +5,7 @@ namespace rmsattn {
 
 using A = Shape<128, 1, 1, 4, 3, 3>;
 using B = Shape<128, 2, 1, 4, 3, 2>;
-using C = Shape<128, 4, 1, 4, 3, 2>;
+using C = Shape<128, 4, 1, 4, 4, 2>;
 
 const AttendEntry* attend_kernels_128(int* n) {
     static const AttendEntry table[] = {

@@ -75,6 +75,7 @@ int rmsattn_qk_rope_fwd(const void* q, const void* k, const void* q_weight, cons
  *   k_scale, v_scale [n_pages, n_kv_heads, page_size / RMSATTN_BLOCK] fp32,
  *                    pages scale_stride floats apart
  *
+ * Scales are finite and not negative (the append makes no others).
  * head_dim is 64, 128 or 256; page_size a multiple of RMSATTN_BLOCK up to
  * 65536.  A block table row lists a sequence's pages in order: token i is
  * row i % page_size of page block_table[seq][i / page_size].
@@ -136,7 +137,7 @@ int rmsattn_kv_append(const rmsattn_cache* cache, const void* k, const void* v, 
  *
  * Query head h reads key head h / (n_q_heads / n_kv_heads).  Products of the
  * codes with q are exact in fp32 sums; softmax statistics and the output sum
- * are fp32; the weights are rounded to fp16 (2^-12 of their value) for the
+ * are fp32; the weights are rounded to fp16 (2^-11 of their value) for the
  * second product.  Tokens past lengths[s], and tokens that no query of the
  * sequence sees, have no influence, whatever their codes are.  A page outside
  * [0, n_pages), or past the table's width, is left out and sets bit 2 (value
@@ -162,7 +163,8 @@ int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache, const int32_
  * current device (>= 0), or a negative rmsn_status.  max_tokens: what a table
  * row holds, table_width * page_size. */
 int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_queries, int64_t n_q_heads,
-                                       int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens);
+                                       int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens,
+                                       int64_t window, int64_t sinks);
 
 /* Status word of this library's kernels on the current device: bit 2 (value
  * 4) is set when a block table named a page outside the cache or a token lay

@@ -58,7 +58,7 @@ def load_attn() -> ctypes.CDLL:
             lib.rmsattn_kv_attention.argtypes = [vp, cache, vp, i64, i64, vp, vp, i64, i64, i64, i64,
                                                  i64, f32, i64, i64, vp, i64, u32, vp]
             lib.rmsattn_kv_attention_workspace.restype = i64
-            lib.rmsattn_kv_attention_workspace.argtypes = [i64] * 6
+            lib.rmsattn_kv_attention_workspace.argtypes = [i64] * 8
             lib.rmsattn_read_status.restype = ctypes.c_int
             lib.rmsattn_read_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
             _loaded = lib

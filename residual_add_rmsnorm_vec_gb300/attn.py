@@ -417,7 +417,7 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
         if out.shape != shape or out.dtype != dt or out.get_device() != index:
             raise ValueError("out must be like q")
         os = _token_stride("out", out, n)
-    need = lib.rmsattn_kv_attention_workspace(B, n, H, Hk, D, width * cache.page_size)
+    need = lib.rmsattn_kv_attention_workspace(B, n, H, Hk, D, width * cache.page_size, window, sinks)
     if need < 0:
         raise _lib.RmsnError(need, "rmsattn_kv_attention_workspace")
     # freed when this returns: the allocator hands it to later work of the

@@ -18,7 +18,6 @@ namespace rmsattn {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int64_t kRowSteps = 16;  // steps of a warp up to which a row stays in one cluster
 constexpr int64_t kMaxTokens = int64_t(1) << 29;  // tokens that a table's row may hold
 
 // Status word of the kernels on each device.
@@ -303,15 +302,16 @@ int check_attend(int64_t n_seqs, int64_t n_queries, int64_t n_q_heads, int64_t n
     return head_dim == 64 || head_dim == 128 || head_dim == 256 ? RMSN_OK : RMSN_EUNSUPPORTED;
 }
 
-const AttendEntry* attend_entry_of(int dt, int64_t D, int64_t cols) {
+const AttendEntry* attend_entry_of(int dt, int64_t D, int64_t cols, int64_t tokens) {
     int n = 0;
     const AttendEntry* t = D == 64 ? attend_kernels_64(&n)
                                    : (D == 128 ? attend_kernels_128(&n) : attend_kernels_256(&n));
-    // the fewest column tiles that hold all columns, or the most there are
+    // the fewest column tiles that hold all columns, or the most there are; of
+    // those the first that takes rows of so many tokens
     const AttendEntry* best = nullptr;
     for (int i = 0; i < n; ++i) {
-        if (t[i].dt != dt) continue;
-        if (!best || best->NT * 8 < cols) best = &t[i];
+        if (t[i].dt != dt || t[i].most < tokens) continue;
+        if (!best || (best->NT * 8 < cols && t[i].NT > best->NT)) best = &t[i];
     }
     return best;
 }
@@ -337,45 +337,57 @@ int64_t attend_blocks(DeviceInfo* d, const AttendEntry* e) {
 // How a call's steps are shared out.
 struct Plan {
     const AttendEntry* e;
-    int64_t rows;    // sequences x key heads x column groups
-    int64_t steps;   // of the longest row that the table holds
-    int groups;
+    int groups;      // column groups of a key head
     int split;       // a row to `split` blocks of a cluster; 0: one line of all steps
-    int64_t blocks;
+    int64_t blocks;  // of the grid; shares of the line
     int64_t min_chunk;
     int64_t workspace;
 };
 
 int plan_attend(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_t n_q_heads,
-                int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens, Plan* p) {
+                int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens, int64_t window,
+                int64_t sinks, Plan* p) {
+    // the most tokens that a row's queries see, borders of steps included
+    if (window > 0 && sinks < kMaxTokens && window + n_queries + sinks + 256 < max_tokens)
+        max_tokens = window + n_queries + sinks + 256;
     const int64_t cols = n_q_heads / n_kv_heads * n_queries;
-    p->e = attend_entry_of(dt, head_dim, cols);
-    const int64_t resident = attend_blocks(d, p->e);
+    const AttendEntry* e = p->e = attend_entry_of(dt, head_dim, cols, max_tokens);
+    const int64_t resident = attend_blocks(d, e);
     if (resident < 1) return RMSN_ECUDA;
-    const int warps = p->e->threads / 32;
-    p->groups = (int)((cols + 8 * p->e->NT - 1) / (8 * p->e->NT));
-    p->rows = n_seqs * n_kv_heads * p->groups;
-    p->steps = (max_tokens + p->e->tok - 1) / p->e->tok;
-    if (p->steps < 1) p->steps = 1;
-    int split = 1;
-    while (split < 8 && p->rows * split * 2 <= resident) split *= 2;
-    const int64_t per = (p->steps + split - 1) / split;  // steps of a block
-    if (per <= kRowSteps * warps && p->rows * split < (int64_t(1) << 31)) {
-        p->split = split;
-        p->blocks = p->rows * split;
+    const int64_t warps = e->threads / 32;
+    p->groups = (int)((cols + 8 * e->NT - 1) / (8 * e->NT));
+    const int64_t rows = n_seqs * n_kv_heads * p->groups;
+    const int64_t steps = max_tokens < 1 ? 1 : (max_tokens + e->tok - 1) / e->tok;
+    const int64_t total = times(rows, steps);
+
+    // A row to a cluster of `split` blocks, or the line?  Measured in tokens
+    // of a warp, a cluster's rows cost their longest share times the waves of
+    // blocks; the line costs an even share and about 5 us more (its scan and
+    // its join: as long as a warp takes for 16384 / head_dim tokens), and
+    // longer joins where a row has many parts.  At head_dim 128 on a GB300:
+    // 8 x 2000 tokens x 8 heads 12.8 against 16.9 us, 256 x 300 45 against 48,
+    // but 64 x 8192 161 against 148, 1 x 131072 138 against 54.
+    int64_t split = 1;
+    while (split < 8 && rows * split * 2 <= resident) split *= 2;
+    const int64_t waves = (rows * split + resident - 1) / resident;
+    const double by_rows = (double)waves * (double)((steps + split - 1) / split) * e->tok / warps;
+    const double by_line = (double)total * e->tok / (double)(resident * warps) +
+                           16384.0 / (double)head_dim + 2.0 * (double)resident / (double)rows;
+    if (by_rows <= by_line && rows * split < (int64_t(1) << 31)) {
+        p->split = (int)split;
+        p->blocks = rows * split;
         p->min_chunk = 0;
         p->workspace = 0;
         return RMSN_OK;
     }
     p->split = 0;
-    // a block takes at least two steps for each of its warps; no more blocks
-    // than the longest rows that the table holds would fill
+    // a share is at least two steps for each of its warps; no more shares than
+    // the longest rows that the table holds would fill
     p->min_chunk = 2 * warps;
-    const int64_t total = times(p->rows, p->steps);
     const int64_t full = (total + p->min_chunk - 1) / p->min_chunk;
     p->blocks = full < resident ? full : resident;
-    if (total / p->blocks > (1 << 30)) return RMSN_EUNSUPPORTED;  // a block counts in 31 bits
-    p->workspace = p->blocks * (kCutBytes + 2 * (int64_t)p->e->part * 4);
+    if (total / p->blocks > (1 << 30)) return RMSN_EUNSUPPORTED;  // a share counts in 31 bits
+    p->workspace = p->blocks * (kCutBytes + 2 * (int64_t)e->part * 4);
     return RMSN_OK;
 }
 
@@ -383,16 +395,17 @@ int plan_attend(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
 
 RMSATTN_API int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_queries,
                                                    int64_t n_q_heads, int64_t n_kv_heads,
-                                                   int64_t head_dim, int64_t max_tokens) {
+                                                   int64_t head_dim, int64_t max_tokens, int64_t window,
+                                                   int64_t sinks) {
     const int st = check_attend(n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim);
     if (st != RMSN_OK) return st;
-    if (max_tokens < 0 || max_tokens > kMaxTokens) return RMSN_EINVAL;
+    if (max_tokens < 0 || max_tokens > kMaxTokens || window < 0 || sinks < 0) return RMSN_EINVAL;
     if (n_seqs == 0) return 0;
     DeviceInfo* d = device_info();
     if (!d) return RMSN_ECUDA;
     Plan p;  // both dtypes' kernels have the same shape
     const int sp = plan_attend(d, RMSN_IN_BF16, n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim,
-                               max_tokens, &p);
+                               max_tokens, window, sinks, &p);
     return sp == RMSN_OK ? p.workspace : sp;
 }
 
@@ -432,7 +445,8 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     DeviceInfo* d = device_info();
     if (!d) return RMSN_ECUDA;
     Plan p;
-    st = plan_attend(d, dt, n_seqs, n_queries, n_q_heads, a.c.H, a.c.D, table_width * a.c.page, &p);
+    st = plan_attend(d, dt, n_seqs, n_queries, n_q_heads, a.c.H, a.c.D, table_width * a.c.page,
+                     window, sinks, &p);
     if (st != RMSN_OK) return st;
     if (p.workspace > 0 && (!workspace || workspace_bytes < p.workspace)) return RMSN_EINVAL;
     a.q = q;
@@ -456,7 +470,7 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     a.groups = p.groups;
     a.page_rcp = ((uint64_t(1) << 37) + a.c.page / kBlock - 1) / (a.c.page / kBlock);
     a.split = p.split;
-    a.blocks = p.blocks;
+    a.shares = p.blocks;
     a.min_chunk = p.min_chunk;
     a.ws = static_cast<char*>(workspace);
     st = launch(p.e->fn, dim3((unsigned)p.blocks), p.e->threads, (size_t)p.e->smem, &a, a.pdl,

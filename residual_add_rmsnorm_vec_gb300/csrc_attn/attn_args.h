@@ -77,9 +77,9 @@ struct AttendArgs {
     int32_t groups;     // column groups of a key head
     int32_t cols;       // columns of a key head: query heads x query tokens
     uint64_t page_rcp;  // ceil(2^37 / (page / 16))
-    int64_t blocks;     // blocks of the grid
-    int64_t min_chunk;  // steps of a block, at least
-    char* ws;           // a Cut and two parts for every block
+    int64_t shares;     // of the line, one for each block
+    int64_t min_chunk;  // steps of a share, at least
+    char* ws;           // a Cut and two parts for every share
 };
 
 constexpr int64_t kCutBytes = 32;
@@ -87,6 +87,7 @@ constexpr int64_t kCutBytes = 32;
 // One compiled attention kernel and the join of its parts.
 struct AttendEntry {
     int32_t dt, D, NT, tok, threads, smem;
+    int32_t most;  // takes rows of up to this many tokens
     int32_t part;  // floats of one part
     const void* fn;
     const void* join;

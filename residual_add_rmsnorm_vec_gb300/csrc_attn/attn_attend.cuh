@@ -22,9 +22,14 @@
 // * P^T is turned from S^T's accumulator layout into the second product's
 //   operand layout by movmatrix: no shared memory, and no exchange between
 //   warps before a row ends.
-// * Each warp streams its own steps (16 or 32 tokens) through its own ring of
-//   cp.async stages, pages and scales included, across row borders: no block
-//   barrier in the stream.
+// * Each warp streams its own steps (16 to 64 tokens) through its own ring of
+//   cp.async stages, scales included, across row borders: no block barrier in
+//   the stream.  K and V have two stages each, and each is filled again as
+//   soon as it has been read (K before the softmax, V behind the second
+//   product): with two stages, two steps are on their way.
+// * Where its next 32 steps lie (page, place in the page, whether a mask
+//   touches them) the warp's lanes work out together, one step each, a batch
+//   ahead of its use.
 // * Long rows: the steps of all rows (sequence x key head x column group) form
 //   one line that the blocks of a resident grid share evenly, whatever the
 //   lengths.  A row inside one block is finished there; the parts of a row
@@ -41,11 +46,16 @@
 namespace rmsattn {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kOpen = 1u << 12;
 constexpr float kTinyScale = 1.17549435e-38f;
-// weights are exp2 of at most 0, times 2^14 before they are rounded to fp16:
-// its subnormals then begin at 2^-38 of a row's largest weight, so that what
-// 2^17 tokens lose at most (2^-39 each) stays below an fp32 rounding
-constexpr float kLift = 16384.f;
+// A row's reference (what is taken from its scores before exp2) follows its
+// maximum only when that has grown by more than 2^kSlack: a sum is then rarely
+// rescaled twice.  Weights are thus up to 2^kSlack; they are multiplied by
+// kLift before they are rounded to fp16, whose subnormals then end 2^-32 below
+// the reference: what 2^17 tokens lose at most (2^-33 each) is 2^-16 of it.
+constexpr float kNone = -3.402823466e38f;  // the reference before any token is seen
+constexpr float kSlack = 7.f;
+constexpr float kLift = 256.f;
 
 // ---------------------------------------------------------------- instructions
 
@@ -119,22 +129,22 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 // ---------------------------------------------------------------- shape
 
 // D head dim; NT column tiles of 8; KT tiles of 16 tokens in a step; W warps;
-// S ring stages.
 // M blocks share an SM.
-template <int D_, int NT_, int KT_, int W_, int S_, int M_>
+template <int D_, int NT_, int KT_, int W_, int M_>
 struct Shape {
-    static constexpr int D = D_, NT = NT_, KT = KT_, W = W_, S = S_, M = M_;
-    static constexpr int kTok = 16 * KT;            // tokens of a step
-    static constexpr int kCols = 8 * NT;            // columns of a row
-    static constexpr int kTile = 16 * D;            // bytes of 16 tokens' K
-    static constexpr int kStage = 2 * KT * kTile;   // K tiles, then V tiles
-    static constexpr int kMeta = 16 * KT;           // per stage: K scale, V scale, valid, -
-    static constexpr int kQPitch = 2 * D + 16;      // fp16 query row; + 16: no bank conflicts
-    static constexpr int kRing = W * S * kStage;
-    static constexpr int kMetaAll = W * S * kMeta;
+    static constexpr int D = D_, NT = NT_, KT = KT_, W = W_, M = M_;
+    static constexpr int kTok = 16 * KT;           // tokens of a step
+    static constexpr int kCols = 8 * NT;           // columns of a row
+    static constexpr int kTile = 16 * D;           // bytes of 16 tokens of K or V
+    static constexpr int kSide = KT * kTile;       // bytes of a step of K or V
+    static constexpr int kWarp = 4 * kSide;        // a warp's ring: K, K, V, V
+    static constexpr int kMeta = 32 * KT;          // a warp's: per step and tile K scale, V scale, state
+    static constexpr int kQPitch = 2 * D + 16;     // fp16 query row; + 16: no bank conflicts
+    static constexpr int kJoin = W * 4 * D * 4;    // fp32, four columns of every warp
+    // the rings; behind the last step, the join of all columns
+    static constexpr int kRing = W * kWarp > 2 * NT * kJoin ? W * kWarp : 2 * NT * kJoin;
+    static constexpr int kMetaAll = W * kMeta;
     static constexpr int kQ = kCols * kQPitch;
-    static constexpr int kJoin = W * 4 * D * 4;     // fp32, four columns of every warp
-    static_assert(kRing >= 2 * NT * kJoin, "the ring holds the join of all columns");
     static constexpr int kSmem = kRing + kMetaAll + kQ + kJoin;
 };
 
@@ -173,6 +183,18 @@ struct Span {
         }
         if (ns < 1) ns = 1;
     }
+    // kOpen if every query sees all of the 16 tokens from j on
+    __device__ __forceinline__ uint32_t open(const AttendArgs& a, int j) const {
+        return j + 15 <= L - a.n && j + 16 <= end &&
+                       (a.window == 0 || j > L - 1 - a.window || j + 16 <= sink)
+                   ? kOpen
+                   : 0u;
+    }
+    // which of the 16 tokens from j on some query sees
+    __device__ __forceinline__ uint32_t rows(int j) const {
+        auto below = [&](int x) { return x <= j ? 0u : (x - j >= 16 ? 0xFFFFu : (1u << (x - j)) - 1u); };
+        return below(end) & (~below(lo) | below(sink)) & 0xFFFFu;
+    }
     __device__ __forceinline__ int first_token(int step) const {
         return (step < n_sink ? step : step + jump) * TOK;
     }
@@ -186,22 +208,22 @@ struct Place {
     int hc;
 };
 
-// Steps of all rows on the line, each block's share of them, and the row that
-// holds place share * chunk (share = the caller's block).
+// Steps of all rows on the line, the size of a share, the place of the caller's
+// own, and the row that holds it.
 struct Line {
     int64_t total, chunk, at;  // at >= total: nothing there
     Place row;
 };
 
 __device__ __forceinline__ int64_t chunk_of(const AttendArgs& a, int64_t total) {
-    const int64_t c = (total + a.blocks - 1) / a.blocks;
+    const int64_t c = (total + a.shares - 1) / a.shares;
     return c < a.min_chunk ? a.min_chunk : c;
 }
 
 // Every thread of the block calls this.  Sequences are scanned THREADS at a
 // time; up to THREADS of them (any usual batch) are scanned once.
 template <int TOK, int THREADS>
-__device__ __forceinline__ void find_share(const AttendArgs& a, int64_t share, Line* line) {
+__device__ __forceinline__ void find_share(const AttendArgs& a, Line* line) {
     __shared__ int64_t sums[THREADS / 32], found[3];
     constexpr int NW = THREADS / 32;
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
@@ -237,7 +259,7 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t share, L
             if (once) {
                 line->total = carry * HC;
                 line->chunk = chunk_of(a, line->total);
-                line->at = share * line->chunk;
+                line->at = blockIdx.x * line->chunk;
             }
             const int64_t p0 = (before + inc - ns) * HC, p1 = (before + inc) * HC;
             if (b < a.B && line->at >= p0 && line->at < p1) {
@@ -250,7 +272,7 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, int64_t share, L
         if (once) break;
         line->total = carry * HC;
         line->chunk = chunk_of(a, line->total);
-        line->at = share * line->chunk;
+        line->at = blockIdx.x * line->chunk;
         if (line->at >= line->total) break;
     }
     __syncthreads();
@@ -309,8 +331,7 @@ __device__ __forceinline__ void finish8(const AttendArgs& a, int64_t b, const Co
 // ---------------------------------------------------------------- the cluster's shared memory
 
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t in_block(uint32_t addr, int rank) {
     uint32_t r;
@@ -334,10 +355,10 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr, int rank) {
     return v;
 }
 
-// The workspace: a Cut for every block, then two parts for every block.
-// Block i's Cut tells of the row that its upper border cuts, if i is the first
-// block that the row lies in: whose it is, which of block i's parts is its
-// first, and the last block it reaches.  Every block writes its Cut.
+// The workspace: a Cut for every share, then two parts for every share.
+// Share i's Cut tells of the row that its upper border cuts, if i is the first
+// share that the row lies in: whose it is, which of share i's parts is its
+// first, and the last share it reaches.  Every share writes its Cut.
 struct __align__(16) Cut {
     int64_t b;
     int64_t last;
@@ -350,23 +371,67 @@ static_assert(sizeof(Cut) == kCutBytes, "the workspace is sized on the host");
 __device__ __forceinline__ Cut* cut_of(const AttendArgs& a, int64_t blk) {
     return reinterpret_cast<Cut*>(a.ws) + blk;
 }
-// Partial results of block `blk`'s first (0) or last (1) row.
+// Partial results of share `blk`'s first (0) or last (1) row.
 template <class C>
 __device__ __forceinline__ float* part_of(const AttendArgs& a, int64_t blk, int which) {
-    return reinterpret_cast<float*>(a.ws + a.blocks * kCutBytes) +
+    return reinterpret_cast<float*>(a.ws + a.shares * kCutBytes) +
            (blk * 2 + which) * (int64_t)(C::kCols * (C::D + 2));
 }
 
 // ---------------------------------------------------------------- the stream
 
+// One tile's weighted values, token by token, for the columns that see each
+// (the values' NaN reaches those alone).  p: the packed weights as the scores
+// lie: tokens g and g + 8, columns 2 t and 2 t + 1; see: their bits.  A path
+// for NaN codes under a mask only: small rather than fast.
+template <class C>
+__device__ __forceinline__ void add_tile(float (&o)[C::D / 16][C::NT][4], const uint32_t (&p)[C::NT][2],
+                                         uint32_t see, uint32_t vt) {
+    constexpr int D = C::D, MT = D / 16;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll 1
+    for (int r = 0; r < 16; ++r) {
+        const int from = (r & 7) * 4 + t, h = r >> 3;
+        const uint32_t bits = __shfl_sync(0xFFFFFFFFu, see, from) >> (2 * h);
+#pragma unroll
+        for (int nt = 0; nt < C::NT; ++nt) {
+            const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, p[nt][0], from);
+            const uint32_t w1 = __shfl_sync(0xFFFFFFFFu, p[nt][1], from);
+            const uint32_t w = h ? w1 : w0;
+            const bool on0 = bits >> (4 * nt) & 1, on1 = bits >> (4 * nt + 1) & 1;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {  // dims 2 i and 2 i + 1 of the lane's
+                const int d = D == 64 ? g * 8 + 2 * i : (g + 8 * (i / 8)) * 16 + 2 * (i % 8);
+                const int e = r * (D / 16) + d / 16;  // 16-byte chunk, swizzled as V is
+                const int at = D == 64 ? (e & ~7) + ((e & 7) ^ (((r >> 1) & 3) * 2)) : e ^ (((r >> 1) & 3) * 2);
+                uint16_t v;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(vt + at * 16 + d % 16) : "memory");
+                const uint32_t x = e4m3x2_to_f16x2(v);
+                const float v0 = rmsn::lo2<F16>(x), v1 = rmsn::hi2<F16>(x);
+                if (on0) {
+                    o[i][nt][0] = fmaf(v0, rmsn::lo2<F16>(w), o[i][nt][0]);
+                    o[i][nt][2] = fmaf(v1, rmsn::lo2<F16>(w), o[i][nt][2]);
+                }
+                if (on1) {
+                    o[i][nt][1] = fmaf(v0, rmsn::hi2<F16>(w), o[i][nt][1]);
+                    o[i][nt][3] = fmaf(v1, rmsn::hi2<F16>(w), o[i][nt][3]);
+                }
+            }
+        }
+    }
+}
+
+// A block's warps take the steps of its share in turn, and are joined where a
+// row ends.
 template <class T, class C>
 __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArgs a) {
-    constexpr int D = C::D, NT = C::NT, KT = C::KT, W = C::W, S = C::S;
+    constexpr int D = C::D, NT = C::NT, KT = C::KT, W = C::W;
     constexpr int CH = D / 16;                 // 16-byte chunks of a token
     constexpr int MT = D / 16;                 // tiles of 16 dims
-    constexpr bool kQRegs = NT == 1 && D <= 128;
+    constexpr bool kQRegs = NT == 1 && D <= 128 && KT == 1;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ float q_scale[C::kCols];
+    __shared__ int q_index[C::kCols];  // a column's query token
     __shared__ float2 part_ml[C::kCols];
     __shared__ float j_m[W][C::kCols], j_l[W][C::kCols];
     rmsn::pdl_wait(a.pdl);
@@ -374,7 +439,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
 
-    // this block's steps: `count` from place `begin`, the first of them in row
+    // this share's steps: `count` from place `begin`, the first of them in row
     // `at` (whose first step lies at at.first <= begin)
     int64_t begin, chunk = 0;
     int count;
@@ -392,7 +457,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         count = left < 0 ? 0 : (left < per ? left : per);
     } else {
         Line line;
-        find_share<C::kTok, W * 32>(a, blockIdx.x, &line);
+        find_share<C::kTok, W * 32>(a, &line);
         begin = line.at;
         chunk = line.chunk;
         at = line.row;
@@ -403,16 +468,16 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         count = (int)(line.total - begin < chunk ? line.total - begin : chunk);
     }
 
-    unsigned char* ring = smem + wp * (S * C::kStage);
-    unsigned char* meta = smem + C::kRing + wp * (S * C::kMeta);
+    unsigned char* meta = smem + C::kRing + wp * C::kMeta;
     unsigned char* qrows = smem + C::kRing + C::kMetaAll;
-    const uint32_t ring_s = smem_addr(ring), meta_s = smem_addr(meta);
+    const uint32_t ring_s = smem_addr(smem) + wp * C::kWarp, meta_s = smem_addr(meta);
 
-    // ---- queries: this warp's columns wp, wp + W, ... of a row, first into
+    // ---- queries: this warp's columns of a row, first into
     // registers (before the wait that they can hide behind), then to shared
     // memory in fp16, each scaled by a power of two to at most 2^8 (so that
     // fp16 holds any bf16 row: what is below 2^-32 of the row's largest value
-    // loses bits); q_scale undoes it, times scale * log2(e)
+    // loses bits); q_scale undoes it, times |scale| log2(e) (a negative scale
+    // turns the queries' sign)
     constexpr int QC = (C::kCols + W - 1) / W, QW = D / 64;
     uint32_t qreg[QC][QW];
     auto load_q = [&](int64_t b, int hc) {
@@ -429,7 +494,9 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                                  : 0u;
         }
     };
-    auto store_q = [&]() {
+    auto store_q = [&](int cg) {
+        for (int c = threadIdx.x; c < C::kCols; c += W * 32)
+            q_index[c] = (cg * C::kCols + c) / (a.Hq / a.c.H);
 #pragma unroll
         for (int i = 0; i < QC; ++i) {
             const int c = wp + i * W;
@@ -440,10 +507,10 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
             m = rmsn::warp_max(m);
             int e = (int)(__float_as_uint(m) >> 23) - 127 - 7;  // 2^e <= m / 128 < 2^(e + 1)
             e = e < -126 ? -126 : (e > 126 ? 126 : e);
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), a.scale);
             const float up = __uint_as_float((uint32_t)(127 + e) << 23);
             if (c >= C::kCols) break;
-            if (lane == 0) q_scale[c] = up * (a.scale * kLog2e);
+            if (lane == 0) q_scale[c] = up * (fabsf(a.scale) * kLog2e);
 #pragma unroll
             for (int k = 0; k < QW; ++k)
                 *reinterpret_cast<uint32_t*>(qrows + c * C::kQPitch + (64 * k + 2 * lane) * 2) =
@@ -452,21 +519,25 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     };
     load_q(at.b, at.hc);
 
-    // ---- producer: this warp's steps wp, wp + W, ... of the block's `count`
+    // ---- producer: this warp's steps of the share's `count`
+    //
+    // A batch: up to 32 of the warp's steps of one row, one to a lane; `next_`
+    // is on its way (its table entries are loading) while the other is used.
+    // A tile's word: its block of 16 tokens in the page (12 bits), whether every
+    // query sees all of it (bit 12), and from bit 16 on which of its rows some
+    // query sees (none where the page is bad).
     int p_at = wp, p_first = (int)(at.first - begin), p_hc = at.hc;  // places relative to begin
     int64_t p_b = at.b;
     Span<C::kTok> p_span;
     p_span.of(a, a.lengths[p_b]);
     int p_len_next = p_b + 1 < a.B ? a.lengths[p_b + 1] : 0;
     const int32_t* p_row = a.table + p_b * a.table_stride;
-    bool p_on = false;
-    int p_t0 = 0, p_in[KT], p_hk = p_hc / a.groups;
-    int32_t p_page[KT];  // the table's entry, or -1 past the sequence
-
-    // the next step's row and pages (loaded here, used one step later)
-    auto locate = [&]() {
-        p_on = p_at < count;
-        if (!p_on) return;
+    int b_n = 0, b_at = 0, b_hk = 0, next_n = 0, next_hk = 0;
+    int32_t b_page[KT], next_page[KT];   // pages
+    uint32_t b_where[KT], next_where[KT];
+    auto look_ahead = [&]() {
+        next_n = 0;
+        if (p_at >= count) return;
         while (p_at >= p_first + p_span.ns) {
             p_first += p_span.ns;
             if (++p_hc == a.c.H * a.groups) {
@@ -476,18 +547,40 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                 p_span.of(a, p_len_next);
                 p_len_next = p_b + 1 < a.B ? a.lengths[p_b + 1] : 0;
             }
-            p_hk = p_hc / a.groups;
         }
-        p_t0 = p_span.first_token(p_at - p_first);
+        const int end = p_first + p_span.ns < count ? p_first + p_span.ns : count;
+        next_n = (end - p_at + W - 1) / W;
+        if (next_n > 32) next_n = 32;
+        next_hk = p_hc / a.groups;
+        const int t0 = p_span.first_token(p_at + lane * W - p_first);
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            const int j = p_t0 + 16 * k;
+            const int j = t0 + 16 * k;
+            const bool any = lane < next_n && j < p_span.end && (j + 15 >= p_span.lo || j < p_span.sink);
             // slot = j / page, both multiples of 16: exact for j < 2^29
             const int slot = (int)(((uint64_t)(uint32_t)(j >> 4) * a.page_rcp) >> 37);
-            p_in[k] = j - slot * a.c.page;
-            p_page[k] = j < p_span.end ? p_row[slot] : -1;  // end lies within the table
+            next_page[k] = any ? p_row[slot] : -1;  // end lies within the table
+            next_where[k] = (uint32_t)((j - slot * a.c.page) >> 4) |
+                            (any ? p_span.open(a, j) | (p_span.rows(j) << 16) : 0u);
         }
-        p_at += W;
+        p_at += next_n * W;
+    };
+    auto turn_page = [&]() {  // the batch that was on its way becomes the one in use
+        b_n = next_n;
+        b_at = 0;
+        if (next_n == 0) return;
+        b_hk = next_hk;
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            b_page[k] = next_page[k];
+            b_where[k] = next_where[k];
+            if ((uint32_t)b_page[k] >= (uint32_t)a.c.n_pages) {
+                if (b_where[k] >> 16) atomicOr(a.status, kBadPage);
+                b_page[k] = 0;
+                b_where[k] = 0;
+            }
+        }
+        look_ahead();
     };
     // Lane constants of the copies: chunk i of a tile is 512 i bytes on in
     // memory, and in the stage too, but for V's swizzle, which flips with i.
@@ -508,59 +601,73 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         if constexpr (D == 256) return v_dst[0] ^ ((i & 3) * 32);
         else return v_dst[i & 1];
     };
-    // copies of the located step into stage `slot`
-    auto issue = [&](int slot) {
-        if (p_on) {
-            const uint32_t st = ring_s + slot * C::kStage, me = meta_s + slot * C::kMeta;
+    // the step to copy: its tiles' places and states
+    bool s_on = false;
+    uint32_t s_where[KT];
+    int32_t s_page[KT], s_tile[KT];
+    int64_t s_off[KT];  // bytes from the cache's begin to the tile, plus the lane's 16
+    auto locate = [&]() {
+        if (b_at == b_n) turn_page();
+        s_on = b_at < b_n;
+        if (!s_on) return;
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            s_page[k] = __shfl_sync(0xFFFFFFFFu, b_page[k], b_at);
+            s_where[k] = __shfl_sync(0xFFFFFFFFu, b_where[k], b_at);
+            s_tile[k] = b_hk * (a.c.page >> 4) + (int)(s_where[k] & 0xFFF);
+            s_off[k] = s_page[k] * a.c.page_stride + (int64_t)(s_tile[k] * (D / 16)) * 256 + lane * 16;
+        }
+        ++b_at;
+    };
+    auto copy_tile = [&](uint32_t dst, const uint8_t* src, bool v, uint32_t where) {
+        if (where & kOpen) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) cp16(dst + (v ? v_at(i) : k_dst) + i * 512, src + i * 512);
+        } else {  // rows that no query sees are zeros
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+                cp16(dst + (v ? v_at(i) : k_dst) + i * 512, src + i * 512,
+                     where >> (16 + l_row + i * (32 / CH)) & 1);
+        }
+    };
+    // the located step's K and scales, or V, into stage `slot`
+    auto issue_k = [&](int slot) {
+        if (s_on) {
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
-                const int j0 = p_t0 + 16 * k;
-                // a tile of which no query sees a token brings nothing in, its scales neither
-                const bool any = j0 < p_span.end && (j0 + 15 >= p_span.lo || j0 < p_span.sink);
-                const bool ok = any && (uint32_t)p_page[k] < (uint32_t)a.c.n_pages;
-                const int64_t pg = ok ? p_page[k] : 0;
-                const int64_t at8 =
-                    pg * a.c.page_stride + (int64_t)(p_hk * a.c.page + p_in[k]) * D + lane * 16;
-                const uint8_t *kp = a.c.k + at8, *vp = a.c.v + at8;
-                const uint32_t kd = st + k * C::kTile + k_dst, vd = st + (KT + k) * C::kTile;
-                if (ok && j0 + 16 <= p_span.end && j0 >= p_span.lo) {
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        cp16(kd + i * 512, kp + i * 512);
-                        cp16(vd + v_at(i) + i * 512, vp + i * 512);
-                    }
-                } else {  // rows that no query sees are zeros
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        const int j = j0 + l_row + i * (32 / CH);
-                        const bool on = ok && j < p_span.end && (j >= p_span.lo || j < p_span.sink);
-                        cp16(kd + i * 512, kp + i * 512, on);
-                        cp16(vd + v_at(i) + i * 512, vp + i * 512, on);
-                    }
-                }
-                if (lane < 2) {
-                    const int64_t sc = pg * a.c.scale_stride + p_hk * (a.c.page / kBlock) +
-                                       p_in[k] / kBlock;
-                    cp4(me + k * 16 + lane * 4, (lane ? a.c.vs : a.c.ks) + sc, ok);
-                } else if (lane == 2) {
-                    *reinterpret_cast<int*>(meta + slot * C::kMeta + k * 16 + 8) = ok;
-                    if (!ok && any) atomicOr(a.status, kBadPage);
-                }
+                copy_tile(ring_s + slot * C::kSide + k * C::kTile, a.c.k + s_off[k], false, s_where[k]);
+                if (lane < 2)
+                    cp4(meta_s + (slot * KT + k) * 16 + lane * 4,
+                        (lane ? a.c.vs : a.c.ks) + s_page[k] * a.c.scale_stride + s_tile[k],
+                        s_where[k] >> 16);
+                else if (lane == 2)
+                    *reinterpret_cast<uint32_t*>(meta + (slot * KT + k) * 16 + 8) = s_where[k];
             }
         }
         cp_commit();
     };
-
-    locate();
+    auto issue_v = [&](int slot) {
+        if (s_on) {
 #pragma unroll
-    for (int s = 0; s < S - 1; ++s) {
-        issue(s);
+            for (int k = 0; k < KT; ++k)
+                copy_tile(ring_s + (2 + slot) * C::kSide + k * C::kTile, a.c.v + s_off[k], true, s_where[k]);
+        }
+        cp_commit();
+    };
+
+    look_ahead();
+    turn_page();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
         locate();
+        issue_k(i);
+        issue_v(i);
     }
+    locate();
 
     // ---- consumer: rows one after another, this warp's steps of each
     int slot = 0;
-    int cur = 0;  // the row's first place within this block
+    int cur = 0;  // the row's first place within this share
     int mine = wp;
     int64_t c_b = at.b;
     int c_first = (int)(at.first - begin), c_hc = at.hc;
@@ -574,7 +681,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         const int hk = c_hc / a.groups, cg = c_hc % a.groups;
         if (span.L > span.end && threadIdx.x == 0) atomicOr(a.status, kBadPage);
 
-        store_q();
+        store_q(cg);
         __syncthreads();
         float cs[NT][2];
 #pragma unroll
@@ -591,30 +698,30 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         float o[MT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = -INFINITY;
+            m[nt][0] = m[nt][1] = kNone;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) o[i][nt][k] = 0.f;
         }
-        float vref = kTinyScale;  // O is in units of vref / kLift
+        float vref = kTinyScale, rv = 1.f / kTinyScale;  // O is in units of vref / kLift
 
         for (; mine < seg_end; mine += W) {
-            cp_wait<S - 2>();
+            cp_wait<3>();  // K and the scales; behind them V, and the next step's both
             __syncwarp();
-            issue(slot == 0 ? S - 1 : slot - 1);
-            locate();
-            const uint32_t st = ring_s + slot * C::kStage;
-            const float* me = reinterpret_cast<const float*>(meta + slot * C::kMeta);
             float ks[KT], vs[KT];
-            bool ok[KT];
+            uint32_t where[KT], all_where = kOpen;
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
-                ks[k] = me[4 * k];
-                vs[k] = me[4 * k + 1];
-                ok[k] = reinterpret_cast<const int*>(me)[4 * k + 2] != 0;
+                const uint4 me = lds16(meta_s + (slot * KT + k) * 16);
+                ks[k] = __uint_as_float(me.x);
+                vs[k] = __uint_as_float(me.y);
+                where[k] = me.z;
+                all_where &= me.z;
             }
+            const bool open = all_where != 0;  // no mask touches this step
+            const uint32_t st = ring_s + slot * C::kSide;
 
             // S^T = K Q^T
             float s[KT][NT][4];
@@ -653,71 +760,64 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                 }
             }
 
-            // scores in units of log2, masked where a column does not see the token
-            const int t0 = span.first_token(mine - c_first);
-            bool all_ok = true;
-#pragma unroll
-            for (int k = 0; k < KT; ++k) all_ok = all_ok && ok[k];
-            const bool open = all_ok && t0 + C::kTok - 1 <= span.L - a.n &&
-                              (a.window == 0 || t0 > span.L - 1 - a.window || t0 + C::kTok <= span.sink);
+            __syncwarp();
+            issue_k(slot);  // every lane has read this stage
+
+            // Scores are S kc - m in units of log2, kc = K scale x query scale
+            // (not negative).  A mask makes S -inf, and the weight 0 below.
             uint32_t see[KT];  // bit 4 nt + x: this lane's element is visible
-#pragma unroll
-            for (int k = 0; k < KT; ++k) {
-                see[k] = 0xFFFFFFFFu;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) s[k][nt][x] *= ks[k] * cs[nt][x & 1];
-            }
             if (!open) {
-                const int G = a.Hq / a.c.H;
+                const int t0 = span.first_token(mine - c_first);
+#pragma unroll
+                for (int k = 0; k < KT; ++k) see[k] = 0u;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const int pos = span.L - a.n + (cg * C::kCols + nt * 8 + 2 * t + x) / G;
+                        const int pos = span.L - a.n + q_index[nt * 8 + 2 * t + x];
+                        const int from = a.window == 0 ? 0 : pos - a.window + 1;
 #pragma unroll
                         for (int k = 0; k < KT; ++k)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const int j = t0 + 16 * k + g + 8 * h;
-                                const bool on = ok[k] && j <= pos && j < span.end &&
-                                                (a.window == 0 || j > pos - a.window || j < a.sinks);
-                                if (!on) {
-                                    s[k][nt][2 * h + x] = -INFINITY;
-                                    see[k] &= ~(1u << (4 * nt + 2 * h + x));
-                                }
+                                const bool on = (where[k] >> (16 + g + 8 * h) & 1) && j <= pos &&
+                                                (j >= from || j < a.sinks);
+                                if (on) see[k] |= 1u << (4 * nt + 2 * h + x);
+                                else s[k][nt][2 * h + x] = -INFINITY;
                             }
                     }
             }
-
-            // running maximum; what was summed so far follows it
+            float kc[KT][NT][2];
             bool grew = false;
-            float mm[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    float v = fmaxf(s[0][nt][x], s[0][nt][2 + x]);
+                for (int x = 0; x < 2; ++x)
 #pragma unroll
-                    for (int k = 1; k < KT; ++k) v = fmaxf(v, fmaxf(s[k][nt][x], s[k][nt][2 + x]));
-                    v = fmaxf(max_over_rows(v), m[nt][x]);
-                    grew = grew || v > m[nt][x];
-                    mm[nt][x] = v;
-                }
+                    for (int k = 0; k < KT; ++k) {
+                        kc[k][nt][x] = ks[k] * cs[nt][x];
+                        grew = grew || fmaxf(s[k][nt][x], s[k][nt][2 + x]) * kc[k][nt][x] > m[nt][x] + kSlack;
+                    }
             float vmax = vref;
 #pragma unroll
             for (int k = 0; k < KT; ++k) vmax = fmaxf(vmax, vs[k]);
             if (__any_sync(0xFFFFFFFFu, grew) || vmax > vref) {
+                // new references; what was summed so far follows them
                 const float vr = vref / vmax;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float keep[2];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        keep[x] = mm[nt][x] == -INFINITY ? 1.f : exp2a(m[nt][x] - mm[nt][x]);
+                        float to = m[nt][x];
+#pragma unroll
+                        for (int k = 0; k < KT; ++k)
+                            to = fmaxf(to, fmaxf(s[k][nt][x], s[k][nt][2 + x]) * kc[k][nt][x]);
+                        to = max_over_rows(to);
+                        keep[x] = exp2a(m[nt][x] - to);
                         l[nt][x] *= keep[x];
-                        m[nt][x] = mm[nt][x];
+                        m[nt][x] = to;
                         keep[x] *= vr;
                     }
 #pragma unroll
@@ -726,33 +826,56 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                         for (int x = 0; x < 4; ++x) o[i][nt][x] *= keep[x & 1];
                 }
                 vref = vmax;
+                rv = 1.f / vmax;
             }
 
             // weights; P^T as the second product's operand
             uint32_t pb[KT][NT][2];
-            const float rv = 1.f / vref;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-                const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+            for (int k = 0; k < KT; ++k) {
+                const float f = vs[k] * rv * kLift;
 #pragma unroll
-                for (int k = 0; k < KT; ++k) {
-                    const float f = vs[k] * rv * kLift;
+                for (int nt = 0; nt < NT; ++nt) {
                     float p[4];
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        p[x] = exp2a(s[k][nt][x] - ((x & 1) ? m1 : m0));
+                        p[x] = exp2a(fmaf(s[k][nt][x], kc[k][nt][x & 1], -m[nt][x & 1]));
+                        if (!open && !(see[k] >> (4 * nt + x) & 1)) p[x] = 0.f;
                         l[nt][x & 1] += p[x];
                     }
-                    pb[k][nt][0] = transpose8(rmsn::pack_f16x2(p[0] * f, p[1] * f));
-                    pb[k][nt][1] = transpose8(rmsn::pack_f16x2(p[2] * f, p[3] * f));
+                    pb[k][nt][0] = rmsn::pack_f16x2(p[0] * f, p[1] * f);
+                    pb[k][nt][1] = rmsn::pack_f16x2(p[2] * f, p[3] * f);
                 }
             }
 
             // O^T += V^T P^T
+            cp_wait<3>();  // V; behind it the next step's K and V, and the K after
+            __syncwarp();
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
-                const uint32_t vt = st + (KT + k) * C::kTile;
+                const uint32_t vt = st + 2 * C::kSide + k * C::kTile;
+                // A token that some columns see and others do not may hold NaN
+                // codes, which weights of 0 would carry into the others' sums:
+                // then the tile is added token by token, where it is seen.
+                bool nan = false;
+                if (!open && a.n > 1) {
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        const uint4 v = lds16(vt + lane * 16 + i * 512);
+                        nan = nan || (nan_bytes(v.x) | nan_bytes(v.y) | nan_bytes(v.z) | nan_bytes(v.w));
+                    }
+                    nan = __any_sync(0xFFFFFFFFu, nan);
+                }
+                if (nan) {
+                    add_tile<C>(o, pb[k], see[k], vt);
+                    continue;
+                }
+                uint32_t pt[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    pt[nt][0] = transpose8(pb[k][nt][0]);
+                    pt[nt][1] = transpose8(pb[k][nt][1]);
+                }
 #pragma unroll
                 for (int cj = 0; cj < (D == 256 ? 2 : 1); ++cj) {
                     constexpr int WD = D == 64 ? 2 : 4;  // words of dims a lane holds per token
@@ -773,24 +896,6 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                             w[x][3] = v.w;
                         }
                     }
-                    // A token that some columns see and others do not may hold
-                    // NaN codes, which 0 weights would carry into the others'
-                    // sums: here they count as 0, and a product of "is NaN"
-                    // with "sees it" finds the sums that become NaN.
-                    uint32_t nan[4][WD];
-                    bool any_nan = false;
-                    if (!open && a.n > 1) {
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-#pragma unroll
-                            for (int i = 0; i < WD; ++i) {
-                                nan[x][i] = nan_bytes(w[x][i]) >> 7;
-                                any_nan = any_nan || nan[x][i];
-                                w[x][i] &= ~(nan[x][i] * 0xFFu);
-                                nan[x][i] *= 0x38u;  // 1.0
-                            }
-                        any_nan = __any_sync(0xFFFFFFFFu, any_nan);
-                    }
 #pragma unroll
                     for (int i = 0; i < WD; ++i) {
                         const uint32_t lo01 = __byte_perm(w[0][i], w[1][i], 0x5140);
@@ -803,40 +908,18 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                         const uint32_t b2 = e4m3x2_to_f16x2(hi23), b3 = e4m3x2_to_f16x2(hi23 >> 16);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(o[cj * 8 + 2 * i][nt], a0, a1, a2, a3, pb[k][nt][0], pb[k][nt][1]);
-                            mma16816(o[cj * 8 + 2 * i + 1][nt], b0, b1, b2, b3, pb[k][nt][0], pb[k][nt][1]);
-                        }
-                    }
-                    if (any_nan) {
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            const uint32_t e = see[k] >> (4 * nt);
-                            const uint32_t v0 = transpose8(((e & 1) ? 0x3C00u : 0) | ((e & 2) ? 0x3C000000u : 0));
-                            const uint32_t v1 = transpose8(((e & 4) ? 0x3C00u : 0) | ((e & 8) ? 0x3C000000u : 0));
-#pragma unroll
-                            for (int i = 0; i < WD; ++i)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    const int sel = h ? 0x7362 : 0x5140;
-                                    const uint32_t n01 = __byte_perm(nan[0][i], nan[1][i], sel);
-                                    const uint32_t n23 = __byte_perm(nan[2][i], nan[3][i], sel);
-                                    float hit[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma16816(hit, e4m3x2_to_f16x2(n01), e4m3x2_to_f16x2(n01 >> 16),
-                                             e4m3x2_to_f16x2(n23), e4m3x2_to_f16x2(n23 >> 16), v0, v1);
-#pragma unroll
-                                    for (int x = 0; x < 4; ++x)
-                                        if (hit[x] > 0.f) o[cj * 8 + 2 * i + h][nt][x] = NAN;
-                                }
+                            mma16816(o[cj * 8 + 2 * i][nt], a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
+                            mma16816(o[cj * 8 + 2 * i + 1][nt], b0, b1, b2, b3, pt[nt][0], pt[nt][1]);
                         }
                     }
                 }
             }
-            slot = slot == S - 1 ? 0 : slot + 1;
+            __syncwarp();
+            issue_v(slot);
+            locate();
+            slot ^= 1;
         }
 
-        // the row's (or the part's) results: join the warps, four columns at a
-        // time (lanes t of one parity hold four of a tile's columns); behind
-        // the block's last step the ring is free, and holds all of them
         const bool last = seg_end >= count;
         const bool whole = a.split > 0 ? a.split == 1 : cur == c_first && seg_end == row_end;
         const float unit = vref / kLift;
@@ -849,7 +932,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
             cut->which = cur == 0 ? 0 : 1;
             cut->last = (begin + row_end - 1) / chunk;
         }
-        // the next row's queries and length, while this one is joined
+        // the next row's queries and length, while this one is finished
         const int64_t row_b = c_b;
         if (!last) {
             if (++c_hc == a.c.H * a.groups) {
@@ -860,13 +943,16 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         }
         int used = a.cols - cg * C::kCols;  // columns of this row
         if (used > C::kCols) used = C::kCols;
-        const int quads = (used + 3) / 4, step = last ? 2 * NT : 1;
         float ls[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             ls[nt][0] = sum_over_rows(l[nt][0]);
             ls[nt][1] = sum_over_rows(l[nt][1]);
         }
+        // join the warps, four columns at a time (lanes t of one parity hold
+        // four of a tile's columns); behind the block's last step the ring is
+        // free, and holds all of them
+        const int quads = (used + 3) / 4, step = last ? 2 * NT : 1;
         float* join = reinterpret_cast<float*>(last ? smem : smem + C::kRing + C::kMetaAll + C::kQ);
         if (last) __syncthreads();  // every warp is through with its stages
         for (int q0 = 0; q0 < quads; q0 += step) {
@@ -898,16 +984,15 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                 const int c = e / (D / 8), d = e % (D / 8) * 8, cc = q0 * 4 + c;
                 const Col col = column(a, hk, cg, cc, C::kCols);
                 if (!col.on) continue;
-                float mx = -INFINITY;
+                float mx = kNone;
 #pragma unroll
                 for (int w = 0; w < W; ++w) mx = fmaxf(mx, j_m[w][cc]);
-                const float ms = mx == -INFINITY ? 0.f : mx;
                 float lsum = 0.f, y[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) y[k] = 0.f;
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
-                    const float f = exp2a(j_m[w][cc] - ms);
+                    const float f = exp2a(j_m[w][cc] - mx);
                     lsum += j_l[w][cc] * f;
                     add8(y, reinterpret_cast<const float4*>(join + (c * W + w) * D + d), f);
                 }
@@ -938,15 +1023,14 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                 if (!col.on) continue;
                 const uint32_t ml = smem_addr(&part_ml[cc]);
                 const uint32_t jr = smem_addr(join + cc * W * D + d);
-                float mx = -INFINITY;
+                float mx = kNone;
                 for (int r = 0; r < a.split; ++r) mx = fmaxf(mx, ld_cluster2(ml, r).x);
-                const float ms = mx == -INFINITY ? 0.f : mx;
                 float lsum = 0.f, y[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) y[k] = 0.f;
                 for (int r = 0; r < a.split; ++r) {
                     const float2 p = ld_cluster2(ml, r);
-                    const float f = exp2a(p.x - ms);
+                    const float f = exp2a(p.x - mx);
                     lsum += p.y * f;
                     const float4 v[2] = {ld_cluster4(jr, r), ld_cluster4(jr + 16, r)};
                     add8(y, v, f);
@@ -967,14 +1051,17 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     cp_wait<0>();
 }
 
-// Joins the parts of the rows that block borders cut, in block order.  Block
-// (i, q): the row of block i's Cut, columns 4 q to 4 q + 3; 512 / D parts at a
-// time, D threads to a part (four dims of a column each).
+// Joins the parts of the rows that the shares' borders cut, in the shares'
+// order.  Block (i, q): the row of share i's Cut, columns 4 q to 4 q + 3; D
+// threads to a part (four dims of a column each), 512 / D groups of them, each
+// with every (512 / D)-th part.  A thread takes up to eight parts at a time,
+// their references and sums and values all on their way at once: the launch
+// is a chain of latencies (Cut, parts, join of the groups), not of bytes.
 template <class T, class C>
 __global__ void __launch_bounds__(512) attend_join_kernel(const AttendArgs a) {
-    constexpr int D = C::D, NG = 512 / D;
+    constexpr int D = C::D, NG = 512 / D, U = 8;
     __shared__ float4 sum[NG][D];
-    __shared__ float top[4], total[4];
+    __shared__ float top[NG][4], total[NG][4];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Cut cut = *cut_of(a, blockIdx.x);
@@ -983,68 +1070,70 @@ __global__ void __launch_bounds__(512) attend_join_kernel(const AttendArgs a) {
     const int n = (int)(cut.last - c0) + 1, q = blockIdx.y * 4;
     const int hk = cut.hc / a.groups, cg = cut.hc % a.groups;
     if (cg * C::kCols + q >= a.cols) return;
-    auto part = [&](int i) { return part_of<C>(a, c0 + i, i == 0 ? cut.which : 0); };
-    const int wp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (wp < 4) {  // the largest maximum of column q + wp, and the sum at it
-        float m = -INFINITY, l = 0.f;
-        for (int i = lane; i < n; i += 32)
-            m = fmaxf(m, part(i)[C::kCols * D + (q + wp) * 2]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const float ms = m == -INFINITY ? 0.f : m;
-        for (int i = lane; i < n; i += 32) {
-            const float2 ml = *reinterpret_cast<const float2*>(part(i) + C::kCols * D + (q + wp) * 2);
-            l += ml.y * exp2a(ml.x - ms);
-        }
-        l = rmsn::warp_sum(l);
-        if (lane == 0) {
-            top[wp] = ms;
-            total[wp] = l;
-        }
-    }
-    __syncthreads();
     const int grp = threadIdx.x / D, c = threadIdx.x % D / (D / 4), d = threadIdx.x % (D / 4) * 4;
-    const float ms = top[c];
+    float m = kNone, l = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = grp; i < n; i += NG) {
-        const float* p = part(i);
-        const float f = exp2a(p[C::kCols * D + (q + c) * 2] - ms);
-        const float4 v = *reinterpret_cast<const float4*>(p + (q + c) * D + d);
-        y.x += v.x * f;
-        y.y += v.y * f;
-        y.z += v.z * f;
-        y.w += v.w * f;
+    for (int i0 = grp; i0 < n; i0 += NG * U) {
+        float2 ml[U];
+        float4 v[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const int i = i0 + k * NG;
+            ml[k] = make_float2(kNone, 0.f);
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < n) {
+                const float* p = part_of<C>(a, c0 + i, i == 0 ? cut.which : 0);
+                ml[k] = *reinterpret_cast<const float2*>(p + C::kCols * D + (q + c) * 2);
+                v[k] = *reinterpret_cast<const float4*>(p + (q + c) * D + d);
+            }
+        }
+        float to = m;
+#pragma unroll
+        for (int k = 0; k < U; ++k) to = fmaxf(to, ml[k].x);
+        const float keep = exp2a(m - to);
+        m = to;
+        l *= keep;
+        y = make_float4(y.x * keep, y.y * keep, y.z * keep, y.w * keep);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const float f = exp2a(ml[k].x - m);
+            l += ml[k].y * f;
+            y.x += v[k].x * f;
+            y.y += v[k].y * f;
+            y.z += v[k].z * f;
+            y.w += v[k].w * f;
+        }
     }
     sum[grp][threadIdx.x % D] = y;
+    if (d == 0) {
+        top[grp][c] = m;
+        total[grp][c] = l;
+    }
     __syncthreads();
     if (threadIdx.x >= D / 2) return;
     const int oc = threadIdx.x / (D / 8), od = threadIdx.x % (D / 8);
     const Col col = column(a, hk, cg, q + oc, C::kCols);
     if (!col.on) return;
-    float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float mx = kNone, ls = 0.f, r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NG; ++k) mx = fmaxf(mx, top[k][oc]);
 #pragma unroll
     for (int k = 0; k < NG; ++k) {
-        const float4 u = sum[k][oc * (D / 4) + 2 * od], v = sum[k][oc * (D / 4) + 2 * od + 1];
-        r[0] += u.x;
-        r[1] += u.y;
-        r[2] += u.z;
-        r[3] += u.w;
-        r[4] += v.x;
-        r[5] += v.y;
-        r[6] += v.z;
-        r[7] += v.w;
+        const float f = exp2a(top[k][oc] - mx);
+        ls += total[k][oc] * f;
+        add8(r, &sum[k][oc * (D / 4) + 2 * od], f);
     }
-    finish8<T>(a, cut.b, col, od * 8, r, total[oc]);
+    finish8<T>(a, cut.b, col, od * 8, r, ls);
 }
 
 template <class C>
-AttendEntry attend_entry(int dt) {
+AttendEntry attend_entry(int dt, int most = INT32_MAX) {
     AttendEntry e;
     e.dt = dt;
     e.D = C::D;
     e.NT = C::NT;
     e.tok = C::kTok;
+    e.most = most;
     e.threads = C::W * 32;
     e.smem = C::kSmem;
     e.part = C::kCols * (C::D + 2);

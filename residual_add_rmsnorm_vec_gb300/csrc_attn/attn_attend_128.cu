@@ -3,12 +3,14 @@
 
 namespace rmsattn {
 
-using A = Shape<128, 1, 1, 4, 3, 3>;
-using B = Shape<128, 2, 1, 4, 3, 2>;
-using C = Shape<128, 4, 1, 4, 4, 2>;
+using Short = Shape<128, 1, 1, 4, 3>;
+using A = Shape<128, 1, 2, 4, 2>;
+using B = Shape<128, 2, 1, 4, 3>;
+using C = Shape<128, 4, 1, 4, 2>;
 
 const AttendEntry* attend_kernels_128(int* n) {
     static const AttendEntry table[] = {
+        attend_entry<Short>(1, 512), attend_entry<Short>(2, 512),
         attend_entry<A>(1), attend_entry<A>(2),
         attend_entry<B>(1), attend_entry<B>(2),
         attend_entry<C>(1), attend_entry<C>(2)};

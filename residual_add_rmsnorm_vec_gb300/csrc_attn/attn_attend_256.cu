@@ -3,8 +3,8 @@
 
 namespace rmsattn {
 
-using A = Shape<256, 1, 1, 8, 2, 1>;
-using B = Shape<256, 2, 1, 8, 2, 1>;
+using A = Shape<256, 1, 1, 4, 2>;
+using B = Shape<256, 2, 1, 4, 2>;
 
 const AttendEntry* attend_kernels_256(int* n) {
     static const AttendEntry table[] = {

@@ -3,9 +3,9 @@
 
 namespace rmsattn {
 
-using A = Shape<64, 1, 2, 4, 3, 3>;
-using B = Shape<64, 2, 2, 4, 3, 3>;
-using C = Shape<64, 4, 1, 4, 4, 2>;
+using A = Shape<64, 1, 2, 4, 3>;
+using B = Shape<64, 2, 2, 4, 3>;
+using C = Shape<64, 4, 1, 4, 2>;
 
 const AttendEntry* attend_kernels_64(int* n) {
     static const AttendEntry table[] = {

@@ -155,12 +155,12 @@ def attend(q, cache, table, lengths, scale, window, sinks):
                 o = p @ vv
                 # a score: D products summed in fp32 (a tensor-core sum may
                 # truncate: 2 u a term), three products and the difference
-                # from the maximum; a weight: that, exp2's two ulp, the fp16
-                # rounding; a sum: one rounding for every 16 tokens
+                # from the maximum; a weight: that, exp2's two ulp, the rounding
+                # to fp16 (half a step: 2^-11); a sum: one rounding for every 16 tokens
                 # and the joins
                 ds = float((qq.abs() @ kk.abs().T).max()) * abs(scale) * (2 * D + 8) * U + float(
                     s.abs().max()) * 4 * U
-                rel = 2.0 ** -12 + 2 * (ds + 4 * U) + (2 * vv.shape[0] / 16 + 64) * 2 * U
+                rel = 2.0 ** -11 + 2 * (ds + 4 * U) + (2 * vv.shape[0] / 16 + 64) * 2 * U
                 out[b, i, h * G:(h + 1) * G] = o
                 bound[b, i, h * G:(h + 1) * G] = rel * (p @ vv.abs())
     dt = q.dtype

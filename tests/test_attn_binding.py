@@ -121,9 +121,10 @@ def test_null_cache_refused(rn):
 
 
 @pytest.mark.parametrize("sizes,status", [
-    ((3, 0, 4, 2, 64, 64), -1), ((3, 33, 4, 2, 64, 64), -1), ((-1, 1, 4, 2, 64, 64), -1),
-    ((3, 1, 5, 2, 64, 64), -1), ((3, 1, 4, 0, 64, 64), -1), ((3, 1, 4, 2, 96, 64), -3),
-    ((3, 1, 4, 2, 64, -1), -1), ((3, 1, 4, 2, 64, 1 << 40), -1), ((0, 1, 4, 2, 64, 64), 0),
+    ((3, 0, 4, 2, 64, 64, 0, 0), -1), ((3, 33, 4, 2, 64, 64, 0, 0), -1), ((-1, 1, 4, 2, 64, 64, 0, 0), -1),
+    ((3, 1, 5, 2, 64, 64, 0, 0), -1), ((3, 1, 4, 0, 64, 64, 0, 0), -1), ((3, 1, 4, 2, 96, 64, 0, 0), -3),
+    ((3, 1, 4, 2, 64, -1, 0, 0), -1), ((3, 1, 4, 2, 64, 1 << 40, 0, 0), -1), ((0, 1, 4, 2, 64, 64, 0, 0), 0),
+    ((3, 1, 4, 2, 64, 64, -1, 0), -1), ((3, 1, 4, 2, 64, 64, 0, -1), -1),
 ])
 def test_workspace_refusals(rn, sizes, status):
     assert rn.load_attn().rmsattn_kv_attention_workspace(*sizes) == status

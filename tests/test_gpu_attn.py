@@ -335,8 +335,25 @@ ATTEND = [
 ]
 
 
+def spread_out(table, how, Hk):
+    """(table, repeats) for the ways that the work is shared out: "rows", short
+    tables, a row to a cluster; "line", tables wide enough for long rows, few
+    rows; "many", the same with more rows than a block's warps could each have
+    eight of (the same sequences over and over)."""
+    if how == "rows":
+        return table, 1
+    page_room = 40000 // 16
+    wide = torch.full((table.shape[0], page_room), -1, dtype=torch.int32, device=table.device)
+    wide[:, :table.shape[1]] = table
+    if how == "line":
+        return wide, 1
+    times = -(-400 // (table.shape[0] * Hk))
+    return wide.repeat(times, 1), times
+
+
 @pytest.mark.parametrize("lengths,n,Hq,Hk,D,page,dtype,window,sinks", ATTEND)
-def test_attention(rn, lengths, n, Hq, Hk, D, page, dtype, window, sinks):
+@pytest.mark.parametrize("how", ["rows", "line", "many"])
+def test_attention(rn, lengths, n, Hq, Hk, D, page, dtype, window, sinks, how):
     B = len(lengths)
     width = -(-max(lengths) // page) + 1
     pages = B * width + 2
@@ -344,8 +361,12 @@ def test_attention(rn, lengths, n, Hq, Hk, D, page, dtype, window, sinks):
     table = ref.tables(B, width, pages, 1, "cuda")
     lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
     q = rand((B, n, Hq, D), 3, DT[dtype]).cuda()
-    got = rn.kv_cache_attention(q if n > 1 else q[:, 0], make_cache(rn, t), table, lens, window=window, sinks=sinks)
-    within(got.reshape(q.shape), *ref.attend(q, t, table, lens, 1 / math.sqrt(D), window, sinks))
+    want, bound = ref.attend(q, t, table, lens, 1 / math.sqrt(D), window, sinks)
+    table, times = spread_out(table, how, Hk)
+    big = q.repeat(times, 1, 1, 1)
+    got = rn.kv_cache_attention(big if n > 1 else big[:, 0], make_cache(rn, t), table, lens.repeat(times),
+                                window=window, sinks=sinks)
+    within(got.reshape(times, *q.shape), want[None], bound[None])
 
 
 @pytest.mark.parametrize("D,dtype,qscale", [(64, "bf16", 1.0), (128, "f16", 30.0), (256, "bf16", 1e-3),
@@ -384,7 +405,8 @@ def test_attention_one_strong_token_among_many(rn):
 @pytest.mark.parametrize("n", [1, 3])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (40, 3)])
-def test_attention_masked_places_hold_anything(rn, n, D, window, sinks):
+@pytest.mark.parametrize("how", ["rows", "line", "many"])
+def test_attention_masked_places_hold_anything(rn, n, D, window, sinks, how):
     # NaN codes and NaN, infinite or huge scales in every place that a query must not see
     L, page, Hk, Hq = 150, 16, 2, 8
     t = ref.random_cache(14, Hk, page, D, 7, "cuda", spread=False)
@@ -404,8 +426,10 @@ def test_attention_masked_places_hold_anything(rn, n, D, window, sinks):
         if unseen:
             t["k_scale"][row[blk]] = (math.nan, math.inf, 1e38)[blk % 3]
             t["v_scale"][row[blk]] = (math.inf, math.nan, 1e38)[blk % 3]
-    got = rn.kv_cache_attention(q, make_cache(rn, t), table, lens, window=window, sinks=sinks)
-    within(got, want, bound)
+    table, times = spread_out(table, how, Hk)
+    got = rn.kv_cache_attention(q.repeat(times, 1, 1, 1), make_cache(rn, t), table, lens.repeat(times),
+                                window=window, sinks=sinks)
+    within(got.reshape(times, *q.shape), want[None], bound[None])
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -478,11 +502,12 @@ def test_attention_strided_queries_and_out(rn, n):
     assert bool((big[:, :8] == 7).all()) and bool((big[:, 8 + Hq * D:] == 7).all())
 
 
-def test_attention_gives_the_same_bits_every_time(rn):
+@pytest.mark.parametrize("how", ["rows", "line", "many"])
+def test_attention_gives_the_same_bits_every_time(rn, how):
     t = ref.random_cache(400, 2, 32, 128, 7, "cuda", spread=False)
-    table = ref.tables(3, 130, 400, 1, "cuda")
-    lens = torch.tensor([4100, 1000, 3], dtype=torch.int32, device="cuda")
-    q = rand((3, 8, 128), 3, torch.bfloat16).cuda()
+    table, times = spread_out(ref.tables(3, 130, 400, 1, "cuda"), how, 2)
+    lens = torch.tensor([4100, 1000, 3], dtype=torch.int32, device="cuda").repeat(times)
+    q = rand((3, 8, 128), 3, torch.bfloat16).cuda().repeat(times, 1, 1)
     first = rn.kv_cache_attention(q, make_cache(rn, t), table, lens)
     for _ in range(5):
         assert torch.equal(rn.kv_cache_attention(q, make_cache(rn, t), table, lens), first)

@@ -340,6 +340,7 @@ struct Plan {
     int groups;      // column groups of a key head
     int split;       // a row to `split` blocks of a cluster; 0: one line of all steps
     int64_t blocks;  // of the grid; shares of the line
+    int join;        // threads of a block of the join
     int64_t min_chunk;
     int64_t workspace;
 };
@@ -387,6 +388,9 @@ int plan_attend(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
     const int64_t full = (total + p->min_chunk - 1) / p->min_chunk;
     p->blocks = full < resident ? full : resident;
     if (total / p->blocks > (1 << 30)) return RMSN_EUNSUPPORTED;  // a share counts in 31 bits
+    // a thread joins eight parts at once; more groups of threads where a row
+    // has more
+    p->join = p->blocks / rows < 8 ? (int)head_dim : 512;
     p->workspace = p->blocks * (kCutBytes + 2 * (int64_t)e->part * 4);
     return RMSN_OK;
 }
@@ -478,8 +482,8 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     if (st != RMSN_OK || p.split > 0 || p.blocks == 1) return st;
     // always behind the stream's own kernel: a programmatic dependent of it
     const int used = a.cols < 8 * p.e->NT ? a.cols : 8 * p.e->NT;
-    return launch(p.e->join, dim3((unsigned)(p.blocks - 1), (unsigned)(used + 3) / 4), 512, 0, &a,
-                  true, stream);
+    return launch(p.e->join, dim3((unsigned)(p.blocks - 1), (unsigned)(used + 3) / 4), p.join, 0,
+                  &a, true, stream);
 }
 
 RMSATTN_API int rmsattn_read_status(uint32_t* status, int clear) {

@@ -1053,13 +1053,14 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 
 // Joins the parts of the rows that the shares' borders cut, in the shares'
 // order.  Block (i, q): the row of share i's Cut, columns 4 q to 4 q + 3; D
-// threads to a part (four dims of a column each), 512 / D groups of them, each
-// with every (512 / D)-th part.  A thread takes up to eight parts at a time,
+// threads to a part (four dims of a column each), blockDim / D groups of them
+// that take the parts in turn.  A thread takes up to eight parts at a time,
 // their references and sums and values all on their way at once: the launch
 // is a chain of latencies (Cut, parts, join of the groups), not of bytes.
 template <class T, class C>
 __global__ void __launch_bounds__(512) attend_join_kernel(const AttendArgs a) {
     constexpr int D = C::D, NG = 512 / D, U = 8;
+    const int groups = blockDim.x / D;
     __shared__ float4 sum[NG][D];
     __shared__ float top[NG][4], total[NG][4];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1073,12 +1074,12 @@ __global__ void __launch_bounds__(512) attend_join_kernel(const AttendArgs a) {
     const int grp = threadIdx.x / D, c = threadIdx.x % D / (D / 4), d = threadIdx.x % (D / 4) * 4;
     float m = kNone, l = 0.f;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = grp; i0 < n; i0 += NG * U) {
+    for (int i0 = grp; i0 < n; i0 += groups * U) {
         float2 ml[U];
         float4 v[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            const int i = i0 + k * NG;
+            const int i = i0 + k * groups;
             ml[k] = make_float2(kNone, 0.f);
             v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i < n) {
@@ -1115,10 +1116,8 @@ __global__ void __launch_bounds__(512) attend_join_kernel(const AttendArgs a) {
     const Col col = column(a, hk, cg, q + oc, C::kCols);
     if (!col.on) return;
     float mx = kNone, ls = 0.f, r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < NG; ++k) mx = fmaxf(mx, top[k][oc]);
-#pragma unroll
-    for (int k = 0; k < NG; ++k) {
+    for (int k = 0; k < groups; ++k) mx = fmaxf(mx, top[k][oc]);
+    for (int k = 0; k < groups; ++k) {
         const float f = exp2a(top[k][oc] - mx);
         ls += total[k][oc] * f;
         add8(r, &sum[k][oc * (D / 4) + 2 * od], f);

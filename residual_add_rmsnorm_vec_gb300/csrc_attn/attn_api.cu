@@ -225,9 +225,9 @@ RMSATTN_API int rmsattn_qk_rope_fwd(const void* q, const void* k, const void* q_
             if (table[i].dt == dt && table[i].tph == tph && table[i].u == u &&
                 table[i].interleaved == a.interleaved)
                 e = &table[i];
-        // W <= 16 warps of 32 / tph heads, groups of them split evenly
+        // warps of 32 / tph heads, split evenly over as few blocks as hold them
         const int64_t nh = 32 / tph, warps = (n_q_heads + n_k_heads + nh - 1) / nh;
-        const int64_t gy = (warps + 15) / 16;
+        const int64_t gy = (warps + kRopeWarps - 1) / kRopeWarps;
         if (e && gy <= 65535)
             return launch(e->fn, dim3((unsigned)((n_tokens + u - 1) / u), (unsigned)gy),
                           (int)((warps + gy - 1) / gy) * 32, (size_t)(u * rot_dim / 2) * 8, &a,

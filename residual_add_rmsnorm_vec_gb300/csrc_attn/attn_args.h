@@ -28,6 +28,8 @@ struct RopeArgs {
     float rcp_d;  // 1 / head_dim when that is exact, else 0
 };
 
+constexpr int kRopeWarps = 8;  // of a block, at most
+
 // One compiled 16-byte-vector rotary kernel: tph lanes a head, u tokens a block.
 struct RopeEntry {
     int32_t dt, tph, u, interleaved;

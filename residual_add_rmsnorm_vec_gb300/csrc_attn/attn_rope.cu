@@ -168,8 +168,13 @@ __device__ __forceinline__ void lds_f2x2(const float* p, F2& a, F2& b) {
 
 // Multi-head, U tokens a block.  Warp w of block (b, y) holds heads
 // (y W + w) NH .. + NH - 1 (NH = 32 / TPH, W warps) of tokens b U .. + U - 1.
+// Bound to 48 registers, so that 40 warps share an SM: every warp waits once
+// for the block's angles, and the others' loads have to fill that time.  On a
+// GB300, 16384 tokens x 40 heads x 128 bf16 (335.7 MB): 54 us with two tokens
+// a block, 57 at 64 registers, 55 with three or four tokens, 61 and 83 where
+// each warp makes its own angles for 8 or 4 heads and nothing waits.
 template <class T, int TPH, int U, bool INTER>
-__global__ void __launch_bounds__(512) rope_vec(const RopeArgs a) {
+__global__ void __launch_bounds__(kRopeWarps * 32, 40 / kRopeWarps) rope_vec(const RopeArgs a) {
     constexpr int VE = Chunk<T>::kElems;  // elements of a chunk
     constexpr int NP = VE / 2;            // F2 of a chunk
     constexpr int NH = 32 / TPH;

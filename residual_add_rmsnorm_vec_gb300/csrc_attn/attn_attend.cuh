@@ -138,7 +138,7 @@ struct Shape {
     static constexpr int kTile = 16 * D;           // bytes of 16 tokens of K or V
     static constexpr int kSide = KT * kTile;       // bytes of a step of K or V
     static constexpr int kWarp = 4 * kSide;        // a warp's ring: K, K, V, V
-    static constexpr int kMeta = 32 * KT;          // a warp's: per step and tile K scale, V scale, state
+    static constexpr int kMeta = 16 * KT;          // a warp's: K scale and V scale of two steps' tiles
     static constexpr int kQPitch = 2 * D + 16;     // fp16 query row; + 16: no bank conflicts
     static constexpr int kJoin = W * 4 * D * 4;    // fp32, four columns of every warp
     // the rings; behind the last step, the join of all columns
@@ -468,9 +468,8 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         count = (int)(line.total - begin < chunk ? line.total - begin : chunk);
     }
 
-    unsigned char* meta = smem + C::kRing + wp * C::kMeta;
     unsigned char* qrows = smem + C::kRing + C::kMetaAll;
-    const uint32_t ring_s = smem_addr(smem) + wp * C::kWarp, meta_s = smem_addr(meta);
+    const uint32_t ring_s = smem_addr(smem) + wp * C::kWarp, meta_s = smem_addr(smem) + C::kRing + wp * C::kMeta;
 
     // ---- queries: this warp's columns of a row, first into
     // registers (before the wait that they can hide behind), then to shared
@@ -609,9 +608,10 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     auto locate = [&]() {
         if (b_at == b_n) turn_page();
         s_on = b_at < b_n;
-        if (!s_on) return;
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
+            s_where[k] = 0;
+            if (!s_on) continue;
             s_page[k] = __shfl_sync(0xFFFFFFFFu, b_page[k], b_at);
             s_where[k] = __shfl_sync(0xFFFFFFFFu, b_where[k], b_at);
             s_tile[k] = b_hk * (a.c.page >> 4) + (int)(s_where[k] & 0xFFF);
@@ -619,42 +619,47 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         }
         ++b_at;
     };
-    auto copy_tile = [&](uint32_t dst, const uint8_t* src, bool v, uint32_t where) {
-        if (where & kOpen) {
+    auto copy_step = [&](uint32_t dst, const uint8_t* base, bool v) {
+        bool open = true;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) cp16(dst + (v ? v_at(i) : k_dst) + i * 512, src + i * 512);
-        } else {  // rows that no query sees are zeros
+        for (int k = 0; k < KT; ++k) open = open && (s_where[k] & kOpen);
+        if (open) {
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-                cp16(dst + (v ? v_at(i) : k_dst) + i * 512, src + i * 512,
-                     where >> (16 + l_row + i * (32 / CH)) & 1);
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+                    cp16(dst + k * C::kTile + (v ? v_at(i) : k_dst) + i * 512, base + s_off[k] + i * 512);
+        } else if (s_on) {  // rows that no query sees are zeros
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+                    cp16(dst + k * C::kTile + (v ? v_at(i) : k_dst) + i * 512, base + s_off[k] + i * 512,
+                         s_where[k] >> (16 + l_row + i * (32 / CH)) & 1);
         }
     };
     // the located step's K and scales, or V, into stage `slot`
     auto issue_k = [&](int slot) {
-        if (s_on) {
+        copy_step(ring_s + slot * C::kSide, a.c.k, false);
+        if (lane < 2 * KT && s_on) {  // lane 2 k: tile k's K scale; 2 k + 1: its V scale
+            int64_t sc = s_page[0] * a.c.scale_stride + s_tile[0];
+            uint32_t rows = s_where[0] >> 16;
 #pragma unroll
-            for (int k = 0; k < KT; ++k) {
-                copy_tile(ring_s + slot * C::kSide + k * C::kTile, a.c.k + s_off[k], false, s_where[k]);
-                if (lane < 2)
-                    cp4(meta_s + (slot * KT + k) * 16 + lane * 4,
-                        (lane ? a.c.vs : a.c.ks) + s_page[k] * a.c.scale_stride + s_tile[k],
-                        s_where[k] >> 16);
-                else if (lane == 2)
-                    *reinterpret_cast<uint32_t*>(meta + (slot * KT + k) * 16 + 8) = s_where[k];
-            }
+            for (int k = 1; k < KT; ++k)
+                if (lane >> 1 == k) {
+                    sc = s_page[k] * a.c.scale_stride + s_tile[k];
+                    rows = s_where[k] >> 16;
+                }
+            cp4(meta_s + slot * (8 * KT) + lane * 4, ((lane & 1) ? a.c.vs : a.c.ks) + sc, rows != 0);
         }
         cp_commit();
     };
     auto issue_v = [&](int slot) {
-        if (s_on) {
-#pragma unroll
-            for (int k = 0; k < KT; ++k)
-                copy_tile(ring_s + (2 + slot) * C::kSide + k * C::kTile, a.c.v + s_off[k], true, s_where[k]);
-        }
+        copy_step(ring_s + (2 + slot) * C::kSide, a.c.v, true);
         cp_commit();
     };
 
+    uint32_t where[2][KT];  // tiles of the step in work and of the next
     look_ahead();
     turn_page();
 #pragma unroll
@@ -662,6 +667,8 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         locate();
         issue_k(i);
         issue_v(i);
+#pragma unroll
+        for (int k = 0; k < KT; ++k) where[i][k] = s_where[k];
     }
     locate();
 
@@ -711,16 +718,14 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
             cp_wait<3>();  // K and the scales; behind them V, and the next step's both
             __syncwarp();
             float ks[KT], vs[KT];
-            uint32_t where[KT], all_where = kOpen;
+            bool open = true;  // no mask touches this step
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
-                const uint4 me = lds16(meta_s + (slot * KT + k) * 16);
-                ks[k] = __uint_as_float(me.x);
-                vs[k] = __uint_as_float(me.y);
-                where[k] = me.z;
-                all_where &= me.z;
+                const uint2 sc = lds8(meta_s + slot * (8 * KT) + k * 8);
+                ks[k] = __uint_as_float(sc.x);
+                vs[k] = __uint_as_float(sc.y);
+                open = open && (where[0][k] & kOpen);
             }
-            const bool open = all_where != 0;  // no mask touches this step
             const uint32_t st = ring_s + slot * C::kSide;
 
             // S^T = K Q^T
@@ -781,7 +786,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const int j = t0 + 16 * k + g + 8 * h;
-                                const bool on = (where[k] >> (16 + g + 8 * h) & 1) && j <= pos &&
+                                const bool on = (where[0][k] >> (16 + g + 8 * h) & 1) && j <= pos &&
                                                 (j >= from || j < a.sinks);
                                 if (on) see[k] |= 1u << (4 * nt + 2 * h + x);
                                 else s[k][nt][2 * h + x] = -INFINITY;
@@ -831,20 +836,32 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 
             // weights; P^T as the second product's operand
             uint32_t pb[KT][NT][2];
+            float p[KT][NT][4];
+#pragma unroll
+            for (int k = 0; k < KT; ++k)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        p[k][nt][x] = exp2a(fmaf(s[k][nt][x], kc[k][nt][x & 1], -m[nt][x & 1]));
+            if (!open) {
+#pragma unroll
+                for (int k = 0; k < KT; ++k)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (!(see[k] >> (4 * nt + x) & 1)) p[k][nt][x] = 0.f;
+            }
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
                 const float f = vs[k] * rv * kLift;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float p[4];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        p[x] = exp2a(fmaf(s[k][nt][x], kc[k][nt][x & 1], -m[nt][x & 1]));
-                        if (!open && !(see[k] >> (4 * nt + x) & 1)) p[x] = 0.f;
-                        l[nt][x & 1] += p[x];
-                    }
-                    pb[k][nt][0] = rmsn::pack_f16x2(p[0] * f, p[1] * f);
-                    pb[k][nt][1] = rmsn::pack_f16x2(p[2] * f, p[3] * f);
+                    l[nt][0] += p[k][nt][0] + p[k][nt][2];
+                    l[nt][1] += p[k][nt][1] + p[k][nt][3];
+                    pb[k][nt][0] = rmsn::pack_f16x2(p[k][nt][0] * f, p[k][nt][1] * f);
+                    pb[k][nt][1] = rmsn::pack_f16x2(p[k][nt][2] * f, p[k][nt][3] * f);
                 }
             }
 
@@ -916,6 +933,11 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
             }
             __syncwarp();
             issue_v(slot);
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+                where[0][k] = where[1][k];
+                where[1][k] = s_where[k];
+            }
             locate();
             slot ^= 1;
         }

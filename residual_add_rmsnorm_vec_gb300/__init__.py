@@ -29,6 +29,7 @@ from .api import (block_format_configs, check_row_args, fused_add_rmsnorm, fused
                   fused_add_rmsnorm_host, make_flags, qk_norm_)
 from ._attn_lib import (  # noqa: F401
     EXPORTED_ATTN, RMSATTN_BAD_PAGE, RMSATTN_BLOCK, RMSATTN_INTERLEAVED, RMSATTN_MAX_QUERIES,
-    RMSATTN_NORM, RMSATTN_POS_I64, attn_library_path, load_attn, rmsattn_read_status)
+    RMSATTN_NORM, RMSATTN_POS_I64, attn_library_path, load_attn, load_fast as load_attn_binding,
+    rmsattn_read_status)
 from .attn import (KVCache, RopeTable, kv_cache_append_, kv_cache_attention, qk_norm_rope,  # noqa: F401
                    rope_table)

@@ -3,11 +3,13 @@ only).  The library is built next to the row norm's; a missing one raises."""
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
 from . import _lib
-from .build import ATTN_PATH
+from .build import ATTN_PATH, FAST_PATH
 
 RMSATTN_NORM = 0x1000
 RMSATTN_INTERLEAVED = 0x2000
@@ -45,7 +47,8 @@ def load_attn() -> ctypes.CDLL:
             if not os.path.exists(ATTN_PATH):
                 raise RuntimeError(f"the CUDA library {ATTN_PATH} is not built; run "
                                    "residual_add_rmsnorm_vec_gb300.build.build() first")
-            lib = ctypes.CDLL(ATTN_PATH)
+            # global: the marshalling module below binds to these symbols
+            lib = ctypes.CDLL(ATTN_PATH, mode=ctypes.RTLD_GLOBAL)
             vp, i64, u32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float
             cache = ctypes.POINTER(RmsattnCache)
             lib.rmsattn_qk_rope_fwd.restype = ctypes.c_int
@@ -63,6 +66,26 @@ def load_attn() -> ctypes.CDLL:
             lib.rmsattn_read_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
             _loaded = lib
     return _loaded
+
+
+_fast = None
+
+
+def load_fast():
+    """The native marshalling module (raises if it has not been built)."""
+    global _fast
+    if _fast is None:
+        load_attn()
+        if not os.path.exists(FAST_PATH):
+            raise RuntimeError(f"the extension module {FAST_PATH} is not built; run "
+                               "residual_add_rmsnorm_vec_gb300.build.build() first")
+        import torch  # noqa: F401  (its libraries hold the module's other symbols)
+
+        loader = importlib.machinery.ExtensionFileLoader("rmsattn_fast", FAST_PATH)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("rmsattn_fast", loader))
+        loader.exec_module(mod)
+        _fast = mod
+    return _fast
 
 
 def rmsattn_read_status(clear: bool = False) -> int:

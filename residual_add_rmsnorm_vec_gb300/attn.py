@@ -2,6 +2,10 @@
 include/rmsnorm_attn.h (marshalling only): QK norm with multi-axis rotary
 positions, the append to a paged E4M3 cache, and the attention over it.
 Nothing here computes: a failed call raises ``RmsnError``.
+
+The usual call (tensors of the current device, the current stream) is
+marshalled natively (binding/attn_fast.cpp), with the same checks; what that
+does not take comes back here, which makes the call or raises the error.
 """
 from __future__ import annotations
 
@@ -140,6 +144,12 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
     results go to q_out / k_out (new tensors where None; pass q and k
     themselves to work in place).  Returns ``(q_out, k_out)``.
     """
+    if stream is None:
+        done = (_al._fast or _al.load_fast()).qk_rope(
+            q, k, positions, table.turns, table.axis, table.n_axes, q_weight, k_weight, head_dim,
+            eps, weight_offset, interleaved, q_out, k_out, pdl)
+        if done is not None:
+            return done
     ref = q if q is not None else k
     if ref is None:
         return q_out, k_out
@@ -233,7 +243,7 @@ class KVCache:
     a model in one tensor), the rest of each tensor is contiguous."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "n_pages", "n_kv_heads", "page_size", "head_dim",
-                 "device", "index", "_c", "_ref")
+                 "device", "index", "_c", "_ref", "_addr")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
                  v_scale: torch.Tensor):
@@ -271,7 +281,7 @@ class KVCache:
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
             k.stride(0) if pages > 1 else heads * page * dim,
             k_scale.stride(0) if pages > 1 else shape[1] * shape[2], heads, page, dim, 0)
-        self._ref = ctypes.byref(self._c)
+        self._ref, self._addr = ctypes.byref(self._c), ctypes.addressof(self._c)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int,
@@ -317,6 +327,9 @@ def kv_cache_append_(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_tab
     tokens share a scale: where a new token's magnitude exceeds it, the scale
     grows and the block's older codes are re-encoded.
     """
+    if stream is None and (_al._fast or _al.load_fast()).kv_append(
+            k, v, cache._addr, cache.index, block_table, lengths, cu_seqlens, pdl):
+        return cache
     hk, ks = _heads("k", k, cache.head_dim)
     hv, vs = _heads("v", v, cache.head_dim)
     T, dt, index = k.shape[0], k.dtype, cache.index
@@ -381,6 +394,11 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     (length 0, a padded row) gives 0.  ``scale``: default 1 / sqrt(head_dim).
     Returns out, shaped like q.
     """
+    if stream is None:
+        done = (_al._fast or _al.load_fast()).kv_attention(
+            q, cache._addr, cache.index, block_table, lengths, scale, window, sinks, out, pdl)
+        if done is not None:
+            return done
     shape, dt, index = q.shape, q.dtype, cache.index
     if len(shape) == 3:
         B, H, D = shape

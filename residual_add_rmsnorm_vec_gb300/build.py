@@ -18,10 +18,12 @@ RMSNORM_GB300_LIB.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -35,6 +37,9 @@ CHECKED_PATH = os.path.join(BUILD_DIR, "librmsnorm_gb300_checked.so")
 # the attention-path operators, a library of their own
 ATTN_CSRC = os.path.join(PKG, "csrc_attn")
 ATTN_PATH = os.path.join(BUILD_DIR, "librmsnorm_attn_gb300.so")
+# native marshalling of its tensor-level calls (a Python extension module)
+FAST_SRC = os.path.join(PKG, "binding", "attn_fast.cpp")
+FAST_PATH = os.path.join(BUILD_DIR, "rmsattn_fast.so")
 # the bench's C timing harness (not part of the library)
 HOSTCOST_SRC = os.path.join(PKG, "bench_src", "host_cost.cu")
 HOSTCOST_PATH = os.path.join(BUILD_DIR, "librmsn_hostcost.so")
@@ -66,12 +71,25 @@ def _inputs() -> list[str]:
             + [os.path.abspath(__file__)])
 
 
+def _fast_command(out: str) -> list[str]:
+    """g++ of the marshalling module: torch's and Python's headers, host code
+    only; torch's own libraries are loaded before it."""
+    spec = importlib.util.find_spec("torch")
+    torch_dir = spec.submodule_search_locations[0]
+    inc = os.path.join(torch_dir, "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
+            "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda,
+            "-I", sysconfig.get_paths()["include"], FAST_SRC, "-o", out,
+            "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
 def up_to_date(checked: bool = False) -> bool:
-    outs = [CHECKED_PATH] if checked else [LIB_PATH, ATTN_PATH, HOSTCOST_PATH]
+    outs = [CHECKED_PATH] if checked else [LIB_PATH, ATTN_PATH, FAST_PATH, HOSTCOST_PATH]
     if not all(os.path.exists(o) for o in outs):
         return False
     t = min(os.path.getmtime(o) for o in outs)
-    return all(os.path.getmtime(f) <= t for f in _inputs() + [HOSTCOST_SRC])
+    return all(os.path.getmtime(f) <= t for f in _inputs() + [HOSTCOST_SRC, FAST_SRC])
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None,
@@ -98,9 +116,21 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None,
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
+    def compile_fast():
+        # the C ABI's symbols stay undefined: that library is loaded before it
+        tmp = FAST_PATH + f".tmp{os.getpid()}"
+        cmd = _fast_command(tmp)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {os.path.basename(FAST_SRC)}:\n{r.stderr}")
+        return tmp
+
     n = jobs or min(len(srcs), os.cpu_count() or 1)
     with ThreadPoolExecutor(max(1, n)) as ex:
+        fast = None if checked else ex.submit(compile_fast)
         logs = list(ex.map(compile_one, zip(srcs, objs)))
+        if fast is not None:
+            os.replace(fast.result(), FAST_PATH)
     if verbose:
         for src, log in zip(srcs, logs):
             sys.stderr.write(f"== {os.path.basename(src)}\n{log}")

@@ -11,7 +11,8 @@
  * All calls are asynchronous on `stream` (NULL = the legacy default stream),
  * run on the current device, may be captured into a CUDA graph, and are
  * thread-safe.  Argument errors are returned before anything is launched; a
- * launch failure returns RMSN_ECUDA.
+ * launch failure returns RMSN_ECUDA.  Inference only: nothing here has a
+ * backward pass.
  */
 #ifndef RMSNORM_ATTN_GB300_H
 #define RMSNORM_ATTN_GB300_H
@@ -112,8 +113,9 @@ typedef struct {
  * other byte of the cache stays as it is.  lengths is not changed.  A
  * sequence with lengths[s] < 0 is left out (a padded batch's row).  A token
  * past the table's width, or in a page outside [0, n_pages), is dropped and
- * sets bit 2 (value 4) of the status word.  No two sequences may append to
- * the same page in one call.
+ * sets bit 2 (value 4) of the status word; a sequence whose rows lie outside
+ * [0, n_tokens) is left out.  In one call no page may get tokens by two table
+ * entries, of two sequences or of one.
  *
  *   k, v        [n_tokens, n_kv_heads, head_dim] bf16 / fp16 / fp32, token
  *               strides in elements (heads back to back)

@@ -453,6 +453,10 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
                      window, sinks, &p);
     if (st != RMSN_OK) return st;
     if (p.workspace > 0 && (!workspace || workspace_bytes < p.workspace)) return RMSN_EINVAL;
+    if (a.c.n_pages == 0) {  // nothing is read; copies of no bytes still name an address
+        a.c.k = a.c.v = (uint8_t*)q;
+        a.c.ks = a.c.vs = (float*)q;
+    }
     a.q = q;
     a.out = out;
     a.q_stride = q_stride;

@@ -537,6 +537,78 @@ def test_attention_offsets_past_32_bits(rn):
     del codes, t, cache
 
 
+@pytest.mark.parametrize("scale", [-0.3, 0.0, 1e-30])
+@pytest.mark.parametrize("how", ["rows", "line"])
+def test_attention_scale_of_any_sign(rn, scale, how):
+    t = ref.random_cache(30, 2, 16, 128, 7, "cuda", spread=False)
+    table = ref.tables(2, 14, 30, 1, "cuda")
+    lens = torch.tensor([200, 37], dtype=torch.int32, device="cuda")
+    q = rand((2, 2, 8, 128), 3, torch.bfloat16).cuda()
+    want, bound = ref.attend(q, t, table, lens, float(torch.tensor(scale, dtype=torch.float32)), 0, 0)
+    got = rn.kv_cache_attention(q, make_cache(rn, t), spread_out(table, how, 2)[0], lens, scale=scale)
+    within(got, want, bound)
+
+
+def test_attention_infinite_and_nan_queries_stay_in_their_row(rn):
+    t = ref.random_cache(12, 1, 16, 64, 7, "cuda", spread=False)
+    table = ref.tables(1, 12, 12, 1, "cuda")
+    lens = torch.tensor([180], dtype=torch.int32, device="cuda")
+    q = rand((1, 1, 8, 64), 3, torch.bfloat16).cuda()
+    want, bound = ref.attend(q, t, table, lens, 0.125, 0, 0)
+    q[0, 0, 2, 5], q[0, 0, 6, 7] = math.nan, math.inf
+    got = rn.kv_cache_attention(q, make_cache(rn, t), table, lens)
+    rest = [0, 1, 3, 4, 5, 7]
+    assert bool(got[0, 0, [2, 6]].isnan().all())
+    within(got[0, 0, rest], want[0, 0, rest], bound[0, 0, rest])
+
+
+def test_attention_many_columns(rn):
+    # 16 query heads a key head x 32 query tokens: 512 columns of a row
+    t = ref.random_cache(10, 1, 16, 64, 7, "cuda", spread=False)
+    table = ref.tables(1, 10, 10, 1, "cuda")
+    lens = torch.tensor([150], dtype=torch.int32, device="cuda")
+    q = rand((1, 32, 16, 64), 3, torch.bfloat16).cuda()
+    got = rn.kv_cache_attention(q, make_cache(rn, t), table, lens, window=100, sinks=2)
+    within(got, *ref.attend(q, t, table, lens, 0.125, 100, 2))
+
+
+def test_attention_largest_page_and_no_pages(rn):
+    t = ref.random_cache(1, 2, 65536, 64, 7, "cuda", spread=False)
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    lens = torch.tensor([65500], dtype=torch.int32, device="cuda")
+    q = rand((1, 1, 4, 64), 3, torch.bfloat16).cuda()
+    got = rn.kv_cache_attention(q, make_cache(rn, t), table, lens, window=300, sinks=20)
+    within(got, *ref.attend(q, t, table, lens, 0.125, 300, 20))
+    none = rn.KVCache.empty(0, 2, 16, 64)
+    assert bool((rn.kv_cache_attention(q, none, table, lens * 0) == 0).all())
+    assert bool((rn.kv_cache_attention(q, none, table, lens * 0 + 5) == 0).all())
+    assert rn.rmsattn_read_status(clear=True) == rn.RMSATTN_BAD_PAGE
+
+
+def test_refused_calls_raise(rn):
+    t = ref.random_cache(2, 1, 16, 64, 7, "cuda")
+    cache = make_cache(rn, t)
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    lens = torch.ones(1, dtype=torch.int32, device="cuda")
+    flat = torch.zeros(4 * 64 + 8, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(rn.RmsnError) as e:  # not on a 16-byte boundary
+        rn.kv_cache_attention(flat[1:257].view(1, 4, 64), cache, table, lens)
+    assert e.value.status == rn.RMSN_EALIGN
+    with pytest.raises(rn.RmsnError) as e:
+        rn.kv_cache_attention(flat[:256].view(1, 4, 64), cache, table, lens, scale=math.inf)
+    assert e.value.status == rn.RMSN_EINVAL
+    with pytest.raises(rn.RmsnError) as e:  # one token on all rows
+        rn.kv_cache_append_(cache, flat[:64].expand(3, 64), flat[:64].expand(3, 64), table.repeat(3, 1),
+                            lens.repeat(3))
+    assert e.value.status == rn.RMSN_EINVAL
+    with pytest.raises(ValueError):
+        rn.kv_cache_attention(flat[:256].view(1, 4, 64), cache, table.cpu(), lens)
+    with pytest.raises(ValueError):
+        rn.kv_cache_append_(cache, flat[:64].view(1, 64).cpu(), flat[:64].view(1, 64), table, lens)
+    with pytest.raises(ValueError):
+        rn.qk_norm_rope(flat[:256].view(4, 64), None, torch.zeros(4, dtype=torch.int32), rn.rope_table(64), head_dim=64)
+
+
 # ---------------------------------------------------------------- the path together
 
 def layer(rn, s, row, weight, residual, pdl=False):

@@ -369,7 +369,7 @@ int plan_attend(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
     // 8 x 2000 tokens x 8 heads 12.8 against 16.9 us, 256 x 300 45 against 48,
     // but 64 x 8192 161 against 148, 1 x 131072 138 against 54.
     int64_t split = 1;
-    while (split < 8 && rows * split * 2 <= resident) split *= 2;
+    while (split < kMaxSplit && rows * split * 2 <= resident) split *= 2;
     const int64_t waves = (rows * split + resident - 1) / resident;
     const double by_rows = (double)waves * (double)((steps + split - 1) / split) * e->tok / warps;
     const double by_line = (double)total * e->tok / (double)(resident * warps) +

@@ -85,6 +85,7 @@ struct AttendArgs {
 };
 
 constexpr int64_t kCutBytes = 32;
+constexpr int kMaxSplit = 8;  // blocks of a cluster
 
 // One compiled attention kernel and the join of its parts.
 struct AttendEntry {

@@ -1045,17 +1045,34 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                 if (!col.on) continue;
                 const uint32_t ml = smem_addr(&part_ml[cc]);
                 const uint32_t jr = smem_addr(join + cc * W * D + d);
-                float mx = kNone;
-                for (int r = 0; r < a.split; ++r) mx = fmaxf(mx, ld_cluster2(ml, r).x);
-                float lsum = 0.f, y[8];
+                // all references at once, then all values: a read of another
+                // block's shared memory takes a few hundred cycles
+                float2 p[kMaxSplit];
+                float mx = kNone, lsum = 0.f, y[8];
+#pragma unroll
+                for (int r = 0; r < kMaxSplit; ++r)
+                    p[r] = r < a.split ? ld_cluster2(ml, r) : make_float2(kNone, 0.f);
+#pragma unroll
+                for (int r = 0; r < kMaxSplit; ++r) mx = fmaxf(mx, p[r].x);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) y[k] = 0.f;
-                for (int r = 0; r < a.split; ++r) {
-                    const float2 p = ld_cluster2(ml, r);
-                    const float f = exp2a(p.x - mx);
-                    lsum += p.y * f;
-                    const float4 v[2] = {ld_cluster4(jr, r), ld_cluster4(jr + 16, r)};
-                    add8(y, v, f);
+#pragma unroll
+                for (int r0 = 0; r0 < kMaxSplit; r0 += 4) {
+                    float4 v[4][2];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        v[r][0] = v[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (r0 + r < a.split) {
+                            v[r][0] = ld_cluster4(jr, r0 + r);
+                            v[r][1] = ld_cluster4(jr + 16, r0 + r);
+                        }
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float f = exp2a(p[r0 + r].x - mx);
+                        lsum += p[r0 + r].y * f;
+                        add8(y, v[r], f);
+                    }
                 }
                 finish8<T>(a, row_b, col, d, y, lsum);
             }

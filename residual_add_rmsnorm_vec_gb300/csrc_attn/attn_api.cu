@@ -475,9 +475,12 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     a.pdl = (flags & RMSN_PDL) ? 1 : 0;
     a.status = d->status;
     a.cols = (int32_t)(n_q_heads / a.c.H * n_queries);
+    a.group = (int32_t)(n_q_heads / a.c.H);
+    a.group_rcp = ((uint64_t(1) << 32) + a.group - 1) / a.group;
     a.groups = p.groups;
     a.page_rcp = ((uint64_t(1) << 37) + a.c.page / kBlock - 1) / (a.c.page / kBlock);
     a.split = p.split;
+    while ((1 << a.split_log) < a.split) ++a.split_log;
     a.shares = p.blocks;
     a.min_chunk = p.min_chunk;
     a.ws = static_cast<char*>(workspace);

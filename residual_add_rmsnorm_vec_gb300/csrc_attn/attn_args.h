@@ -75,9 +75,11 @@ struct AttendArgs {
     int32_t pdl;
     uint32_t* status;
     // how the steps are shared out: 0, as one line; else a row to `split` blocks
-    int32_t split;
+    int32_t split, split_log;  // a power of two
     int32_t groups;     // column groups of a key head
     int32_t cols;       // columns of a key head: query heads x query tokens
+    int32_t group;      // query heads of a key head
+    uint64_t group_rcp; // ceil(2^32 / group): exact quotients of up to 2^17 columns
     uint64_t page_rcp;  // ceil(2^37 / (page / 16))
     int64_t shares;     // of the line, one for each block
     int64_t min_chunk;  // steps of a share, at least

@@ -141,11 +141,13 @@ struct Shape {
     static constexpr int kMeta = 16 * KT;          // a warp's: K scale and V scale of two steps' tiles
     static constexpr int kQPitch = 2 * D + 16;     // fp16 query row; + 16: no bank conflicts
     static constexpr int kJoin = W * 4 * D * 4;    // fp32, four columns of every warp
+    // a join between the block's rows, or a cluster's parts of the block's dims
+    static constexpr int kParts = kJoin > kCols * D * 4 ? kJoin : kCols * D * 4;
     // the rings; behind the last step, the join of all columns
     static constexpr int kRing = W * kWarp > 2 * NT * kJoin ? W * kWarp : 2 * NT * kJoin;
     static constexpr int kMetaAll = W * kMeta;
     static constexpr int kQ = kCols * kQPitch;
-    static constexpr int kSmem = kRing + kMetaAll + kQ + kJoin;
+    static constexpr int kSmem = kRing + kMetaAll + kQ + kParts;
 };
 
 // ---------------------------------------------------------------- rows and steps
@@ -289,11 +291,11 @@ struct Col {
     bool on;
 };
 __device__ __forceinline__ Col column(const AttendArgs& a, int hk, int cg, int c, int cols) {
-    const int G = a.Hq / a.c.H, cc = cg * cols + c;
+    const int cc = cg * cols + c;
     Col r;
-    r.on = cc < G * a.n;
-    r.qi = cc / G;
-    r.head = hk * G + cc % G;
+    r.on = cc < a.cols;
+    r.qi = (int)((uint64_t)(uint32_t)cc * a.group_rcp >> 32);  // cc / group
+    r.head = (hk - r.qi) * a.group + cc;
     return r;
 }
 
@@ -319,6 +321,16 @@ __device__ __forceinline__ void add8(float (&y)[8], const float4* p, float f) {
     y[6] += v.z * f;
     y[7] += v.w * f;
 }
+// The four-float unit that holds dim d of a join row: the lanes that write a
+// row's units 4 or 2 apart, and those that read it, meet different banks.
+__device__ __forceinline__ int unit_at(int d) {
+    const int u = d >> 2;
+    return (u ^ ((u >> 3) & 3)) << 2;
+}
+__device__ __forceinline__ void read8(float4 (&v)[2], const float* row, int d) {
+    v[0] = *reinterpret_cast<const float4*>(row + unit_at(d));
+    v[1] = *reinterpret_cast<const float4*>(row + unit_at(d + 4));
+}
 // Eight dims of a row's sums over its weights' sum; nothing seen gives 0.
 template <class T>
 __device__ __forceinline__ void finish8(const AttendArgs& a, int64_t b, const Col& c, int d,
@@ -330,29 +342,29 @@ __device__ __forceinline__ void finish8(const AttendArgs& a, int64_t b, const Co
 
 // ---------------------------------------------------------------- the cluster's shared memory
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_begin() {  // arrives; orders no memory
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t in_block(uint32_t addr, int rank) {
     uint32_t r;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-__device__ __forceinline__ float2 ld_cluster2(uint32_t addr, int rank) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
-                 : "=f"(v.x), "=f"(v.y)
-                 : "r"(in_block(addr, rank))
+__device__ __forceinline__ void st_cluster2(uint32_t addr, int rank, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(in_block(addr, rank)), "f"(v.x),
+                 "f"(v.y)
                  : "memory");
-    return v;
 }
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, int rank) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(in_block(addr, rank))
+__device__ __forceinline__ void st_cluster4(uint32_t addr, int rank, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(in_block(addr, rank)),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
-    return v;
 }
 
 // The workspace: a Cut for every share, then two parts for every share.
@@ -432,12 +444,14 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ float q_scale[C::kCols];
     __shared__ int q_index[C::kCols];  // a column's query token
-    __shared__ float2 part_ml[C::kCols];
+    __shared__ float2 part_ml[kMaxSplit][C::kCols];  // references and sums of a cluster's blocks
     __shared__ float j_m[W][C::kCols], j_l[W][C::kCols];
     rmsn::pdl_wait(a.pdl);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
+    // a block's shared memory may be written to once the block has begun
+    if (a.split > 1) cluster_begin();
 
     // this share's steps: `count` from place `begin`, the first of them in row
     // `at` (whose first step lies at at.first <= begin)
@@ -445,14 +459,14 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     int count;
     Place at;
     if (a.split > 0) {
-        const int64_t HC = (int64_t)a.c.H * a.groups, row = blockIdx.x / (uint32_t)a.split;
+        const uint32_t HC = (uint32_t)(a.c.H * a.groups), row = blockIdx.x >> a.split_log;
         at.b = row / HC;
         at.hc = (int)(row % HC);
         at.first = 0;
         Span<C::kTok> s;
         s.of(a, a.lengths[at.b]);
-        const int per = (s.ns + a.split - 1) / a.split;
-        begin = (int64_t)(blockIdx.x % (uint32_t)a.split) * per;
+        const int per = (s.ns + a.split - 1) >> a.split_log;
+        begin = (int64_t)((int)blockIdx.x & (a.split - 1)) * per;
         const int left = s.ns - (int)begin;
         count = left < 0 ? 0 : (left < per ? left : per);
     } else {
@@ -495,7 +509,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     };
     auto store_q = [&](int cg) {
         for (int c = threadIdx.x; c < C::kCols; c += W * 32)
-            q_index[c] = (cg * C::kCols + c) / (a.Hq / a.c.H);
+            q_index[c] = column(a, 0, cg, c, C::kCols).qi;
 #pragma unroll
         for (int i = 0; i < QC; ++i) {
             const int c = wp + i * W;
@@ -975,6 +989,8 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         // four of a tile's columns); behind the block's last step the ring is
         // free, and holds all of them
         const int quads = (used + 3) / 4, step = last ? 2 * NT : 1;
+        if (a.split > 1) cluster_wait();
+        float* parts = reinterpret_cast<float*>(smem + C::kRing + C::kMetaAll + C::kQ);  // of a cluster
         float* join = reinterpret_cast<float*>(last ? smem : smem + C::kRing + C::kMetaAll + C::kQ);
         if (last) __syncthreads();  // every warp is through with its stages
         for (int q0 = 0; q0 < quads; q0 += step) {
@@ -994,7 +1010,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 #pragma unroll
                     for (int i = 0; i < MT; i += 2) {
                         const int d = D == 64 ? g * 8 + 2 * i : (g + 8 * (i / 8)) * 16 + 2 * (i % 8);
-                        *reinterpret_cast<float4*>(jr + d) =
+                        *reinterpret_cast<float4*>(jr + unit_at(d)) =
                             make_float4(o[i][nt][x] * unit, o[i][nt][2 + x] * unit,
                                         o[i + 1][nt][x] * unit, o[i + 1][nt][2 + x] * unit);
                     }
@@ -1016,15 +1032,22 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                 for (int w = 0; w < W; ++w) {
                     const float f = exp2a(j_m[w][cc] - mx);
                     lsum += j_l[w][cc] * f;
-                    add8(y, reinterpret_cast<const float4*>(join + (c * W + w) * D + d), f);
+                    float4 v[2];
+                    read8(v, join + (c * W + w) * D, d);
+                    add8(y, v, f);
                 }
                 if (whole) {
                     finish8<T>(a, row_b, col, d, y, lsum);
-                } else if (a.split > 0) {  // for the cluster, in the place of warp 0's
-                    float4* dst = reinterpret_cast<float4*>(join + c * W * D + d);
-                    dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-                    dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-                    if (d == 0) part_ml[cc] = make_float2(mx, lsum);
+                } else if (a.split > 0) {
+                    // to the block that finishes these dims, each sender its place
+                    const int rank = (int)blockIdx.x & (a.split - 1);
+                    const int item = cc * (D / 8) + d / 8, owner = item & (a.split - 1);
+                    const uint32_t at = smem_addr(parts) + (item - owner + rank) * 32;
+                    st_cluster4(at, owner, make_float4(y[0], y[1], y[2], y[3]));
+                    st_cluster4(at + 16, owner, make_float4(y[4], y[5], y[6], y[7]));
+                    if (d == 0)
+                        for (int r = 0; r < a.split; ++r)
+                            st_cluster2(smem_addr(&part_ml[rank][cc]), r, make_float2(mx, lsum));
                 } else {
                     float4* dst = reinterpret_cast<float4*>(part + cc * D + d);
                     dst[0] = make_float4(y[0], y[1], y[2], y[3]);
@@ -1036,47 +1059,28 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
             }
         }
         if (a.split > 1) {
-            // the parts of the cluster's blocks, each block its share of the vectors
-            cluster_sync();
-            const uint32_t rank = blockIdx.x % (uint32_t)a.split;
-            for (int e = rank * (W * 32) + threadIdx.x; e < quads * (D / 2); e += a.split * (W * 32)) {
-                const int cc = e / (D / 8), d = e % (D / 8) * 8;
+            // every block's parts have arrived; nothing is sent behind this, so
+            // a block may leave once it has read its own
+            cluster_arrive();
+            cluster_wait();
+            const int rank = (int)blockIdx.x & (a.split - 1), items = quads * (D / 2);
+            for (int i = threadIdx.x; i * a.split + rank < items; i += W * 32) {
+                const int item = i * a.split + rank, cc = item / (D / 8), d = item % (D / 8) * 8;
                 const Col col = column(a, hk, cg, cc, C::kCols);
                 if (!col.on) continue;
-                const uint32_t ml = smem_addr(&part_ml[cc]);
-                const uint32_t jr = smem_addr(join + cc * W * D + d);
-                // all references at once, then all values: a read of another
-                // block's shared memory takes a few hundred cycles
-                float2 p[kMaxSplit];
+                const float4* from = reinterpret_cast<const float4*>(parts + i * a.split * 8);
                 float mx = kNone, lsum = 0.f, y[8];
 #pragma unroll
-                for (int r = 0; r < kMaxSplit; ++r)
-                    p[r] = r < a.split ? ld_cluster2(ml, r) : make_float2(kNone, 0.f);
-#pragma unroll
-                for (int r = 0; r < kMaxSplit; ++r) mx = fmaxf(mx, p[r].x);
-#pragma unroll
                 for (int k = 0; k < 8; ++k) y[k] = 0.f;
-#pragma unroll
-                for (int r0 = 0; r0 < kMaxSplit; r0 += 4) {
-                    float4 v[4][2];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        v[r][0] = v[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (r0 + r < a.split) {
-                            v[r][0] = ld_cluster4(jr, r0 + r);
-                            v[r][1] = ld_cluster4(jr + 16, r0 + r);
-                        }
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const float f = exp2a(p[r0 + r].x - mx);
-                        lsum += p[r0 + r].y * f;
-                        add8(y, v[r], f);
-                    }
+                for (int r = 0; r < a.split; ++r) mx = fmaxf(mx, part_ml[r][cc].x);
+                for (int r = 0; r < a.split; ++r) {
+                    const float2 p = part_ml[r][cc];
+                    const float f = exp2a(p.x - mx);
+                    lsum += p.y * f;
+                    add8(y, from + 2 * r, f);
                 }
                 finish8<T>(a, row_b, col, d, y, lsum);
             }
-            cluster_sync();  // no block leaves while another reads its shared memory
         }
         cur = seg_end;
         if (!last) {

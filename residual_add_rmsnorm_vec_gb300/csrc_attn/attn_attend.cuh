@@ -140,14 +140,15 @@ struct Shape {
     static constexpr int kWarp = 4 * kSide;        // a warp's ring: K, K, V, V
     static constexpr int kMeta = 16 * KT;          // a warp's: K scale and V scale of two steps' tiles
     static constexpr int kQPitch = 2 * D + 16;     // fp16 query row; + 16: no bank conflicts
-    static constexpr int kJoin = W * 4 * D * 4;    // fp32, four columns of every warp
-    // a join between the block's rows, or a cluster's parts of the block's dims
-    static constexpr int kParts = kJoin > kCols * D * 4 ? kJoin : kCols * D * 4;
+    // fp32 of a tile of every warp: the join between the block's rows; the same
+    // room takes a cluster's parts of the block's dims
+    static constexpr int kJoin = W * 8 * D * 4;
+    static_assert(W * 8 >= kCols, "a cluster's parts: D / split dims of all columns, split times");
     // the rings; behind the last step, the join of all columns
-    static constexpr int kRing = W * kWarp > 2 * NT * kJoin ? W * kWarp : 2 * NT * kJoin;
+    static constexpr int kRing = W * kWarp > NT * kJoin ? W * kWarp : NT * kJoin;
     static constexpr int kMetaAll = W * kMeta;
     static constexpr int kQ = kCols * kQPitch;
-    static constexpr int kSmem = kRing + kMetaAll + kQ + kParts;
+    static constexpr int kSmem = kRing + kMetaAll + kQ + kJoin;
 };
 
 // ---------------------------------------------------------------- rows and steps
@@ -985,28 +986,27 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
             ls[nt][0] = sum_over_rows(l[nt][0]);
             ls[nt][1] = sum_over_rows(l[nt][1]);
         }
-        // join the warps, four columns at a time (lanes t of one parity hold
-        // four of a tile's columns); behind the block's last step the ring is
-        // free, and holds all of them
-        const int quads = (used + 3) / 4, step = last ? 2 * NT : 1;
+        // join the warps, a tile of eight columns at a time; behind the block's
+        // last step the ring is free, and holds all of them
+        const int tiles = (used + 7) / 8, step = last ? NT : 1;
         if (a.split > 1) cluster_wait();
         float* parts = reinterpret_cast<float*>(smem + C::kRing + C::kMetaAll + C::kQ);  // of a cluster
         float* join = reinterpret_cast<float*>(last ? smem : smem + C::kRing + C::kMetaAll + C::kQ);
         if (last) __syncthreads();  // every warp is through with its stages
-        for (int q0 = 0; q0 < quads; q0 += step) {
-            if (q0 > 0) __syncthreads();
+        for (int n0 = 0; n0 < tiles; n0 += step) {
+            if (n0 > 0) __syncthreads();
 #pragma unroll
-            for (int q = 0; q < 2 * NT; ++q) {
-                const int nt = q >> 1;
-                if (q < q0 || q >= q0 + step || q >= quads || (t >> 1) != (q & 1)) continue;
+            for (int nt = 0; nt < NT; ++nt) {
+                if (nt < n0 || nt >= n0 + step) continue;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int c = (q - q0) * 4 + 2 * (t & 1) + x;
+                    const int cc = nt * 8 + 2 * t + x;
+                    if (cc >= used) continue;
                     if (g == 0) {
-                        j_m[wp][q * 4 + 2 * (t & 1) + x] = m[nt][x];
-                        j_l[wp][q * 4 + 2 * (t & 1) + x] = ls[nt][x];
+                        j_m[wp][cc] = m[nt][x];
+                        j_l[wp][cc] = ls[nt][x];
                     }
-                    float* jr = join + (c * W + wp) * D;
+                    float* jr = join + ((cc - n0 * 8) * W + wp) * D;
 #pragma unroll
                     for (int i = 0; i < MT; i += 2) {
                         const int d = D == 64 ? g * 8 + 2 * i : (g + 8 * (i / 8)) * 16 + 2 * (i % 8);
@@ -1017,11 +1017,10 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                 }
             }
             __syncthreads();
-            const int in = quads - q0 < step ? quads - q0 : step;
-            for (int e = threadIdx.x; e < in * (D / 2); e += W * 32) {  // columns x D / 8 vectors
-                const int c = e / (D / 8), d = e % (D / 8) * 8, cc = q0 * 4 + c;
+            const int in = (used - n0 * 8 < step * 8 ? used - n0 * 8 : step * 8) * (D / 8);
+            for (int e = threadIdx.x; e < in; e += W * 32) {  // columns x D / 8 vectors
+                const int c = e / (D / 8), d = e % (D / 8) * 8, cc = n0 * 8 + c;
                 const Col col = column(a, hk, cg, cc, C::kCols);
-                if (!col.on) continue;
                 float mx = kNone;
 #pragma unroll
                 for (int w = 0; w < W; ++w) mx = fmaxf(mx, j_m[w][cc]);
@@ -1063,11 +1062,10 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
             // a block may leave once it has read its own
             cluster_arrive();
             cluster_wait();
-            const int rank = (int)blockIdx.x & (a.split - 1), items = quads * (D / 2);
+            const int rank = (int)blockIdx.x & (a.split - 1), items = used * (D / 8);
             for (int i = threadIdx.x; i * a.split + rank < items; i += W * 32) {
                 const int item = i * a.split + rank, cc = item / (D / 8), d = item % (D / 8) * 8;
                 const Col col = column(a, hk, cg, cc, C::kCols);
-                if (!col.on) continue;
                 const float4* from = reinterpret_cast<const float4*>(parts + i * a.split * 8);
                 float mx = kNone, lsum = 0.f, y[8];
 #pragma unroll

@@ -74,7 +74,8 @@ int rmsattn_qk_rope_fwd(const void* q, const void* k, const void* q_weight, cons
  *   k, v             [n_pages, n_kv_heads, page_size, head_dim] bytes, pages
  *                    page_stride bytes apart, 16-byte aligned
  *   k_scale, v_scale [n_pages, n_kv_heads, page_size / RMSATTN_BLOCK] fp32,
- *                    pages scale_stride floats apart
+ *                    pages scale_stride floats apart (n_pages * scale_stride
+ *                    < 2^32, else RMSN_EUNSUPPORTED)
  *
  * Scales are finite and not negative (the append makes no others).
  * head_dim is 64, 128 or 256; page_size a multiple of RMSATTN_BLOCK up to

@@ -103,6 +103,8 @@ int check_cache(const rmsattn_cache* c, Cache* out) {
         return RMSN_EINVAL;
     if (too_big(times(c->n_pages, c->page_stride)) || too_big(times(c->n_pages, c->scale_stride)))
         return RMSN_EINVAL;
+    // a scale's place is counted in 32 bits
+    if (times(c->n_pages, c->scale_stride) >= (int64_t(1) << 32)) return RMSN_EUNSUPPORTED;
     if (c->n_pages > 0 && (!c->k || !c->v || !c->k_scale || !c->v_scale)) return RMSN_EINVAL;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
         !aligned(c->v_scale, 4))

@@ -67,10 +67,8 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool on) {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool on) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
-                 "r"(on ? 4 : 0)
-                 : "memory");
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -546,9 +544,11 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     p_span.of(a, a.lengths[p_b]);
     int p_len_next = p_b + 1 < a.B ? a.lengths[p_b + 1] : 0;
     const int32_t* p_row = a.table + p_b * a.table_stride;
-    int b_n = 0, b_at = 0, b_hk = 0, next_n = 0, next_hk = 0;
-    int32_t b_page[KT], next_page[KT];   // pages
+    int b_n = 0, b_at = 0, next_n = 0, next_hk = 0;
+    int32_t next_page[KT];
     uint32_t b_where[KT], next_where[KT];
+    int64_t b_off[KT];   // bytes from the cache's begin to the tile
+    uint32_t b_scale[KT];  // the tile's scale, counted from the first
     auto look_ahead = [&]() {
         next_n = 0;
         if (p_at >= count) return;
@@ -583,16 +583,18 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         b_n = next_n;
         b_at = 0;
         if (next_n == 0) return;
-        b_hk = next_hk;
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            b_page[k] = next_page[k];
             b_where[k] = next_where[k];
-            if ((uint32_t)b_page[k] >= (uint32_t)a.c.n_pages) {
+            int64_t page = next_page[k];
+            if ((uint32_t)next_page[k] >= (uint32_t)a.c.n_pages) {
                 if (b_where[k] >> 16) atomicOr(a.status, kBadPage);
-                b_page[k] = 0;
+                page = 0;
                 b_where[k] = 0;
             }
+            const int tile = next_hk * (a.c.page >> 4) + (int)(b_where[k] & 0xFFF);
+            b_off[k] = page * a.c.page_stride + (int64_t)tile * C::kTile;
+            b_scale[k] = (uint32_t)(page * a.c.scale_stride) + (uint32_t)tile;
         }
         look_ahead();
     };
@@ -617,23 +619,22 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     };
     // the step to copy: its tiles' places and states
     bool s_on = false;
-    uint32_t s_where[KT];
-    int32_t s_page[KT], s_tile[KT];
-    int64_t s_off[KT];  // bytes from the cache's begin to the tile, plus the lane's 16
+    uint32_t s_where[KT], s_scale[KT];
+    int64_t s_off[KT];
     auto locate = [&]() {
         if (b_at == b_n) turn_page();
         s_on = b_at < b_n;
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            s_where[k] = 0;
-            if (!s_on) continue;
-            s_page[k] = __shfl_sync(0xFFFFFFFFu, b_page[k], b_at);
-            s_where[k] = __shfl_sync(0xFFFFFFFFu, b_where[k], b_at);
-            s_tile[k] = b_hk * (a.c.page >> 4) + (int)(s_where[k] & 0xFFF);
-            s_off[k] = s_page[k] * a.c.page_stride + (int64_t)(s_tile[k] * (D / 16)) * 256 + lane * 16;
+            s_off[k] = __shfl_sync(0xFFFFFFFFu, b_off[k], b_at);
+            s_scale[k] = __shfl_sync(0xFFFFFFFFu, b_scale[k], b_at);
+            s_where[k] = s_on ? __shfl_sync(0xFFFFFFFFu, b_where[k], b_at) : 0u;
         }
         ++b_at;
     };
+    // this lane's 16 bytes of a tile; lanes 2 k and 2 k + 1 copy tile k's scales
+    const uint8_t *k_src = a.c.k + lane * 16, *v_src = a.c.v + lane * 16;
+    const float* scale_src = (lane & 1) ? a.c.vs : a.c.ks;
     auto copy_step = [&](uint32_t dst, const uint8_t* base, bool v) {
         bool open = true;
 #pragma unroll
@@ -655,22 +656,20 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     };
     // the located step's K and scales, or V, into stage `slot`
     auto issue_k = [&](int slot) {
-        copy_step(ring_s + slot * C::kSide, a.c.k, false);
-        if (lane < 2 * KT && s_on) {  // lane 2 k: tile k's K scale; 2 k + 1: its V scale
-            int64_t sc = s_page[0] * a.c.scale_stride + s_tile[0];
-            uint32_t rows = s_where[0] >> 16;
+        copy_step(ring_s + slot * C::kSide, k_src, false);
+        uint32_t at = s_scale[0], rows = s_where[0];
 #pragma unroll
-            for (int k = 1; k < KT; ++k)
-                if (lane >> 1 == k) {
-                    sc = s_page[k] * a.c.scale_stride + s_tile[k];
-                    rows = s_where[k] >> 16;
-                }
-            cp4(meta_s + slot * (8 * KT) + lane * 4, ((lane & 1) ? a.c.vs : a.c.ks) + sc, rows != 0);
-        }
+        for (int k = 1; k < KT; ++k)
+            if (lane >> 1 == k) {
+                at = s_scale[k];
+                rows = s_where[k];
+            }
+        if (lane < 2 * KT && rows >> 16)
+            cp4(meta_s + slot * (8 * KT) + lane * 4, scale_src + at);
         cp_commit();
     };
     auto issue_v = [&](int slot) {
-        copy_step(ring_s + (2 + slot) * C::kSide, a.c.v, true);
+        copy_step(ring_s + (2 + slot) * C::kSide, v_src, true);
         cp_commit();
     };
 
@@ -740,6 +739,11 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                 ks[k] = __uint_as_float(sc.x);
                 vs[k] = __uint_as_float(sc.y);
                 open = open && (where[0][k] & kOpen);
+            }
+            if (!open) {  // a tile that brought nothing in left an older scale
+#pragma unroll
+                for (int k = 0; k < KT; ++k)
+                    if (!(where[0][k] >> 16)) ks[k] = vs[k] = 0.f;
             }
             const uint32_t st = ring_s + slot * C::kSide;
 

@@ -78,7 +78,7 @@ CACHE_BAD = [
     (dict(reserved=1), -1), (dict(n_pages=-1), -1), (dict(n_kv_heads=0), -1), (dict(page_size=24), -1),
     (dict(page_size=0), -1), (dict(page_size=65552), -1), (dict(head_dim=96), -3),
     (dict(page_stride=4095), -1), (dict(page_stride=4104), -1), (dict(scale_stride=3), -1),
-    (dict(k=None), -1), (dict(v_scale=None), -1), (dict(k=8), -2), (dict(k_scale=18), -2),
+    (dict(k=None), -1), (dict(v_scale=None), -1), (dict(scale_stride=1 << 30), -3), (dict(k=8), -2), (dict(k_scale=18), -2),
 ]
 
 

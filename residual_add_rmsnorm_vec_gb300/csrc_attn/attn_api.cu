@@ -363,20 +363,32 @@ int plan_attend(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
     const int64_t steps = max_tokens < 1 ? 1 : (max_tokens + e->tok - 1) / e->tok;
     const int64_t total = times(rows, steps);
 
-    // A row to a cluster of `split` blocks, or the line?  Measured in tokens
-    // of a warp, a cluster's rows cost their longest share times the waves of
-    // blocks; the line costs an even share and about 5 us more (its scan and
-    // its join: as long as a warp takes for 16384 / head_dim tokens), and
-    // longer joins where a row has many parts.  At head_dim 128 on a GB300:
-    // 8 x 2000 tokens x 8 heads 12.8 against 16.9 us, 256 x 300 45 against 48,
-    // but 64 x 8192 161 against 148, 1 x 131072 138 against 54.
+    // A row to a cluster of `split` blocks, or the line?  The host knows the
+    // tables' width, not the lengths: a long sequence among short ones keeps
+    // its clusters busy alone, while the line shares everything evenly.  So
+    // rows are left to clusters only while a warp's part of the longest is at
+    // most 65536 / head_dim tokens (about 20 us), and then where the estimate
+    // says so, measured in tokens of a warp.  A cluster's rows cost their longest share times the waves of
+    // blocks; a last wave that fills part of the GPU costs its part where DRAM
+    // is the bound (one column tile, head_dim 128 or 256), but no less than
+    // two thirds of a full one, below which its blocks wait for themselves;
+    // where instructions are the bound it costs a full one.  The line costs an
+    // even share, about 5 us more (its scan and its join: as long as a warp
+    // takes for 16384 / head_dim tokens), and longer joins where a row has many
+    // parts.  At head_dim 128 on a GB300, rows against line: 8 x 2000 tokens x
+    // 8 heads 10.5 against 14.6 us, 256 x 300 40 against 42, 16 x 4000 24.7
+    // against 27.9; and where all are as long as the first, 64 x 8192 147
+    // against 151, 1 x 131072 111 against 52.
     int64_t split = 1;
     while (split < kMaxSplit && rows * split * 2 <= resident) split *= 2;
-    const int64_t waves = (rows * split + resident - 1) / resident;
-    const double by_rows = (double)waves * (double)((steps + split - 1) / split) * e->tok / warps;
+    const double f = (double)(rows * split) / (double)resident, full_waves = floor(f);
+    const double least = e->NT == 1 && head_dim >= 128 ? 0.65 : 1.0;
+    const double rest = f - full_waves, waves = full_waves + (rest == 0 ? 0 : (rest > least ? rest : least));
+    const double part = (double)((steps + split - 1) / split) * e->tok / (double)warps;
+    const double by_rows = waves * part;
     const double by_line = (double)total * e->tok / (double)(resident * warps) +
                            16384.0 / (double)head_dim + 2.0 * (double)resident / (double)rows;
-    if (by_rows <= by_line && rows * split < (int64_t(1) << 31)) {
+    if (part <= 65536.0 / (double)head_dim && by_rows <= by_line && rows * split < (int64_t(1) << 31)) {
         p->split = (int)split;
         p->blocks = rows * split;
         p->min_chunk = 0;

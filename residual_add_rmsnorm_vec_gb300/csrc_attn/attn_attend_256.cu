@@ -4,7 +4,7 @@
 namespace rmsattn {
 
 using A = Shape<256, 1, 1, 4, 2>;
-using B = Shape<256, 2, 1, 4, 2>;
+using B = Shape<256, 2, 1, 8, 1>;
 
 const AttendEntry* attend_kernels_256(int* n) {
     static const AttendEntry table[] = {

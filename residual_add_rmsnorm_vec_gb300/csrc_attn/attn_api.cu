@@ -354,58 +354,63 @@ int plan_attend(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
     if (window > 0 && sinks < kMaxTokens && window + n_queries + sinks + 256 < max_tokens)
         max_tokens = window + n_queries + sinks + 256;
     const int64_t cols = n_q_heads / n_kv_heads * n_queries;
-    const AttendEntry* e = p->e = attend_entry_of(dt, head_dim, cols, max_tokens);
-    const int64_t resident = attend_blocks(d, e);
-    if (resident < 1) return RMSN_ECUDA;
-    const int64_t warps = e->threads / 32;
-    p->groups = (int)((cols + 8 * e->NT - 1) / (8 * e->NT));
-    const int64_t rows = n_seqs * n_kv_heads * p->groups;
-    const int64_t steps = max_tokens < 1 ? 1 : (max_tokens + e->tok - 1) / e->tok;
-    const int64_t total = times(rows, steps);
-
     // A row to a cluster of `split` blocks, or the line?  The host knows the
     // tables' width, not the lengths: a long sequence among short ones keeps
     // its clusters busy alone, while the line shares everything evenly.  So
     // rows are left to clusters only while a warp's part of the longest is at
     // most 65536 / head_dim tokens (about 20 us), and then where the estimate
-    // says so, measured in tokens of a warp.  A cluster's rows cost their longest share times the waves of
-    // blocks; a last wave that fills part of the GPU costs its part where DRAM
-    // is the bound (one column tile, head_dim 128 or 256), but no less than
-    // two thirds of a full one, below which its blocks wait for themselves;
-    // where instructions are the bound it costs a full one.  The line costs an
-    // even share, about 5 us more (its scan and its join: as long as a warp
-    // takes for 16384 / head_dim tokens), and longer joins where a row has many
-    // parts.  At head_dim 128 on a GB300, rows against line: 8 x 2000 tokens x
-    // 8 heads 10.5 against 14.6 us, 256 x 300 40 against 42, 16 x 4000 24.7
-    // against 27.9; and where all are as long as the first, 64 x 8192 147
-    // against 151, 1 x 131072 111 against 52.
-    int64_t split = 1;
-    while (split < kMaxSplit && rows * split * 2 <= resident) split *= 2;
-    const double f = (double)(rows * split) / (double)resident, full_waves = floor(f);
-    const double least = e->NT == 1 && head_dim >= 128 ? 0.65 : 1.0;
-    const double rest = f - full_waves, waves = full_waves + (rest == 0 ? 0 : (rest > least ? rest : least));
-    const double part = (double)((steps + split - 1) / split) * e->tok / (double)warps;
-    const double by_rows = waves * part;
-    const double by_line = (double)total * e->tok / (double)(resident * warps) +
-                           16384.0 / (double)head_dim + 2.0 * (double)resident / (double)rows;
-    if (part <= 65536.0 / (double)head_dim && by_rows <= by_line && rows * split < (int64_t(1) << 31)) {
-        p->split = (int)split;
-        p->blocks = rows * split;
-        p->min_chunk = 0;
-        p->workspace = 0;
-        return RMSN_OK;
+    // says so, measured in tokens of a warp.  A cluster's rows cost their
+    // longest share times the waves of blocks; a last wave that fills part of
+    // the GPU costs its part where DRAM is the bound (one column tile, head_dim
+    // 128 or 256), but no less than two thirds of a full one, below which its
+    // blocks wait for themselves; where instructions are the bound it costs a
+    // full one.  The line costs an even share, about 5 us more (its scan and
+    // its join: as long as a warp takes for 16384 / head_dim tokens), and
+    // longer joins where a row has many parts.  At head_dim 128 on a GB300,
+    // rows against line: 8 x 2000 tokens x 8 heads 10.5 against 14.6 us, 256 x
+    // 300 40 against 42, 16 x 4000 24.7 against 27.9; and where all are as long
+    // as the first, 64 x 8192 147 against 147, 1 x 131072 111 against 52.
+    for (int line = 0; line < 2; ++line) {
+        // the line takes the first of the fitting kernels, whatever the rows
+        const AttendEntry* e = p->e = attend_entry_of(dt, head_dim, cols, line ? 0 : max_tokens);
+        const int64_t resident = attend_blocks(d, e);
+        if (resident < 1) return RMSN_ECUDA;
+        const int64_t warps = e->threads / 32;
+        p->groups = (int)((cols + 8 * e->NT - 1) / (8 * e->NT));
+        const int64_t rows = n_seqs * n_kv_heads * p->groups;
+        const int64_t steps = max_tokens < 1 ? 1 : (max_tokens + e->tok - 1) / e->tok;
+        const int64_t total = times(rows, steps);
+        if (!line) {
+            int64_t split = 1;
+            while (split < kMaxSplit && rows * split * 2 <= resident) split *= 2;
+            const double f = (double)(rows * split) / (double)resident, full = floor(f);
+            const double least = e->NT == 1 && head_dim >= 128 ? 0.65 : 1.0;
+            const double rest = f - full;
+            const double waves = full + (rest == 0 ? 0 : (rest > least ? rest : least));
+            const double part = (double)((steps + split - 1) / split) * e->tok / (double)warps;
+            const double by_line = (double)total * e->tok / (double)(resident * warps) +
+                                   16384.0 / (double)head_dim + 2.0 * (double)resident / (double)rows;
+            if (part > 65536.0 / (double)head_dim || waves * part > by_line ||
+                rows * split >= (int64_t(1) << 31))
+                continue;
+            p->split = (int)split;
+            p->blocks = rows * split;
+            p->min_chunk = 0;
+            p->workspace = 0;
+            return RMSN_OK;
+        }
+        p->split = 0;
+        // a share is at least two steps for each of its warps; no more shares
+        // than the longest rows that the table holds would fill
+        p->min_chunk = 2 * warps;
+        const int64_t full = (total + p->min_chunk - 1) / p->min_chunk;
+        p->blocks = full < resident ? full : resident;
+        if (total / p->blocks > (1 << 30)) return RMSN_EUNSUPPORTED;  // a share counts in 31 bits
+        // a thread joins eight parts at once; more groups of threads where a
+        // row has more
+        p->join = p->blocks / rows < 8 ? (int)head_dim : 512;
+        p->workspace = p->blocks * (kCutBytes + 2 * (int64_t)e->part * 4);
     }
-    p->split = 0;
-    // a share is at least two steps for each of its warps; no more shares than
-    // the longest rows that the table holds would fill
-    p->min_chunk = 2 * warps;
-    const int64_t full = (total + p->min_chunk - 1) / p->min_chunk;
-    p->blocks = full < resident ? full : resident;
-    if (total / p->blocks > (1 << 30)) return RMSN_EUNSUPPORTED;  // a share counts in 31 bits
-    // a thread joins eight parts at once; more groups of threads where a row
-    // has more
-    p->join = p->blocks / rows < 8 ? (int)head_dim : 512;
-    p->workspace = p->blocks * (kCutBytes + 2 * (int64_t)e->part * 4);
     return RMSN_OK;
 }
 

@@ -140,8 +140,8 @@ int rmsattn_kv_append(const rmsattn_cache* cache, const void* k, const void* v, 
  *
  * Query head h reads key head h / (n_q_heads / n_kv_heads).  Products of the
  * codes with q are exact in fp32 sums; softmax statistics and the output sum
- * are fp32; the weights are rounded to fp16 (2^-11 of their value) for the
- * second product.  Tokens past lengths[s], and tokens that no query of the
+ * are fp32; the weights are rounded to fp16 (2^-11 of their value, or 2^-33 of
+ * the row's largest) for the second product.  Tokens past lengths[s], and tokens that no query of the
  * sequence sees, have no influence, whatever their codes are.  A page outside
  * [0, n_pages), or past the table's width, is left out and sets bit 2 (value
  * 4) of the status word.

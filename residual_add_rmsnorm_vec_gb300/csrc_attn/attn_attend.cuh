@@ -7,8 +7,16 @@
 //
 // What bounds it.  A decode step reads 2 D + 1/2 bytes per token and key head
 // and does 4 D products for each of the G query heads that share it: DRAM, as
-// long as the G n columns (query head x query token) of a row stay few.  So
-// the work is laid out around the reads:
+// long as the G n columns (query head x query token) of a row stay few.  Each
+// token also costs instructions, about 17 a warp at head_dim 128 and one
+// column tile (a conversion for every two codes, a third of them; then the
+// copies, the softmax of eight columns, the matrix products); with half the
+// bytes (head_dim 64) or twice the columns they become the bound.  On one
+// GB300, of the copy peak of 6.78 TB/s: 64 sequences of 6144 to 8192 tokens,
+// 32 / 8 heads x 128, 0.94 GB in 146 us (0.95); the same at head_dim 64, 80 us
+// (0.87), at 256, 148 us for half as many (0.94); 4 query tokens, 16 columns,
+// 176 MB in 47 us (0.55); one sequence of 131072 tokens 52 us (0.76).
+// So the work is laid out around the reads:
 //
 // * Columns are the narrow side of mma.m16n8k16: S^T = K Q^T with 16 tokens
 //   as its rows, O^T = V^T P^T with 16 dims as its rows.  The codes are

@@ -139,7 +139,9 @@ def attend(q, cache, table, lengths, scale, window, sinks):
         good = (pg >= 0) & (pg < pages)
         pg = pg.clamp(0, max(0, pages - 1))
         k = e4m3(kc[pg, :, j % page].contiguous()) * cache["k_scale"][pg, :, j % page // 16].double()[..., None]
-        v = e4m3(vc[pg, :, j % page].contiguous()) * cache["v_scale"][pg, :, j % page // 16].double()[..., None]
+        code = e4m3(vc[pg, :, j % page].contiguous())
+        vs = cache["v_scale"][pg, :, j % page // 16].double()
+        v = code * vs[..., None]
         for i in range(n):
             pos = L - n + i
             seen = good & (j <= pos)
@@ -161,8 +163,13 @@ def attend(q, cache, table, lengths, scale, window, sinks):
                 ds = float((qq.abs() @ kk.abs().T).max()) * abs(scale) * (2 * D + 8) * U + float(
                     s.abs().max()) * 4 * U
                 rel = 2.0 ** -11 + 2 * (ds + 4 * U) + (2 * vv.shape[0] / 16 + 64) * 2 * U
+                # fp16 rounds a weight below its normal range by 2^-25 at most,
+                # in units of 2^-8 of the row's reference (which is no more
+                # than the largest weight, so than the weights' sum) times the
+                # row's largest value scale
+                lost = 2.0 ** -33 * vs[good, h].nan_to_num(0, 0, 0).max() * code[seen, h].abs().sum(0)
                 out[b, i, h * G:(h + 1) * G] = o
-                bound[b, i, h * G:(h + 1) * G] = rel * (p @ vv.abs())
+                bound[b, i, h * G:(h + 1) * G] = rel * (p @ vv.abs()) + lost
     dt = q.dtype
     bound = bound + HALF[dt] * (out.abs() + bound) + TINY[dt]
     return out, bound

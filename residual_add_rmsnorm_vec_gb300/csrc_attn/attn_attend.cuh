@@ -53,6 +53,8 @@
 
 namespace rmsattn {
 
+using rmsn::F2;
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kOpen = 1u << 12;
 constexpr float kTinyScale = 1.17549435e-38f;
@@ -116,6 +118,11 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {  // NaN left out
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 __device__ __forceinline__ float max_over_rows(float v) {  // over lanes of equal lane % 4
     v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
@@ -712,23 +719,22 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 
         store_q(cg);
         __syncthreads();
-        float cs[NT][2];
+        F2 cs[NT];  // the lane's two columns of each tile, here and below
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            cs[nt][0] = q_scale[nt * 8 + 2 * t];
-            cs[nt][1] = q_scale[nt * 8 + 2 * t + 1];
-        }
+        for (int nt = 0; nt < NT; ++nt)
+            cs[nt] = rmsn::f2(q_scale[nt * 8 + 2 * t], q_scale[nt * 8 + 2 * t + 1]);
         const uint32_t q_s = smem_addr(qrows) + g * C::kQPitch + t * 32;
         uint4 qf[kQRegs ? CH / 2 : 1];
         if constexpr (kQRegs) {
 #pragma unroll
             for (int i = 0; i < CH / 2; ++i) qf[i] = lds16(q_s + (i / 2) * 128 + (i & 1) * 16);
         }
-        float o[MT][NT][4], m[NT][2], l[NT][2];
+        float o[MT][NT][4];
+        F2 less[NT], l[NT];  // minus the references; the weights' sums
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = kNone;
-            l[nt][0] = l[nt][1] = 0.f;
+            less[nt] = rmsn::f2(-kNone, -kNone);
+            l[nt] = rmsn::f2(0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -795,8 +801,8 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
             __syncwarp();
             issue_k(slot);  // every lane has read this stage
 
-            // Scores are S kc - m in units of log2, kc = K scale x query scale
-            // (not negative).  A mask makes S -inf, and the weight 0 below.
+            // Exponents are S kc - m in units of log2, kc = K scale x query
+            // scale (not negative).  A mask makes S -inf, and the weight 0 below.
             uint32_t see[KT];  // bit 4 nt + x: this lane's element is visible
             if (!open) {
                 const int t0 = span.first_token(mine - c_first);
@@ -820,42 +826,56 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                             }
                     }
             }
-            float kc[KT][NT][2];
-            bool grew = false;
+            F2 kc[KT][NT], e[KT][NT][2];
+            float top = -INFINITY, vmax = vref;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int k = 0; k < KT; ++k) {
+                vmax = fmaxf(vmax, vs[k]);
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int nt = 0; nt < NT; ++nt) {
+                    kc[k][nt] = rmsn::mul2(rmsn::f2(ks[k], ks[k]), cs[nt]);
 #pragma unroll
-                    for (int k = 0; k < KT; ++k) {
-                        kc[k][nt][x] = ks[k] * cs[nt][x];
-                        grew = grew || fmaxf(s[k][nt][x], s[k][nt][2 + x]) * kc[k][nt][x] > m[nt][x] + kSlack;
+                    for (int h = 0; h < 2; ++h) {
+                        float lo, hi;
+                        e[k][nt][h] = rmsn::fma2(rmsn::f2(s[k][nt][2 * h], s[k][nt][2 * h + 1]), kc[k][nt], less[nt]);
+                        rmsn::f2split(e[k][nt][h], lo, hi);
+                        top = max3(top, lo, hi);
                     }
-            float vmax = vref;
-#pragma unroll
-            for (int k = 0; k < KT; ++k) vmax = fmaxf(vmax, vs[k]);
-            if (__any_sync(0xFFFFFFFFu, grew) || vmax > vref) {
+                }
+            }
+            if (__any_sync(0xFFFFFFFFu, top > kSlack) || vmax > vref) {
                 // new references; what was summed so far follows them
                 const float vr = vref / vmax;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float keep[2];
+                    float to[2], was[2], keep[2];
+                    rmsn::f2split(less[nt], was[0], was[1]);
+                    to[0] = -was[0];
+                    to[1] = -was[1];
+#pragma unroll
+                    for (int k = 0; k < KT; ++k) {
+                        float c[2];
+                        rmsn::f2split(kc[k][nt], c[0], c[1]);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            to[x] = max3(to[x], s[k][nt][x] * c[x], s[k][nt][2 + x] * c[x]);
+                    }
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        float to = m[nt][x];
-#pragma unroll
-                        for (int k = 0; k < KT; ++k)
-                            to = fmaxf(to, fmaxf(s[k][nt][x], s[k][nt][2 + x]) * kc[k][nt][x]);
-                        to = max_over_rows(to);
-                        keep[x] = exp2a(m[nt][x] - to);
-                        l[nt][x] *= keep[x];
-                        m[nt][x] = to;
-                        keep[x] *= vr;
+                        to[x] = max_over_rows(to[x]);
+                        keep[x] = exp2a(-was[x] - to[x]);
                     }
+                    less[nt] = rmsn::f2(-to[0], -to[1]);
+                    l[nt] = rmsn::mul2(l[nt], rmsn::f2(keep[0], keep[1]));
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) o[i][nt][x] *= keep[x & 1];
+                        for (int x = 0; x < 4; ++x) o[i][nt][x] *= keep[x & 1] * vr;
+#pragma unroll
+                    for (int k = 0; k < KT; ++k)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            e[k][nt][h] = rmsn::fma2(rmsn::f2(s[k][nt][2 * h], s[k][nt][2 * h + 1]), kc[k][nt], less[nt]);
                 }
                 vref = vmax;
                 rv = 1.f / vmax;
@@ -869,8 +889,12 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        p[k][nt][x] = exp2a(fmaf(s[k][nt][x], kc[k][nt][x & 1], -m[nt][x & 1]));
+                    for (int h = 0; h < 2; ++h) {
+                        float lo, hi;
+                        rmsn::f2split(e[k][nt][h], lo, hi);
+                        p[k][nt][2 * h] = exp2a(lo);
+                        p[k][nt][2 * h + 1] = exp2a(hi);
+                    }
             if (!open) {
 #pragma unroll
                 for (int k = 0; k < KT; ++k)
@@ -883,13 +907,17 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
                 const float f = vs[k] * rv * kLift;
+                const F2 f2 = rmsn::f2(f, f);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    l[nt][0] += p[k][nt][0] + p[k][nt][2];
-                    l[nt][1] += p[k][nt][1] + p[k][nt][3];
-                    pb[k][nt][0] = rmsn::pack_f16x2(p[k][nt][0] * f, p[k][nt][1] * f);
-                    pb[k][nt][1] = rmsn::pack_f16x2(p[k][nt][2] * f, p[k][nt][3] * f);
-                }
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const F2 w = rmsn::f2(p[k][nt][2 * h], p[k][nt][2 * h + 1]);
+                        float lo, hi;
+                        l[nt] = rmsn::add2(l[nt], w);
+                        rmsn::f2split(rmsn::mul2(w, f2), lo, hi);
+                        pb[k][nt][h] = rmsn::pack_f16x2(lo, hi);
+                    }
             }
 
             // O^T += V^T P^T
@@ -992,11 +1020,16 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         }
         int used = a.cols - cg * C::kCols;  // columns of this row
         if (used > C::kCols) used = C::kCols;
-        float ls[NT][2];
+        float ls[NT][2], m[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            ls[nt][0] = sum_over_rows(l[nt][0]);
-            ls[nt][1] = sum_over_rows(l[nt][1]);
+            rmsn::f2split(l[nt], ls[nt][0], ls[nt][1]);
+            rmsn::f2split(less[nt], m[nt][0], m[nt][1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                ls[nt][x] = sum_over_rows(ls[nt][x]);
+                m[nt][x] = -m[nt][x];
+            }
         }
         // join the warps, a tile of eight columns at a time; behind the block's
         // last step the ring is free, and holds all of them

@@ -91,7 +91,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t count) {
     try {
         const Tensor *q = count == 10 ? tensor(a[0]) : nullptr, *table = q ? tensor(a[3]) : nullptr,
                      *lengths = table ? tensor(a[4]) : nullptr;
-        if (!lengths || !PyLong_Check(a[6]) || !PyLong_Check(a[7]) || (a[5] != Py_None && !PyFloat_Check(a[5])))
+        if (!lengths || !PyLong_Check(a[6]) || !PyLong_Check(a[7]) || !PyBool_Check(a[9]) || (a[5] != Py_None && !PyFloat_Check(a[5])))
             return leave();
         const rmsattn_cache* cache = cache_at(a[1]);
         const int64_t index = PyLong_AsLongLong(a[2]), window = PyLong_AsLongLong(a[6]),
@@ -150,7 +150,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t count) {
     try {
         const Tensor *k = count == 8 ? tensor(a[0]) : nullptr, *v = k ? tensor(a[1]) : nullptr,
                      *table = v ? tensor(a[4]) : nullptr, *lengths = table ? tensor(a[5]) : nullptr;
-        if (!lengths) return leave();
+        if (!lengths || !PyBool_Check(a[7])) return leave();
         const rmsattn_cache* cache = cache_at(a[2]);
         const int64_t index = PyLong_AsLongLong(a[3]);
         if (PyErr_Occurred()) {
@@ -242,7 +242,8 @@ PyObject* qk_rope(PyObject*, PyObject* const* a, Py_ssize_t count) {
         const Tensor *pos = tensor(a[2]), *turns = tensor(a[3]), *axis = tensor(a[4]);
         const Tensor* ref = a[0] != Py_None ? tensor(a[0]) : tensor(a[1]);
         if (!pos || !turns || !axis || !ref || ref->dim() < 1 || !PyLong_Check(a[8]) ||
-            (a[9] != Py_None && !PyFloat_Check(a[9])) || !PyFloat_Check(a[10]))
+            (a[9] != Py_None && !PyFloat_Check(a[9])) || !PyFloat_Check(a[10]) || !PyBool_Check(a[11]) ||
+            !PyBool_Check(a[14]))
             return leave();
         const int64_t n_axes = PyLong_AsLongLong(a[5]), D = PyLong_AsLongLong(a[8]);
         if (PyErr_Occurred()) {

@@ -331,7 +331,9 @@ int64_t attend_blocks(DeviceInfo* d, const AttendEntry* e) {
         cudaGetLastError();
         return 0;
     }
-    const int64_t n = (int64_t)bps * d->num_sms;
+    // no more than the shape was bounded for: both dtypes' kernels then have
+    // the same grid, and so the same workspace
+    const int64_t n = (int64_t)(bps < e->per_sm ? bps : e->per_sm) * d->num_sms;
     if (n > 0) d->resident.emplace_back(e->fn, n);
     return n;
 }

@@ -92,6 +92,7 @@ constexpr int kMaxSplit = 8;  // blocks of a cluster
 // One compiled attention kernel and the join of its parts.
 struct AttendEntry {
     int32_t dt, D, NT, tok, threads, smem;
+    int32_t per_sm;  // blocks an SM holds: the same for every dtype of a shape
     int32_t most;  // takes rows of up to this many tokens
     int32_t part;  // floats of one part
     const void* fn;

@@ -15,7 +15,7 @@
 // GB300, of the copy peak of 6.78 TB/s: 64 sequences of 6144 to 8192 tokens,
 // 32 / 8 heads x 128, 0.94 GB in 146 us (0.95); the same at head_dim 64, 80 us
 // (0.87), at 256, 148 us for half as many (0.94); 4 query tokens, 16 columns,
-// 176 MB in 47 us (0.55); one sequence of 131072 tokens 52 us (0.76).
+// 176 MB in 46 us (0.57); one sequence of 131072 tokens 52 us (0.77).
 // So the work is laid out around the reads:
 //
 // * Columns are the narrow side of mma.m16n8k16: S^T = K Q^T with 16 tokens
@@ -30,7 +30,7 @@
 // * P^T is turned from S^T's accumulator layout into the second product's
 //   operand layout by movmatrix: no shared memory, and no exchange between
 //   warps before a row ends.
-// * Each warp streams its own steps (16 to 64 tokens) through its own ring of
+// * Each warp streams its own steps (16 or 32 tokens) through its own ring of
 //   cp.async stages, scales included, across row borders: no block barrier in
 //   the stream.  K and V have two stages each, and each is filled again as
 //   soon as it has been read (K before the softmax, V behind the second
@@ -56,8 +56,8 @@ namespace rmsattn {
 using rmsn::F2;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr uint32_t kOpen = 1u << 12;
-constexpr float kTinyScale = 1.17549435e-38f;
+constexpr uint32_t kOpen = 1u << 12;  // of a tile's word: every query sees all of it
+constexpr float kTinyScale = 1.17549435e-38f;  // value scales are measured against at least this
 // A row's reference (what is taken from its scores before exp2) follows its
 // maximum only when that has grown by more than 2^kSlack: a sum is then rarely
 // rescaled twice.  Weights are thus up to 2^kSlack; they are multiplied by
@@ -499,12 +499,11 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     unsigned char* qrows = smem + C::kRing + C::kMetaAll;
     const uint32_t ring_s = smem_addr(smem) + wp * C::kWarp, meta_s = smem_addr(smem) + C::kRing + wp * C::kMeta;
 
-    // ---- queries: this warp's columns of a row, first into
-    // registers (before the wait that they can hide behind), then to shared
-    // memory in fp16, each scaled by a power of two to at most 2^8 (so that
-    // fp16 holds any bf16 row: what is below 2^-32 of the row's largest value
-    // loses bits); q_scale undoes it, times |scale| log2(e) (a negative scale
-    // turns the queries' sign)
+    // ---- queries: this warp's columns of a row, first into registers (before
+    // the wait that they can hide behind), then to shared memory in fp16, each
+    // scaled by a power of two to at most 2^8 (so that fp16 holds any bf16 row:
+    // what is below 2^-32 of the row's largest value loses bits); q_scale
+    // undoes it, times |scale| log2(e) (a negative scale turns the queries' sign)
     constexpr int QC = (C::kCols + W - 1) / W, QW = D / 64;
     uint32_t qreg[QC][QW];
     auto load_q = [&](int64_t b, int hc) {
@@ -1218,6 +1217,7 @@ AttendEntry attend_entry(int dt, int most = INT32_MAX) {
     e.D = C::D;
     e.NT = C::NT;
     e.tok = C::kTok;
+    e.per_sm = C::M;
     e.most = most;
     e.threads = C::W * 32;
     e.smem = C::kSmem;

@@ -1114,11 +1114,17 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                 float mx = kNone, lsum = 0.f, y[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) y[k] = 0.f;
-                for (int r = 0; r < a.split; ++r) mx = fmaxf(mx, part_ml[r][cc].x);
-                for (int r = 0; r < a.split; ++r) {
-                    const float2 p = part_ml[r][cc];
-                    const float f = exp2a(p.x - mx);
-                    lsum += p.y * f;
+                float2 ml[kMaxSplit];
+#pragma unroll
+                for (int r = 0; r < kMaxSplit; ++r) {
+                    ml[r] = r < a.split ? part_ml[r][cc] : make_float2(kNone, 0.f);
+                    mx = fmaxf(mx, ml[r].x);
+                }
+#pragma unroll
+                for (int r = 0; r < kMaxSplit; ++r) {
+                    if (r >= a.split) break;
+                    const float f = exp2a(ml[r].x - mx);
+                    lsum += ml[r].y * f;
                     add8(y, from + 2 * r, f);
                 }
                 finish8<T>(a, row_b, col, d, y, lsum);

@@ -6,8 +6,6 @@
 #include <string.h>
 
 #include <mutex>
-#include <utility>
-#include <vector>
 
 #include "../../include/rmsnorm_attn.h"
 #include "attn_args.h"
@@ -29,7 +27,11 @@ struct DeviceInfo {
     uint32_t* status = nullptr;
     cudaError_t err = cudaSuccess;
     std::mutex mu;
-    std::vector<std::pair<const void*, int64_t>> resident;  // attention kernel -> resident blocks
+    struct {
+        const void* fn;
+        int64_t blocks;
+    } resident[32];  // an attention kernel's resident blocks, once asked for
+    int n_resident = 0;
 };
 DeviceInfo g_dev[kMaxDevices];
 
@@ -321,8 +323,8 @@ const AttendEntry* attend_entry_of(int dt, int64_t D, int64_t cols, int64_t toke
 // Resident blocks of an entry on the device (its grid), or 0.
 int64_t attend_blocks(DeviceInfo* d, const AttendEntry* e) {
     std::lock_guard<std::mutex> lock(d->mu);
-    for (const auto& f : d->resident)
-        if (f.first == e->fn) return f.second;
+    for (int i = 0; i < d->n_resident; ++i)
+        if (d->resident[i].fn == e->fn) return d->resident[i].blocks;
     int bps = 0;
     if (cudaFuncSetAttribute(e->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, e->smem) !=
             cudaSuccess ||
@@ -334,7 +336,10 @@ int64_t attend_blocks(DeviceInfo* d, const AttendEntry* e) {
     // no more than the shape was bounded for: both dtypes' kernels then have
     // the same grid, and so the same workspace
     const int64_t n = (int64_t)(bps < e->per_sm ? bps : e->per_sm) * d->num_sms;
-    if (n > 0) d->resident.emplace_back(e->fn, n);
+    if (n > 0 && d->n_resident < 32) {
+        d->resident[d->n_resident].fn = e->fn;
+        d->resident[d->n_resident++].blocks = n;
+    }
     return n;
 }
 

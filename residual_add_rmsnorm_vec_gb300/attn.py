@@ -252,6 +252,8 @@ class KVCache:
         pages, heads, page, dim = k.shape
         if page % _al.RMSATTN_BLOCK or not page:
             raise ValueError(f"page_size must be a multiple of {_al.RMSATTN_BLOCK}, got {page}")
+        if heads < 1 or dim < 1:
+            raise ValueError(f"a cache needs heads and a head_dim, got {heads} of {dim}")
         shape = (pages, heads, page // _al.RMSATTN_BLOCK)
         for name, t, want, dtypes in (("k", k, k.shape, _CODES), ("v", v, k.shape, _CODES),
                                       ("k_scale", k_scale, shape, (torch.float32,)),

@@ -191,6 +191,16 @@ def test_cache_arguments(rn, kw, err):
     assert host_cache(rn).page_size == 32
 
 
+@pytest.mark.parametrize("heads,dim", [(0, 64), (2, 0), (0, 0)])
+def test_cache_without_heads_or_dims_refused(rn, heads, dim):
+    # nothing divides by either once a cache exists
+    codes, scales = z(4, heads, 32, dim, dtype=torch.uint8), z(4, heads, 2, dtype=torch.float32)
+    with pytest.raises(ValueError, match="heads"):
+        rn.KVCache(codes, codes.clone(), scales, scales.clone())
+    with pytest.raises(ValueError, match="heads"):
+        rn.KVCache.empty(4, heads, 32, dim, device="cpu")
+
+
 I32 = torch.int32
 
 

@@ -418,6 +418,8 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
         raise TypeError(f"q must be bfloat16 or float16, got {dt}")
     if window < 0 or sinks < 0:
         raise ValueError("window and sinks must not be negative")
+    # the C ABI's int64 would wrap; no table holds so many tokens
+    window, sinks = min(window, 2**62), min(sinks, 2**62)
     stride, width = _check_seqs(cache, block_table, lengths, B)
     if index < 0 or q.get_device() != index:
         raise ValueError(f"q must be on the cache's CUDA device, {cache.device}")

@@ -2,6 +2,9 @@
 kv_cache_attention against 64-bit references (tests/attn_ref.py), at the
 sizes, masks, strides and values where they can go wrong."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -727,3 +730,51 @@ def test_stream_of_another_call_is_used(rn):
     out, _ = rn.qk_norm_rope(x, None, pos, table, head_dim=D, stream=s)
     torch.cuda.current_stream().wait_stream(s)
     within(out, *ref.rope(want, None, table, pos.cpu()[None], D, None, 0.0, False))
+
+
+@pytest.mark.parametrize("past", [2**62, 2**64, 2**64 + 5])
+def test_attention_masks_wider_than_any_integer(rn, past):
+    t = ref.random_cache(16, 2, 16, 64, 3, "cuda")
+    cache, table = make_cache(rn, t), ref.tables(2, 8, 16, 4, "cuda")
+    lens = torch.tensor([100, 7], dtype=torch.int32, device="cuda")
+    q = rand((2, 4, 64), 5, torch.bfloat16).cuda()
+    want = rn.kv_cache_attention(q, cache, table, lens)
+    assert torch.equal(rn.kv_cache_attention(q, cache, table, lens, window=past), want)
+    assert torch.equal(rn.kv_cache_attention(q, cache, table, lens, window=9, sinks=past), want)
+
+
+FIRST = """
+import torch
+import residual_add_rmsnorm_vec_gb300 as rn
+B, Hq, Hk, D, pages = 3, 8, 2, 128, {pages}
+x = torch.randn((B, (Hq + 2 * Hk) * D), device="cuda").to(torch.bfloat16)
+pos = torch.arange(B, dtype=torch.int32, device="cuda")
+cache = rn.KVCache.empty(B * pages, Hk, 16, D)
+for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+    t.zero_()
+table = torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages)
+before = torch.zeros(B, dtype=torch.int32, device="cuda")
+rope = rn.rope_table(D)
+def step():
+    q, k, v = x.split([Hq * D, Hk * D, Hk * D], 1)
+    q, k = rn.qk_norm_rope(q, k, pos, rope, head_dim=D, eps=1e-6)
+    rn.kv_cache_append_(cache, k, v, table, before)
+    return rn.kv_cache_attention(q.view(B, Hq, D), cache, table, before + 1)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = step()
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(got, step())
+v = x[:, (Hq + Hk) * D:].view(B, Hk, 1, D).expand(B, Hk, Hq // Hk, D).reshape(B, Hq, D).float()
+# one token seen: its value, rounded to E4M3 (2^-4, or half of 2^-9 of the scale) and bf16 (2^-8); products below 2^-9
+assert ((got.float() - v).abs() <= v.abs() * (2.0 ** -4 + 2.0 ** -7) + v.abs().amax() * 2.0 ** -18).all()
+"""
+
+
+@pytest.mark.parametrize("pages", [4, 4096])
+def test_the_first_call_of_a_process_may_be_captured(rn, pages):
+    # clusters (4 pages) and the line with its workspace (4096)
+    r = subprocess.run([sys.executable, "-c", FIRST.format(pages=pages)], capture_output=True, text=True,
+                       timeout=300, cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]

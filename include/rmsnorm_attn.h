@@ -53,6 +53,7 @@ extern "C" {
  *                   any other overlap is undefined
  *   q_weight, k_weight [head_dim] or NULL (1); only read with RMSATTN_NORM
  *   positions       [n_axes, n_tokens] int32 or int64, rows pos_stride apart
+ *                   (0: every axis reads the same row)
  *   turns, axis     [rot_dim / 2] on the device
  *
  * rot_dim is even and at most head_dim (0: no rotation); head_dim <= 4096.

@@ -138,8 +138,8 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
 
     q is [T, Hq * head_dim] or [T, Hq, head_dim], likewise k (either may be
     None); both may be column slices of a fused qkv matrix.  positions is [T]
-    for a table of one axis, else [n_axes, T], int32 or int64.  ``eps``: the
-    norm's; None leaves the norm (and the weights) out.  ``interleaved``:
+    for a table of one axis, else [n_axes, T] (``p.expand(n_axes, T)`` where
+    all axes agree), int32 or int64.  ``eps``: the norm's; None leaves the norm (and the weights) out.  ``interleaved``:
     pairs are neighbouring elements, else halves of the first rot_dim.  The
     results go to q_out / k_out (new tensors where None; pass q and k
     themselves to work in place).  Returns ``(q_out, k_out)``.

@@ -167,7 +167,8 @@ RMSATTN_API int rmsattn_qk_rope_fwd(const void* q, const void* k, const void* q_
         if (too_big(times(n_tokens, times(s, 4)))) return RMSN_EINVAL;
     if (rot_dim && (n_axes < 1 || pos_stride < 0 || too_big(times(n_axes, times(pos_stride, 8)))))
         return RMSN_EINVAL;
-    if (n_axes > 1 && pos_stride < n_tokens) return RMSN_EINVAL;
+    // 0: one row serves every axis (text among images)
+    if (n_axes > 1 && pos_stride != 0 && pos_stride < n_tokens) return RMSN_EINVAL;
     if (n_tokens == 0 || n_q_heads + n_k_heads == 0) return RMSN_OK;
     if ((n_q_heads && (!q || !q_out)) || (n_k_heads && (!k || !k_out))) return RMSN_EINVAL;
     if (rot_dim && (!positions || !turns || !axis)) return RMSN_EINVAL;

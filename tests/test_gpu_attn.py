@@ -105,6 +105,16 @@ def test_rope_far_and_negative_positions(rn, bits, top):
     within(out, *ref.rope(x, None, table, pos, D, None, 0.0, False))
 
 
+@pytest.mark.parametrize("T", [1, 5])
+def test_rope_one_row_of_positions_for_all_axes(rn, T):
+    table = rn.rope_table(64, sections=[8, 12, 12])
+    x = rand((T, 4 * 64), 1, torch.bfloat16).cuda()
+    pos = torch.arange(3, 3 + T, dtype=torch.int32, device="cuda")
+    got, _ = rn.qk_norm_rope(x, None, pos.expand(3, T), table, head_dim=64, eps=1e-6)
+    want, _ = rn.qk_norm_rope(x, None, pos.expand(3, T).contiguous(), table, head_dim=64, eps=1e-6)
+    assert torch.equal(got, want)
+
+
 def test_rope_axis_order_and_pair_tables(rn):
     # pairs handed to the axes in turn, with frequencies of the caller's own
     D, T = 32, 5

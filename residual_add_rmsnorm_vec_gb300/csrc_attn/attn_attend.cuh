@@ -57,12 +57,16 @@ using rmsn::F2;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kOpen = 1u << 12;  // of a tile's word: every query sees all of it
-constexpr float kTinyScale = 1.17549435e-38f;  // value scales are measured against at least this
 // A row's reference (what is taken from its scores before exp2) follows its
 // maximum only when that has grown by more than 2^kSlack: a sum is then rarely
 // rescaled twice.  Weights are thus up to 2^kSlack; they are multiplied by
 // kLift before they are rounded to fp16, whose subnormals then end 2^-32 below
 // the reference: what 2^17 tokens lose at most (2^-33 each) is 2^-16 of it.
+// The values' scales stay out of the rounded weights: they may differ by any
+// factor from tile to tile, and a weight would lose as many bits.  A tile's
+// products are summed by themselves and enter the row's sum through an fp32
+// multiply-add with the scale (16 packed ones a tile and column tile at
+// head_dim 128).
 constexpr float kNone = -3.402823466e38f;  // the reference before any token is seen
 constexpr float kSlack = 7.f;
 constexpr float kLift = 256.f;
@@ -408,11 +412,12 @@ __device__ __forceinline__ float* part_of(const AttendArgs& a, int64_t blk, int 
 
 // One tile's weighted values, token by token, for the columns that see each
 // (the values' NaN reaches those alone).  p: the packed weights as the scores
-// lie: tokens g and g + 8, columns 2 t and 2 t + 1; see: their bits.  A path
-// for NaN codes under a mask only: small rather than fast.
+// lie: tokens g and g + 8, columns 2 t and 2 t + 1; see: their bits; f: the
+// tile's value scale.  A path for NaN codes under a mask only: small rather
+// than fast.
 template <class C>
-__device__ __forceinline__ void add_tile(float (&o)[C::D / 16][C::NT][4], const uint32_t (&p)[C::NT][2],
-                                         uint32_t see, uint32_t vt) {
+__device__ __forceinline__ void add_tile(F2 (&o)[C::D / 16][C::NT][2], const uint32_t (&p)[C::NT][2],
+                                         uint32_t see, uint32_t vt, float f) {
     constexpr int D = C::D, MT = D / 16;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll 1
@@ -424,7 +429,9 @@ __device__ __forceinline__ void add_tile(float (&o)[C::D / 16][C::NT][4], const 
             const uint32_t w0 = __shfl_sync(0xFFFFFFFFu, p[nt][0], from);
             const uint32_t w1 = __shfl_sync(0xFFFFFFFFu, p[nt][1], from);
             const uint32_t w = h ? w1 : w0;
+            // weights of 0, and values of 0 beside them, where a column sees nothing
             const bool on0 = bits >> (4 * nt) & 1, on1 = bits >> (4 * nt + 1) & 1;
+            const float p0 = rmsn::lo2<F16>(w) * f, p1 = rmsn::hi2<F16>(w) * f;
 #pragma unroll
             for (int i = 0; i < MT; ++i) {  // dims 2 i and 2 i + 1 of the lane's
                 const int d = D == 64 ? g * 8 + 2 * i : (g + 8 * (i / 8)) * 16 + 2 * (i % 8);
@@ -434,14 +441,9 @@ __device__ __forceinline__ void add_tile(float (&o)[C::D / 16][C::NT][4], const 
                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(vt + at * 16 + d % 16) : "memory");
                 const uint32_t x = e4m3x2_to_f16x2(v);
                 const float v0 = rmsn::lo2<F16>(x), v1 = rmsn::hi2<F16>(x);
-                if (on0) {
-                    o[i][nt][0] = fmaf(v0, rmsn::lo2<F16>(w), o[i][nt][0]);
-                    o[i][nt][2] = fmaf(v1, rmsn::lo2<F16>(w), o[i][nt][2]);
-                }
-                if (on1) {
-                    o[i][nt][1] = fmaf(v0, rmsn::hi2<F16>(w), o[i][nt][1]);
-                    o[i][nt][3] = fmaf(v1, rmsn::hi2<F16>(w), o[i][nt][3]);
-                }
+                const F2 pp = rmsn::f2(p0, p1);
+                o[i][nt][0] = rmsn::fma2(rmsn::f2(on0 ? v0 : 0.f, on1 ? v0 : 0.f), pp, o[i][nt][0]);
+                o[i][nt][1] = rmsn::fma2(rmsn::f2(on0 ? v1 : 0.f, on1 ? v1 : 0.f), pp, o[i][nt][1]);
             }
         }
     }
@@ -728,7 +730,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 #pragma unroll
             for (int i = 0; i < CH / 2; ++i) qf[i] = lds16(q_s + (i / 2) * 128 + (i & 1) * 16);
         }
-        float o[MT][NT][4];
+        F2 o[MT][NT][2];  // two columns each, of two dims
         F2 less[NT], l[NT];  // minus the references; the weights' sums
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -737,9 +739,8 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) o[i][nt][k] = 0.f;
+                for (int k = 0; k < 2; ++k) o[i][nt][k] = rmsn::f2(0.f, 0.f);
         }
-        float vref = kTinyScale, rv = 1.f / kTinyScale;  // O is in units of vref / kLift
 
         for (; mine < seg_end; mine += W) {
             cp_wait<3>();  // K and the scales; behind them V, and the next step's both
@@ -826,10 +827,9 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                     }
             }
             F2 kc[KT][NT], e[KT][NT][2];
-            float top = -INFINITY, vmax = vref;
+            float top = -INFINITY;
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
-                vmax = fmaxf(vmax, vs[k]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     kc[k][nt] = rmsn::mul2(rmsn::f2(ks[k], ks[k]), cs[nt]);
@@ -842,9 +842,8 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                     }
                 }
             }
-            if (__any_sync(0xFFFFFFFFu, top > kSlack) || vmax > vref) {
+            if (__any_sync(0xFFFFFFFFu, top > kSlack)) {
                 // new references; what was summed so far follows them
-                const float vr = vref / vmax;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float to[2], was[2], keep[2];
@@ -865,19 +864,18 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                         keep[x] = exp2a(-was[x] - to[x]);
                     }
                     less[nt] = rmsn::f2(-to[0], -to[1]);
-                    l[nt] = rmsn::mul2(l[nt], rmsn::f2(keep[0], keep[1]));
+                    const F2 keep2 = rmsn::f2(keep[0], keep[1]);
+                    l[nt] = rmsn::mul2(l[nt], keep2);
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) o[i][nt][x] *= keep[x & 1] * vr;
+                        for (int x = 0; x < 2; ++x) o[i][nt][x] = rmsn::mul2(o[i][nt][x], keep2);
 #pragma unroll
                     for (int k = 0; k < KT; ++k)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             e[k][nt][h] = rmsn::fma2(rmsn::f2(s[k][nt][2 * h], s[k][nt][2 * h + 1]), kc[k][nt], less[nt]);
                 }
-                vref = vmax;
-                rv = 1.f / vmax;
             }
 
             // weights; P^T as the second product's operand
@@ -905,8 +903,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
             }
 #pragma unroll
             for (int k = 0; k < KT; ++k) {
-                const float f = vs[k] * rv * kLift;
-                const F2 f2 = rmsn::f2(f, f);
+                const F2 lift = rmsn::f2(kLift, kLift);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -914,7 +911,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                         const F2 w = rmsn::f2(p[k][nt][2 * h], p[k][nt][2 * h + 1]);
                         float lo, hi;
                         l[nt] = rmsn::add2(l[nt], w);
-                        rmsn::f2split(rmsn::mul2(w, f2), lo, hi);
+                        rmsn::f2split(rmsn::mul2(w, lift), lo, hi);
                         pb[k][nt][h] = rmsn::pack_f16x2(lo, hi);
                     }
             }
@@ -937,10 +934,14 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                     }
                     nan = __any_sync(0xFFFFFFFFu, nan);
                 }
+                // O's unit is 1: the scale takes the lift back (it stays exact
+                // down to 2^-118; below, it keeps 16 bits)
+                const float f = vs[k] * (1.f / kLift);
                 if (nan) {
-                    add_tile<C>(o, pb[k], see[k], vt);
+                    add_tile<C>(o, pb[k], see[k], vt, f);
                     continue;
                 }
+                const F2 f2 = rmsn::f2(f, f);
                 uint32_t pt[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -979,8 +980,14 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                         const uint32_t b2 = e4m3x2_to_f16x2(hi23), b3 = e4m3x2_to_f16x2(hi23 >> 16);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(o[cj * 8 + 2 * i][nt], a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
-                            mma16816(o[cj * 8 + 2 * i + 1][nt], b0, b1, b2, b3, pt[nt][0], pt[nt][1]);
+                            float u[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+                            mma16816(u[0], a0, a1, a2, a3, pt[nt][0], pt[nt][1]);
+                            mma16816(u[1], b0, b1, b2, b3, pt[nt][0], pt[nt][1]);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                F2& y = o[cj * 8 + 2 * i + (x >> 1)][nt][x & 1];
+                                y = rmsn::fma2(rmsn::f2(u[x >> 1][2 * (x & 1)], u[x >> 1][2 * (x & 1) + 1]), f2, y);
+                            }
                         }
                     }
                 }
@@ -998,7 +1005,6 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 
         const bool last = seg_end >= count;
         const bool whole = a.split > 0 ? a.split == 1 : cur == c_first && seg_end == row_end;
-        const float unit = vref / kLift;
         float* part = part_of<C>(a, blockIdx.x, cur == 0 ? 0 : 1);
         if (threadIdx.x == 0 && last && a.split == 0) {
             Cut* cut = cut_of(a, blockIdx.x);
@@ -1054,9 +1060,13 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 #pragma unroll
                     for (int i = 0; i < MT; i += 2) {
                         const int d = D == 64 ? g * 8 + 2 * i : (g + 8 * (i / 8)) * 16 + 2 * (i % 8);
+                        float y[4][2];  // dims d to d + 3 of both columns
+                        rmsn::f2split(o[i][nt][0], y[0][0], y[0][1]);
+                        rmsn::f2split(o[i][nt][1], y[1][0], y[1][1]);
+                        rmsn::f2split(o[i + 1][nt][0], y[2][0], y[2][1]);
+                        rmsn::f2split(o[i + 1][nt][1], y[3][0], y[3][1]);
                         *reinterpret_cast<float4*>(jr + unit_at(d)) =
-                            make_float4(o[i][nt][x] * unit, o[i][nt][2 + x] * unit,
-                                        o[i + 1][nt][x] * unit, o[i + 1][nt][2 + x] * unit);
+                            make_float4(y[0][x], y[1][x], y[2][x], y[3][x]);
                     }
                 }
             }

@@ -1,0 +1,154 @@
+"""GPU tests of the attention path where values, masks and work sharing meet:
+value scales far apart, scores beyond fp32's whole numbers, windows on the
+shared line, two launches a call under streams, graphs and programmatic
+launches.  The bound of a result is its own here: it counts only what a right
+kernel may lose on the tokens that the query sees."""
+import math
+
+import pytest
+import torch
+
+import attn_ref as ref
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def rn():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from residual_add_rmsnorm_vec_gb300 import build
+
+    build.build()
+    import residual_add_rmsnorm_vec_gb300 as p
+
+    torch.cuda.set_device(0)
+    p.rmsattn_read_status(clear=True)
+    yield p
+    assert p.rmsattn_read_status() == 0
+
+
+def rand(shape, seed, dtype=torch.float32):
+    return torch.randn(shape, generator=torch.Generator().manual_seed(seed)).to(dtype)
+
+
+def make_cache(rn, t):
+    return rn.KVCache(t["k"], t["v"], t["k_scale"], t["v_scale"])
+
+
+def widened(table, tokens, page):
+    """The table with bad pages behind it, up to `tokens` tokens a row."""
+    wide = torch.full((table.shape[0], tokens // page), -1, dtype=torch.int32, device=table.device)
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
+def workspace(rn, q, Hk, table, page, window=0, sinks=0):
+    """Bytes of workspace of a call: 0 where clusters take the rows."""
+    B, n, Hq, D = q.shape
+    return rn.load_attn().rmsattn_kv_attention_workspace(B, n, Hq, Hk, D, table.shape[1] * page, window, sinks)
+
+
+def attend(q, t, table, lengths, scale, window=0, sinks=0, more=0.0):
+    """(out, bound) in fp64, [B, n, Hq, D].
+
+    With u = 2^-24: a score is D products of exact factors in fp32 sums (2 u a
+    term where a tensor-core sum truncates) and four roundings of its own size;
+    a weight has that, exp2's 2 ulp, and a rounding to fp16: half a step (2^-11
+    of it), or, below fp16's normal range, at most 2^-33 of the row's largest
+    weight and at most itself; its sums take a rounding for every 16 tokens and
+    the joins.  more: a relative error of every term beside these."""
+    B, n, Hq, D = q.shape
+    Hk, page = t["k"].shape[1:3]
+    G = Hq // Hk
+    out = torch.zeros((B, n, Hq, D), dtype=torch.float64, device=q.device)
+    bound = torch.zeros_like(out)
+    for b, L in enumerate(lengths.tolist()):
+        for i in range(n):
+            pos = L - n + i
+            j = torch.arange(max(0, pos + 1), device=q.device)
+            if window:
+                j = j[(j > pos - window) | (j < sinks)]
+            if not j.numel():
+                continue
+            pg, at = table[b].long()[j // page], j % page
+            for h in range(Hk):
+                k = ref.e4m3(t["k"][pg, h, at]) * t["k_scale"][pg, h, at // 16].double()[:, None]
+                v = ref.e4m3(t["v"][pg, h, at]) * t["v_scale"][pg, h, at // 16].double()[:, None]
+                qq = q[b, i, h * G:(h + 1) * G].double()
+                s = qq @ k.T * scale
+                p = torch.softmax(s, -1)
+                ds = float((qq.abs() @ k.abs().T).max()) * abs(scale) * (2 * D + 8) * ref.U + float(s.abs().max()) * 4 * ref.U
+                rel = 2.0 ** -11 + 2 * (ds + 4 * ref.U) + (2 * j.numel() / 16 + 64) * 2 * ref.U + more
+                lost = torch.minimum(p, 2.0 ** -33 * p.amax(-1, keepdim=True)) @ v.abs()
+                heads = slice(h * G, (h + 1) * G)
+                out[b, i, heads] = p @ v
+                bound[b, i, heads] = rel * (p @ v.abs()) + lost
+    half = ref.HALF[q.dtype]
+    return out, bound + half * (out.abs() + bound) + ref.TINY[q.dtype]
+
+
+def within(got, want, bound):
+    off = (got.double() - want).abs()
+    assert bool((off <= bound).all()), f"{float((off / bound).nan_to_num(9e9).max())} of the bound"
+
+
+# ---------------------------------------------------------------- value scales
+
+HOW = {"rows": 0, "line": 40000}  # tokens of a table's row; 0: as the sequence needs
+
+
+def case(D, L, n, dtype="bf16", page=16, Hk=2, Hq=8, how="rows"):
+    pages = -(-L // page)
+    t = ref.random_cache(pages, Hk, page, D, 5, "cuda", spread=False)
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(2)).to(torch.int32)[None].cuda()
+    q = rand((1, n, Hq, D), 3, DT[dtype]).cuda()
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    return t, table, widened(table, HOW[how], page) if HOW[how] else table, q, lens
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("how", HOW)
+@pytest.mark.parametrize("bits", [20, 26, 32, 40])
+@pytest.mark.parametrize("below", [30.0, 400.0])
+def test_a_large_value_scale_of_no_weight_coarsens_nothing(rn, D, how, bits, below):
+    # one block of 16 tokens: values 2^bits times the rest's, scores `below` (nats) under them
+    t, table, given, q, lens = case(D, 700, 1, how=how)
+    q[..., 0] = 8.0
+    first = int(table[0, 3])
+    t["k"][:, :, :, 0] = 0
+    t["k"][first, :, :, 0] = 0xF8  # -256
+    t["k_scale"][first] = below * math.sqrt(D) / (8 * 256)
+    t["k"][first, :, :, 1:] = 0
+    t["v_scale"][first] *= 2.0 ** bits
+    assert (workspace(rn, q, 2, given, 16) > 0) == (how == "line")
+    got = rn.kv_cache_attention(q, make_cache(rn, t), given, lens)
+    within(got, *attend(q, t, table, lens, 1 / math.sqrt(D)))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("bits", [26, 34])
+def test_a_large_value_scale_seen_by_another_query_alone(rn, D, bits):
+    # the window of the first drafted query reaches one token, with a large value scale, that the
+    # window of the second does not
+    n, L, window = 2, 420, 420 - 2 + 1 - 47  # reaches from token 47, the last of its block
+    t, table, given, q, lens = case(D, L, n)
+    t["v_scale"][int(table[0, 2])] *= 2.0 ** bits
+    got = rn.kv_cache_attention(q, make_cache(rn, t), given, lens, window=window)
+    want, bound = attend(q, t, table, lens, 1 / math.sqrt(D), window)
+    within(got[:, 1], want[:, 1], bound[:, 1])
+    within(got, want, bound)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("low,high", [(-20, 20), (-126, -100), (60, 90)])
+def test_value_scales_of_any_size(rn, D, n, low, high):
+    t, table, given, q, lens = case(D, 333, n)
+    e = torch.randint(low, high + 1, t["v_scale"].shape, generator=torch.Generator().manual_seed(1))
+    part = torch.rand(e.shape, generator=torch.Generator().manual_seed(4))
+    t["v_scale"] = (torch.exp2(e.double()).float() * (1 + part)).cuda()
+    got = rn.kv_cache_attention(q, make_cache(rn, t), given, lens)
+    # scales below 2^-118 lose up to 8 of their 24 bits on their way into the sum
+    within(got, *attend(q, t, table, lens, 1 / math.sqrt(D), more=2.0 ** -16 if low < -118 else 0.0))

@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                         rmsn::f2split(kc[k][nt], c[0], c[1]);
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
-                            to[x] = max3(to[x], s[k][nt][x] * c[x], s[k][nt][2 + x] * c[x]);
+                            to[x] = max3(to[x], __fmul_rn(s[k][nt][x], c[x]), __fmul_rn(s[k][nt][2 + x], c[x]));
                     }
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
@@ -870,11 +870,18 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) o[i][nt][x] = rmsn::mul2(o[i][nt][x], keep2);
+                    // from the rounded products, as the reference was taken: the
+                    // largest then weighs 1 where scores are beyond 2^28, too
+                    // (what a product rounds off there is a large exponent)
 #pragma unroll
-                    for (int k = 0; k < KT; ++k)
+                    for (int k = 0; k < KT; ++k) {
+                        float c[2];
+                        rmsn::f2split(kc[k][nt], c[0], c[1]);
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            e[k][nt][h] = rmsn::fma2(rmsn::f2(s[k][nt][2 * h], s[k][nt][2 * h + 1]), kc[k][nt], less[nt]);
+                            e[k][nt][h] = rmsn::f2(__fsub_rn(__fmul_rn(s[k][nt][2 * h], c[0]), to[0]),
+                                                   __fsub_rn(__fmul_rn(s[k][nt][2 * h + 1], c[1]), to[1]));
+                    }
                 }
             }
 

@@ -152,3 +152,34 @@ def test_value_scales_of_any_size(rn, D, n, low, high):
     got = rn.kv_cache_attention(q, make_cache(rn, t), given, lens)
     # scales below 2^-118 lose up to 8 of their 24 bits on their way into the sum
     within(got, *attend(q, t, table, lens, 1 / math.sqrt(D), more=2.0 ** -16 if low < -118 else 0.0))
+
+
+# ---------------------------------------------------------------- scores
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("how", HOW)
+@pytest.mark.parametrize("top", [1e7, 3e9, -3e9, 1e15, 1e30])
+def test_scores_beyond_whole_numbers_of_fp32(rn, D, n, how, top):
+    # Scores that fp32 holds to hundreds and more: the largest must still weigh 1.  The 16 tokens of a
+    # block have equal scores, the blocks' lie at least 0.05 of their size apart: a mean of 16 values.
+    L = 160
+    t, table, given, q, lens = case(D, L + n - 1, n, how=how)
+    q[...] = 1.0 / 3
+    t["k"][...] = 0x39  # 1.125
+    t["k_scale"][...] = 1e-9  # of the drafted tokens behind the first query's position
+    order = [(7 * i) % 10 for i in range(10)]  # up and down
+    for i in range(10):
+        t["k_scale"][int(table[0, i])] = 1.0 + 0.137 * order[i]
+    scale = top / (float(q[0, 0, 0, 0]) * 1.125 * D)
+    got = rn.kv_cache_attention(q, make_cache(rn, t), given, lens, scale=scale)
+    page = int(table[0, order.index(9 if top > 0 else 0)])
+    v = ref.e4m3(t["v"][page]) * t["v_scale"][page].double()[:, :, None]  # [Hk, 16, D]
+    want = v.mean(1).repeat_interleave(4, 0)
+    # weights of 1 are exact; a sum of 16 terms (2 u a term), a multiply-add, the joins and a division: 64 u
+    bound = v.abs().mean(1).repeat_interleave(4, 0) * 64 * ref.U
+    bound = bound + ref.HALF[q.dtype] * (want.abs() + bound)
+    within(got[0, 0], want, bound)
+    if top > 0:
+        within(got[0], want.expand(n, -1, -1), bound.expand(n, -1, -1))
+    assert bool(torch.isfinite(got).all())

@@ -42,22 +42,50 @@ def _other(device, stream):
         yield stream.cuda_stream, (lambda t: t.record_stream(caller)) if stream != caller else None
 
 
-class RopeTable:
+class _Fixed:
+    """Attributes are set once, by ``_set``: what a call reads beside the
+    tensors (their shapes, addresses, device) cannot fall out of step with them."""
+
+    __slots__ = ()
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"{type(self).__name__}.{name} cannot be changed: make another")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{type(self).__name__}.{name} cannot be removed")
+
+    def _set(self, **values):
+        for name, value in values.items():
+            object.__setattr__(self, name, value)
+
+
+class RopeTable(_Fixed):
     """Frequencies of the rotary pairs: ``turns`` (int64 bit patterns of 64-bit
     fractions of a turn per position), ``axis`` (int32, the axis whose position
-    turns the pair), both [rot_dim / 2] on the device; made by ``rope_table``."""
+    turns the pair), both [rot_dim / 2] on the device; made by ``rope_table``.
+    The attributes are fixed."""
 
-    __slots__ = ("turns", "axis", "rot_dim", "n_axes", "index", "turns_ptr", "axis_ptr")
+    __slots__ = ("turns", "axis", "rot_dim", "n_axes", "index")
 
     def __init__(self, turns: torch.Tensor, axis: torch.Tensor, n_axes: int):
         if turns.dim() != 1:
             raise ValueError("turns must be [rot_dim / 2]")
-        _check("turns", turns, (turns.numel(),), (torch.int64,))
-        _check("axis", axis, (turns.numel(),), (torch.int32,), turns.device)
-        self.turns, self.axis = turns, axis
-        self.rot_dim, self.n_axes = 2 * turns.numel(), int(n_axes)
-        self.index = turns.get_device()
-        self.turns_ptr, self.axis_ptr = turns.data_ptr(), axis.data_ptr()
+        self._set(turns=turns, axis=axis, rot_dim=2 * turns.numel(), n_axes=int(n_axes),
+                  index=turns.get_device())
+        self._pointers()
+
+    def _pointers(self):
+        """Addresses of turns and axis, which are still what they were made as
+        (a tensor can be given other data in place)."""
+        pairs = (self.rot_dim // 2,)
+        _check("turns", self.turns, pairs, (torch.int64,))
+        _check("axis", self.axis, pairs, (torch.int32,), self.turns.device)
+        if self.turns.get_device() != self.index:
+            raise ValueError(f"the table was moved to {self.turns.device}")
+        return self.turns.data_ptr(), self.axis.data_ptr()
+
+    def __reduce__(self):
+        return RopeTable, (self.turns, self.axis, self.n_axes)
 
 
 def rope_table(rot_dim: int, *, base: float = 10000.0, sections=None, axis=None, inv_freq=None,
@@ -226,7 +254,7 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
         None if q_weight is None else q_weight.data_ptr(),
         None if k_weight is None else k_weight.data_ptr(),
         None if q is None else q_out.data_ptr(), None if k is None else k_out.data_ptr(),
-        positions.data_ptr(), pstride[0] if n_axes > 1 else T, table.turns_ptr, table.axis_ptr, T,
+        positions.data_ptr(), pstride[0] if n_axes > 1 else T, *table._pointers(), T,
         hq, hk, head_dim, rot, n_axes, qs, ks, qos, kos, eps, weight_offset, flags,
         _raw_stream(index))
     if st:
@@ -234,19 +262,30 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, positions: torc
     return q_out, k_out
 
 
-class KVCache:
+class KVCache(_Fixed):
     """A paged cache of keys and values in E4M3 codes with one fp32 scale for
     every block of 16 tokens and head (``rmsattn_cache``): k and v are
     [n_pages, n_kv_heads, page_size, head_dim] uint8 (or float8_e4m3fn), the
     scales [n_pages, n_kv_heads, page_size / 16]; a token's value is code *
     scale.  The tensors are the caller's; pages may be strided (all layers of
-    a model in one tensor), the rest of each tensor is contiguous."""
+    a model in one tensor), the rest of each tensor is contiguous.  The
+    attributes are fixed; a tensor that was given other memory in place
+    (``resize_`` of its storage, ``set_``) is looked at again by the next call."""
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "n_pages", "n_kv_heads", "page_size", "head_dim",
-                 "device", "index", "_c", "_ref", "_addr")
+                 "device", "index", "_c", "_ref", "_addr", "_tensors")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
                  v_scale: torch.Tensor):
+        c = self._described(k, v, k_scale, v_scale)
+        self._set(k=k, v=v, k_scale=k_scale, v_scale=v_scale, n_pages=c.n_pages,
+                  n_kv_heads=c.n_kv_heads, page_size=c.page_size, head_dim=c.head_dim, device=k.device,
+                  index=k.get_device(), _c=c, _ref=ctypes.byref(c), _addr=ctypes.addressof(c),
+                  _tensors=(k, v, k_scale, v_scale))
+
+    @staticmethod
+    def _described(k, v, k_scale, v_scale):
+        """The C ABI's description of the tensors, checked."""
         if k.dim() != 4:
             raise ValueError("k must be [n_pages, n_kv_heads, page_size, head_dim]")
         pages, heads, page, dim = k.shape
@@ -264,6 +303,9 @@ class KVCache:
                 raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
             if t.device != k.device:
                 raise ValueError(f"{name} must be on {k.device}, got {t.device}")
+            last = sum((size - 1) * step for size, step in zip(t.shape, t.stride())) + 1 if t.numel() else 0
+            if (t.storage_offset() + last) * t.element_size() > t.untyped_storage().nbytes():
+                raise ValueError(f"{name} is larger than its storage")
             # each page contiguous; pages any stride apart
             inner = 1
             for size, step in zip(want[:0:-1], t.stride()[:0:-1]):
@@ -276,14 +318,24 @@ class KVCache:
                 raise ValueError(f"{name}: each page must be contiguous")
         if pages > 1 and (k.stride(0) != v.stride(0) or k_scale.stride(0) != v_scale.stride(0)):
             raise ValueError("k and v need the same page stride, and so do their scales")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = pages, heads, page, dim
-        self.device, self.index = k.device, k.get_device()
-        self._c = _al.RmsattnCache(
+        return _al.RmsattnCache(
             k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages,
             k.stride(0) if pages > 1 else heads * page * dim,
             k_scale.stride(0) if pages > 1 else shape[1] * shape[2], heads, page, dim, 0)
-        self._ref, self._addr = ctypes.byref(self._c), ctypes.addressof(self._c)
+
+    def __reduce__(self):
+        return KVCache, self._tensors
+
+    def _current(self):
+        """The description as the C ABI takes it, where the tensors lie now."""
+        c, at = self._c, tuple(t.data_ptr() for t in self._tensors)
+        if at != (c.k or 0, c.v or 0, c.k_scale or 0, c.v_scale or 0):
+            now = self._described(*self._tensors)
+            if (tuple(self.k.shape) != (self.n_pages, self.n_kv_heads, self.page_size, self.head_dim)
+                    or self.k.device != self.device):
+                raise ValueError("the cache's tensors have another shape or device than it was made for")
+            ctypes.memmove(self._addr, ctypes.addressof(now), ctypes.sizeof(now))
+        return self._ref
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int,
@@ -330,7 +382,7 @@ def kv_cache_append_(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_tab
     grows and the block's older codes are re-encoded.
     """
     if stream is None and (_al._fast or _al.load_fast()).kv_append(
-            k, v, cache._addr, cache.index, block_table, lengths, cu_seqlens, pdl):
+            k, v, cache._addr, cache._tensors, cache.index, block_table, lengths, cu_seqlens, pdl):
         return cache
     hk, ks = _heads("k", k, cache.head_dim)
     hv, vs = _heads("v", v, cache.head_dim)
@@ -357,7 +409,7 @@ def kv_cache_append_(cache: KVCache, k: torch.Tensor, v: torch.Tensor, block_tab
         with _other(cache.device, stream):
             return kv_cache_append_(cache, k, v, block_table, lengths, cu_seqlens, pdl=pdl)
     st = _al.load_attn().rmsattn_kv_append(
-        cache._ref, k.data_ptr(), v.data_ptr(), ks, vs, block_table.data_ptr(), stride, width,
+        cache._current(), k.data_ptr(), v.data_ptr(), ks, vs, block_table.data_ptr(), stride, width,
         lengths.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(), T, n,
         flags | _lib.RMSN_PDL if pdl else flags, _raw_stream(index))
     if st:
@@ -398,7 +450,7 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     """
     if stream is None:
         done = (_al._fast or _al.load_fast()).kv_attention(
-            q, cache._addr, cache.index, block_table, lengths, scale, window, sinks, out, pdl)
+            q, cache._addr, cache._tensors, cache.index, block_table, lengths, scale, window, sinks, out, pdl)
         if done is not None:
             return done
     shape, dt, index = q.shape, q.dtype, cache.index
@@ -447,7 +499,7 @@ def kv_cache_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tenso
     ws = torch.empty(need, dtype=torch.uint8, device=cache.device) if need else None
     flags = _IN[dt]
     st = lib.rmsattn_kv_attention(
-        q.data_ptr(), cache._ref, block_table.data_ptr(), stride, width, lengths.data_ptr(),
+        q.data_ptr(), cache._current(), block_table.data_ptr(), stride, width, lengths.data_ptr(),
         out.data_ptr(), qs, os, B, n, H, 1.0 / math.sqrt(D) if scale is None else scale, window,
         sinks, ws.data_ptr() if need else None, need, flags | _lib.RMSN_PDL if pdl else flags, _raw_stream(index))
     if st:

@@ -82,25 +82,34 @@ bool token_stride(const Tensor& t, int64_t n, int64_t* step) {
     return true;
 }
 
-const rmsattn_cache* cache_at(PyObject* address) {
-    return static_cast<const rmsattn_cache*>(PyLong_AsVoidPtr(address));
+// The cache described at `address`, if its four tensors still lie where the
+// description says (one may have been given other memory since).
+const rmsattn_cache* cache_at(PyObject* address, PyObject* tensors) {
+    const rmsattn_cache* c = static_cast<const rmsattn_cache*>(PyLong_AsVoidPtr(address));
+    if (!c || !PyTuple_Check(tensors) || PyTuple_GET_SIZE(tensors) != 4) return nullptr;
+    const void* const at[4] = {c->k, c->v, c->k_scale, c->v_scale};
+    for (int i = 0; i < 4; ++i) {
+        const Tensor* t = tensor(PyTuple_GET_ITEM(tensors, i));
+        if (!t || t->const_data_ptr() != at[i]) return nullptr;
+    }
+    return c;
 }
 
-// (q, cache, index, block_table, lengths, scale, window, sinks, out, pdl) -> out
+// (q, cache, tensors, index, block_table, lengths, scale, window, sinks, out, pdl) -> out
 PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t count) {
     try {
-        const Tensor *q = count == 10 ? tensor(a[0]) : nullptr, *table = q ? tensor(a[3]) : nullptr,
-                     *lengths = table ? tensor(a[4]) : nullptr;
-        if (!lengths || !PyLong_Check(a[6]) || !PyLong_Check(a[7]) || !PyBool_Check(a[9]) || (a[5] != Py_None && !PyFloat_Check(a[5])))
+        const Tensor *q = count == 11 ? tensor(a[0]) : nullptr, *table = q ? tensor(a[4]) : nullptr,
+                     *lengths = table ? tensor(a[5]) : nullptr;
+        if (!lengths || !PyLong_Check(a[7]) || !PyLong_Check(a[8]) || !PyBool_Check(a[10]) || (a[6] != Py_None && !PyFloat_Check(a[6])))
             return leave();
-        const rmsattn_cache* cache = cache_at(a[1]);
-        const int64_t index = PyLong_AsLongLong(a[2]), window = PyLong_AsLongLong(a[6]),
-                      sinks = PyLong_AsLongLong(a[7]);
+        const rmsattn_cache* cache = cache_at(a[1], a[2]);
+        const int64_t index = PyLong_AsLongLong(a[3]), window = PyLong_AsLongLong(a[7]),
+                      sinks = PyLong_AsLongLong(a[8]);
         if (PyErr_Occurred()) {
             PyErr_Clear();
             return leave();
         }
-        if (index < 0 || index != c10::cuda::current_device() || !on_device(*q, index)) return leave();
+        if (!cache || index < 0 || index != c10::cuda::current_device() || !on_device(*q, index)) return leave();
         const int64_t d = q->dim();
         if (d != 3 && d != 4) return leave();
         const int64_t B = q->size(0), n = d == 4 ? q->size(1) : 1, H = q->size(d - 2), D = q->size(d - 1);
@@ -111,8 +120,8 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t count) {
         int64_t stride, qs, os = H * D;
         if (!sequences(*table, *lengths, B, index, &stride) || !token_stride(*q, n, &qs)) return leave();
         Tensor out;
-        if (a[8] != Py_None) {
-            const Tensor* o = tensor(a[8]);
+        if (a[9] != Py_None) {
+            const Tensor* o = tensor(a[9]);
             if (!o || !on_device(*o, index) || o->scalar_type() != type || o->sizes() != q->sizes() ||
                 !token_stride(*o, n, &os))
                 return leave();
@@ -127,16 +136,16 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t count) {
         // same stream only, which runs behind the kernels
         Tensor ws;
         if (need > 0) ws = make({need}, at::kByte, index);
-        const double scale = a[5] == Py_None ? 1.0 / std::sqrt((double)D) : PyFloat_AS_DOUBLE(a[5]);
+        const double scale = a[6] == Py_None ? 1.0 / std::sqrt((double)D) : PyFloat_AS_DOUBLE(a[6]);
         const int st = rmsattn_kv_attention(
             q->const_data_ptr(), cache, static_cast<const int32_t*>(table->const_data_ptr()), stride, width,
             static_cast<const int32_t*>(lengths->const_data_ptr()), out.mutable_data_ptr(), qs, os, B, n, H,
             (float)scale, window, sinks, need > 0 ? ws.mutable_data_ptr() : nullptr, need,
-            (uint32_t)dtype_flag(type) | (a[9] == Py_True ? RMSN_PDL : 0u), stream_of(index));
+            (uint32_t)dtype_flag(type) | (a[10] == Py_True ? RMSN_PDL : 0u), stream_of(index));
         if (st != RMSN_OK) return leave();
-        if (a[8] != Py_None) {
-            Py_INCREF(a[8]);
-            return a[8];
+        if (a[9] != Py_None) {
+            Py_INCREF(a[9]);
+            return a[9];
         }
         return THPVariable_Wrap(out);
     } catch (...) {
@@ -145,19 +154,19 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t count) {
     }
 }
 
-// (k, v, cache, index, block_table, lengths, cu_seqlens, pdl) -> True
+// (k, v, cache, tensors, index, block_table, lengths, cu_seqlens, pdl) -> True
 PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t count) {
     try {
-        const Tensor *k = count == 8 ? tensor(a[0]) : nullptr, *v = k ? tensor(a[1]) : nullptr,
-                     *table = v ? tensor(a[4]) : nullptr, *lengths = table ? tensor(a[5]) : nullptr;
-        if (!lengths || !PyBool_Check(a[7])) return leave();
-        const rmsattn_cache* cache = cache_at(a[2]);
-        const int64_t index = PyLong_AsLongLong(a[3]);
+        const Tensor *k = count == 9 ? tensor(a[0]) : nullptr, *v = k ? tensor(a[1]) : nullptr,
+                     *table = v ? tensor(a[5]) : nullptr, *lengths = table ? tensor(a[6]) : nullptr;
+        if (!lengths || !PyBool_Check(a[8])) return leave();
+        const rmsattn_cache* cache = cache_at(a[2], a[3]);
+        const int64_t index = PyLong_AsLongLong(a[4]);
         if (PyErr_Occurred()) {
             PyErr_Clear();
             return leave();
         }
-        if (index < 0 || index != c10::cuda::current_device() || !on_device(*k, index) || !on_device(*v, index))
+        if (!cache || index < 0 || index != c10::cuda::current_device() || !on_device(*k, index) || !on_device(*v, index))
             return leave();
         const int type = dtype_flag(k->scalar_type());
         int64_t hk, ks, hv, vs, stride;
@@ -168,8 +177,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t count) {
         const int64_t T = k->size(0), n = lengths->size(0);
         if (!sequences(*table, *lengths, n, index, &stride)) return leave();
         const int32_t* cu = nullptr;
-        if (a[6] != Py_None) {
-            const Tensor* c = tensor(a[6]);
+        if (a[7] != Py_None) {
+            const Tensor* c = tensor(a[7]);
             if (!c || c->dim() != 1 || c->size(0) != n + 1 || c->scalar_type() != at::kInt ||
                 !on_device(*c, index) || (n && c->stride(0) != 1))
                 return leave();
@@ -181,7 +190,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t count) {
             cache, k->const_data_ptr(), v->const_data_ptr(), ks, vs,
             static_cast<const int32_t*>(table->const_data_ptr()), stride, table->size(1),
             static_cast<const int32_t*>(lengths->const_data_ptr()), cu, T, n,
-            (uint32_t)type | (a[7] == Py_True ? RMSN_PDL : 0u), stream_of(index));
+            (uint32_t)type | (a[8] == Py_True ? RMSN_PDL : 0u), stream_of(index));
         if (st != RMSN_OK) return leave();
         Py_RETURN_TRUE;
     } catch (...) {
@@ -251,11 +260,15 @@ PyObject* qk_rope(PyObject*, PyObject* const* a, Py_ssize_t count) {
             return leave();
         }
         if (!ref->is_cuda() || D < 1) return leave();
-        const int64_t index = ref->get_device(), T = ref->size(0), R = 2 * turns->size(0);
+        const int64_t index = ref->get_device(), T = ref->size(0), R = turns->dim() == 1 ? 2 * turns->size(0) : D + 1;
         const at::ScalarType type = ref->scalar_type();
         int flags = dtype_flag(type);
         if (flags < 0 || index != c10::cuda::current_device() || R > D || !on_device(*turns, index) ||
             !on_device(*axis, index) || !on_device(*pos, index))
+            return leave();
+        // the table is as it was made
+        if (turns->scalar_type() != at::kLong || axis->scalar_type() != at::kInt || axis->dim() != 1 ||
+            axis->size(0) * 2 != R || !turns->is_contiguous() || !axis->is_contiguous())
             return leave();
         Side q, k;
         if (!q.of(a[0], a[12], D, type, T, index) || !k.of(a[1], a[13], D, type, T, index)) return leave();

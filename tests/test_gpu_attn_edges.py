@@ -183,3 +183,34 @@ def test_scores_beyond_whole_numbers_of_fp32(rn, D, n, how, top):
     if top > 0:
         within(got[0], want.expand(n, -1, -1), bound.expand(n, -1, -1))
     assert bool(torch.isfinite(got).all())
+
+
+# ---------------------------------------------------------------- handles
+
+def test_a_cache_whose_tensors_were_given_other_memory(rn):
+    # the next calls read and write where the tensors lie now; the old memory stays as it is
+    t, table, _, q, lens = case(64, 30, 1)
+    cache = make_cache(rn, t)
+    rn.kv_cache_attention(q, cache, table, lens)
+    old = {name: x.detach() for name, x in t.items()}  # keeps the memory
+    was = {name: x.clone() for name, x in old.items()}
+    for name, x in t.items():
+        x.data = torch.empty_like(x).copy_(x)
+    k, v = rand((1, 2, 64), 1, torch.bfloat16).cuda(), rand((1, 2, 64), 2, torch.bfloat16).cuda()
+    rn.kv_cache_append_(cache, k, v, table, lens)
+    for name in t:
+        assert torch.equal(old[name], was[name])
+    for side, x in (("k", k), ("v", v)):
+        ref.check_append(was, t, x, side, table.cpu(), lens.cpu(), None)
+    within(rn.kv_cache_attention(q, cache, table, lens + 1), *attend(q, t, table, lens + 1, 0.125))
+    t["v"].untyped_storage().resize_(0)  # given back
+    with pytest.raises(ValueError):
+        rn.kv_cache_attention(q, cache, table, lens)
+    with pytest.raises(ValueError):
+        rn.kv_cache_append_(cache, k, v, table, lens)
+    table = rn.rope_table(64)
+    x, pos = rand((1, 64), 1).cuda(), torch.ones(1, dtype=torch.int32, device="cuda")
+    rn.qk_norm_rope(x, None, pos, table, head_dim=64)
+    table.axis.data = table.axis.long()
+    with pytest.raises(TypeError):
+        rn.qk_norm_rope(x, None, pos, table, head_dim=64)

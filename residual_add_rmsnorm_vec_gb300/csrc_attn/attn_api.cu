@@ -358,8 +358,11 @@ struct Plan {
 int plan_attend(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_t n_q_heads,
                 int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens, int64_t window,
                 int64_t sinks, Plan* p) {
-    // the most tokens that a row's queries see, borders of steps included
-    if (window > 0 && sinks < kMaxTokens && window + n_queries + sinks + 256 < max_tokens)
+    // the most tokens that a row's queries see, borders of steps included (no
+    // table holds kMaxTokens: beyond that neither limits anything, and the sum
+    // stays within 64 bits)
+    if (window > 0 && window < kMaxTokens && sinks < kMaxTokens &&
+        window + n_queries + sinks + 256 < max_tokens)
         max_tokens = window + n_queries + sinks + 256;
     const int64_t cols = n_q_heads / n_kv_heads * n_queries;
     // A row to a cluster of `split` blocks, or the line?  The host knows the

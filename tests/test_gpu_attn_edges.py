@@ -214,3 +214,23 @@ def test_a_cache_whose_tensors_were_given_other_memory(rn):
     table.axis.data = table.axis.long()
     with pytest.raises(TypeError):
         rn.qk_norm_rope(x, None, pos, table, head_dim=64)
+
+
+# ---------------------------------------------------------------- windows
+
+@pytest.mark.parametrize("window", [2**29 - 1, 2**29, 2**31, 2**62, 2**63 - 257, 2**63 - 256, 2**63 - 1])
+@pytest.mark.parametrize("sinks", [0, 5, 2**62, 2**63 - 1])
+def test_a_window_wider_than_any_row_is_planned_as_none(rn, window, sinks):
+    # a row of 131072 tokens belongs on the shared line, whose workspace it needs
+    q = torch.empty((1, 1, 32, 128), dtype=torch.bfloat16)
+    table = torch.empty((1, 2048), dtype=torch.int32)
+    none = workspace(rn, q, 8, table, 64)
+    assert none > 0 and workspace(rn, q, 8, table, 64, window, sinks) == none
+
+
+def test_a_window_of_the_largest_integer(rn):
+    t, table, given, q, lens = case(128, 300, 2, how="line")
+    want = rn.kv_cache_attention(q, make_cache(rn, t), given, lens)
+    got = rn.kv_cache_attention(q, make_cache(rn, t), given, lens, window=2**63 - 1)
+    assert torch.equal(got, want)
+    within(got, *attend(q, t, table, lens, 1 / math.sqrt(128)))

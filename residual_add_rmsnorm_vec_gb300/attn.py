@@ -11,6 +11,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import decimal
+import functools
 import math
 
 import torch
@@ -88,12 +90,36 @@ class RopeTable(_Fixed):
         return RopeTable, (self.turns, self.axis, self.n_axes)
 
 
+@functools.lru_cache(maxsize=16)
+def _pi(bits: int) -> int:
+    """pi * 2^bits to within a few units (Machin: 16 atan(1/5) - 4 atan(1/239))."""
+    def atan_of_one_over(n):
+        term = total = (1 << bits) // n
+        k = 1
+        while term:
+            term //= -n * n
+            k += 2
+            total += term // k
+        return total
+
+    return 16 * atan_of_one_over(5) - 4 * atan_of_one_over(239)
+
+
+def _turn_bits(num: int, den: int) -> int:
+    """num / den radians in turns: the fraction of a turn, rounded to 64 bits."""
+    guard = 32  # beyond the whole turns and the 64 bits: far more than _pi is off by
+    bits = max(0, abs(num).bit_length() - den.bit_length() + 1) + 64 + guard
+    num, den = num << (63 + bits), den * (_pi(bits + guard) >> guard)
+    return (2 * num + den) // (2 * den) % 2**64
+
+
 def rope_table(rot_dim: int, *, base: float = 10000.0, sections=None, axis=None, inv_freq=None,
                device="cuda") -> RopeTable:
     """Table of ``rot_dim / 2`` rotary pairs.
 
     Pair p turns by ``inv_freq[p]`` radians per position, by default
-    ``base ** (-2 p / rot_dim)``.  ``sections`` gives consecutive pairs to the
+    ``base ** (-2 p / rot_dim)``; the table holds either to the nearest 2^-64
+    of a turn.  ``sections`` gives consecutive pairs to the
     axes (time, height, width, ...; they add up to rot_dim / 2); ``axis`` names
     each pair's axis instead; neither: one axis.
     """
@@ -113,16 +139,25 @@ def rope_table(rot_dim: int, *, base: float = 10000.0, sections=None, axis=None,
             raise ValueError(f"axis must name {pairs} axes")
         n_axes = max(axes, default=0) + 1
     if inv_freq is None:
+        base = float(base)
         if not base > 0:
             raise ValueError("base must be positive")
-        freqs = [float(base) ** (-2.0 * p / rot_dim) for p in range(pairs)]
+        b = decimal.Decimal(base)
+        # 60 digits behind the point of the largest: a product for each pair
+        # loses none that count
+        with decimal.localcontext(decimal.Context(prec=60 + max(0, -b.adjusted()))):
+            step, freqs = b ** (decimal.Decimal(-2) / max(rot_dim, 1)), [decimal.Decimal(1)] * min(pairs, 1)
+            while len(freqs) < pairs:
+                freqs.append(freqs[-1] * step)
+        freqs = [f.as_integer_ratio() for f in freqs]
     else:
         freqs = [float(f) for f in inv_freq]
         if len(freqs) != pairs:
             raise ValueError(f"inv_freq must hold {pairs} values")
-    if not all(math.isfinite(f) for f in freqs):
-        raise ValueError("frequencies must be finite")
-    bits = [int(math.ldexp(f / (2.0 * math.pi), 64)) % 2**64 for f in freqs]
+        if not all(math.isfinite(f) for f in freqs):
+            raise ValueError("frequencies must be finite")
+        freqs = [f.as_integer_ratio() for f in freqs]
+    bits = [_turn_bits(*f) for f in freqs]
     bits = [b - 2**64 if b >= 2**63 else b for b in bits]
     return RopeTable(torch.tensor(bits, dtype=torch.int64, device=device),
                      torch.tensor(axes, dtype=torch.int32, device=device), n_axes)

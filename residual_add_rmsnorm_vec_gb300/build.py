@@ -6,7 +6,9 @@ the ``rmsnorm_*`` symbols of ``include/rmsnorm.h``.  The CUDA runtime is
 linked statically, so the library needs nothing but the driver at run time.
 The attention-path operators (``csrc_attn``) are built the same way into a
 library of their own (``_build/librmsnorm_attn_gb300.so``, the ``rmsattn_*``
-symbols of ``include/rmsnorm_attn.h``).
+symbols of ``include/rmsnorm_attn.h``).  Both need nvcc alone.  The module that
+marshals the attention path's Python calls is compiled against torch and
+Python; without torch there is nothing to marshal and it is left out.
 
 ``build(checked=True)`` makes the bounds-checked debug library
 (``_build/librmsnorm_gb300_checked.so``, compiled with -DRMSNORM_BOUNDS_CHECK):
@@ -71,11 +73,15 @@ def _inputs() -> list[str]:
             + [os.path.abspath(__file__)])
 
 
-def _fast_command(out: str) -> list[str]:
+def _torch_dir() -> str | None:
+    """Where torch is installed, if it is."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
+def _fast_command(torch_dir: str, out: str) -> list[str]:
     """g++ of the marshalling module: torch's and Python's headers, host code
     only; torch's own libraries are loaded before it."""
-    spec = importlib.util.find_spec("torch")
-    torch_dir = spec.submodule_search_locations[0]
     inc = os.path.join(torch_dir, "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
@@ -85,7 +91,9 @@ def _fast_command(out: str) -> list[str]:
 
 
 def up_to_date(checked: bool = False) -> bool:
-    outs = [CHECKED_PATH] if checked else [LIB_PATH, ATTN_PATH, FAST_PATH, HOSTCOST_PATH]
+    outs = [CHECKED_PATH] if checked else [LIB_PATH, ATTN_PATH, HOSTCOST_PATH]
+    if not checked and _torch_dir():
+        outs.append(FAST_PATH)
     if not all(os.path.exists(o) for o in outs):
         return False
     t = min(os.path.getmtime(o) for o in outs)
@@ -116,21 +124,19 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None,
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
-    def compile_fast():
+    def compile_fast(torch_dir):
         # the C ABI's symbols stay undefined: that library is loaded before it
         tmp = FAST_PATH + f".tmp{os.getpid()}"
-        cmd = _fast_command(tmp)
-        r = subprocess.run(cmd, capture_output=True, text=True)
+        r = subprocess.run(_fast_command(torch_dir, tmp), capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"g++ failed on {os.path.basename(FAST_SRC)}:\n{r.stderr}")
-        return tmp
+        os.replace(tmp, FAST_PATH)
 
     n = jobs or min(len(srcs), os.cpu_count() or 1)
     with ThreadPoolExecutor(max(1, n)) as ex:
-        fast = None if checked else ex.submit(compile_fast)
+        torch_dir = None if checked else _torch_dir()
+        fast = ex.submit(compile_fast, torch_dir) if torch_dir else None
         logs = list(ex.map(compile_one, zip(srcs, objs)))
-        if fast is not None:
-            os.replace(fast.result(), FAST_PATH)
     if verbose:
         for src, log in zip(srcs, logs):
             sys.stderr.write(f"== {os.path.basename(src)}\n{log}")
@@ -152,6 +158,8 @@ def build(force: bool = False, verbose: bool = False, jobs: int | None = None,
     if r.returncode != 0:
         raise RuntimeError(f"host-cost harness failed to build:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, HOSTCOST_PATH)
+    if fast is not None:
+        fast.result()  # raises if it failed: the C libraries are there all the same
     return LIB_PATH
 
 

@@ -1,0 +1,69 @@
+"""CPU tests of the build's parts, with compilers that only write their output
+file: what is built without torch, and what is rebuilt when."""
+import os
+import stat
+
+import pytest
+
+from residual_add_rmsnorm_vec_gb300 import build as b
+
+COMPILER = """#!/bin/sh
+echo "$@" >> {log}
+case "$*" in *{failing}*) echo refused >&2; exit 1;; esac
+while [ $# -gt 1 ]; do [ "$1" = -o ] && echo built > "$2"; shift; done
+exit 0
+"""
+
+
+@pytest.fixture
+def fake(tmp_path, monkeypatch):
+    """A build folder of its own; set(failing) makes commands with that text fail."""
+    def compilers(failing="no such text"):
+        for name in ("nvcc", "g++"):
+            path = tmp_path / name
+            path.write_text(COMPILER.format(log=tmp_path / "log", failing=failing.replace(" ", "\\ ")))
+            path.chmod(path.stat().st_mode | stat.S_IXUSR)
+
+    compilers()
+    monkeypatch.setenv("PATH", f"{tmp_path}{os.pathsep}{os.environ['PATH']}")
+    monkeypatch.setenv("NVCC", str(tmp_path / "nvcc"))
+    out = tmp_path / "out"
+    for name in ("LIB_PATH", "CHECKED_PATH", "ATTN_PATH", "FAST_PATH", "HOSTCOST_PATH"):
+        monkeypatch.setattr(b, name, str(out / os.path.basename(getattr(b, name))))
+    monkeypatch.setattr(b, "BUILD_DIR", str(out))
+    monkeypatch.setattr(b, "log", lambda: (tmp_path / "log").read_text(), raising=False)
+    return compilers
+
+
+def without_torch(monkeypatch):
+    find = b.importlib.util.find_spec
+    monkeypatch.setattr(b.importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+
+
+def test_everything_is_built_and_then_up_to_date(fake):
+    assert not b.up_to_date()
+    assert b.build() == b.LIB_PATH
+    for path in (b.LIB_PATH, b.ATTN_PATH, b.FAST_PATH, b.HOSTCOST_PATH):
+        assert os.path.exists(path)
+    assert b.up_to_date()
+
+
+def test_the_c_libraries_need_no_torch(fake, monkeypatch):
+    without_torch(monkeypatch)
+    assert b.build() == b.LIB_PATH
+    for path in (b.LIB_PATH, b.ATTN_PATH, b.HOSTCOST_PATH):
+        assert os.path.exists(path)
+    assert not os.path.exists(b.FAST_PATH) and "attn_fast" not in b.log()
+    assert b.up_to_date()
+
+
+def test_the_c_libraries_are_linked_although_the_module_fails(fake):
+    fake(failing="attn_fast")
+    with pytest.raises(RuntimeError, match="attn_fast"):
+        b.build()
+    for path in (b.LIB_PATH, b.ATTN_PATH, b.HOSTCOST_PATH):
+        assert os.path.exists(path)
+    assert not os.path.exists(b.FAST_PATH) and not b.up_to_date()
+    fake()
+    b.build()
+    assert b.up_to_date()

@@ -20,6 +20,7 @@ RMSNORM_GB300_LIB.
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -41,7 +42,19 @@ ATTN_CSRC = os.path.join(PKG, "csrc_attn")
 ATTN_PATH = os.path.join(BUILD_DIR, "librmsnorm_attn_gb300.so")
 # native marshalling of its tensor-level calls (a Python extension module)
 FAST_SRC = os.path.join(PKG, "binding", "attn_fast.cpp")
-FAST_PATH = os.path.join(BUILD_DIR, "rmsattn_fast.so")
+
+
+def fast_path() -> str:
+    """The module's file for this torch, Python and machine: it is compiled
+    against their object layouts, so another one's is not loaded."""
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch = "unknown"
+    return os.path.join(BUILD_DIR, f"rmsattn_fast-torch{torch}-{sysconfig.get_config_var('SOABI')}.so")
+
+
+FAST_PATH = fast_path()
 # the bench's C timing harness (not part of the library)
 HOSTCOST_SRC = os.path.join(PKG, "bench_src", "host_cost.cu")
 HOSTCOST_PATH = os.path.join(BUILD_DIR, "librmsn_hostcost.so")

@@ -67,3 +67,15 @@ def test_the_c_libraries_are_linked_although_the_module_fails(fake):
     fake()
     b.build()
     assert b.up_to_date()
+
+
+def test_the_module_of_another_torch_is_not_taken(fake, monkeypatch):
+    assert os.path.basename(b.FAST_PATH) == os.path.basename(b.fast_path())
+    b.build()
+    have = b.importlib.metadata.version("torch")
+    assert have in b.fast_path() and b.sysconfig.get_config_var("SOABI") in b.fast_path()
+    monkeypatch.setattr(b.importlib.metadata, "version", lambda name: "99.0")
+    monkeypatch.setattr(b, "FAST_PATH", b.fast_path())
+    assert not b.up_to_date()
+    b.build()
+    assert os.path.exists(b.FAST_PATH) and b.up_to_date()

@@ -79,11 +79,12 @@ def attn_sources() -> list[str]:
     return sorted(glob.glob(os.path.join(ATTN_CSRC, "*.cu")))
 
 
-def _inputs() -> list[str]:
-    return (sources() + attn_sources() + glob.glob(os.path.join(ATTN_CSRC, "*.cuh"))
-            + glob.glob(os.path.join(ATTN_CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(CSRC, "*.inc")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-            + [os.path.abspath(__file__)])
+def _inputs(checked: bool = False) -> list[str]:
+    """What the libraries are made of; ``checked``: the row norm's alone."""
+    dirs = [CSRC] if checked else [CSRC, ATTN_CSRC]
+    return ([f for d in dirs for ext in ("cu", "cuh", "h", "inc") for f in glob.glob(os.path.join(d, "*." + ext))]
+            + ([os.path.join(INCLUDE, "rmsnorm.h")] if checked else glob.glob(os.path.join(INCLUDE, "*.h")))
+            + [os.path.abspath(__file__)] + ([] if checked else [HOSTCOST_SRC, FAST_SRC]))
 
 
 def _torch_dir() -> str | None:
@@ -110,7 +111,7 @@ def up_to_date(checked: bool = False) -> bool:
     if not all(os.path.exists(o) for o in outs):
         return False
     t = min(os.path.getmtime(o) for o in outs)
-    return all(os.path.getmtime(f) <= t for f in _inputs() + [HOSTCOST_SRC, FAST_SRC])
+    return all(os.path.getmtime(f) <= t for f in _inputs(checked))
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int | None = None,

@@ -79,3 +79,22 @@ def test_the_module_of_another_torch_is_not_taken(fake, monkeypatch):
     assert not b.up_to_date()
     b.build()
     assert os.path.exists(b.FAST_PATH) and b.up_to_date()
+
+
+def test_the_checked_library_is_the_row_norms(fake, monkeypatch):
+    # files of the attention path are no part of it and do not make it stale
+    assert b.build(checked=True) == b.CHECKED_PATH
+    assert "csrc_attn" not in b.log() and "attn_fast" not in b.log()
+    time = os.path.getmtime
+    later = lambda part: lambda f: time(f) + (1e6 if part in str(f) else 0)
+    for part in ("csrc_attn", "rmsnorm_attn.h", "attn_fast.cpp", "host_cost.cu"):
+        monkeypatch.setattr(b.os.path, "getmtime", later(part))
+        assert b.up_to_date(checked=True), part
+    for part in (os.sep + "csrc" + os.sep, "rmsnorm.h", "build.py"):
+        monkeypatch.setattr(b.os.path, "getmtime", later(part))
+        assert not b.up_to_date(checked=True), part
+    monkeypatch.setattr(b.os.path, "getmtime", time)
+    b.build()
+    for part in ("csrc_attn", "rmsnorm_attn.h", "attn_fast.cpp", "host_cost.cu", os.sep + "csrc" + os.sep):
+        monkeypatch.setattr(b.os.path, "getmtime", later(part))
+        assert not b.up_to_date(), part

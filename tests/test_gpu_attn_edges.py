@@ -234,3 +234,69 @@ def test_a_window_of_the_largest_integer(rn):
     got = rn.kv_cache_attention(q, make_cache(rn, t), given, lens, window=2**63 - 1)
     assert torch.equal(got, want)
     within(got, *attend(q, t, table, lens, 1 / math.sqrt(128)))
+
+
+# the shared line's steps skip from the sinks to the window; rows are cut by the shares' borders on
+# both sides of that gap, and joined
+ON_THE_LINE = [
+    # lengths, n, Hq, Hk, D, page, dtype, window, sinks
+    ([26000, 21000, 24017], 1, 8, 2, 128, 64, "bf16", 20000, 5),
+    ([26000, 700, 24017, 0], 3, 8, 2, 128, 16, "f16", 20000, 40),
+    ([30000, 19999, 20001], 2, 32, 4, 128, 48, "bf16", 20000, 0),
+    ([22003], 5, 8, 1, 128, 64, "bf16", 18000, 1000),
+    ([14000, 9000, 10016], 1, 8, 2, 256, 32, "bf16", 9000, 20),
+    ([20011, 25000], 3, 8, 1, 256, 64, "f16", 18000, 17),
+    ([5000, 4096, 7001, 300, 4100, 6011, 1, 5555] * 8, 1, 8, 4, 64, 64, "f16", 4096, 4),
+    ([5000, 4096, 7001, 300, 4100, 6011, 0, 5555] * 8, 3, 8, 4, 64, 16, "bf16", 4096, 33),
+    ([5000, 4096, 7001, 3000] * 24, 1, 4, 4, 128, 16, "bf16", 3000, 100),
+]
+
+
+def shared_pages(lengths, Hk, D, page, seed=3):
+    """Sequences that read the same few pages in orders of their own."""
+    pool, width = 90, -(-max(lengths) // page)
+    t = ref.random_cache(pool, Hk, page, D, 7, "cuda", spread=False)
+    g = torch.Generator().manual_seed(seed)
+    return t, torch.randint(0, pool, (len(lengths), width), generator=g, dtype=torch.int32).cuda()
+
+
+@pytest.mark.parametrize("lengths,n,Hq,Hk,D,page,dtype,window,sinks", ON_THE_LINE)
+def test_windows_on_the_shared_line(rn, lengths, n, Hq, Hk, D, page, dtype, window, sinks):
+    t, table = shared_pages(lengths, Hk, D, page)
+    lens = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    q = rand((len(lengths), n, Hq, D), 3, DT[dtype]).cuda()
+    assert workspace(rn, q, Hk, table, page, window, sinks) > 0
+    got = rn.kv_cache_attention(q, make_cache(rn, t), table, lens, window=window, sinks=sinks)
+    within(got, *attend(q, t, table, lens, 1 / math.sqrt(D), window, sinks))
+
+
+@pytest.mark.parametrize("D,n", [(64, 1), (64, 3), (128, 1), (128, 3), (256, 2)])
+def test_masked_places_on_the_shared_line_hold_anything(rn, D, n):
+    # NaN codes, and NaN or infinite scales, between the sinks and the window and behind the length
+    page, Hk, Hq, L, sinks = 16, 2, 8, 40011, 21
+    window = 33000 if D == 64 else 20000
+    pages = -(-L // page) + 1
+    t = ref.random_cache(pages, Hk, page, D, 7, "cuda", spread=False)
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(1)).to(torch.int32)[None].cuda()
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    q = rand((1, n, Hq, D), 3, torch.bfloat16).cuda()
+    want, bound = attend(q, t, table, lens, 1 / math.sqrt(D), window, sinks)
+    j = torch.arange(pages * page, device="cuda")
+    hidden = (j >= L) | ((j < L - n + 1 - window) & (j >= sinks))
+    pg, at = table[0].long()[j // page], j % page
+    t["k"][pg[hidden], :, at[hidden]] = 0x7F
+    t["v"][pg[hidden], :, at[hidden]] = 0xFF
+    blocks = hidden.view(-1, 16).all(1).nonzero()[:, 0]
+    t["k_scale"][table[0].long()[blocks]] = math.nan
+    t["v_scale"][table[0].long()[blocks]] = math.inf
+    assert workspace(rn, q, Hk, table, page, window, sinks) > 0
+    got = rn.kv_cache_attention(q, make_cache(rn, t), table, lens, window=window, sinks=sinks)
+    within(got, want, bound)
+
+
+@pytest.mark.parametrize("B,tokens,window,line", [(2, 128, 0, False), (1, 131072, 0, True), (1, 131072, 60, False),
+                                                  (3, 40000, 20000, True), (2, 40000, 0, True)])
+def test_which_calls_take_the_line(rn, B, tokens, window, line):
+    # so that the tests of either way of sharing the work stay tests of that way
+    q, table = torch.empty((B, 1, 8, 128), dtype=torch.bfloat16), torch.empty((B, tokens // 16), dtype=torch.int32)
+    assert (workspace(rn, q, 2, table, 16, window, 3 if window else 0) > 0) == line

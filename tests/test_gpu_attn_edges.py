@@ -300,3 +300,140 @@ def test_which_calls_take_the_line(rn, B, tokens, window, line):
     # so that the tests of either way of sharing the work stay tests of that way
     q, table = torch.empty((B, 1, 8, 128), dtype=torch.bfloat16), torch.empty((B, tokens // 16), dtype=torch.int32)
     assert (workspace(rn, q, 2, table, 16, window, 3 if window else 0) > 0) == line
+
+
+# ---------------------------------------------------------------- two launches a call
+
+def test_calls_with_workspaces_on_two_streams_at_once(rn):
+    # each stream's calls have parts and cuts of their own, although the pool hands out freed memory
+    t, table = shared_pages([5400, 4000], 2, 128, 16)
+    table = widened(table, 40000, 16)
+    cache, lens = make_cache(rn, t), torch.tensor([5400, 4000], dtype=torch.int32, device="cuda")
+    qs = [rand((2, 8, 128), i, torch.bfloat16).cuda() for i in range(12)]
+    assert workspace(rn, qs[0][:, None], 2, table, 16) > 0
+    alone = [rn.kv_cache_attention(q, cache, table, lens) for q in qs]
+    for q, a in zip(qs[:2], alone):
+        within(a[:, None], *attend(q[:, None], t, table, lens, 1 / math.sqrt(128)))
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s in streams:  # all start behind a pause, and then run side by side
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(1_000_000)
+        got = [rn.kv_cache_attention(q, cache, table, lens, stream=streams[i % 4]) for i, q in enumerate(qs)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, alone):
+            assert torch.equal(a, b)
+
+
+def step(rn, s, row, pdl):
+    """Rotary QK norm, append, attention over the cache."""
+    B, n, Hq, Hk, D = s["B"], s["n"], 8, 2, 128
+    q, k, v = row.split([Hq * D, Hk * D, Hk * D], 1)
+    q, k = rn.qk_norm_rope(q, k, s["pos"], s["rope"], s["w"], s["w"], head_dim=D, eps=1e-6, pdl=pdl)
+    rn.kv_cache_append_(s["cache"], k, v, s["table"], s["before"], s["cu"], pdl=pdl)
+    o = rn.kv_cache_attention(q.view(B, n, Hq, D), s["cache"], s["table"], s["after"], window=s["window"], sinks=4,
+                              pdl=pdl)
+    return q, o
+
+
+def state(rn, n, lengths, window):
+    """Sequences whose tables hold 40000 tokens: the attention makes two launches."""
+    B, page = len(lengths), 16
+    used = -(-(max(lengths) + 40) // page)
+    s = dict(B=B, n=n, window=window, rope=rn.rope_table(128), w=rand((128,), 1, torch.bfloat16).cuda())
+    s["t"] = ref.random_cache(B * used, 2, page, 128, 7, "cuda", spread=False)
+    order = torch.randperm(B * used, generator=torch.Generator().manual_seed(2)).to(torch.int32).cuda()
+    s["table"], s["cache"] = widened(order.view(B, used), 40000, page), make_cache(rn, s["t"])
+    s["before"] = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    s["after"], s["pos"] = s["before"] + n, s["before"].repeat_interleave(n)
+    s["cu"] = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    q = torch.empty((B, n, 8, 128), dtype=torch.bfloat16)
+    assert workspace(rn, q, 2, s["table"], page, window, 4) > 0
+    return s
+
+
+@pytest.mark.parametrize("n", [1, 4])
+@pytest.mark.parametrize("window", [0, 20000])
+@pytest.mark.parametrize("pdl", [False, True])
+def test_steps_with_two_launches(rn, n, window, pdl):
+    # one call right behind the other: what the launches hand on is there, and workspaces are not mixed up
+    s = state(rn, n, [9000, 0, 2047] if not window else [30000, 100, 23000], window)
+    e = state(rn, n, [9000, 0, 2047] if not window else [30000, 100, 23000], window)
+    rows = [rand((s["B"] * n, 12 * 128), i, torch.bfloat16).cuda() for i in range(6)]
+    torch.cuda.synchronize()
+    got = []
+    for row in rows:
+        got.append(step(rn, s, row, pdl))
+        for name in ("before", "after", "pos"):
+            s[name] = s[name] + n
+    for row, (q, o) in zip(rows, got):
+        q2, o2 = step(rn, e, row, False)
+        torch.cuda.synchronize()
+        assert torch.equal(q, q2) and torch.equal(o, o2)
+        for name in ("before", "after", "pos"):
+            e[name] = e[name] + n
+    for name in s["t"]:
+        assert torch.equal(s["t"][name], e["t"][name])
+    within(o2, *attend(q2.view(s["B"], n, 8, 128), e["t"], e["table"], e["after"] - n, 1 / math.sqrt(128), window,
+                       4 if window else 0))
+
+
+@pytest.mark.parametrize("pdl", [False, True])
+def test_two_launches_captured_and_replayed_as_lengths_change(rn, pdl):
+    s, e = state(rn, 1, [4000, 0, 2047], 0), state(rn, 1, [4000, 0, 2047], 0)
+    row = rand((3, 12 * 128), 3, torch.bfloat16).cuda()
+    warm = state(rn, 1, [4000, 0, 2047], 0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(rn, warm, row, pdl)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q, o = step(rn, s, row, pdl)
+    for i in range(20):
+        row.copy_(rand(row.shape, 10 + i, torch.bfloat16))
+        graph.replay()
+        q2, o2 = step(rn, e, row, False)
+        assert torch.equal(q, q2) and torch.equal(o, o2), i
+        for x in (s, e):
+            for name in ("before", "after", "pos"):
+                x[name] += 1 if i < 15 else -300  # and shorter again
+            x["before"].clamp_(min=0)
+            x["after"].copy_(x["before"] + 1)
+            x["pos"].clamp_(min=0)
+    for name in s["t"]:
+        assert torch.equal(s["t"][name], e["t"][name])
+
+
+def test_calls_are_ordered_behind_the_stream_they_name(rn):
+    # inputs that arrive late on that stream, while the current one is idle: a launch on the current
+    # stream would read what was there before
+    D, s = 64, torch.cuda.Stream()
+    t, table, given, q, lens = case(D, 500, 1, how="line")
+    cache, late = make_cache(rn, t), {name: torch.zeros_like(x) for name, x in t.items()}
+    into = make_cache(rn, late)
+    rope, pos = rn.rope_table(D), torch.full((1,), 3, dtype=torch.int32, device="cuda")
+    kv = rand((1, 2, D), 4, torch.bfloat16).cuda()
+    x, y, z = torch.zeros_like(q), torch.zeros_like(kv), torch.zeros_like(q)
+    old = lens - 1
+    want_q, _ = rn.qk_norm_rope(q.view(1, -1), None, pos, rope, head_dim=D)
+    want_o = rn.kv_cache_attention(q, cache, given, lens)
+    after = {name: a.clone() for name, a in t.items()}
+    rn.kv_cache_append_(make_cache(rn, after), kv, kv, table, old)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)  # some 100 ms
+        for a, b in ((x, q), (y, kv), (z, q)):
+            a.copy_(b)
+        for name in t:
+            late[name].copy_(t[name])
+    got_q, _ = rn.qk_norm_rope(x.view(1, -1), None, pos, rope, head_dim=D, stream=s)
+    got_o = rn.kv_cache_attention(z, into, given, lens, stream=s)
+    rn.kv_cache_append_(into, y, y, table, old, stream=s)
+    assert not s.query()  # the calls came before their inputs
+    torch.cuda.synchronize()
+    assert torch.equal(got_q, want_q) and torch.equal(got_o, want_o)
+    for name in t:
+        assert torch.equal(late[name], after[name])

@@ -91,8 +91,9 @@ class RopeTable(_Fixed):
 
 
 @functools.lru_cache(maxsize=16)
-def _pi(bits: int) -> int:
-    """pi * 2^bits to within a few units (Machin: 16 atan(1/5) - 4 atan(1/239))."""
+def _turns_per_radian(bits: int) -> int:
+    """2^bits / (2 pi) to within a few units (pi by Machin's formula,
+    16 atan(1/5) - 4 atan(1/239))."""
     def atan_of_one_over(n):
         term = total = (1 << bits) // n
         k = 1
@@ -102,15 +103,16 @@ def _pi(bits: int) -> int:
             total += term // k
         return total
 
-    return 16 * atan_of_one_over(5) - 4 * atan_of_one_over(239)
+    bits += 16
+    pi = 16 * atan_of_one_over(5) - 4 * atan_of_one_over(239)
+    return (1 << (2 * bits - 1)) // pi >> 16
 
 
-def _turn_bits(num: int, den: int) -> int:
-    """num / den radians in turns: the fraction of a turn, rounded to 64 bits."""
-    guard = 32  # beyond the whole turns and the 64 bits: far more than _pi is off by
-    bits = max(0, abs(num).bit_length() - den.bit_length() + 1) + 64 + guard
-    num, den = num << (63 + bits), den * (_pi(bits + guard) >> guard)
-    return (2 * num + den) // (2 * den) % 2**64
+def _turn_bits(num: int, shift: int) -> int:
+    """num / 2^shift radians in turns: the fraction of a turn, rounded to 64 bits."""
+    # the whole turns, the 64 bits, and 64 to round by; in steps, for the cache
+    bits = (max(0, abs(num).bit_length() - shift) + 191) // 64 * 64
+    return ((num * _turns_per_radian(bits) >> (shift + bits - 65)) + 1 >> 1) % 2**64
 
 
 def rope_table(rot_dim: int, *, base: float = 10000.0, sections=None, axis=None, inv_freq=None,
@@ -142,21 +144,21 @@ def rope_table(rot_dim: int, *, base: float = 10000.0, sections=None, axis=None,
         base = float(base)
         if not base > 0:
             raise ValueError("base must be positive")
-        b = decimal.Decimal(base)
-        # 60 digits behind the point of the largest: a product for each pair
-        # loses none that count
-        with decimal.localcontext(decimal.Context(prec=60 + max(0, -b.adjusted()))):
-            step, freqs = b ** (decimal.Decimal(-2) / max(rot_dim, 1)), [decimal.Decimal(1)] * min(pairs, 1)
-            while len(freqs) < pairs:
-                freqs.append(freqs[-1] * step)
-        freqs = [f.as_integer_ratio() for f in freqs]
+        # fixed-point powers of one step; a base below 1 makes large ones
+        large = max(0, 1 - math.frexp(base)[1])
+        shift = 192 + 2 * large
+        with decimal.localcontext(decimal.Context(prec=64 + large)):
+            step = int(decimal.Decimal(base) ** (decimal.Decimal(-2) / max(rot_dim, 1)) * (1 << shift))
+        freqs = [(1 << shift, shift)][:pairs]
+        while len(freqs) < pairs:
+            freqs.append((freqs[-1][0] * step >> shift, shift))
     else:
         freqs = [float(f) for f in inv_freq]
         if len(freqs) != pairs:
             raise ValueError(f"inv_freq must hold {pairs} values")
         if not all(math.isfinite(f) for f in freqs):
             raise ValueError("frequencies must be finite")
-        freqs = [f.as_integer_ratio() for f in freqs]
+        freqs = [(n, d.bit_length() - 1) for n, d in map(float.as_integer_ratio, freqs)]
     bits = [_turn_bits(*f) for f in freqs]
     bits = [b - 2**64 if b >= 2**63 else b for b in bits]
     return RopeTable(torch.tensor(bits, dtype=torch.int64, device=device),
@@ -338,9 +340,6 @@ class KVCache(_Fixed):
                 raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
             if t.device != k.device:
                 raise ValueError(f"{name} must be on {k.device}, got {t.device}")
-            last = sum((size - 1) * step for size, step in zip(t.shape, t.stride())) + 1 if t.numel() else 0
-            if (t.storage_offset() + last) * t.element_size() > t.untyped_storage().nbytes():
-                raise ValueError(f"{name} is larger than its storage")
             # each page contiguous; pages any stride apart
             inner = 1
             for size, step in zip(want[:0:-1], t.stride()[:0:-1]):
@@ -348,6 +347,9 @@ class KVCache(_Fixed):
                     break
                 inner *= size
             else:
+                end = t.storage_offset() + (pages - 1) * t.stride(0) + inner
+                if pages and end * t.element_size() > t.untyped_storage().nbytes():
+                    raise ValueError(f"{name} is larger than its storage")
                 continue
             if pages:
                 raise ValueError(f"{name}: each page must be contiguous")

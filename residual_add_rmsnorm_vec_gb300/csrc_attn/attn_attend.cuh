@@ -504,8 +504,9 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     // ---- queries: this warp's columns of a row, first into registers (before
     // the wait that they can hide behind), then to shared memory in fp16, each
     // scaled by a power of two to at most 2^8 (so that fp16 holds any bf16 row:
-    // what is below 2^-32 of the row's largest value loses bits); q_scale
-    // undoes it, times |scale| log2(e) (a negative scale turns the queries' sign)
+    // each element exactly, or to within 2^-32 of the row's largest, half of
+    // the subnormals' step over 2^7); q_scale undoes it, times |scale| log2(e)
+    // (a negative scale turns the queries' sign)
     constexpr int QC = (C::kCols + W - 1) / W, QW = D / 64;
     uint32_t qreg[QC][QW];
     auto load_q = [&](int64_t b, int hc) {
@@ -535,7 +536,11 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
             m = rmsn::warp_max(m);
             int e = (int)(__float_as_uint(m) >> 23) - 127 - 7;  // 2^e <= m / 128 < 2^(e + 1)
             e = e < -126 ? -126 : (e > 126 ? 126 : e);
-            const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), a.scale);
+            // an infinite element makes every score of the row infinite or NaN,
+            // and any softmax of such scores NaN (all of -inf among them)
+            const float down = m > 3.402823466e38f
+                                   ? __uint_as_float(0x7FFFFFFFu)
+                                   : copysignf(__uint_as_float((uint32_t)(127 - e) << 23), a.scale);
             const float up = __uint_as_float((uint32_t)(127 + e) << 23);
             if (c >= C::kCols) break;
             if (lane == 0) q_scale[c] = up * (fabsf(a.scale) * kLog2e);

@@ -185,6 +185,25 @@ def test_scores_beyond_whole_numbers_of_fp32(rn, D, n, how, top):
     assert bool(torch.isfinite(got).all())
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", DT)
+@pytest.mark.parametrize("how", HOW)
+@pytest.mark.parametrize("code", [0x38, 0xB8, 0])  # 1, -1, 0: the keys where the query is infinite
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+def test_an_infinite_query_gives_nan(rn, D, dtype, how, code, value):
+    # scores of +inf, -inf or NaN alone: a softmax of any of them is NaN, where a token is seen
+    n, L = 3, 2
+    t, table, given, q, lens = case(D, 40, n, dtype, how=how)
+    lens[0] = L  # the first of the three queries sees nothing
+    q[0, :, 5, 7] = value
+    t["k"][..., 7] = code
+    got = rn.kv_cache_attention(q, make_cache(rn, t), given, lens)
+    assert bool(got[0, 1:, 5].isnan().all()) and bool((got[0, 0] == 0).all())
+    want, bound = attend(q.nan_to_num(0, 0, 0), t, table, lens, 1 / math.sqrt(D))
+    rest = [h for h in range(8) if h != 5]
+    within(got[:, :, rest], want[:, :, rest], bound[:, :, rest])
+
+
 # ---------------------------------------------------------------- handles
 
 def test_a_cache_whose_tensors_were_given_other_memory(rn):

@@ -44,9 +44,9 @@ extern "C" {
  * frequency in turns per position as a 64-bit fixed-point fraction,
  * round(inv_freq[p] / (2 pi) * 2^64) mod 2^64: the product with an integer
  * position wraps exactly as the angle does, so far and negative positions
- * lose nothing (the phase is off by less than |position| * 2^-64 turns plus
- * fp32's rounding of one turn).  axis[p] < n_axes names the axis (time,
- * height, width, ...) whose position turns the pair.
+ * lose nothing (the phase is off by |position| * 2^-65 turns at most, the
+ * rounding of turns[p], plus fp32's rounding of one turn).  axis[p] < n_axes
+ * names the axis (time, height, width, ...) whose position turns the pair.
  *
  *   q, k            [n_tokens, heads, head_dim], token strides in elements
  *   q_out, k_out    the same; q_out may be q (and k_out k) at the same stride;
@@ -139,13 +139,18 @@ int rmsattn_kv_append(const rmsattn_cache* cache, const void* k, const void* v, 
  *
  *   out = sum_j softmax_j(scale * q . k_j) v_j     (0 where nothing is seen)
  *
- * Query head h reads key head h / (n_q_heads / n_kv_heads).  Products of the
- * codes with q are exact in fp32 sums; softmax statistics and the output sum
- * are fp32; the weights are rounded to fp16 (2^-11 of their value, or 2^-33 of
- * the row's largest) for the second product.  Tokens past lengths[s], and tokens that no query of the
- * sequence sees, have no influence, whatever their codes are.  A page outside
- * [0, n_pages), or past the table's width, is left out and sets bit 2 (value
- * 4) of the status word.
+ * Query head h reads key head h / (n_q_heads / n_kv_heads).  A row of q is held
+ * in fp16 times a power of two: each element exactly, or to within 2^-32 of the
+ * row's largest.  Its products with the codes are exact in fp32 sums; scores
+ * (finite below 3.4e38), softmax statistics and the output sum are fp32; the
+ * weights are rounded to fp16 (2^-11 of their value, or 2^-33 of the row's
+ * largest) for the second product, whose value scales are applied in fp32 (one
+ * below 2^-118 keeps 16 bits).  An infinity or NaN in a row of q gives NaN
+ * wherever that row sees a token.  Tokens past lengths[s], and tokens that no
+ * query of the sequence sees, have no influence, whatever their codes are; one
+ * that another query of the sequence sees may change a result's last roundings.
+ * A page outside [0, n_pages), or past the table's width, is left out and sets
+ * bit 2 (value 4) of the status word.
  *
  *   q, out      [n_seqs, n_queries, n_q_heads, head_dim] bf16 / fp16, tokens
  *               q_stride / out_stride elements apart, heads back to back, 16-byte
@@ -172,7 +177,9 @@ int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_queries, int64_
 
 /* Status word of this library's kernels on the current device: bit 2 (value
  * 4) is set when a block table named a page outside the cache or a token lay
- * past the table.  Reads synchronously; `clear` != 0 resets the word. */
+ * past the table.  Reads synchronously, behind the legacy default stream's work:
+ * synchronise with streams made non-blocking (PyTorch's own) first.  `clear` !=
+ * 0 resets the word. */
 int rmsattn_read_status(uint32_t* status, int clear);
 
 #ifdef __cplusplus

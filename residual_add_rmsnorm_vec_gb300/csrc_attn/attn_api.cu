@@ -378,9 +378,9 @@ int plan_attend(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
     // full one.  The line costs an even share, about 5 us more (its scan and
     // its join: as long as a warp takes for 16384 / head_dim tokens), and
     // longer joins where a row has many parts.  At head_dim 128 on a GB300,
-    // rows against line: 8 x 2000 tokens x 8 heads 10.5 against 14.6 us, 256 x
-    // 300 40 against 42, 16 x 4000 24.7 against 27.9; and where all are as long
-    // as the first, 64 x 8192 147 against 147, 1 x 131072 111 against 52.
+    // rows against line: 8 x 2000 tokens x 8 heads 10.6 against 14.3 us, 256 x
+    // 300 38.3 against 40.4, 16 x 4000 24.7 against 27.7; and where all are as
+    // long as the first, 64 x 8192 152 against 149, 1 x 131072 121 against 52.
     for (int line = 0; line < 2; ++line) {
         // the line takes the first of the fitting kernels, whatever the rows
         const AttendEntry* e = p->e = attend_entry_of(dt, head_dim, cols, line ? 0 : max_tokens);

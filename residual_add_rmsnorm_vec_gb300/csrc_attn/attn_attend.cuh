@@ -8,14 +8,17 @@
 // What bounds it.  A decode step reads 2 D + 1/2 bytes per token and key head
 // and does 4 D products for each of the G query heads that share it: DRAM, as
 // long as the G n columns (query head x query token) of a row stay few.  Each
-// token also costs instructions, about 17 a warp at head_dim 128 and one
+// token also costs instructions, about 20 a warp at head_dim 128 and one
 // column tile (a conversion for every two codes, a third of them; then the
-// copies, the softmax of eight columns, the matrix products); with half the
-// bytes (head_dim 64) or twice the columns they become the bound.  On one
-// GB300, of the copy peak of 6.78 TB/s: 64 sequences of 6144 to 8192 tokens,
-// 32 / 8 heads x 128, 0.94 GB in 146 us (0.95); the same at head_dim 64, 80 us
-// (0.87), at 256, 148 us for half as many (0.94); 4 query tokens, 16 columns,
-// 176 MB in 46 us (0.57); one sequence of 131072 tokens 52 us (0.77).
+// copies, the softmax of eight columns, the matrix products).  168 registers
+// leave 12 warps an SM; with half the bytes a token (head_dim 64) or twice the
+// columns those no longer cover each other's fixed latencies, the first stall
+// there, with 40 to 50 % of the issue slots in use: latency at low occupancy is
+// then the bound.  On one GB300, of the copy peak of 6.78 TB/s: 64 sequences of
+// 6144 to 8192 tokens, 32 / 8 heads x 128, 0.94 GB in 146 us (0.95); the same
+// at head_dim 64, 80 us (0.87), at 256, 149 us for half as many (0.93); 4 query
+// tokens, 16 columns, 176 MB in 47 us (0.55); one sequence of 131072 tokens
+// 52 us (0.77).
 // So the work is laid out around the reads:
 //
 // * Columns are the narrow side of mma.m16n8k16: S^T = K Q^T with 16 tokens
@@ -66,7 +69,10 @@ constexpr uint32_t kOpen = 1u << 12;  // of a tile's word: every query sees all 
 // factor from tile to tile, and a weight would lose as many bits.  A tile's
 // products are summed by themselves and enter the row's sum through an fp32
 // multiply-add with the scale (16 packed ones a tile and column tile at
-// head_dim 128).
+// head_dim 128).  Against weights times scale over the largest scale so far,
+// which lost every bit at a ratio of 2^33: one column tile 38.4 / 40.2 us (256 x
+// 300 tokens, no rescaling for scales), two 47.1 / 46.1 (48 x 2000), four 102 /
+// 93.5 (the same with 8 queries).
 constexpr float kNone = -3.402823466e38f;  // the reference before any token is seen
 constexpr float kSlack = 7.f;
 constexpr float kLift = 256.f;
@@ -877,7 +883,8 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                         for (int x = 0; x < 2; ++x) o[i][nt][x] = rmsn::mul2(o[i][nt][x], keep2);
                     // from the rounded products, as the reference was taken: the
                     // largest then weighs 1 where scores are beyond 2^28, too
-                    // (what a product rounds off there is a large exponent)
+                    // (what a product rounds off there is a large exponent); one
+                    // by one, for the compiler contracts the packed forms
 #pragma unroll
                     for (int k = 0; k < KT; ++k) {
                         float c[2];

@@ -4,9 +4,9 @@
 namespace rmsattn {
 
 // For rows of a few steps, of which steps of 32 tokens would leave warps idle
-// (256 x 300 tokens 40 against 50 us), and for the line (64 x 8192 147 against
-// 151); A where a row's clusters have 32-token steps enough (8 x 2000 10.5
-// against 11.7).
+// (256 x 300 tokens 38 against 49 us), and for the line (64 x 8192 149 either
+// way); A where a row's clusters have 32-token steps enough (8 x 2000 10.6
+// against 11.2, 16 x 4000 24.7 against 26.8).
 using Short = Shape<128, 1, 1, 4, 3>;
 using A = Shape<128, 1, 2, 4, 2>;
 using B = Shape<128, 2, 1, 4, 3>;

@@ -45,16 +45,22 @@ def _other(device, stream):
 
 
 class _Fixed:
-    """Attributes are set once, by ``_set``: what a call reads beside the
-    tensors (their shapes, addresses, device) cannot fall out of step with them."""
+    """The attributes in ``_fixed`` are set once, by ``_set``: what a call reads
+    beside the tensors (their shapes, addresses, device) cannot fall out of step
+    with them.  A subclass may have others."""
 
     __slots__ = ()
+    _fixed: tuple = ()
 
     def __setattr__(self, name, value):
-        raise AttributeError(f"{type(self).__name__}.{name} cannot be changed: make another")
+        if name in self._fixed:
+            raise AttributeError(f"{type(self).__name__}.{name} cannot be changed: make another")
+        object.__setattr__(self, name, value)
 
     def __delattr__(self, name):
-        raise AttributeError(f"{type(self).__name__}.{name} cannot be removed")
+        if name in self._fixed:
+            raise AttributeError(f"{type(self).__name__}.{name} cannot be removed")
+        object.__delattr__(self, name)
 
     def _set(self, **values):
         for name, value in values.items():
@@ -67,7 +73,7 @@ class RopeTable(_Fixed):
     turns the pair), both [rot_dim / 2] on the device; made by ``rope_table``.
     The attributes are fixed."""
 
-    __slots__ = ("turns", "axis", "rot_dim", "n_axes", "index")
+    _fixed = __slots__ = ("turns", "axis", "rot_dim", "n_axes", "index")
 
     def __init__(self, turns: torch.Tensor, axis: torch.Tensor, n_axes: int):
         if turns.dim() != 1:
@@ -87,7 +93,7 @@ class RopeTable(_Fixed):
         return self.turns.data_ptr(), self.axis.data_ptr()
 
     def __reduce__(self):
-        return RopeTable, (self.turns, self.axis, self.n_axes)
+        return type(self), (self.turns, self.axis, self.n_axes)
 
 
 @functools.lru_cache(maxsize=16)
@@ -309,8 +315,8 @@ class KVCache(_Fixed):
     attributes are fixed; a tensor that was given other memory in place
     (``resize_`` of its storage, ``set_``) is looked at again by the next call."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "n_pages", "n_kv_heads", "page_size", "head_dim",
-                 "device", "index", "_c", "_ref", "_addr", "_tensors")
+    _fixed = __slots__ = ("k", "v", "k_scale", "v_scale", "n_pages", "n_kv_heads", "page_size",
+                          "head_dim", "device", "index", "_c", "_ref", "_addr", "_tensors")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor,
                  v_scale: torch.Tensor):
@@ -361,7 +367,7 @@ class KVCache(_Fixed):
             k_scale.stride(0) if pages > 1 else shape[1] * shape[2], heads, page, dim, 0)
 
     def __reduce__(self):
-        return KVCache, self._tensors
+        return type(self), self._tensors
 
     def _current(self):
         """The description as the C ABI takes it, where the tensors lie now."""

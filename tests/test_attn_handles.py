@@ -113,3 +113,19 @@ def test_copies(rn):
     table = rn.rope_table(64, sections=[8, 12, 12], device="cpu")
     far = copy.deepcopy(table)
     assert torch.equal(far.turns, table.turns) and far.n_axes == 3
+
+
+def test_a_subclass_has_attributes_of_its_own(rn):
+    class Named(rn.KVCache):
+        def __init__(self, *tensors):
+            super().__init__(*tensors)
+            self.name = "layer 3"
+
+    cache = Named(*tensors())
+    cache.name = "layer 4"
+    del cache.name
+    with pytest.raises(AttributeError):
+        cache.k = cache.v
+    with pytest.raises(AttributeError):
+        rn.KVCache(*tensors()).name = "a slot that is not there"
+    assert type(copy.copy(cache)) is Named

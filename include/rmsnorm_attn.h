@@ -2,7 +2,9 @@
  * rmsnorm_attn.h -- C ABI of the GB300 (sm_103a) attention-path operators
  * that stand next to the QK norm of rmsnorm.h: rotary positions with several
  * axes fused with that norm, the append of keys and values to a paged 8-bit
- * cache, and the attention that reads it.  Built into a library of its own
+ * cache, the attention that reads it (with a form for sequences that share a
+ * long prefix), the page plan of a serving step, and the norms at a block's end.
+ * Built into a library of its own
  * (librmsnorm_attn_gb300.so); statuses, dtype flags and RMSN_PDL are those of
  * rmsnorm.h.
  *
@@ -175,9 +177,139 @@ int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_queries, int64_
                                        int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens,
                                        int64_t window, int64_t sinks);
 
+/*
+ * The same attention where groups of sequences share a long first part (a system
+ * prompt, a document): the shared tokens are read once for a group, and all of
+ * its queries are multiplied with them on the tensor cores.  The result is that
+ * of rmsattn_kv_attention without window and sinks, up to the order of sums.
+ *
+ *   group_cu       [n_groups + 1] int32, non-decreasing: group g is the sequences
+ *                  group_cu[g] .. group_cu[g + 1] - 1; sequences of no group
+ *                  share nothing.  NULL: one group of all (n_groups 1, or 0)
+ *   prefix_lengths [n_groups] int32: the first tokens that are the same for all
+ *                  of the group, in the same pages (the rows of the block table
+ *                  begin with the same entries).  Any length, 0 among them; whole
+ *                  blocks of RMSATTN_BLOCK tokens are shared, the rest is read by
+ *                  each sequence.
+ *
+ * block_table and lengths count the shared tokens too, as everywhere.  A sequence
+ * whose first query does not see all of the prefix, one of length 0 among them,
+ * and one that is alone in its group shares nothing: it reads its own row.  The
+ * shared pages are those of the group's first sequence that shares.  Borders that
+ * decrease or leave [0, n_seqs] share nothing, and set bit 2 (value 4) of the
+ * status word.
+ *
+ * The second product's weights are rounded to fp16 after they have been
+ * multiplied with the significand of their block's value scale (2^-11 of their
+ * value, or 2^-34 of the row's largest); the scale's power of two goes to the
+ * codes, which stay exact.
+ *
+ *   workspace   rmsattn_kv_prefix_attention_workspace(...) bytes on the device,
+ *               16-byte aligned, used by this call alone until it has finished
+ */
+int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* cache, const int32_t* block_table,
+                                int64_t table_stride, int64_t table_width, const int32_t* lengths,
+                                const int32_t* prefix_lengths, const int32_t* group_cu, int64_t n_groups,
+                                void* out, int64_t q_stride, int64_t out_stride, int64_t n_seqs,
+                                int64_t n_queries, int64_t n_q_heads, float scale, void* workspace,
+                                int64_t workspace_bytes, uint32_t flags, cudaStream_t stream);
+
+/* Bytes of workspace for these sizes on the current device (>= 0), or a negative
+ * rmsn_status.  max_tokens: table_width * page_size. */
+int64_t rmsattn_kv_prefix_attention_workspace(int64_t n_seqs, int64_t n_queries, int64_t n_q_heads,
+                                              int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens,
+                                              int64_t n_groups);
+
+/*
+ * A serving step's plan from the requests' lengths.  Sequence s holds lengths[s]
+ * tokens and gets new_tokens[s] more, the next new_tokens[s] rows of the step's
+ * batch of n_rows (as rmsattn_kv_append takes them); a negative new_tokens[s]
+ * says that it is finished, a negative lengths[s] that there is no sequence s.
+ *
+ *   own(s)  = ceil(lengths[s] / page_size) pages, need(s) with the new tokens
+ *   returned, in the sequences' order: the pages [shared_pages[s], own(s)) of the
+ *     rows of finished sequences (within the table's width); they go behind the
+ *     n_free first entries of free_pages: F = n_free + returned, at most n_pages
+ *   taken, in the sequences' order: need(s) - own(s) pages; the k-th of all that
+ *     is taken is entry F - 1 - k, and becomes block_table[s][own(s) ...]
+ *   left out: a sequence whose pages outrun F (with all pages asked for before
+ *     it) or the table's width, whose rows outrun n_rows, or whose tokens outrun
+ *     31 bits.  It takes nothing, and its table row stays as it is.
+ *
+ * Results, all int32 but slots:
+ *   cu_seqlens [n_seqs + 1]  the sequences' first rows, and the end (at most n_rows)
+ *   positions  [n_rows]      lengths[s] + i for a sequence's row i; 0 behind the last
+ *   slots      [n_rows]      int64: page * page_size + row in the page; -1 behind
+ *                            the last row and for a sequence that is left out
+ *   rows       [n_rows]      the row's sequence; -1 behind the last
+ *   before     [n_seqs]      lengths[s], what rmsattn_kv_append takes; -1 for a
+ *                            sequence that is left out, finished or not there
+ *   after      [n_seqs]      tokens behind the step, what the attention takes: 0
+ *                            for a finished sequence, lengths[s] for one left out
+ *   n_free_out [1]           free pages behind the step, F - taken
+ * and in place block_table (the new entries alone) and free_pages (the returned
+ * pages among its first n_free_out entries).  lengths and n_free are not changed
+ * (the outputs may not be those arrays), so the same call gives the same results
+ * again; a program goes on with `after` and n_free_out.
+ *
+ * free_pages holds n_pages entries, of which the first n_free (kept within
+ * [0, n_pages]) count; page numbers outside [0, n_pages) and more returned pages
+ * than free_pages holds set bit 2 (value 4) of the status word (slots are then -1).
+ * shared_pages may be NULL (0); page_size as in rmsattn_cache.  positions, rows
+ * and slots are 16-byte aligned.
+ */
+int rmsattn_pages_step(int32_t* free_pages, int64_t n_pages, const int32_t* n_free,
+                       int32_t* block_table, int64_t table_stride, int64_t table_width,
+                       const int32_t* lengths, const int32_t* new_tokens, const int32_t* shared_pages,
+                       int64_t n_seqs, int64_t page_size, int64_t n_rows, int32_t* cu_seqlens,
+                       int32_t* positions, int64_t* slots, int32_t* rows, int32_t* before,
+                       int32_t* after, int32_t* n_free_out, void* workspace, int64_t workspace_bytes,
+                       uint32_t flags, cudaStream_t stream);
+
+/* Bytes of workspace that rmsattn_pages_step needs (16-byte aligned; 0 up to 2048
+ * sequences), or a negative rmsn_status. */
+int64_t rmsattn_pages_workspace(int64_t n_seqs);
+
+/*
+ * The end of a block and the begin of the next, for each row of `hidden` elements:
+ *
+ *   p = (post_weight + weight_offset) * (x * rsqrt(mean(x^2) + eps))
+ *   h = RN(residual_scale * residual + gate * p)     -> residual_out
+ *   y = (weight + weight_offset) * (h * rsqrt(mean(h^2) + eps))   -> out
+ *
+ * in fp32, h rounded once to the residual's type, y (of the rounded h) once to
+ * x's; with RMSATTN_OUT_FP8, out holds E4M3_RN_SATFINITE(y * (448 / max|y|)) and
+ * out_scale max|y| / 448 (a row of zeros: codes and scale 0).
+ *
+ *   x            [n_tokens, hidden] bf16 / fp16 / fp32, weights [hidden] of its type
+ *                or NULL (1, without the offset)
+ *   residual     [n_tokens, hidden] of x's type, or fp32 with RMSN_RESIDUAL_F32
+ *                (bf16 / fp16 x); residual_out the same, may be residual itself
+ *   out          of x's type (may be x itself), or bytes
+ *   gate         NULL (1); or rows of x's type gate_stride elements apart:
+ *                gate_stride 0, n_gates 1: one row for all; n_gates == n_tokens: a
+ *                row each; with gate_index [n_tokens], token t takes row
+ *                gate_index[t] of n_gates, and one with a negative index (a row
+ *                behind the last sequence) is left out, out and residual_out
+ *                untouched.  An index >= n_gates is left out too, and sets bit 2
+ *                (value 4) of the status word.
+ *
+ * Sums of squares are fp32: rows need sum(x^2), sum(h^2) < FLT_MAX.  Rows, gates
+ * and weights are contiguous; 16-byte vectors are used where every operand's rows
+ * allow it (hidden a multiple of 8).
+ */
+#define RMSATTN_OUT_FP8 0x8000u
+
+int rmsattn_block_norms(const void* x, const void* residual, const void* post_weight,
+                        const void* weight, const void* gate, int64_t gate_stride,
+                        const int32_t* gate_index, int64_t n_gates, void* out, void* residual_out,
+                        float* out_scale, int64_t n_tokens, int64_t hidden, float eps,
+                        float residual_scale, float weight_offset, uint32_t flags,
+                        cudaStream_t stream);
+
 /* Status word of this library's kernels on the current device: bit 2 (value
  * 4) is set when a block table named a page outside the cache or a token lay
- * past the table.  Reads synchronously, behind the legacy default stream's work:
+ * past the table (and by what the plan and the norms say above).  Reads synchronously, behind the legacy default stream's work:
  * synchronise with streams made non-blocking (PyTorch's own) first.  `clear` !=
  * 0 resets the word. */
 int rmsattn_read_status(uint32_t* status, int clear);

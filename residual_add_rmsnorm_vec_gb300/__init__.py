@@ -11,7 +11,11 @@ the FP8 output of section "Blackwell support"):
     out = RN_out(y)   or   FP8-E4M3 codes of y * 448 / max|y| with scale max|y| / 448
 
 The attention path around the QK norm (``qk_norm_rope``, ``kv_cache_append_``,
-``kv_cache_attention``) has the C ABI of ``include/rmsnorm_attn.h``.
+``kv_cache_attention``) has the C ABI of ``include/rmsnorm_attn.h``, and so
+have the operators around it in a serving step: ``kv_pages_step_`` (block
+tables and slots from the requests' lengths), ``kv_cache_prefix_attention``
+(sequences that share a long prefix) and ``fused_block_norms`` (the norms at a
+block's end, with its gate and residual update).
 """
 from __future__ import annotations
 
@@ -29,7 +33,9 @@ from .api import (block_format_configs, check_row_args, fused_add_rmsnorm, fused
                   fused_add_rmsnorm_host, make_flags, qk_norm_)
 from ._attn_lib import (  # noqa: F401
     EXPORTED_ATTN, RMSATTN_BAD_PAGE, RMSATTN_BLOCK, RMSATTN_INTERLEAVED, RMSATTN_MAX_QUERIES,
-    RMSATTN_NORM, RMSATTN_POS_I64, attn_library_path, load_attn, load_fast as load_attn_binding,
+    RMSATTN_NORM, RMSATTN_OUT_FP8, RMSATTN_POS_I64, attn_library_path, load_attn, load_fast as load_attn_binding,
     rmsattn_read_status)
 from .attn import (KVCache, RopeTable, kv_cache_append_, kv_cache_attention, qk_norm_rope,  # noqa: F401
                    rope_table)
+from .step import (KVStep, fused_block_norms, kv_cache_prefix_attention, kv_free_pages,  # noqa: F401
+                   kv_pages_step_)

@@ -14,12 +14,15 @@ from .build import ATTN_PATH, FAST_PATH
 RMSATTN_NORM = 0x1000
 RMSATTN_INTERLEAVED = 0x2000
 RMSATTN_POS_I64 = 0x4000
+RMSATTN_OUT_FP8 = 0x8000
 RMSATTN_BLOCK = 16
 RMSATTN_MAX_QUERIES = 32
 RMSATTN_BAD_PAGE = 4  # bit of the status word
 
 EXPORTED_ATTN = ("rmsattn_qk_rope_fwd", "rmsattn_kv_append", "rmsattn_kv_attention",
-                 "rmsattn_kv_attention_workspace", "rmsattn_read_status")
+                 "rmsattn_kv_attention_workspace", "rmsattn_read_status", "rmsattn_kv_prefix_attention",
+                 "rmsattn_kv_prefix_attention_workspace", "rmsattn_pages_step", "rmsattn_pages_workspace",
+                 "rmsattn_block_norms")
 
 
 class RmsattnCache(ctypes.Structure):
@@ -62,6 +65,19 @@ def load_attn() -> ctypes.CDLL:
                                                  i64, f32, i64, i64, vp, i64, u32, vp]
             lib.rmsattn_kv_attention_workspace.restype = i64
             lib.rmsattn_kv_attention_workspace.argtypes = [i64] * 8
+            lib.rmsattn_kv_prefix_attention.restype = ctypes.c_int
+            lib.rmsattn_kv_prefix_attention.argtypes = [vp, cache, vp, i64, i64, vp, vp, vp, i64, vp, i64, i64,
+                                                        i64, i64, i64, f32, vp, i64, u32, vp]
+            lib.rmsattn_kv_prefix_attention_workspace.restype = i64
+            lib.rmsattn_kv_prefix_attention_workspace.argtypes = [i64] * 7
+            lib.rmsattn_pages_step.restype = ctypes.c_int
+            lib.rmsattn_pages_step.argtypes = [vp, i64, vp, vp, i64, i64, vp, vp, vp, i64, i64, i64,
+                                               vp, vp, vp, vp, vp, vp, vp, vp, i64, u32, vp]
+            lib.rmsattn_pages_workspace.restype = i64
+            lib.rmsattn_pages_workspace.argtypes = [i64]
+            lib.rmsattn_block_norms.restype = ctypes.c_int
+            lib.rmsattn_block_norms.argtypes = [vp, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, i64, i64,
+                                                f32, f32, f32, u32, vp]
             lib.rmsattn_read_status.restype = ctypes.c_int
             lib.rmsattn_read_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
             _loaded = lib

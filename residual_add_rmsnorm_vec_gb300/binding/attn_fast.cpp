@@ -3,10 +3,10 @@
 // A decode step's launches take 2 to 10 us on the GPU; reading a dozen tensors'
 // shapes, strides and pointers from Python and converting two dozen arguments
 // takes longer than that.  These functions make the same checks as attn.py and
-// call the same C ABI (include/rmsnorm_attn.h) on the current stream.  What
+// step.py and call the same C ABI (include/rmsnorm_attn.h) on the current stream.  What
 // they do not take (a tensor on another device than the current one, a wrong
 // shape, a refused call) they leave: they return None before anything is
-// launched, and attn.py makes the call, or raises the error, itself.
+// launched, and attn.py (or step.py) makes the call, or raises the error, itself.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -67,6 +67,17 @@ bool sequences(const Tensor& table, const Tensor& lengths, int64_t n, int64_t in
         return false;
     *stride = n > 1 ? table.stride(0) : table.size(1);
     return true;
+}
+
+// n contiguous int32, on the device, and their address (NULL: None).
+bool ints(PyObject* o, int64_t n, int64_t index) {
+    const Tensor* t = tensor(o);
+    return t && t->dim() == 1 && t->size(0) == n && t->scalar_type() == at::kInt && on_device(*t, index) &&
+           t->is_contiguous();
+}
+const int32_t* words(PyObject* o) {
+    const Tensor* t = tensor(o);
+    return t ? static_cast<const int32_t*>(t->const_data_ptr()) : nullptr;
 }
 
 // Tokens of [B, n, H, D] (or [B, H, D], n = 1): evenly spaced, heads back to back.
@@ -309,9 +320,209 @@ PyObject* qk_rope(PyObject*, PyObject* const* a, Py_ssize_t count) {
     }
 }
 
+// (q, cache, tensors, index, block_table, lengths, prefix_lengths, groups, scale, out, pdl) -> out
+PyObject* kv_prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    try {
+        const Tensor *q = count == 11 ? tensor(a[0]) : nullptr, *table = q ? tensor(a[4]) : nullptr,
+                     *lengths = table ? tensor(a[5]) : nullptr, *shared = lengths ? tensor(a[6]) : nullptr;
+        if (!shared || !PyBool_Check(a[10]) || (a[8] != Py_None && !PyFloat_Check(a[8]))) return leave();
+        const rmsattn_cache* cache = cache_at(a[1], a[2]);
+        const int64_t index = PyLong_AsLongLong(a[3]);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            return leave();
+        }
+        if (!cache || index < 0 || index != c10::cuda::current_device() || !on_device(*q, index)) return leave();
+        const int64_t d = q->dim();
+        if (d != 3 && d != 4) return leave();
+        const int64_t B = q->size(0), n = d == 4 ? q->size(1) : 1, H = q->size(d - 2), D = q->size(d - 1);
+        const at::ScalarType type = q->scalar_type();
+        if ((type != at::kBFloat16 && type != at::kHalf) || D != cache->head_dim || H < 1 ||
+            H % cache->n_kv_heads || n < 1 || n > RMSATTN_MAX_QUERIES)
+            return leave();
+        int64_t stride, qs, os = H * D;
+        if (!sequences(*table, *lengths, B, index, &stride) || !token_stride(*q, n, &qs)) return leave();
+        if (!ints(a[6], shared->dim() == 1 ? shared->size(0) : -1, index)) return leave();
+        const int64_t n_groups = shared->size(0);
+        if (a[7] == Py_None ? n_groups != 1 : !ints(a[7], n_groups + 1, index)) return leave();
+        Tensor out;
+        if (a[9] != Py_None) {
+            const Tensor* o = tensor(a[9]);
+            if (!o || !on_device(*o, index) || o->scalar_type() != type || o->sizes() != q->sizes() ||
+                !token_stride(*o, n, &os))
+                return leave();
+            out = *o;
+        }
+        const int64_t width = table->size(1);
+        const int64_t need = rmsattn_kv_prefix_attention_workspace(B, n, H, cache->n_kv_heads, D,
+                                                                   width * cache->page_size, n_groups);
+        if (need < 0) return leave();
+        if (!out.defined()) out = make(q->sizes(), type, index);
+        // freed when this returns, as above
+        Tensor ws = make({need}, at::kByte, index);
+        const double scale = a[8] == Py_None ? 1.0 / std::sqrt((double)D) : PyFloat_AS_DOUBLE(a[8]);
+        const int st = rmsattn_kv_prefix_attention(
+            q->const_data_ptr(), cache, static_cast<const int32_t*>(table->const_data_ptr()), stride, width,
+            static_cast<const int32_t*>(lengths->const_data_ptr()), words(a[6]), words(a[7]), n_groups,
+            out.mutable_data_ptr(), qs, os, B, n, H, (float)scale, ws.mutable_data_ptr(), need,
+            (uint32_t)dtype_flag(type) | (a[10] == Py_True ? RMSN_PDL : 0u), stream_of(index));
+        if (st != RMSN_OK) return leave();
+        if (a[9] != Py_None) {
+            Py_INCREF(a[9]);
+            return a[9];
+        }
+        return THPVariable_Wrap(out);
+    } catch (...) {
+        PyErr_Clear();
+        return leave();
+    }
+}
+
+// (free_pages, n_free, block_table, lengths, new_tokens, shared_pages, page_size, n_rows, pdl)
+//   -> (cu_seqlens, positions, slots, rows, before, after, n_free)
+PyObject* pages_step(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    try {
+        const Tensor *free_pages = count == 9 ? tensor(a[0]) : nullptr, *table = free_pages ? tensor(a[2]) : nullptr,
+                     *lengths = table ? tensor(a[3]) : nullptr;
+        if (!lengths || !PyLong_Check(a[6]) || !PyLong_Check(a[7]) || !PyBool_Check(a[8])) return leave();
+        const int64_t page = PyLong_AsLongLong(a[6]), T = PyLong_AsLongLong(a[7]);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            return leave();
+        }
+        if (!free_pages->is_cuda() || free_pages->dim() != 1 || lengths->dim() != 1) return leave();
+        const int64_t index = free_pages->get_device(), n = lengths->size(0), pages = free_pages->size(0);
+        int64_t stride;
+        if (index != c10::cuda::current_device() || !sequences(*table, *lengths, n, index, &stride) ||
+            !ints(a[0], pages, index) || !ints(a[1], 1, index) || !ints(a[4], n, index) ||
+            (a[5] != Py_None && !ints(a[5], n, index)) || T < 0 || page < RMSATTN_BLOCK)
+            return leave();
+        const int64_t need = rmsattn_pages_workspace(n);
+        // (a size that the library refuses is not allocated for)
+        if (need < 0 || T > (int64_t(1) << 29)) return leave();
+        Tensor out[7] = {make({n + 1}, at::kInt, index), make({T}, at::kInt, index), make({T}, at::kLong, index),
+                         make({T}, at::kInt, index),     make({n}, at::kInt, index), make({n}, at::kInt, index),
+                         make({1}, at::kInt, index)};
+        Tensor ws;
+        if (need > 0) ws = make({need}, at::kByte, index);
+        auto to = [&](int i) { return static_cast<int32_t*>(out[i].mutable_data_ptr()); };
+        const int st = rmsattn_pages_step(
+            const_cast<int32_t*>(words(a[0])), pages, words(a[1]),
+            static_cast<int32_t*>(table->mutable_data_ptr()), stride, table->size(1), words(a[3]), words(a[4]),
+            words(a[5]), n, page, T, to(0), to(1), static_cast<int64_t*>(out[2].mutable_data_ptr()), to(3), to(4),
+            to(5), to(6), need > 0 ? ws.mutable_data_ptr() : nullptr, need, a[8] == Py_True ? RMSN_PDL : 0u,
+            stream_of(index));
+        if (st != RMSN_OK) return leave();
+        PyObject* all = PyTuple_New(7);
+        for (int i = 0; all && i < 7; ++i) {
+            PyObject* o = THPVariable_Wrap(out[i]);
+            if (!o) {
+                Py_DECREF(all);
+                return nullptr;
+            }
+            PyTuple_SET_ITEM(all, i, o);
+        }
+        return all;
+    } catch (...) {
+        PyErr_Clear();
+        return leave();
+    }
+}
+
+// [rows, cols] of a type, contiguous, on the device
+bool matrix(const Tensor& t, int64_t rows, int64_t cols, at::ScalarType type, int64_t index) {
+    return t.dim() == 2 && t.size(0) == rows && t.size(1) == cols && t.scalar_type() == type &&
+           on_device(t, index) && t.is_contiguous();
+}
+
+// (x, residual, post_weight, weight, eps, gate, gate_index, residual_scale, weight_offset, out_dtype, out,
+//  residual_out, out_scale, pdl) -> (out, residual_out, out_scale)
+PyObject* block_norms(PyObject*, PyObject* const* a, Py_ssize_t count) {
+    try {
+        const Tensor *x = count == 14 ? tensor(a[0]) : nullptr, *residual = x ? tensor(a[1]) : nullptr;
+        if (!residual || !PyFloat_Check(a[4]) || !PyFloat_Check(a[7]) || !PyFloat_Check(a[8]) || !PyBool_Check(a[13]))
+            return leave();
+        if (!x->is_cuda() || x->dim() != 2) return leave();
+        const int64_t index = x->get_device(), T = x->size(0), H = x->size(1);
+        const at::ScalarType type = x->scalar_type(), rtype = residual->scalar_type();
+        int flags = dtype_flag(type);
+        if (flags < 0 || index != c10::cuda::current_device() || !matrix(*x, T, H, type, index) ||
+            (rtype != type && rtype != at::kFloat) || !matrix(*residual, T, H, rtype, index))
+            return leave();
+        bool fp8 = false;
+        if (a[9] != Py_None) {  // (x's own type is the other way's)
+            if (!PyUnicode_Check(a[9]) || PyUnicode_CompareWithASCIIString(a[9], "fp8") != 0) return leave();
+            fp8 = true;
+        }
+        const at::ScalarType otype = fp8 ? at::kByte : type;
+        const void *post = nullptr, *weight = nullptr, *gates = nullptr;
+        if (!weight_ok(a[2], H, type, index, &post) || !weight_ok(a[3], H, type, index, &weight)) return leave();
+        int64_t n_gates = 0, stride = 0;
+        if (a[5] == Py_None) {
+            if (a[6] != Py_None) return leave();
+        } else {
+            const Tensor* g = tensor(a[5]);
+            if (!g) return leave();
+            if (g->dim() == 1 && a[6] == Py_None) {
+                if (!weight_ok(a[5], H, type, index, &gates)) return leave();
+                n_gates = 1;
+            } else {
+                if (g->dim() != 2 || g->size(1) != H || g->scalar_type() != type || !on_device(*g, index) ||
+                    (H > 1 && g->stride(1) != 1))
+                    return leave();
+                n_gates = g->size(0);
+                stride = n_gates > 1 ? g->stride(0) : H;
+                if (stride < H || (a[6] == Py_None ? n_gates != T : !ints(a[6], T, index))) return leave();
+                gates = g->const_data_ptr();
+            }
+            if (!gates) return leave();
+        }
+        Tensor out[3];
+        for (int i = 0; i < 3; ++i) {
+            if (a[10 + i] == Py_None) continue;
+            const Tensor* o = tensor(a[10 + i]);
+            if (!o || (i == 2 ? !fp8 || o->dim() != 1 || o->size(0) != T || o->scalar_type() != at::kFloat ||
+                                    !on_device(*o, index) || !o->is_contiguous()
+                              : !matrix(*o, T, H, i == 0 ? otype : rtype, index)))
+                return leave();
+            out[i] = *o;
+        }
+        if (rtype != type) flags |= RMSN_RESIDUAL_F32;
+        if (fp8) flags |= RMSATTN_OUT_FP8;
+        if (a[13] == Py_True) flags |= RMSN_PDL;
+        if (!out[0].defined()) out[0] = make({T, H}, otype, index);
+        if (!out[1].defined()) out[1] = make({T, H}, rtype, index);
+        if (fp8 && !out[2].defined()) out[2] = make({T}, at::kFloat, index);
+        const int st = rmsattn_block_norms(
+            x->const_data_ptr(), residual->const_data_ptr(), post, weight, gates, stride, words(a[6]), n_gates,
+            out[0].mutable_data_ptr(), out[1].mutable_data_ptr(),
+            fp8 ? static_cast<float*>(out[2].mutable_data_ptr()) : nullptr, T, H, (float)PyFloat_AS_DOUBLE(a[4]),
+            (float)PyFloat_AS_DOUBLE(a[7]), (float)PyFloat_AS_DOUBLE(a[8]), (uint32_t)flags, stream_of(index));
+        if (st != RMSN_OK) return leave();
+        PyObject* all = PyTuple_New(3);
+        for (int i = 0; all && i < 3; ++i) {
+            PyObject* o = a[10 + i];
+            if (o != Py_None || !out[i].defined()) Py_INCREF(o);
+            else o = THPVariable_Wrap(out[i]);
+            if (!o) {
+                Py_DECREF(all);
+                return nullptr;
+            }
+            PyTuple_SET_ITEM(all, i, o);
+        }
+        return all;
+    } catch (...) {
+        PyErr_Clear();
+        return leave();
+    }
+}
+
 PyMethodDef methods[] = {
     {"qk_rope", (PyCFunction)(void (*)(void))qk_rope, METH_FASTCALL, nullptr},
     {"kv_append", (PyCFunction)(void (*)(void))kv_append, METH_FASTCALL, nullptr},
+    {"kv_prefix_attention", (PyCFunction)(void (*)(void))kv_prefix_attention, METH_FASTCALL, nullptr},
+    {"pages_step", (PyCFunction)(void (*)(void))pages_step, METH_FASTCALL, nullptr},
+    {"block_norms", (PyCFunction)(void (*)(void))block_norms, METH_FASTCALL, nullptr},
     {"kv_attention", (PyCFunction)(void (*)(void))kv_attention, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -1,39 +1,19 @@
 // C ABI of the attention-path operators (include/rmsnorm_attn.h): argument
 // checks, launch shapes and launches.
-#include <cuda_runtime.h>
 #include <math.h>
-#include <stdint.h>
 #include <string.h>
 
-#include <mutex>
-
-#include "../../include/rmsnorm_attn.h"
-#include "attn_args.h"
-
-#define RMSATTN_API extern "C" __attribute__((visibility("default")))
+#include "attn_host.h"
 
 namespace rmsattn {
 namespace {
 
-constexpr int kMaxDevices = 64;
-constexpr int64_t kMaxTokens = int64_t(1) << 29;  // tokens that a table's row may hold
-
 // Status word of the kernels on each device.
 __device__ uint32_t g_status;
 
-struct DeviceInfo {
-    std::once_flag once;
-    int num_sms = 0;
-    uint32_t* status = nullptr;
-    cudaError_t err = cudaSuccess;
-    std::mutex mu;
-    struct {
-        const void* fn;
-        int64_t blocks;
-    } resident[32];  // an attention kernel's resident blocks, once asked for
-    int n_resident = 0;
-};
 DeviceInfo g_dev[kMaxDevices];
+
+}  // namespace
 
 DeviceInfo* device_info() {
     int dev = 0;
@@ -46,25 +26,8 @@ DeviceInfo* device_info() {
     return d.err == cudaSuccess ? &d : nullptr;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// RMSN_IN_* of flags, or -1; `bytes`: its element size.
-int dtype_of(uint32_t flags, int64_t* bytes) {
-    const uint32_t in = flags & RMSN_IN_MASK;
-    if (in != RMSN_IN_F32 && in != RMSN_IN_BF16 && in != RMSN_IN_F16) return -1;
-    *bytes = in == RMSN_IN_F32 ? 4 : 2;
-    return (int)in;
-}
-
-// a * b without overflow for sizes (>= 0), saturating far above any memory.
-int64_t times(int64_t a, int64_t b) {
-    if (a != 0 && b > (INT64_MAX / 64) / a) return INT64_MAX / 64;
-    return a * b;
-}
-bool too_big(int64_t n) { return n >= INT64_MAX / 64; }
-
 int launch(const void* fn, dim3 grid, int threads, size_t smem, void* args, bool pdl,
-           cudaStream_t stream, int cluster = 1) {
+           cudaStream_t stream, int cluster) {
     void* list[] = {args};
     if (!pdl && cluster == 1)
         return cudaLaunchKernel(fn, grid, dim3(threads), list, smem, stream) == cudaSuccess
@@ -92,7 +55,6 @@ int launch(const void* fn, dim3 grid, int threads, size_t smem, void* args, bool
     return cudaLaunchKernelExC(&lc, fn, list) == cudaSuccess ? RMSN_OK : RMSN_ECUDA;
 }
 
-// The cache's shape and pointers; fills the kernels' form of it.
 int check_cache(const rmsattn_cache* c, Cache* out) {
     if (!c || c->reserved != 0) return RMSN_EINVAL;
     if (c->n_pages < 0 || c->n_pages > INT32_MAX || c->n_kv_heads < 1 || c->n_kv_heads > 4096)
@@ -124,7 +86,6 @@ int check_cache(const rmsattn_cache* c, Cache* out) {
     return RMSN_OK;
 }
 
-// Block table of n_seqs rows.
 int check_table(const int32_t* table, int64_t stride, int64_t width, int64_t n_seqs, int page) {
     if (width < 0 || stride < width || times(width, page) > kMaxTokens) return RMSN_EINVAL;
     if (too_big(times(n_seqs, stride))) return RMSN_EINVAL;
@@ -132,7 +93,6 @@ int check_table(const int32_t* table, int64_t stride, int64_t width, int64_t n_s
     return aligned(table, 4) ? RMSN_OK : RMSN_EALIGN;
 }
 
-}  // namespace
 }  // namespace rmsattn
 
 using namespace rmsattn;
@@ -296,9 +256,8 @@ RMSATTN_API int rmsattn_kv_append(const rmsattn_cache* cache, const void* k, con
                   &a, a.pdl, stream);
 }
 
-namespace {
+namespace rmsattn {
 
-// Sizes of an attention call, before any device is asked.
 int check_attend(int64_t n_seqs, int64_t n_queries, int64_t n_q_heads, int64_t n_kv_heads,
                  int64_t head_dim) {
     if (n_seqs < 0 || n_seqs > (1 << 24) || n_queries < 1 || n_queries > RMSATTN_MAX_QUERIES ||
@@ -307,10 +266,15 @@ int check_attend(int64_t n_seqs, int64_t n_queries, int64_t n_q_heads, int64_t n
     return head_dim == 64 || head_dim == 128 || head_dim == 256 ? RMSN_OK : RMSN_EUNSUPPORTED;
 }
 
-const AttendEntry* attend_entry_of(int dt, int64_t D, int64_t cols, int64_t tokens) {
+namespace {
+
+const AttendEntry* attend_entry_of(bool behind, int dt, int64_t D, int64_t cols, int64_t tokens) {
     int n = 0;
-    const AttendEntry* t = D == 64 ? attend_kernels_64(&n)
-                                   : (D == 128 ? attend_kernels_128(&n) : attend_kernels_256(&n));
+    const AttendEntry* t = nullptr;
+    if (behind)
+        t = D == 64 ? attend_behind_64(&n) : (D == 128 ? attend_behind_128(&n) : attend_behind_256(&n));
+    else
+        t = D == 64 ? attend_kernels_64(&n) : (D == 128 ? attend_kernels_128(&n) : attend_kernels_256(&n));
     // the fewest column tiles that hold all columns, or the most there are; of
     // those the first that takes rows of so many tokens
     const AttendEntry* best = nullptr;
@@ -321,41 +285,29 @@ const AttendEntry* attend_entry_of(int dt, int64_t D, int64_t cols, int64_t toke
     return best;
 }
 
-// Resident blocks of an entry on the device (its grid), or 0.
-int64_t attend_blocks(DeviceInfo* d, const AttendEntry* e) {
+}  // namespace
+
+int64_t resident_blocks(DeviceInfo* d, const void* fn, int threads, int smem, int per_sm) {
     std::lock_guard<std::mutex> lock(d->mu);
     for (int i = 0; i < d->n_resident; ++i)
-        if (d->resident[i].fn == e->fn) return d->resident[i].blocks;
+        if (d->resident[i].fn == fn) return d->resident[i].blocks;
     int bps = 0;
-    if (cudaFuncSetAttribute(e->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, e->smem) !=
-            cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&bps, e->fn, e->threads, e->smem) !=
-            cudaSuccess) {
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&bps, fn, threads, smem) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
     // no more than the shape was bounded for: both dtypes' kernels then have
     // the same grid, and so the same workspace
-    const int64_t n = (int64_t)(bps < e->per_sm ? bps : e->per_sm) * d->num_sms;
-    if (n > 0 && d->n_resident < 32) {
-        d->resident[d->n_resident].fn = e->fn;
+    const int64_t n = (int64_t)(bps < per_sm ? bps : per_sm) * d->num_sms;
+    if (n > 0 && d->n_resident < 64) {
+        d->resident[d->n_resident].fn = fn;
         d->resident[d->n_resident++].blocks = n;
     }
     return n;
 }
 
-// How a call's steps are shared out.
-struct Plan {
-    const AttendEntry* e;
-    int groups;      // column groups of a key head
-    int split;       // a row to `split` blocks of a cluster; 0: one line of all steps
-    int64_t blocks;  // of the grid; shares of the line
-    int join;        // threads of a block of the join
-    int64_t min_chunk;
-    int64_t workspace;
-};
-
-int plan_attend(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_t n_q_heads,
+int plan_attend(DeviceInfo* d, bool behind, int dt, int64_t n_seqs, int64_t n_queries, int64_t n_q_heads,
                 int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens, int64_t window,
                 int64_t sinks, Plan* p) {
     // the most tokens that a row's queries see, borders of steps included (no
@@ -383,8 +335,8 @@ int plan_attend(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
     // long as the first, 64 x 8192 152 against 149, 1 x 131072 121 against 52.
     for (int line = 0; line < 2; ++line) {
         // the line takes the first of the fitting kernels, whatever the rows
-        const AttendEntry* e = p->e = attend_entry_of(dt, head_dim, cols, line ? 0 : max_tokens);
-        const int64_t resident = attend_blocks(d, e);
+        const AttendEntry* e = p->e = attend_entry_of(behind, dt, head_dim, cols, line ? 0 : max_tokens);
+        const int64_t resident = resident_blocks(d, e->fn, e->threads, e->smem, e->per_sm);
         if (resident < 1) return RMSN_ECUDA;
         const int64_t warps = e->threads / 32;
         p->groups = (int)((cols + 8 * e->NT - 1) / (8 * e->NT));
@@ -425,7 +377,31 @@ int plan_attend(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
     return RMSN_OK;
 }
 
-}  // namespace
+void fill_attend(const Plan& p, int64_t n_queries, int64_t n_q_heads, AttendArgs* a) {
+    a->n = (int32_t)n_queries;
+    a->Hq = (int32_t)n_q_heads;
+    a->cols = (int32_t)(n_q_heads / a->c.H * n_queries);
+    a->group = (int32_t)(n_q_heads / a->c.H);
+    a->group_rcp = ((uint64_t(1) << 32) + a->group - 1) / a->group;
+    a->groups = p.groups;
+    a->page_rcp = ((uint64_t(1) << 37) + a->c.page / kBlock - 1) / (a->c.page / kBlock);
+    a->split = p.split;
+    while ((1 << a->split_log) < a->split) ++a->split_log;
+    a->shares = p.blocks;
+    a->min_chunk = p.min_chunk;
+}
+
+int launch_attend(const Plan& p, AttendArgs* a, bool pdl, cudaStream_t stream) {
+    const int st = launch(p.e->fn, dim3((unsigned)p.blocks), p.e->threads, (size_t)p.e->smem, a, pdl,
+                          stream, p.split > 1 ? p.split : 1);
+    if (st != RMSN_OK || p.split > 0 || p.blocks == 1) return st;
+    // always behind the stream's own kernel: a programmatic dependent of it
+    const int used = a->cols < 8 * p.e->NT ? a->cols : 8 * p.e->NT;
+    return launch(p.e->join, dim3((unsigned)(p.blocks - 1), (unsigned)(used + 3) / 4), p.join, 0, a, true,
+                  stream);
+}
+
+}  // namespace rmsattn
 
 RMSATTN_API int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_queries,
                                                    int64_t n_q_heads, int64_t n_kv_heads,
@@ -438,7 +414,7 @@ RMSATTN_API int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_que
     DeviceInfo* d = device_info();
     if (!d) return RMSN_ECUDA;
     Plan p;  // both dtypes' kernels have the same shape
-    const int sp = plan_attend(d, RMSN_IN_BF16, n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim,
+    const int sp = plan_attend(d, false, RMSN_IN_BF16, n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim,
                                max_tokens, window, sinks, &p);
     return sp == RMSN_OK ? p.workspace : sp;
 }
@@ -479,7 +455,7 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     DeviceInfo* d = device_info();
     if (!d) return RMSN_ECUDA;
     Plan p;
-    st = plan_attend(d, dt, n_seqs, n_queries, n_q_heads, a.c.H, a.c.D, table_width * a.c.page,
+    st = plan_attend(d, false, dt, n_seqs, n_queries, n_q_heads, a.c.H, a.c.D, table_width * a.c.page,
                      window, sinks, &p);
     if (st != RMSN_OK) return st;
     if (p.workspace > 0 && (!workspace || workspace_bytes < p.workspace)) return RMSN_EINVAL;
@@ -496,31 +472,15 @@ RMSATTN_API int rmsattn_kv_attention(const void* q, const rmsattn_cache* cache,
     a.table_width = table_width;
     a.lengths = lengths;
     a.B = n_seqs;
-    a.n = (int32_t)n_queries;
-    a.Hq = (int32_t)n_q_heads;
     a.scale = scale;
     // wider than any position: every earlier token
     a.window = window >= kMaxTokens ? 0 : (int32_t)window;
     a.sinks = (int32_t)(sinks > kMaxTokens ? kMaxTokens : sinks);
     a.pdl = (flags & RMSN_PDL) ? 1 : 0;
     a.status = d->status;
-    a.cols = (int32_t)(n_q_heads / a.c.H * n_queries);
-    a.group = (int32_t)(n_q_heads / a.c.H);
-    a.group_rcp = ((uint64_t(1) << 32) + a.group - 1) / a.group;
-    a.groups = p.groups;
-    a.page_rcp = ((uint64_t(1) << 37) + a.c.page / kBlock - 1) / (a.c.page / kBlock);
-    a.split = p.split;
-    while ((1 << a.split_log) < a.split) ++a.split_log;
-    a.shares = p.blocks;
-    a.min_chunk = p.min_chunk;
     a.ws = static_cast<char*>(workspace);
-    st = launch(p.e->fn, dim3((unsigned)p.blocks), p.e->threads, (size_t)p.e->smem, &a, a.pdl,
-                stream, p.split > 1 ? p.split : 1);
-    if (st != RMSN_OK || p.split > 0 || p.blocks == 1) return st;
-    // always behind the stream's own kernel: a programmatic dependent of it
-    const int used = a.cols < 8 * p.e->NT ? a.cols : 8 * p.e->NT;
-    return launch(p.e->join, dim3((unsigned)(p.blocks - 1), (unsigned)(used + 3) / 4), p.join, 0,
-                  &a, true, stream);
+    fill_attend(p, n_queries, n_q_heads, &a);
+    return launch_attend(p, &a, a.pdl, stream);
 }
 
 RMSATTN_API int rmsattn_read_status(uint32_t* status, int clear) {

@@ -60,6 +60,93 @@ struct AppendArgs {
     uint32_t* status;
 };
 
+// A serving step's plan; `more`: the tokens that each sequence gets (negative:
+// it is finished).
+struct PagesArgs {
+    int32_t* free_pages;
+    const int32_t* n_free;
+    int32_t* table;
+    int64_t table_stride, width, n_pages;
+    const int32_t* lengths;
+    const int32_t* more;
+    const int32_t* shared;  // pages of a row that are not the sequence's own, or NULL
+    int64_t B, T;
+    int32_t page, pdl;
+    int32_t *cu, *positions, *rows, *before, *after, *n_free_out;
+    int64_t* slots;
+    int32_t* ws;
+    uint32_t* status;
+};
+constexpr int64_t kPagesOnce = 2048;  // sequences that one launch takes
+// 0: one launch; 1, 2: the scan and the rows
+const void* pages_kernel_of(int which);
+
+// The norms at a block's end; gate_stride 0: one row for all.
+struct NormsArgs {
+    const void *x, *residual, *post_w, *w, *gate;
+    const int32_t* index;  // a row's gate row; negative: the row is left out
+    void *out, *residual_out;
+    float* out_scale;
+    int64_t T, gate_stride, n_gates;
+    int32_t H, pdl;
+    float eps, alpha, w_off;
+    uint32_t* status;
+};
+// v elements to a vector, ch vectors to a thread (v = 1, ch = 0: any row)
+const void* norms_kernel_of(int dt, bool r32, bool fp8, int v, int ch);
+
+// A group of sequences [s0, s1) that share their first `shared` tokens: `tiles`
+// row tiles of kPrefixRows columns (sequence x query token x head) for each key
+// head, an item each, from item0 on; an item is ns steps, the group's items lie
+// one behind the other on the line of all steps from `first` on.
+struct PrefixGroup {
+    int32_t s0, s1, shared;
+    int32_t seq;  // the sequence whose table row names the shared pages
+    int32_t ns, first, item0, tiles;
+};
+constexpr int kPrefixRows = 128;
+
+// The line of the shared parts: total steps, and the steps of a share.
+struct PrefixLine {
+    int32_t total, chunk, pad[2];
+};
+// A sequence's shared tokens (0: it does not share) and its group.
+struct PrefixSeq {
+    int32_t start, group;
+};
+
+struct PrefixArgs {
+    Cache c;
+    const void* q;
+    int64_t q_stride;
+    const int32_t* table;
+    int64_t table_stride, table_width;
+    const int32_t* lengths;
+    const int32_t* cu;      // borders of the groups, or NULL: one group of all
+    const int32_t* shared;  // tokens that each group shares
+    int64_t B;
+    int32_t n_groups, n, group;  // group: query heads of a key head
+    int32_t tok;                 // tokens of a step
+    int32_t shares, min_chunk;
+    int32_t pdl;
+    float scale;
+    uint64_t page_rcp;  // ceil(2^37 / (page / 16))
+    uint32_t* status;
+    PrefixLine* line;
+    PrefixGroup* groups;
+    PrefixSeq* seqs;
+    float* parts;  // one for each pair of a share and an item that it meets
+};
+// Floats of a part: sums [D / 8][kPrefixRows][8], then reference and weight of each row.
+__host__ __device__ constexpr int64_t prefix_part(int D) { return (int64_t)kPrefixRows * (D + 2); }
+
+struct PrefixEntry {
+    int32_t dt, D, tok, threads, smem;
+    const void* fn;
+};
+const void* prefix_plan_kernel();
+const PrefixEntry* prefix_kernels(int* n);
+
 struct AttendArgs {
     Cache c;
     const void* q;
@@ -84,6 +171,11 @@ struct AttendArgs {
     int64_t shares;     // of the line, one for each block
     int64_t min_chunk;  // steps of a share, at least
     char* ws;           // a Cut and two parts for every share
+    // behind a shared prefix: its parts
+    const PrefixLine* line;
+    const PrefixGroup* prefix;
+    const PrefixSeq* seqs;
+    const float* parts;
 };
 
 constexpr int64_t kCutBytes = 32;
@@ -101,6 +193,10 @@ struct AttendEntry {
 const AttendEntry* attend_kernels_64(int* n);
 const AttendEntry* attend_kernels_128(int* n);
 const AttendEntry* attend_kernels_256(int* n);
+// the same for sequences that begin behind a shared prefix
+const AttendEntry* attend_behind_64(int* n);
+const AttendEntry* attend_behind_128(int* n);
+const AttendEntry* attend_behind_256(int* n);
 
 // dt: 0 fp32, 1 bf16, 2 fp16 (the RMSN_IN_* values)
 const void* rope_generic_kernel(int dt);

@@ -187,9 +187,10 @@ struct Span {
     int jump;   // step numbers from n_sink on are this much higher
     int ns;     // steps, at least 1
 
-    __device__ __forceinline__ void of(const AttendArgs& a, int len) {
-        L = len < 0 ? 0 : len;
-        const int room = (int)(a.table_width * a.c.page);
+    // tokens are counted from `start` on (a multiple of 16)
+    __device__ __forceinline__ void of(const AttendArgs& a, int len, int start = 0) {
+        L = len < 0 ? 0 : len - start;
+        const int room = (int)(a.table_width * a.c.page) - start;
         end = L < room ? L : room;
         lo = 0;
         sink = a.sinks < end ? a.sinks : end;
@@ -246,9 +247,16 @@ __device__ __forceinline__ int64_t chunk_of(const AttendArgs& a, int64_t total) 
     return c < a.min_chunk ? a.min_chunk : c;
 }
 
+// First token of sequence b that is not in a shared prefix.
+template <bool PRE>
+__device__ __forceinline__ int start_of(const AttendArgs& a, int64_t b) {
+    if constexpr (PRE) return a.seqs[b].start;
+    else return 0;
+}
+
 // Every thread of the block calls this.  Sequences are scanned THREADS at a
 // time; up to THREADS of them (any usual batch) are scanned once.
-template <int TOK, int THREADS>
+template <int TOK, int THREADS, bool PRE>
 __device__ __forceinline__ void find_share(const AttendArgs& a, Line* line) {
     __shared__ int64_t sums[THREADS / 32], found[3];
     constexpr int NW = THREADS / 32;
@@ -263,7 +271,7 @@ __device__ __forceinline__ void find_share(const AttendArgs& a, Line* line) {
             int64_t ns = 0;
             if (b < a.B) {
                 Span<TOK> s;
-                s.of(a, a.lengths[b]);
+                s.of(a, a.lengths[b], start_of<PRE>(a, b));
                 ns = s.ns;
             }
             int64_t inc = ns;
@@ -355,10 +363,58 @@ __device__ __forceinline__ void read8(float4 (&v)[2], const float* row, int d) {
     v[0] = *reinterpret_cast<const float4*>(row + unit_at(d));
     v[1] = *reinterpret_cast<const float4*>(row + unit_at(d + 4));
 }
+// Adds the shared prefix's parts to a column's: y its sums of dims d to d + 7
+// and l its weights' sum, both taken with reference mx.  The parts lie in the
+// order of the line's shares.
+__device__ __forceinline__ void add_prefix(const AttendArgs& a, int64_t b, int hk, const Col& c, int d,
+                                           float (&y)[8], float& l, float mx) {
+    const PrefixSeq sq = a.seqs[b];
+    if (sq.start == 0) return;
+    const PrefixGroup g = a.prefix[sq.group];
+    const uint32_t chunk = a.line->chunk;
+    const int cc = (((int)b - g.s0) * a.n + c.qi) * a.group + c.head - hk * a.group;
+    const int item = hk * g.tiles + cc / kPrefixRows, row = cc % kPrefixRows;
+    const uint32_t at = (uint32_t)g.first + (uint32_t)item * (uint32_t)g.ns;
+    const int i0 = (int)(at / chunk), n = (int)((at + (uint32_t)g.ns - 1) / chunk) - i0 + 1;
+    const int64_t size = prefix_part(a.c.D);
+    const float* p = a.parts + (i0 + g.item0 + item) * size;
+    const int at_y = d * kPrefixRows + row * 8, at_ml = a.c.D * kPrefixRows + row * 2;
+    constexpr int U = 4;
+    for (int k0 = 0; k0 < n; k0 += U) {
+        float2 ml[U];
+        float4 v[U][2];
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            ml[k] = make_float2(kNone, 0.f);
+            v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k0 + k >= n) continue;
+            const float* q = p + (k0 + k) * size;
+            ml[k] = *reinterpret_cast<const float2*>(q + at_ml);
+            v[k][0] = *reinterpret_cast<const float4*>(q + at_y);
+            v[k][1] = *reinterpret_cast<const float4*>(q + at_y + 4);
+        }
+        float to = mx;
+#pragma unroll
+        for (int k = 0; k < U; ++k) to = fmaxf(to, ml[k].x);
+        const float keep = exp2a(mx - to);
+        mx = to;
+        l *= keep;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] *= keep;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const float f = exp2a(ml[k].x - mx);
+            l += ml[k].y * f;
+            add8(y, v[k], f);
+        }
+    }
+}
+
 // Eight dims of a row's sums over its weights' sum; nothing seen gives 0.
-template <class T>
-__device__ __forceinline__ void finish8(const AttendArgs& a, int64_t b, const Col& c, int d,
-                                        float (&y)[8], float l) {
+template <class T, bool PRE>
+__device__ __forceinline__ void finish8(const AttendArgs& a, int64_t b, int hk, const Col& c, int d,
+                                        float (&y)[8], float l, float mx) {
+    if constexpr (PRE) add_prefix(a, b, hk, c, d, y, l, mx);
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] = l == 0.f ? 0.f : y[k] / l;
     store8<T>(a, b, c, d, y);
@@ -457,7 +513,7 @@ __device__ __forceinline__ void add_tile(F2 (&o)[C::D / 16][C::NT][2], const uin
 
 // A block's warps take the steps of its share in turn, and are joined where a
 // row ends.
-template <class T, class C>
+template <class T, class C, bool PRE = false>
 __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArgs a) {
     constexpr int D = C::D, NT = C::NT, KT = C::KT, W = C::W;
     constexpr int CH = D / 16;                 // 16-byte chunks of a token
@@ -486,14 +542,14 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
         at.hc = (int)(row % HC);
         at.first = 0;
         Span<C::kTok> s;
-        s.of(a, a.lengths[at.b]);
+        s.of(a, a.lengths[at.b], start_of<PRE>(a, at.b));
         const int per = (s.ns + a.split - 1) >> a.split_log;
         begin = (int64_t)((int)blockIdx.x & (a.split - 1)) * per;
         const int left = s.ns - (int)begin;
         count = left < 0 ? 0 : (left < per ? left : per);
     } else {
         Line line;
-        find_share<C::kTok, W * 32>(a, &line);
+        find_share<C::kTok, W * 32, PRE>(a, &line);
         begin = line.at;
         chunk = line.chunk;
         at = line.row;
@@ -568,8 +624,13 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     int p_at = wp, p_first = (int)(at.first - begin), p_hc = at.hc;  // places relative to begin
     int64_t p_b = at.b;
     Span<C::kTok> p_span;
-    p_span.of(a, a.lengths[p_b]);
-    int p_len_next = p_b + 1 < a.B ? a.lengths[p_b + 1] : 0;
+    int p_start = start_of<PRE>(a, p_b), p_start_next = 0;
+    p_span.of(a, a.lengths[p_b], p_start);
+    int p_len_next = 0;
+    if (p_b + 1 < a.B) {
+        p_len_next = a.lengths[p_b + 1];
+        p_start_next = start_of<PRE>(a, p_b + 1);
+    }
     const int32_t* p_row = a.table + p_b * a.table_stride;
     int b_n = 0, b_at = 0, next_n = 0, next_hk = 0;
     int32_t next_page[KT];
@@ -585,8 +646,12 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                 p_hc = 0;
                 ++p_b;
                 p_row += a.table_stride;
-                p_span.of(a, p_len_next);
-                p_len_next = p_b + 1 < a.B ? a.lengths[p_b + 1] : 0;
+                p_start = p_start_next;
+                p_span.of(a, p_len_next, p_start);
+                if (p_b + 1 < a.B) {
+                    p_len_next = a.lengths[p_b + 1];
+                    p_start_next = start_of<PRE>(a, p_b + 1);
+                }
             }
         }
         const int end = p_first + p_span.ns < count ? p_first + p_span.ns : count;
@@ -599,9 +664,10 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
             const int j = t0 + 16 * k;
             const bool any = lane < next_n && j < p_span.end && (j + 15 >= p_span.lo || j < p_span.sink);
             // slot = j / page, both multiples of 16: exact for j < 2^29
-            const int slot = (int)(((uint64_t)(uint32_t)(j >> 4) * a.page_rcp) >> 37);
+            const int at = PRE ? j + p_start : j;
+            const int slot = (int)(((uint64_t)(uint32_t)(at >> 4) * a.page_rcp) >> 37);
             next_page[k] = any ? p_row[slot] : -1;  // end lies within the table
-            next_where[k] = (uint32_t)((j - slot * a.c.page) >> 4) |
+            next_where[k] = (uint32_t)((at - slot * a.c.page) >> 4) |
                             (any ? p_span.open(a, j) | (p_span.rows(j) << 16) : 0u);
         }
         p_at += next_n * W;
@@ -720,8 +786,12 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
     int64_t c_b = at.b;
     int c_first = (int)(at.first - begin), c_hc = at.hc;
     Span<C::kTok> span;
-    span.of(a, a.lengths[c_b]);
-    int c_len_next = c_b + 1 < a.B ? a.lengths[c_b + 1] : 0;
+    span.of(a, a.lengths[c_b], start_of<PRE>(a, c_b));
+    int c_len_next = 0, c_start_next = 0;
+    if (c_b + 1 < a.B) {
+        c_len_next = a.lengths[c_b + 1];
+        c_start_next = start_of<PRE>(a, c_b + 1);
+    }
     do {  // once at least: a block of a cluster may have no steps
         const int row_end = c_first + span.ns;
         // (a cluster's block works on one row, and may lie behind its end)
@@ -1109,7 +1179,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                     add8(y, v, f);
                 }
                 if (whole) {
-                    finish8<T>(a, row_b, col, d, y, lsum);
+                    finish8<T, PRE>(a, row_b, hk, col, d, y, lsum, mx);
                 } else if (a.split > 0) {
                     // to the block that finishes these dims, each sender its place
                     const int rank = (int)blockIdx.x & (a.split - 1);
@@ -1156,15 +1226,18 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                     lsum += ml[r].y * f;
                     add8(y, from + 2 * r, f);
                 }
-                finish8<T>(a, row_b, col, d, y, lsum);
+                finish8<T, PRE>(a, row_b, hk, col, d, y, lsum, mx);
             }
         }
         cur = seg_end;
         if (!last) {
             c_first = row_end;
             if (c_b != row_b) {
-                span.of(a, c_len_next);
-                c_len_next = c_b + 1 < a.B ? a.lengths[c_b + 1] : 0;
+                span.of(a, c_len_next, c_start_next);
+                if (c_b + 1 < a.B) {
+                    c_len_next = a.lengths[c_b + 1];
+                    c_start_next = start_of<PRE>(a, c_b + 1);
+                }
             }
         }
     } while (cur < count);
@@ -1177,7 +1250,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
 // that take the parts in turn.  A thread takes up to eight parts at a time,
 // their references and sums and values all on their way at once: the launch
 // is a chain of latencies (Cut, parts, join of the groups), not of bytes.
-template <class T, class C>
+template <class T, class C, bool PRE = false>
 __global__ void __launch_bounds__(512) attend_join_kernel(const AttendArgs a) {
     constexpr int D = C::D, NG = 512 / D, U = 8;
     const int groups = blockDim.x / D;
@@ -1242,10 +1315,10 @@ __global__ void __launch_bounds__(512) attend_join_kernel(const AttendArgs a) {
         ls += total[k][oc] * f;
         add8(r, &sum[k][oc * (D / 4) + 2 * od], f);
     }
-    finish8<T>(a, cut.b, col, od * 8, r, ls);
+    finish8<T, PRE>(a, cut.b, hk, col, od * 8, r, ls, mx);
 }
 
-template <class C>
+template <class C, bool PRE = false>
 AttendEntry attend_entry(int dt, int most = INT32_MAX) {
     AttendEntry e;
     e.dt = dt;
@@ -1257,9 +1330,10 @@ AttendEntry attend_entry(int dt, int most = INT32_MAX) {
     e.threads = C::W * 32;
     e.smem = C::kSmem;
     e.part = C::kCols * (C::D + 2);
-    e.fn = dt == 1 ? (const void*)&attend_kernel<BF16, C> : (const void*)&attend_kernel<F16, C>;
-    e.join = dt == 1 ? (const void*)&attend_join_kernel<BF16, C>
-                     : (const void*)&attend_join_kernel<F16, C>;
+    e.fn = dt == 1 ? (const void*)&attend_kernel<BF16, C, PRE>
+                   : (const void*)&attend_kernel<F16, C, PRE>;
+    e.join = dt == 1 ? (const void*)&attend_join_kernel<BF16, C, PRE>
+                     : (const void*)&attend_join_kernel<F16, C, PRE>;
     return e;
 }
 

@@ -1,0 +1,309 @@
+// A serving step's plan from the requests' lengths: pages returned and taken,
+// block table, positions, slots.
+//
+// What bounds it: latency.  A step of 1024 sequences reads 12 KB and writes 30;
+// the chain is lengths -> two scans -> free list -> stores.  So one launch, and
+// no exchange between blocks: with up to kPagesOnce sequences every block scans
+// all of them for itself into shared memory (12 bytes a sequence from L2) and
+// then plans its own rows.  Larger batches scan once, in a first launch of one
+// block, into the workspace.
+//
+// Nothing that a block writes is read by another one: the free list is read
+// below n_free and written from there on, the table's new entries are found from
+// the free list again by every row that needs them, and the count goes out to a
+// word of its own.  The same inputs thus give the same results however often the
+// call is made.
+#include "attn_common.cuh"
+
+namespace rmsattn {
+
+namespace {
+
+// What the scan leaves for a sequence.
+//   cu     its first row, at most T
+//   base   pages taken by earlier sequences; -1: left out, finished or empty
+//   back   pages returned by earlier sequences, at most n_pages
+struct Scan {
+    int32_t *cu, *base, *back;  // cu and back: one more, behind the last
+    int32_t top;                // free pages once all are returned
+    int32_t left;               // free pages in the end
+    int32_t count;              // free pages before
+};
+
+__device__ __forceinline__ int64_t ceil_div(int64_t a, int32_t b) { return (a + b - 1) / b; }
+
+// A sequence as the scan sees it.
+struct Seq {
+    int64_t len, more, has, need, back;
+    bool live, done;
+    __device__ __forceinline__ void of(const PagesArgs& a, int64_t s) {
+        len = a.lengths[s];
+        const int64_t n = a.more[s];
+        live = len >= 0;
+        done = live && n < 0;
+        more = live && n > 0 ? n : 0;
+        if (len < 0) len = 0;
+        has = ceil_div(len, a.page);
+        need = ceil_div(len + more, a.page);
+        back = 0;
+        if (done) {
+            const int64_t own = has < a.width ? has : a.width, first = kept(a, s);
+            back = own > first ? own - first : 0;
+        }
+    }
+    // pages that a finished sequence leaves where they are
+    static __device__ __forceinline__ int64_t kept(const PagesArgs& a, int64_t s) {
+        const int64_t k = a.shared ? a.shared[s] : 0;
+        return k > 0 ? k : 0;
+    }
+    __device__ __forceinline__ bool fits(const PagesArgs& a, int64_t begin) const {
+        return live && !done && need <= a.width && begin + more <= a.T && len + more <= INT32_MAX;
+    }
+    __device__ __forceinline__ int64_t take() const { return need - has; }
+};
+
+// Exclusive sum over the block of one value a thread, and the total.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t* total) {
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    int64_t inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    __syncthreads();  // an earlier scan's sums have been read
+    if (lane == 31) sums[wp] = inc;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w < wp) before += sums[w];
+        all += sums[w];
+    }
+    *total = all;
+    return before + inc - v;
+}
+
+__device__ __forceinline__ int32_t clamp_to(int64_t v, int64_t most) {
+    return (int32_t)(v < most ? v : most);
+}
+
+// All sequences, a run of them to each thread.
+__device__ __forceinline__ void scan(const PagesArgs& a, Scan* sc) {
+    __shared__ int64_t sums[32];
+    __shared__ int32_t most[32];
+    const int64_t per = (a.B + blockDim.x - 1) / blockDim.x, s0 = threadIdx.x * per;
+    const int64_t s1 = s0 + per < a.B ? s0 + per : a.B;
+    int64_t count = *a.n_free;
+    count = count < 0 ? 0 : (count < a.n_pages ? count : a.n_pages);
+    int64_t rows = 0, back = 0;
+    for (int64_t s = s0; s < s1; ++s) {
+        Seq q;
+        q.of(a, s);
+        rows += q.more;
+        back += q.back;
+    }
+    int64_t all_rows, all_back, all_taken;
+    int64_t begin = block_scan(rows, sums, &all_rows), from = block_scan(back, sums, &all_back);
+    const int64_t top = count + all_back < a.n_pages ? count + all_back : a.n_pages;
+    if (count + all_back > a.n_pages && threadIdx.x == 0) atomicOr(a.status, kBadPage);
+    int64_t taken = 0;
+    {
+        int64_t b = begin;
+        for (int64_t s = s0; s < s1; ++s) {
+            Seq q;
+            q.of(a, s);
+            if (q.fits(a, b)) taken += q.take();
+            b += q.more;
+        }
+    }
+    int64_t at = block_scan(taken, sums, &all_taken), out = 0;
+    for (int64_t s = s0; s < s1; ++s) {
+        Seq q;
+        q.of(a, s);
+        sc->cu[s] = clamp_to(begin, a.T);
+        sc->back[s] = clamp_to(from, a.n_pages);
+        int32_t base = -1;
+        if (q.fits(a, begin)) {
+            const int64_t n = q.take();
+            if (n == 0 || at + n <= top) {
+                base = clamp_to(at, INT32_MAX);
+                if (n > 0) out = at + n;
+            }
+            at += n;
+        }
+        sc->base[s] = base;
+        begin += q.more;
+        from += q.back;
+    }
+    if (s1 == a.B && s0 < s1) {
+        sc->cu[a.B] = clamp_to(begin, a.T);
+        sc->back[a.B] = clamp_to(from, a.n_pages);
+    }
+    if (a.B == 0 && threadIdx.x == 0) sc->cu[0] = sc->back[0] = 0;
+    // the last page that went out
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    int32_t m = (int32_t)out;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const int32_t v = __shfl_xor_sync(0xFFFFFFFFu, m, o);
+        m = v > m ? v : m;
+    }
+    if (lane == 0) most[wp] = m;
+    __syncthreads();
+    for (int w = 0; w < nw; ++w) m = most[w] > m ? most[w] : m;
+    sc->count = (int32_t)count;
+    sc->top = (int32_t)top;
+    sc->left = (int32_t)(top - m);
+}
+
+// The last of v[0 .. n - 1] (non-decreasing, v[0] <= x) that is at most x.
+__device__ __forceinline__ int64_t last_at_most(const int32_t* v, int64_t n, int32_t x) {
+    int64_t lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (v[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Entry i of the free pages with the returned ones behind them.
+__device__ __forceinline__ int32_t page_at(const PagesArgs& a, const Scan& sc, int32_t i) {
+    if (i < sc.count) return a.free_pages[i];
+    const int32_t f = i - sc.count;
+    const int64_t s = last_at_most(sc.back, a.B, f);
+    return a.table[s * a.table_stride + Seq::kept(a, s) + f - sc.back[s]];
+}
+
+__device__ __forceinline__ void plan_rows(const PagesArgs& a, const Scan& sc) {
+    const int64_t threads = (int64_t)gridDim.x * blockDim.x, me = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
+    // sequences
+    for (int64_t s = me; s < a.B; s += threads) {
+        Seq q;
+        q.of(a, s);
+        const bool ok = sc.base[s] >= 0;
+        a.cu[s] = sc.cu[s];
+        a.before[s] = ok ? (int32_t)q.len : -1;
+        a.after[s] = q.done ? 0 : (ok ? (int32_t)(q.len + q.more) : a.lengths[s]);
+    }
+    if (me == 0) {
+        a.cu[a.B] = sc.cu[a.B];
+        *a.n_free_out = sc.left;
+    }
+    // returned pages, a warp to a sequence
+    for (int64_t s = me >> 5; s < a.B; s += threads >> 5) {
+        const int32_t f0 = sc.back[s], f1 = sc.back[s + 1];
+        if (f0 == f1) continue;
+        const int32_t* row = a.table + s * a.table_stride + Seq::kept(a, s);
+        for (int32_t f = f0 + (threadIdx.x & 31); f < f1; f += 32) {
+            const int32_t p = row[f - f0];
+            if ((uint32_t)p >= (uint32_t)a.n_pages) atomicOr(a.status, kBadPage);
+            if (sc.count + f < sc.left) a.free_pages[sc.count + f] = p;
+        }
+    }
+    // rows, four to a thread
+    const int32_t all = sc.cu[a.B];
+    for (int64_t t0 = me * 4; t0 < a.T; t0 += threads * 4) {
+        int32_t pos[4], row[4];
+        int64_t slot[4];
+        int64_t s = t0 < all ? last_at_most(sc.cu, a.B, (int32_t)t0) : 0;
+        int64_t at = -1;  // the sequence that len and has are of
+        int64_t len = 0, has = 0;
+        int32_t base = -1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int32_t t = (int32_t)(t0 + k);
+            pos[k] = 0;
+            row[k] = -1;
+            slot[k] = -1;
+            if (t >= all) continue;
+            while (sc.cu[s + 1] <= t) ++s;
+            if (s != at) {
+                at = s;
+                len = a.lengths[s];
+                has = ceil_div(len, a.page);
+                base = sc.base[s];
+            }
+            const int64_t p = len + (t - sc.cu[s]);
+            pos[k] = (int32_t)p;
+            row[k] = (int32_t)s;
+            if (base < 0) continue;
+            const int64_t j = p / a.page;
+            int32_t* entry = a.table + s * a.table_stride + j;
+            int32_t page;
+            if (j < has) {
+                page = *entry;
+            } else {
+                page = page_at(a, sc, sc.top - 1 - (base + (int32_t)(j - has)));
+                if (p == j * a.page) *entry = page;  // the page's first row brings it in
+            }
+            if ((uint32_t)page < (uint32_t)a.n_pages) slot[k] = (int64_t)page * a.page + (p - j * a.page);
+            else atomicOr(a.status, kBadPage);
+        }
+        if (t0 + 4 <= a.T) {
+            *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            *reinterpret_cast<int4*>(a.rows + t0) = make_int4(row[0], row[1], row[2], row[3]);
+            *reinterpret_cast<longlong2*>(a.slots + t0) = make_longlong2(slot[0], slot[1]);
+            *reinterpret_cast<longlong2*>(a.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (t0 + k >= a.T) break;
+                a.positions[t0 + k] = pos[k];
+                a.rows[t0 + k] = row[k];
+                a.slots[t0 + k] = slot[k];
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(512) pages_kernel(const PagesArgs a) {
+    extern __shared__ int32_t seqs[];
+    rmsn::pdl_wait(a.pdl);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Scan sc;
+    sc.cu = seqs;
+    sc.back = seqs + a.B + 1;
+    sc.base = seqs + 2 * (a.B + 1);
+    scan(a, &sc);
+    __syncthreads();
+    plan_rows(a, sc);
+}
+
+// The workspace: three counts, then cu, back and base.
+__global__ void __launch_bounds__(1024) pages_scan_kernel(const PagesArgs a) {
+    rmsn::pdl_wait(a.pdl);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Scan sc;
+    sc.cu = a.ws + 4;
+    sc.back = sc.cu + a.B + 1;
+    sc.base = sc.back + a.B + 1;
+    scan(a, &sc);
+    if (threadIdx.x == 0) {
+        a.ws[0] = sc.top;
+        a.ws[1] = sc.left;
+        a.ws[2] = sc.count;
+    }
+}
+
+__global__ void __launch_bounds__(512) pages_rows_kernel(const PagesArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Scan sc;
+    sc.cu = a.ws + 4;
+    sc.back = sc.cu + a.B + 1;
+    sc.base = sc.back + a.B + 1;
+    sc.top = a.ws[0];
+    sc.left = a.ws[1];
+    sc.count = a.ws[2];
+    plan_rows(a, sc);
+}
+
+}  // namespace
+
+const void* pages_kernel_of(int which) {
+    return which == 0 ? (const void*)&pages_kernel
+                      : (which == 1 ? (const void*)&pages_scan_kernel : (const void*)&pages_rows_kernel);
+}
+
+}  // namespace rmsattn

@@ -1,0 +1,109 @@
+// Attention with a shared prefix: which sequences share how much, and the line of
+// the shared parts' steps (PrefixGroup).  One block; a warp to a group.
+#include "attn_common.cuh"
+
+namespace rmsattn {
+
+namespace {
+
+constexpr int kThreads = 512;
+
+// A sequence shares a prefix if each of its queries sees all of it.
+__device__ __forceinline__ bool shares(const PrefixArgs& a, int64_t b, int shared) {
+    return a.lengths[b] - a.n + 1 >= shared;
+}
+
+__global__ void __launch_bounds__(kThreads) prefix_plan(const PrefixArgs a) {
+    __shared__ int64_t sums[2][kThreads / 32];
+    rmsn::pdl_wait(a.pdl);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+    const PrefixSeq alone = {0, 0};
+    for (int64_t b = threadIdx.x; b < a.B; b += kThreads) a.seqs[b] = alone;
+    // borders that are out of order, or of other sequences: nobody shares
+    bool bad = false;
+    if (a.cu) {
+        for (int g = threadIdx.x; g < a.n_groups; g += kThreads)
+            bad = bad || a.cu[g] < 0 || a.cu[g + 1] < a.cu[g] || a.cu[g + 1] > a.B;
+    }
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) atomicOr(a.status, kBadPage);
+    const int64_t room = a.table_width * a.c.page;
+    for (int g = wp; g < a.n_groups; g += kThreads / 32) {
+        PrefixGroup G = {0, 0, 0, -1, 0, 0, 0, 0};
+        if (!bad) {
+            G.s0 = a.cu ? a.cu[g] : 0;
+            G.s1 = a.cu ? a.cu[g + 1] : (int32_t)a.B;
+            // whole blocks; the rest is each sequence's own
+            int32_t shared = a.shared[g];
+            if (shared > room) shared = (int32_t)room;
+            shared = shared < 0 ? 0 : shared & ~(kBlock - 1);
+            int count = 0;
+            if (shared > 0)
+                for (int b0 = G.s0; b0 < G.s1; b0 += 32) {
+                    const bool on = b0 + lane < G.s1 && shares(a, b0 + lane, shared);
+                    const uint32_t who = __ballot_sync(0xFFFFFFFFu, on);
+                    if (G.seq < 0 && who) G.seq = b0 + __ffs(who) - 1;
+                    count += __popc(who);
+                }
+            if (count > 1) {
+                G.shared = shared;
+                G.ns = (shared + a.tok - 1) / a.tok;
+                G.tiles = (int)(((int64_t)(G.s1 - G.s0) * a.n * a.group + kPrefixRows - 1) / kPrefixRows);
+                for (int b = G.s0 + lane; b < G.s1; b += 32)
+                    if (shares(a, b, shared)) a.seqs[b] = PrefixSeq{shared, g};
+            }
+        }
+        if (lane == 0) a.groups[g] = G;
+    }
+    __syncthreads();
+    // the groups' places on the line, and of their items
+    int64_t steps = 0, items = 0;
+    for (int g0 = 0; g0 < a.n_groups; g0 += kThreads) {
+        const int g = g0 + threadIdx.x;
+        int64_t it = 0, st = 0;
+        if (g < a.n_groups) {
+            it = (int64_t)a.groups[g].tiles * a.c.H;
+            st = it * a.groups[g].ns;
+        }
+        int64_t i1 = it, s1 = st;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, i1, o), v = __shfl_up_sync(0xFFFFFFFFu, s1, o);
+            if (lane >= o) {
+                i1 += u;
+                s1 += v;
+            }
+        }
+        if (lane == 31) {
+            sums[0][wp] = i1;
+            sums[1][wp] = s1;
+        }
+        __syncthreads();
+        int64_t i0 = items + i1 - it, s0 = steps + s1 - st;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < wp) {
+                i0 += sums[0][w];
+                s0 += sums[1][w];
+            }
+            items += sums[0][w];
+            steps += sums[1][w];
+        }
+        __syncthreads();
+        if (g < a.n_groups) {
+            a.groups[g].first = (int32_t)s0;
+            a.groups[g].item0 = (int32_t)i0;
+        }
+    }
+    if (threadIdx.x == 0) {
+        int64_t chunk = (steps + a.shares - 1) / a.shares;
+        if (chunk < a.min_chunk) chunk = a.min_chunk;
+        *a.line = PrefixLine{(int32_t)steps, (int32_t)chunk, {0, 0}};
+    }
+}
+
+}  // namespace
+
+const void* prefix_plan_kernel() { return (const void*)&prefix_plan; }
+
+}  // namespace rmsattn

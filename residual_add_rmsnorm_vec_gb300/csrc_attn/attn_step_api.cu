@@ -1,0 +1,316 @@
+// C ABI of the operators around the attention in a serving step: the page plan,
+// attention with a shared prefix, the norms at a block's end.
+#include <math.h>
+#include <string.h>
+
+#include "attn_host.h"
+
+using namespace rmsattn;
+
+// ---------------------------------------------------------------- pages
+
+RMSATTN_API int64_t rmsattn_pages_workspace(int64_t n_seqs) {
+    if (n_seqs < 0 || n_seqs > (1 << 24)) return RMSN_EINVAL;
+    return n_seqs <= kPagesOnce ? 0 : (4 + 3 * (n_seqs + 1)) * 4;
+}
+
+RMSATTN_API int rmsattn_pages_step(int32_t* free_pages, int64_t n_pages, const int32_t* n_free,
+                                   int32_t* block_table, int64_t table_stride, int64_t table_width,
+                                   const int32_t* lengths, const int32_t* new_tokens,
+                                   const int32_t* shared_pages, int64_t n_seqs, int64_t page_size,
+                                   int64_t n_rows, int32_t* cu_seqlens, int32_t* positions,
+                                   int64_t* slots, int32_t* rows, int32_t* before, int32_t* after,
+                                   int32_t* n_free_out, void* workspace, int64_t workspace_bytes,
+                                   uint32_t flags, cudaStream_t stream) {
+    if (flags & ~RMSN_PDL) return RMSN_EINVAL;
+    if (n_pages < 0 || n_pages > INT32_MAX || n_seqs < 0 || n_seqs > (1 << 24) || n_rows < 0 ||
+        n_rows > kMaxTokens || page_size < kBlock || page_size > 65536 || page_size % kBlock)
+        return RMSN_EINVAL;
+    const int st = check_table(block_table, table_stride, table_width, n_seqs, (int)page_size);
+    if (st != RMSN_OK) return st;
+    if (!n_free || !cu_seqlens || !n_free_out || (n_pages && !free_pages)) return RMSN_EINVAL;
+    if (n_seqs && (!lengths || !new_tokens || !before || !after)) return RMSN_EINVAL;
+    if (n_rows && (!positions || !slots || !rows)) return RMSN_EINVAL;
+    const void* words[] = {free_pages, n_free, lengths, new_tokens, shared_pages, cu_seqlens,
+                           before,     after,  n_free_out};
+    for (const void* p : words)
+        if (!aligned(p, 4)) return RMSN_EALIGN;
+    if (!aligned(positions, 16) || !aligned(slots, 16) || !aligned(rows, 16) || !aligned(workspace, 16))
+        return RMSN_EALIGN;
+    if (n_free_out == n_free || (n_seqs && (before == lengths || after == lengths || before == new_tokens ||
+                                            after == new_tokens)))
+        return RMSN_EINVAL;
+    const int64_t need = rmsattn_pages_workspace(n_seqs);
+    if (need && (!workspace || workspace_bytes < need)) return RMSN_EINVAL;
+    DeviceInfo* d = device_info();
+    if (!d) return RMSN_ECUDA;
+    PagesArgs a;
+    memset(&a, 0, sizeof(a));
+    a.free_pages = free_pages;
+    a.n_free = n_free;
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.width = table_width;
+    a.n_pages = n_pages;
+    a.lengths = lengths;
+    a.more = new_tokens;
+    a.shared = shared_pages;
+    a.B = n_seqs;
+    a.T = n_rows;
+    a.page = (int32_t)page_size;
+    a.pdl = (flags & RMSN_PDL) ? 1 : 0;
+    a.cu = cu_seqlens;
+    a.positions = positions;
+    a.rows = rows;
+    a.before = before;
+    a.after = after;
+    a.n_free_out = n_free_out;
+    a.slots = slots;
+    a.ws = static_cast<int32_t*>(workspace);
+    a.status = d->status;
+    // four rows to a thread; a warp to a sequence that returns pages
+    const int threads = n_seqs <= 128 && n_rows <= 512 ? 128 : 512;
+    int64_t blocks = (n_rows + 4 * threads - 1) / (4 * threads);
+    const int64_t by_seqs = (n_seqs + threads - 1) / threads;
+    if (blocks < by_seqs) blocks = by_seqs;
+    if (blocks > 2 * d->num_sms) blocks = 2 * d->num_sms;
+    if (blocks < 1) blocks = 1;
+    if (n_seqs <= kPagesOnce)
+        return launch(pages_kernel_of(0), dim3((unsigned)blocks), threads, (size_t)(3 * (n_seqs + 1)) * 4, &a,
+                      a.pdl, stream);
+    const int sc = launch(pages_kernel_of(1), dim3(1), 1024, 0, &a, a.pdl, stream);
+    return sc != RMSN_OK ? sc : launch(pages_kernel_of(2), dim3((unsigned)blocks), threads, 0, &a, true, stream);
+}
+
+// ---------------------------------------------------------------- norms
+
+RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const void* post_weight,
+                                    const void* weight, const void* gate, int64_t gate_stride,
+                                    const int32_t* gate_index, int64_t n_gates, void* out,
+                                    void* residual_out, float* out_scale, int64_t n_tokens,
+                                    int64_t hidden, float eps, float residual_scale, float weight_offset,
+                                    uint32_t flags, cudaStream_t stream) {
+    if (flags & ~(RMSN_IN_MASK | RMSN_RESIDUAL_F32 | RMSATTN_OUT_FP8 | RMSN_PDL)) return RMSN_EINVAL;
+    int64_t bytes = 0;
+    const int dt = dtype_of(flags, &bytes);
+    if (dt < 0) return RMSN_EINVAL;
+    const bool r32 = (flags & RMSN_RESIDUAL_F32) != 0, fp8 = (flags & RMSATTN_OUT_FP8) != 0;
+    if (r32 && dt == RMSN_IN_F32) return RMSN_EINVAL;
+    if (n_tokens < 0 || n_tokens > INT32_MAX || hidden < 1 || hidden > (1 << 24)) return RMSN_EINVAL;
+    if (too_big(times(n_tokens, hidden * 4))) return RMSN_EINVAL;
+    if (!(eps >= 0.f) || !isfinite(eps) || !isfinite(residual_scale) || !isfinite(weight_offset))
+        return RMSN_EINVAL;
+    if (gate ? (gate_stride < 0 || (gate_stride > 0 && gate_stride < hidden) || n_gates < 0 ||
+                too_big(times(n_gates, gate_stride * 4)))
+             : (gate_stride != 0 || gate_index != nullptr || n_gates != 0))
+        return RMSN_EINVAL;
+    if (gate && (gate_index ? n_gates > INT32_MAX : n_gates != (gate_stride ? n_tokens : 1))) return RMSN_EINVAL;
+    if (fp8 ? (n_tokens && !out_scale) : out_scale != nullptr) return RMSN_EINVAL;
+    if (n_tokens == 0) return RMSN_OK;
+    if (!x || !residual || !out || !residual_out) return RMSN_EINVAL;
+    const int64_t rbytes = r32 ? 4 : bytes;
+    const void* same[] = {x, post_weight, weight, gate};
+    for (const void* p : same)
+        if (!aligned(p, (uintptr_t)bytes)) return RMSN_EALIGN;
+    if (!aligned(residual, (uintptr_t)rbytes) || !aligned(residual_out, (uintptr_t)rbytes) ||
+        !aligned(out, fp8 ? 1 : (uintptr_t)bytes) || !aligned(out_scale, 4) || !aligned(gate_index, 4))
+        return RMSN_EALIGN;
+    DeviceInfo* d = device_info();
+    if (!d) return RMSN_ECUDA;
+    NormsArgs a;
+    memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.residual = residual;
+    a.post_w = post_weight;
+    a.w = weight;
+    a.gate = gate;
+    a.index = gate_index;
+    a.out = out;
+    a.residual_out = residual_out;
+    a.out_scale = out_scale;
+    a.T = n_tokens;
+    a.gate_stride = gate_stride;
+    a.n_gates = n_gates;
+    a.H = (int32_t)hidden;
+    a.pdl = (flags & RMSN_PDL) ? 1 : 0;
+    a.eps = eps;
+    a.alpha = residual_scale;
+    a.w_off = weight_offset;
+    a.status = d->status;
+    // vectors of eight elements where every row of every operand starts on one
+    bool vec = hidden % 8 == 0 && gate_stride % 8 == 0 && aligned(out, fp8 ? 8 : (uintptr_t)(8 * bytes)) &&
+               aligned(residual, (uintptr_t)(8 * rbytes)) && aligned(residual_out, (uintptr_t)(8 * rbytes));
+    for (const void* p : same) vec = vec && aligned(p, (uintptr_t)(8 * bytes));
+    int v = vec ? 8 : 1, ch = vec ? 1 : 8;
+    if (vec)
+        while (ch < 4 && hidden > 8 * 512 * ch) ch *= 2;
+    if (hidden > (int64_t)(vec ? 512 : 1024) * v * ch) v = 1, ch = 0;
+    const int64_t lanes = ch ? (hidden + v * ch - 1) / (v * ch) : 1024;
+    const int threads = (int)((lanes + 31) / 32 * 32);
+    return launch(norms_kernel_of(dt, r32, fp8, v, ch), dim3((unsigned)n_tokens), threads, 0, &a, a.pdl, stream);
+}
+
+// ---------------------------------------------------------------- shared prefix
+
+namespace {
+
+const PrefixEntry* prefix_entry_of(int dt, int64_t D) {
+    int n = 0;
+    const PrefixEntry* t = prefix_kernels(&n);
+    for (int i = 0; i < n; ++i)
+        if (t[i].dt == dt && t[i].D == D) return &t[i];
+    return nullptr;
+}
+
+// Where a call's workspace holds what.
+struct PrefixPlan {
+    const PrefixEntry* e;
+    int64_t shares, groups, seqs, parts, own, total;  // offsets in bytes
+    Plan behind;
+};
+
+int64_t round_up(int64_t n) { return (n + 255) / 256 * 256; }
+
+int plan_prefix(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_t n_q_heads,
+                int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens, int64_t n_groups, PrefixPlan* p) {
+    p->e = prefix_entry_of(dt, head_dim);
+    p->shares = resident_blocks(d, p->e->fn, p->e->threads, p->e->smem, 1);
+    if (p->shares < 1) return RMSN_ECUDA;
+    const int64_t group = n_q_heads / n_kv_heads;
+    // a group of two sequences or more shares: its columns fill whole tiles but for one
+    const int64_t some = n_groups < n_seqs / 2 ? n_groups : n_seqs / 2;
+    const int64_t tiles = n_seqs * n_queries * group / kPrefixRows + some;
+    const int64_t items = times(tiles, n_kv_heads);
+    if (times(items, (max_tokens + p->e->tok - 1) / p->e->tok) + p->shares >= (int64_t(1) << 31))
+        return RMSN_EUNSUPPORTED;  // steps are counted in 31 bits
+    const int st = plan_attend(d, true, dt, n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim, max_tokens,
+                               0, 0, &p->behind);
+    if (st != RMSN_OK) return st;
+    p->groups = round_up(sizeof(PrefixLine));
+    p->seqs = p->groups + round_up(n_groups * (int64_t)sizeof(PrefixGroup));
+    p->parts = p->seqs + round_up(n_seqs * (int64_t)sizeof(PrefixSeq));
+    p->own = p->parts + times(p->shares + items, prefix_part((int)head_dim) * 4);
+    p->total = p->own + p->behind.workspace;
+    return too_big(p->total) ? RMSN_EUNSUPPORTED : RMSN_OK;
+}
+
+int check_prefix(int64_t n_seqs, int64_t n_queries, int64_t n_q_heads, int64_t n_kv_heads,
+                 int64_t head_dim, int64_t n_groups) {
+    if (n_groups < 0 || n_groups > (1 << 24)) return RMSN_EINVAL;
+    return check_attend(n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim);
+}
+
+}  // namespace
+
+RMSATTN_API int64_t rmsattn_kv_prefix_attention_workspace(int64_t n_seqs, int64_t n_queries,
+                                                          int64_t n_q_heads, int64_t n_kv_heads,
+                                                          int64_t head_dim, int64_t max_tokens,
+                                                          int64_t n_groups) {
+    const int st = check_prefix(n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim, n_groups);
+    if (st != RMSN_OK) return st;
+    if (max_tokens < 0 || max_tokens > kMaxTokens) return RMSN_EINVAL;
+    if (n_seqs == 0) return 0;
+    DeviceInfo* d = device_info();
+    if (!d) return RMSN_ECUDA;
+    PrefixPlan p;  // both dtypes' kernels have the same shape
+    const int sp = plan_prefix(d, RMSN_IN_BF16, n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim, max_tokens,
+                               n_groups, &p);
+    return sp == RMSN_OK ? p.total : sp;
+}
+
+RMSATTN_API int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* cache,
+                                            const int32_t* block_table, int64_t table_stride,
+                                            int64_t table_width, const int32_t* lengths,
+                                            const int32_t* prefix_lengths, const int32_t* group_cu,
+                                            int64_t n_groups, void* out, int64_t q_stride,
+                                            int64_t out_stride, int64_t n_seqs, int64_t n_queries,
+                                            int64_t n_q_heads, float scale, void* workspace,
+                                            int64_t workspace_bytes, uint32_t flags, cudaStream_t stream) {
+    if (flags & ~(RMSN_IN_MASK | RMSN_PDL)) return RMSN_EINVAL;
+    int64_t bytes = 0;
+    const int dt = dtype_of(flags, &bytes);
+    if (dt < 0) return RMSN_EINVAL;
+    if (dt == RMSN_IN_F32) return RMSN_EUNSUPPORTED;
+    AttendArgs a;
+    memset(&a, 0, sizeof(a));
+    int st = check_cache(cache, &a.c);
+    if (st != RMSN_OK) return st;
+    st = check_prefix(n_seqs, n_queries, n_q_heads, a.c.H, a.c.D, n_groups);
+    if (st != RMSN_OK) return st;
+    if (!isfinite(scale)) return RMSN_EINVAL;
+    const int64_t width = n_q_heads * a.c.D;
+    if (q_stride < width || out_stride < width || (q_stride * bytes) % 16 || (out_stride * bytes) % 16)
+        return RMSN_EINVAL;
+    if (too_big(times(n_seqs * n_queries, times(q_stride, 2))) ||
+        too_big(times(n_seqs * n_queries, times(out_stride, 2))))
+        return RMSN_EINVAL;
+    st = check_table(block_table, table_stride, table_width, n_seqs, a.c.page);
+    if (st != RMSN_OK) return st;
+    if (!group_cu && n_groups > 1) return RMSN_EINVAL;
+    if (n_seqs == 0) return RMSN_OK;
+    if (!q || !out || !lengths || (n_groups && !prefix_lengths) || !workspace) return RMSN_EINVAL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(workspace, 16) ||
+        !aligned(prefix_lengths, 4) || !aligned(group_cu, 4))
+        return RMSN_EALIGN;
+    DeviceInfo* d = device_info();
+    if (!d) return RMSN_ECUDA;
+    PrefixPlan p;
+    st = plan_prefix(d, dt, n_seqs, n_queries, n_q_heads, a.c.H, a.c.D, table_width * a.c.page, n_groups, &p);
+    if (st != RMSN_OK) return st;
+    if (workspace_bytes < p.total) return RMSN_EINVAL;
+    if (a.c.n_pages == 0) {  // nothing is read; copies of no bytes still name an address
+        a.c.k = a.c.v = (uint8_t*)q;
+        a.c.ks = a.c.vs = (float*)q;
+    }
+    char* ws = static_cast<char*>(workspace);
+    a.q = q;
+    a.out = out;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.table = block_table;
+    a.table_stride = table_stride;
+    a.table_width = table_width;
+    a.lengths = lengths;
+    a.B = n_seqs;
+    a.scale = scale;
+    a.status = d->status;
+    a.pdl = 1;
+    a.ws = ws + p.own;
+    fill_attend(p.behind, n_queries, n_q_heads, &a);
+
+    PrefixArgs f;
+    memset(&f, 0, sizeof(f));
+    f.c = a.c;
+    f.q = q;
+    f.q_stride = q_stride;
+    f.table = block_table;
+    f.table_stride = table_stride;
+    f.table_width = table_width;
+    f.lengths = lengths;
+    f.cu = group_cu;
+    f.shared = prefix_lengths;
+    f.B = n_seqs;
+    f.n_groups = (int32_t)n_groups;
+    f.n = (int32_t)n_queries;
+    f.group = a.group;
+    f.tok = p.e->tok;
+    f.shares = (int32_t)p.shares;
+    f.min_chunk = 1;
+    f.pdl = (flags & RMSN_PDL) ? 1 : 0;
+    f.scale = scale;
+    f.page_rcp = a.page_rcp;
+    f.status = d->status;
+    f.line = reinterpret_cast<PrefixLine*>(ws);
+    f.groups = reinterpret_cast<PrefixGroup*>(ws + p.groups);
+    f.seqs = reinterpret_cast<PrefixSeq*>(ws + p.seqs);
+    f.parts = reinterpret_cast<float*>(ws + p.parts);
+    a.line = f.line;
+    a.prefix = f.groups;
+    a.seqs = f.seqs;
+    a.parts = f.parts;
+    // each launch behind the one before: programmatic dependents of the call's own
+    st = launch(prefix_plan_kernel(), dim3(1), 512, 0, &f, f.pdl, stream);
+    if (st == RMSN_OK && n_groups)
+        st = launch(p.e->fn, dim3((unsigned)p.shares), p.e->threads, (size_t)p.e->smem, &f, true, stream);
+    return st == RMSN_OK ? launch_attend(p.behind, &a, true, stream) : st;
+}

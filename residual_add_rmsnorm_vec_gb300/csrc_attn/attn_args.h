@@ -8,6 +8,7 @@ namespace rmsattn {
 
 constexpr int kBlock = 16;          // tokens that share a cache scale
 constexpr uint32_t kBadPage = 4u;   // status bit: a page or token outside the cache
+constexpr uint32_t kWaitRanOut = 1u;  // status bit: a kernel gave up a wait
 
 // q / k: first element of token 0's first head; strides in elements.
 struct RopeArgs {
@@ -96,16 +97,14 @@ struct NormsArgs {
 const void* norms_kernel_of(int dt, bool r32, bool fp8, int v, int ch);
 
 // A group of sequences [s0, s1) that share their first `shared` tokens: `tiles`
-// row tiles of kPrefixRows columns (sequence x query token x head) for each key
-// head, an item each, from item0 on; an item is ns steps, the group's items lie
+// tiles of `rows` columns (sequence x query token x head) for each key head,
+// an item each, from item0 on; an item is ns steps, the group's items lie
 // one behind the other on the line of all steps from `first` on.
 struct PrefixGroup {
     int32_t s0, s1, shared;
     int32_t seq;  // the sequence whose table row names the shared pages
     int32_t ns, first, item0, tiles;
 };
-constexpr int kPrefixRows = 128;
-
 // The line of the shared parts: total steps, and the steps of a share.
 struct PrefixLine {
     int32_t total, chunk, pad[2];
@@ -126,7 +125,7 @@ struct PrefixArgs {
     const int32_t* shared;  // tokens that each group shares
     int64_t B;
     int32_t n_groups, n, group;  // group: query heads of a key head
-    int32_t tok;                 // tokens of a step
+    int32_t tok, rows;           // tokens of a step, columns of an item
     int32_t shares, min_chunk;
     int32_t pdl;
     float scale;
@@ -137,15 +136,18 @@ struct PrefixArgs {
     PrefixSeq* seqs;
     float* parts;  // one for each pair of a share and an item that it meets
 };
-// Floats of a part: sums [D / 8][kPrefixRows][8], then reference and weight of each row.
-__host__ __device__ constexpr int64_t prefix_part(int D) { return (int64_t)kPrefixRows * (D + 2); }
+// Floats of a part: sums [D / 8][rows][8], then reference and weight of each row.
+__host__ __device__ constexpr int64_t prefix_part(int D, int rows) { return (int64_t)rows * (D + 2); }
 
+// One compiled kernel: R tiles of 128 rows.
 struct PrefixEntry {
-    int32_t dt, D, tok, threads, smem;
+    int32_t dt, D, R, tok, threads, smem;
     const void* fn;
 };
 const void* prefix_plan_kernel();
-const PrefixEntry* prefix_kernels(int* n);
+const PrefixEntry* prefix_kernels_64(int* n);
+const PrefixEntry* prefix_kernels_128(int* n);
+const PrefixEntry* prefix_kernels_256(int* n);
 
 struct AttendArgs {
     Cache c;
@@ -176,6 +178,7 @@ struct AttendArgs {
     const PrefixGroup* prefix;
     const PrefixSeq* seqs;
     const float* parts;
+    int32_t prefix_rows;  // columns of an item
 };
 
 constexpr int64_t kCutBytes = 32;

@@ -373,12 +373,12 @@ __device__ __forceinline__ void add_prefix(const AttendArgs& a, int64_t b, int h
     const PrefixGroup g = a.prefix[sq.group];
     const uint32_t chunk = a.line->chunk;
     const int cc = (((int)b - g.s0) * a.n + c.qi) * a.group + c.head - hk * a.group;
-    const int item = hk * g.tiles + cc / kPrefixRows, row = cc % kPrefixRows;
+    const int rows = a.prefix_rows, tile = cc / rows, row = cc - tile * rows, item = hk * g.tiles + tile;
     const uint32_t at = (uint32_t)g.first + (uint32_t)item * (uint32_t)g.ns;
     const int i0 = (int)(at / chunk), n = (int)((at + (uint32_t)g.ns - 1) / chunk) - i0 + 1;
-    const int64_t size = prefix_part(a.c.D);
+    const int64_t size = prefix_part(a.c.D, rows);
     const float* p = a.parts + (i0 + g.item0 + item) * size;
-    const int at_y = d * kPrefixRows + row * 8, at_ml = a.c.D * kPrefixRows + row * 2;
+    const int at_y = d * rows + row * 8, at_ml = a.c.D * rows + row * 2;
     constexpr int U = 4;
     for (int k0 = 0; k0 < n; k0 += U) {
         float2 ml[U];

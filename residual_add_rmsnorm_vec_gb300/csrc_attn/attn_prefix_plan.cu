@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan(const PrefixArgs a) {
             if (count > 1) {
                 G.shared = shared;
                 G.ns = (shared + a.tok - 1) / a.tok;
-                G.tiles = (int)(((int64_t)(G.s1 - G.s0) * a.n * a.group + kPrefixRows - 1) / kPrefixRows);
+                G.tiles = (int)(((int64_t)(G.s1 - G.s0) * a.n * a.group + a.rows - 1) / a.rows);
                 for (int b = G.s0 + lane; b < G.s1; b += 32)
                     if (shares(a, b, shared)) a.seqs[b] = PrefixSeq{shared, g};
             }

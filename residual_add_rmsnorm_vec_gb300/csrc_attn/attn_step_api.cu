@@ -154,12 +154,16 @@ RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const v
 
 namespace {
 
-const PrefixEntry* prefix_entry_of(int dt, int64_t D) {
+// Two row tiles where the groups have more than 128 columns on average (they share
+// the widening of each key and value), else one.
+const PrefixEntry* prefix_entry_of(int dt, int64_t D, int64_t cols, int64_t n_groups) {
     int n = 0;
-    const PrefixEntry* t = prefix_kernels(&n);
+    const PrefixEntry* t = D == 64 ? prefix_kernels_64(&n)
+                                   : (D == 128 ? prefix_kernels_128(&n) : prefix_kernels_256(&n));
+    const PrefixEntry* best = nullptr;
     for (int i = 0; i < n; ++i)
-        if (t[i].dt == dt && t[i].D == D) return &t[i];
-    return nullptr;
+        if (t[i].dt == dt && (!best || cols > 128 * (n_groups < 1 ? 1 : n_groups))) best = &t[i];
+    return best;
 }
 
 // Where a call's workspace holds what.
@@ -173,13 +177,14 @@ int64_t round_up(int64_t n) { return (n + 255) / 256 * 256; }
 
 int plan_prefix(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_t n_q_heads,
                 int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens, int64_t n_groups, PrefixPlan* p) {
-    p->e = prefix_entry_of(dt, head_dim);
+    const int64_t cols = n_seqs * n_queries * (n_q_heads / n_kv_heads);
+    p->e = prefix_entry_of(dt, head_dim, cols, n_groups);
     p->shares = resident_blocks(d, p->e->fn, p->e->threads, p->e->smem, 1);
     if (p->shares < 1) return RMSN_ECUDA;
-    const int64_t group = n_q_heads / n_kv_heads;
+    const int rows = 128 * p->e->R;
     // a group of two sequences or more shares: its columns fill whole tiles but for one
     const int64_t some = n_groups < n_seqs / 2 ? n_groups : n_seqs / 2;
-    const int64_t tiles = n_seqs * n_queries * group / kPrefixRows + some;
+    const int64_t tiles = cols / rows + some;
     const int64_t items = times(tiles, n_kv_heads);
     if (times(items, (max_tokens + p->e->tok - 1) / p->e->tok) + p->shares >= (int64_t(1) << 31))
         return RMSN_EUNSUPPORTED;  // steps are counted in 31 bits
@@ -189,7 +194,7 @@ int plan_prefix(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
     p->groups = round_up(sizeof(PrefixLine));
     p->seqs = p->groups + round_up(n_groups * (int64_t)sizeof(PrefixGroup));
     p->parts = p->seqs + round_up(n_seqs * (int64_t)sizeof(PrefixSeq));
-    p->own = p->parts + times(p->shares + items, prefix_part((int)head_dim) * 4);
+    p->own = p->parts + times(p->shares + items, prefix_part((int)head_dim, rows) * 4);
     p->total = p->own + p->behind.workspace;
     return too_big(p->total) ? RMSN_EUNSUPPORTED : RMSN_OK;
 }
@@ -294,6 +299,7 @@ RMSATTN_API int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* 
     f.n = (int32_t)n_queries;
     f.group = a.group;
     f.tok = p.e->tok;
+    f.rows = a.prefix_rows = 128 * p.e->R;
     f.shares = (int32_t)p.shares;
     f.min_chunk = 1;
     f.pdl = (flags & RMSN_PDL) ? 1 : 0;

@@ -9,18 +9,19 @@
 // token.  From about 150 rows on the tensor cores bound it, below that DRAM.
 //
 // A block holds R tiles of 128 rows (R = 2 where a group has more than 128 rows)
-// and walks over its share of the line of all steps, TOK tokens of an item (group x
-// key head x R tiles) each.  Its warps have fixed parts:
+// and walks over its share of the line of all steps, 64 tokens of an item (group x key
+// head x R tiles) each.  Its warps have fixed parts:
 //
+//   plan     one warp: pages, scales, what a step is (32 blocks of 16 tokens at a time,
+//            so that their loads' latencies are met once), some steps ahead of the rest
+//   K, V     four warps each: asynchronous copies of the codes into slots, from there
+//            widened to fp16 into the swizzled stages of the B operands
+//   MMA      two threads: one issues S = Q K^T, a step ahead, the other O += P V
 //   softmax  four warps to a row tile, a thread to a row: scores from TMEM, weights
 //            back into TMEM as the second product's A operand, in fp16
-//   K, V     four warps: codes from the pages (16-byte loads, a tile's on their way in
-//            registers while the stages are full), widened to fp16 into the swizzled
-//            stages of the B operands
-//   MMA      one warp, one of its lanes issues: for each row tile O += P V of the step
-//            before, then S = Q K^T of this one; the other row tile's softmax runs
-//            meanwhile
 //
+// * S has two buffers (the weights go over the scores that they are made of), so the
+//   products of the next scores do not wait for this step's softmax.
 // * Widening 16-bit copies into shared memory pays here, other than in attn_attend.cuh:
 //   256 rows use each copy.
 // * A value's scale is 2^e times a significand in [1, 2).  The significand multiplies
@@ -30,13 +31,14 @@
 //   a step of its own, for which what was summed so far is added to the part in memory
 //   and E set anew.  Scales that lie 2^22 apart are rare, so that path is small.
 // * A row's reference m follows its maximum only when that has grown by more than
-//   2^kSlack; then the row's sum is multiplied in TMEM by the softmax warp itself: the
-//   commit that announced the scores covers the product before them.  Weights are
-//   lifted by kLift: a lifted weight times a significand stays below 2^15, and fp16's
-//   subnormals end 2^-34 below the reference.
+//   2^kSlack; then the row's sum is multiplied in TMEM by the softmax warp itself, behind
+//   the product before.  Weights are lifted by kLift: a lifted weight times a significand
+//   stays below 2^15 + 2^12, and fp16's subnormals end 2^-34 below the reference.
 // * Parts go to the workspace in the order of the line: nothing depends on timing.
 // * Every wait gives up after a second: the block then stops, waits for its products
-//   in flight, gives TMEM back, and bit 0 of the status word is set.
+//   and copies in flight, gives TMEM back, and bit 0 of the status word is set.
+// * Code is kept small (loops over a tile's pieces are rolled): most calls run a few
+//   steps a block, and each instruction that runs once is fetched from L2 first.
 #pragma once
 
 #include "attn_common.cuh"
@@ -60,24 +62,32 @@ constexpr uint32_t kFirst = 1u, kLast = 2u, kFlush = 4u, kEnd = 8u, kTwo = 16u;
 template <int D_, int R_>
 struct Shape {
     static constexpr int D = D_, R = R_;
-    static constexpr int TOK = D == 256 ? 64 : 128;
-    static constexpr int BLK = TOK / kBlock;
-    static constexpr int PARTS = D / 64;              // 64-dim parts of 128-byte lines
-    static constexpr int S = D == 64 ? 3 : 2;         // stages of K and of V
-    static constexpr int M = 4;                       // slots of the steps' words, >= S + 2
-    static constexpr int kTile = TOK * D * 2;
+    static constexpr int TOK = 64, BLK = TOK / kBlock;
+    static constexpr int PARTS = D / 64;      // 64-dim parts of 128-byte lines
+    static constexpr int M = 8;               // slots of the steps' words
+    static constexpr int kTile = TOK * D * 2; // a stage of K or V; there are two of each
     static constexpr int kQ = 128 * D * 2;
-    static constexpr int kSmem = R * kQ + 2 * S * kTile + 1024;
-    static constexpr int kThreads = (4 * R + 5) * 32;
-    static constexpr int kCols = 512;                 // of TMEM: S at 128 x, O behind
+    static constexpr int kRaw = kTile;        // codes of a step of K and V
+    static constexpr int N = D == 256 ? 1 : 4;  // slots of codes
+    static constexpr int kSmem = R * kQ + 4 * kTile + N * kRaw + 1024;
+    static constexpr int kWarps = 4 * R + 12;  // softmax; K; V; products, plan and an idle one
+    // four warps to a role: registers move between them at the begin (of the 480 or 512
+    // that four threads have, one of each role)
+    static constexpr int kRegsS = R == 2 ? 136 : 200, kRegsW = R == 2 ? 64 : 96, kRegsM = R == 2 ? 80 : 104;
+    static constexpr int kCols = 512;         // of TMEM: S at 64 (2 x + buffer), O behind
     static constexpr int kO = 256;
-    static constexpr int ITERS = TOK / 8 * PARTS / 4; // 16-byte loads of a thread and tile
+    static constexpr int ITERS = TOK / 8 * PARTS / 4;  // 16-byte pieces of a thread, K or V
 };
 
+// What the plan says of a step.
 struct Step {
-    float ks[8], vm[8];
-    uint32_t mask, flags;
-    int32_t e, pad;
+    int64_t off[4];    // the blocks' codes, in bytes from the cache's begin; -1: none
+    float ks[4];       // K scales
+    float vm[4];       // significands of the V scales, lifted
+    uint32_t f[4];     // 2^(7 + e - E), packed fp16
+    uint32_t mask;     // blocks of this step
+    uint32_t flags;
+    int32_t e;         // E
 };
 
 // ---------------------------------------------------------------- instructions
@@ -106,42 +116,78 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 
 // Shared-memory operand: rows of 128 bytes, 128-byte swizzle, eight rows to 1024
 // bytes; `lead`: bytes between 64-element parts of an operand whose rows are the
-// product's inner dimension.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(lead >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           uint64_t(1) << 46 | uint64_t(2) << 61;
+// product's inner dimension.  The low word has the place; the high one is the same
+// for all.
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lead) {
+    return (addr & 0x3FFFF) >> 4 | (lead >> 4) << 16;
 }
+constexpr uint32_t kOperandHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
 // fp16 operands, fp32 sums, 128 rows, n columns; `inner`: B's rows are the inner dimension.
 __host__ __device__ constexpr uint32_t product(int n, bool inner) {
     return 1u << 4 | (inner ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
+// The k-th of a chain of products; the first one of a chain sets the sums, with FRESH.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int k) {
+    if (k == 0)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, 0, 0;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(idesc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.eq.b32 p, 0, 0;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(idesc)
+            : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
+template <bool FRESH>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, int k) {
+    if (FRESH && k == 0)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, 0, 0;\n\tmov.b64 db, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(idesc)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.eq.b32 p, 0, 0;\n\tmov.b64 db, {%2, %3};\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(kOperandHigh), "r"(idesc)
+            : "memory");
 }
-// 32 columns of the warp's 32 rows, waited for.
-__device__ __forceinline__ void tmem_load(float (&v)[32], uint32_t at) {
+// 32 columns of the warp's 32 rows, on their way: the registers hold them behind
+// tmem_loaded(), which names them so that nothing reads them before.
+__device__ __forceinline__ void tmem_begin(float* v, uint32_t at) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
           "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
           "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
           "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
         : "r"(at)
         : "memory");
+}
+__device__ __forceinline__ void tmem_begin16(float* v, uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_named(float* v) {  // 16 registers
+    asm volatile(""
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                   "+f"(v[15])
+                 :
+                 : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tmem_loaded(float (&v)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; i += 16) tmem_named(v + i);
 }
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16]) {
     asm volatile(
@@ -151,39 +197,41 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16
         "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-__device__ __forceinline__ void tmem_store32(uint32_t at, const float (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
-        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
-        "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]),
-        "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]),
-        "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31])
-        : "memory");
-}
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ---------------------------------------------------------------- the block
 
 struct Bars {
-    uint64_t k_full[4], k_free[4], v_full[4], v_free[4], step[4], s_full[2], p_full[2], q_full[2], o_done[2], last;
+    uint64_t step[8], step_free[8], k_full[2], v_full[2], s_full[2][2], p_full[2][2], pv[2], q_full[2], last[2];
     uint32_t tmem, stop;
 };
 
 // All of a warp's lanes wait together, for a second at most; false: the block stops.
-__device__ __forceinline__ bool wait(const uint64_t* bar, uint32_t parity, uint32_t* stop) {
+__device__ __forceinline__ bool wait(const uint64_t* bar, int phase, uint32_t* stop) {
     const uint32_t b = smem_of(bar);
-    bool ok = rmsn::mbar_try_wait(b, parity & 1);
+    bool ok = rmsn::mbar_try_wait(b, phase & 1);
     if (!__all_sync(0xFFFFFFFFu, ok)) {
         const long long t0 = clock64();
         while (!__all_sync(0xFFFFFFFFu, ok)) {
-            if (!ok) ok = rmsn::mbar_try_wait(b, parity & 1);
+            if (!ok) ok = rmsn::mbar_try_wait(b, phase & 1);
             const bool out = *reinterpret_cast<volatile uint32_t*>(stop) != 0 || clock64() - t0 > kWaitCycles;
             if (__any_sync(0xFFFFFFFFu, out && !ok)) {
                 *reinterpret_cast<volatile uint32_t*>(stop) = 1;
                 return false;
             }
+        }
+    }
+    return true;
+}
+// The same for one thread.
+__device__ __forceinline__ bool wait_alone(const uint64_t* bar, int phase, uint32_t* stop) {
+    const uint32_t b = smem_of(bar);
+    if (rmsn::mbar_try_wait(b, phase & 1)) return true;
+    const long long t0 = clock64();
+    while (!rmsn::mbar_try_wait(b, phase & 1)) {
+        if (*reinterpret_cast<volatile uint32_t*>(stop) != 0 || clock64() - t0 > kWaitCycles) {
+            *reinterpret_cast<volatile uint32_t*>(stop) = 1;
+            return false;
         }
     }
     return true;
@@ -232,280 +280,305 @@ struct Walk {
     }
 };
 
-// A tile of TOK tokens as a producer warp sees it: lane b (< BLK) has block b.
-struct Tile {
-    bool on, first, last;  // on: there is one; first / last of its piece
-    bool two;              // the second row tile has rows
-    int hk, j;             // its first token
-    int shared;
-    const int32_t* row;
-};
-
-template <class C>
-struct Tiles {
+// A softmax warp's way through its share, in shared memory (its registers hold
+// scores): lane 0 goes on, all read.
+struct Way {
     Walk walk;
     Piece p;
-    int step;
     bool more;
-    __device__ __forceinline__ void begin(const PrefixArgs& a) {
-        walk.begin(a);
-        more = walk.next(a, &p);
-        step = 0;
-    }
-    __device__ __forceinline__ void next(const PrefixArgs& a, Tile* t) {
-        t->on = more;
-        if (!more) return;
-        t->first = step == 0;
-        t->last = step == p.steps - 1;
-        t->hk = p.hk;
-        t->j = (p.step0 + step) * C::TOK;
-        t->shared = p.g.shared;
-        t->row = a.table + p.g.seq * a.table_stride;
-        t->two = C::R == 2 && ((p.g.s1 - p.g.s0) * a.n * a.group - p.tile * (128 * C::R)) > 128;
-        if (++step == p.steps) {
+    __device__ __forceinline__ void begin(const PrefixArgs& a, int lane) {
+        if (lane == 0) {
+            walk.begin(a);
             more = walk.next(a, &p);
-            step = 0;
         }
+        __syncwarp();
+    }
+    __device__ __forceinline__ void next_piece(const PrefixArgs& a, int lane) {
+        __syncwarp();
+        if (lane == 0) more = walk.next(a, &p);
+        __syncwarp();
     }
 };
 
-// Page of the lane's block, or -1 (no such block, or no such page).
+// The warp that plans the steps, 8 tiles of 4 blocks at a time: lane 4 i + b has block
+// b of tile i.
 template <class C>
-__device__ __forceinline__ int32_t page_entry(const PrefixArgs& a, const Tile& t, int lane, int* at) {
-    const int j = t.j + lane * kBlock;
-    *at = 0;
-    if (!t.on || lane >= C::BLK || j >= t.shared) return -1;
-    const int slot = (int)(((uint64_t)(uint32_t)(j >> 4) * a.page_rcp) >> 37);
-    *at = (j - slot * a.c.page) >> 4;
-    const int32_t page = t.row[slot];
-    if ((uint32_t)page >= (uint32_t)a.c.n_pages) {
-        atomicOr(a.status, kBadPage);
-        return -1;
-    }
-    return page;
-}
-
-// The four warps that fill the stages of K and V and write the steps' words.
-template <class C>
-__device__ __forceinline__ void produce(const PrefixArgs& a, unsigned char* stages, Bars* bars, Step* steps, int wp) {
-    constexpr int D = C::D;
+__device__ __forceinline__ void plan(const PrefixArgs& a, Bars* bars, Step* steps) {
     const int lane = threadIdx.x & 31;
-    Tiles<C> tiles;
-    tiles.begin(a);
-    Tile t;
-    tiles.next(a, &t);
-    int at;
-    int32_t page = page_entry<C>(a, t, lane, &at);
-    // this lane's 16 bytes of eight tokens' 64 dims: a quarter warp's stores (two
-    // tokens whose numbers differ in bit 0, four chunks each) meet all banks
-    const int r8 = (lane >> 3) * 2 + ((lane >> 2) & 1), c4 = lane & 3;
-    const int mine = r8 * D + c4 * 16;
-    uint4 kv[2][C::ITERS];
+    Walk walk;
+    Piece p;
+    walk.begin(a);
     int n = 0;  // steps so far
-    int E = 0;  // the piece's reference
-    while (t.on) {
-        // the tile's scales and codes
-        const int64_t tile = (int64_t)t.hk * (a.c.page >> 4) + at;
-        const bool have = page >= 0;
-        float ks = 0.f, vs = 0.f;
-        if (have) {
-            const int64_t i = (int64_t)page * a.c.scale_stride + tile;
-            ks = a.c.ks[i];
-            vs = a.c.vs[i];
-        }
-        const int64_t off = have ? (int64_t)page * a.c.page_stride + tile * (kBlock * D) : -1;
-        uint32_t rem = __ballot_sync(0xFFFFFFFFu, have);
-#pragma unroll
-        for (int i = 0; i < C::ITERS; ++i) {
-            const int u = i * 4 + wp, tg = u / C::PARTS, h = u % C::PARTS;
-            const int64_t o = __shfl_sync(0xFFFFFFFFu, off, tg >> 1);
-            kv[0][i] = kv[1][i] = make_uint4(0, 0, 0, 0);
-            if (o >= 0) {
-                const int64_t e = o + ((tg & 1) * 8 * D + h * 64 + mine);
-                kv[0][i] = rmsn::ld_stream16(a.c.k + e);
-                kv[1][i] = rmsn::ld_stream16(a.c.v + e);
+    while (walk.next(a, &p)) {
+        const bool two = C::R == 2 && (p.g.s1 - p.g.s0) * a.n * a.group - p.tile * (128 * C::R) > 128;
+        const int32_t* row = a.table + p.g.seq * a.table_stride;
+        bool begin = true;
+        int E = 0;  // the piece's reference
+        for (int t0 = 0; t0 < p.steps; t0 += 8) {
+            const int j = (p.step0 + t0) * C::TOK + lane * kBlock;
+            const bool there = t0 + (lane >> 2) < p.steps && j < p.g.shared;
+            const int slot = there ? (int)(((uint64_t)(uint32_t)(j >> 4) * a.page_rcp) >> 37) : 0;
+            const int32_t entry = row[slot];
+            const bool have = there && (uint32_t)entry < (uint32_t)a.c.n_pages;
+            if (there && !have) atomicOr(a.status, kBadPage);
+            // (a block that is not there reads page 0's scale, and is left out)
+            const int64_t page = have ? entry : 0;
+            const int64_t block = have ? (int64_t)p.hk * (a.c.page >> 4) + ((j - slot * a.c.page) >> 4) : 0;
+            float ks = a.c.ks[page * a.c.scale_stride + block], vs = a.c.vs[page * a.c.scale_stride + block];
+            if (!have) ks = vs = 0.f;
+            const int64_t off = page * a.c.page_stride + block * (kBlock * C::D);
+            const uint32_t valid = __ballot_sync(0xFFFFFFFFu, have);
+            // the lane's value scale: 2^e vm, vm in [1, 2); 0 fits any reference
+            uint32_t bits = __float_as_uint(vs) & 0x7FFFFFFFu;
+            int e = -127;
+            if (bits != 0 && bits < 0x00800000u) {  // below fp32's normal range
+                bits = __float_as_uint(__uint_as_float(bits) * 16777216.f);
+                e -= 24;
             }
-        }
-        bool begin = t.first;
-        const bool last = t.last, two = t.two;
-        tiles.next(a, &t);
-        page = page_entry<C>(a, t, lane, &at);
-        // the lane's value scale: 2^e vm, vm in [1, 2); 0 fits any reference
-        uint32_t bits = __float_as_uint(vs) & 0x7FFFFFFFu;
-        int down = 0;
-        if (bits != 0 && bits < 0x00800000u) {  // below fp32's normal range
-            bits = __float_as_uint(__uint_as_float(bits) * 16777216.f);
-            down = 24;
-        }
-        const bool zero = bits == 0;
-        const int e = (int)(bits >> 23) - 127 - down;
-        const float vm = zero ? 1.f : __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
-        do {
-            uint32_t flags = (begin ? kFirst : 0u) | (two ? kTwo : 0u);
-            auto fitting = [&]() { return __ballot_sync(0xFFFFFFFFu, zero || (e <= E && e >= E - 22)) & rem; };
-            uint32_t mask = fitting();
-            if (begin || (rem != 0 && mask == 0)) {
-                const int top = __reduce_max_sync(0xFFFFFFFFu, !zero && (rem >> lane & 1) ? e : -1000);
-                if (!begin) flags |= kFlush;
-                E = top == -1000 ? 0 : top + 3;
-                mask = fitting();
-            }
-            rem &= ~mask;
-            if (rem == 0 && last) flags |= kLast;
-            begin = false;
-            const int st = n % C::S;
-            const uint32_t turn = (uint32_t)(n / C::S + 1);
-            if (!wait(&bars->k_free[st], turn, &bars->stop)) return;
-            if (wp == 0) {
-                Step* w = steps + n % C::M;
-                if (lane < C::BLK) {
-                    w->ks[lane] = ks;
-                    w->vm[lane] = vm * kLift;
-                }
-                if (lane == 0) {
-                    w->mask = mask;
-                    w->flags = flags;
-                    w->e = E;
-                }
-                __syncwarp();
-                if (lane == 0) arrive(smem_of(&bars->step[n % C::M]));
-            }
-            // 2^(7 + e - E) as packed fp16
-            const int k7 = 7 + e - E;
-            uint32_t f = zero ? 0u : (k7 >= -14 ? (uint32_t)(k7 + 15) << 10 : 0x200u);
-            f |= f << 16;
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                if (v && !wait(&bars->v_free[st], turn, &bars->stop)) return;
-                const uint32_t dst = smem_of(stages) + (v * C::S + st) * C::kTile;
-#pragma unroll
-                for (int i = 0; i < C::ITERS; ++i) {
-                    const int u = i * 4 + wp, tg = u / C::PARTS, h = u % C::PARTS;
-                    const uint32_t w[4] = {kv[v][i].x, kv[v][i].y, kv[v][i].z, kv[v][i].w};
-                    uint32_t y[8];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        y[2 * k] = e4m3x2_to_f16x2(w[k]);
-                        y[2 * k + 1] = e4m3x2_to_f16x2(w[k] >> 16);
+            const bool zero = bits == 0;
+            e += (int)(bits >> 23);
+            const float vm = (zero ? 1.f : __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u)) * kLift;
+            const int tiles = p.steps - t0 < 8 ? p.steps - t0 : 8;
+            for (int i = 0; i < tiles; ++i) {
+                uint32_t rem = valid & (15u << (4 * i));
+                const bool last = t0 + i == p.steps - 1;
+                do {
+                    uint32_t flags = (begin ? kFirst : 0u) | (two ? kTwo : 0u);
+                    auto fitting = [&]() {
+                        return __ballot_sync(0xFFFFFFFFu, zero || (e <= E && e >= E - 22)) & rem;
+                    };
+                    uint32_t mask = fitting();
+                    if (begin || (rem != 0 && mask == 0)) {
+                        const int top = __reduce_max_sync(0xFFFFFFFFu, !zero && (rem >> lane & 1) ? e : -1000);
+                        if (!begin) flags |= kFlush;
+                        E = top == -1000 ? 0 : top + 3;
+                        mask = fitting();
                     }
-                    if (v) {
-                        const uint32_t fb = __shfl_sync(0xFFFFFFFFu, f, tg >> 1);
-                        const bool on = mask >> (tg >> 1) & 1;
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y[k]) : "r"(fb));
-                            if (!on) y[k] = 0u;  // (a NaN code times 0 is not)
+                    rem &= ~mask;
+                    if (rem == 0 && last) flags |= kLast;
+                    begin = false;
+                    Step* w = steps + n % C::M;
+                    if (n >= C::M && !wait(&bars->step_free[n % C::M], n / C::M - 1, &bars->stop)) return;
+                    if (lane >> 2 == i) {
+                        const int b = lane & 3, k7 = 7 + e - E;
+                        const bool on = mask >> lane & 1;
+                        uint32_t f = zero || !on ? 0u : (k7 >= -14 ? (uint32_t)(k7 + 15) << 10 : 0x200u);
+                        w->off[b] = have ? off : -1;
+                        w->ks[b] = ks;
+                        w->vm[b] = vm;
+                        w->f[b] = f | f << 16;
+                        if (b == 0) {
+                            w->mask = mask >> (4 * i);
+                            w->flags = flags;
+                            w->e = E;
                         }
                     }
-                    const int r = tg * 8 + r8;
-                    const uint32_t line = dst + h * (C::TOK * 128) + r * 128;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                                         line + (((2 * c4 + k) ^ (r & 7)) << 4)),
-                                     "r"(y[4 * k]), "r"(y[4 * k + 1]), "r"(y[4 * k + 2]), "r"(y[4 * k + 3])
-                                     : "memory");
-                }
-                fence_async();
-                __syncwarp();
-                if (lane == 0) arrive(smem_of(v ? &bars->v_full[st] : &bars->k_full[st]));
+                    __syncwarp();
+                    if (lane == 0) arrive(smem_of(&bars->step[n % C::M]));
+                    ++n;
+                } while (rem != 0);
             }
-            ++n;
-        } while (rem != 0);
+        }
     }
     // one more step's word: there are none left
-    const int st = n % C::S;
-    if (!wait(&bars->k_free[st], (uint32_t)(n / C::S + 1), &bars->stop)) return;
-    if (wp == 0 && lane == 0) {
+    if (n >= C::M && !wait(&bars->step_free[n % C::M], n / C::M - 1, &bars->stop)) return;
+    if (lane == 0) {
         steps[n % C::M].flags = kEnd;
         arrive(smem_of(&bars->step[n % C::M]));
     }
-    __syncwarp();
-    if (lane == 0) arrive(smem_of(&bars->k_full[st]));
 }
 
-// The warp that issues the products.
-template <class C>
-__device__ __forceinline__ void multiply(unsigned char* smem, Bars* bars, const Step* steps) {
-    constexpr uint32_t kS = product(C::TOK, false), kP = product(C::D, true);
+// The four warps that fill the stages of K (V = false) or V.  A lane's pieces are 16
+// codes of eight tokens' 64 dims, which it copies and widens itself, so that nobody else
+// waits for its copies (a bulk copy's operands move to uniform registers lane by lane:
+// 16 of them took 2000 cycles).  A quarter warp has two tokens whose numbers differ in
+// bit 0, four chunks each, of different parts where a token has several: it meets all
+// banks once, reading the codes and storing the halves.
+template <class C, bool V>
+__device__ __forceinline__ void widen(const PrefixArgs& a, unsigned char* stages, unsigned char* raw, Bars* bars,
+                                      const Step* steps, int wp) {
+    constexpr int D = C::D, N = C::N, kSlot = C::kRaw / 2;
     const int lane = threadIdx.x & 31;
-    const uint32_t q_at = smem_of(smem), k_at = q_at + C::R * C::kQ, v_at = k_at + C::S * C::kTile;
-    const uint32_t tmem = bars->tmem;
-    uint32_t p_turn[2] = {0, 0}, q_turn[2] = {0, 0};
-    uint32_t was = 0;  // flags of the step before
-    for (int n = 0;; ++n) {
-        const int st = n % C::S, pst = (n - 1) % C::S;
-        if (!wait(&bars->k_full[st], (uint32_t)(n / C::S), &bars->stop)) break;
-        const uint32_t flags = steps[n % C::M].flags;
-        if (n > 0 && !wait(&bars->v_full[pst], (uint32_t)((n - 1) / C::S), &bars->stop)) break;
-        bool ok = true;
+    const int r8 = (lane >> 3) * 2 + ((lane >> 2) & 1), c4 = lane & 3, odd = C::PARTS > 1 ? r8 & 1 : 0;
+    const int mine = r8 * D + odd * 64 + c4 * 16;
+    const uint32_t stages_s = smem_of(stages), raw_s = smem_of(raw);
+    const uint8_t* codes = V ? a.c.v : a.c.k;
+    // unit u: tokens 8 (u / PARTS) on, part u % PARTS of them (^ odd)
+    auto place = [&](int u) { return u / C::PARTS * (8 * D) + ((u % C::PARTS ^ odd) - odd) * 64 + mine; };
+    bool ok = true, more = true;
+    int fetched = 0;
+    auto fetch = [&]() {  // the next step's codes into its slot
+        if (more) {
+            if (!(ok = wait(&bars->step[fetched % C::M], fetched / C::M, &bars->stop))) return;
+            const Step* w = steps + fetched % C::M;
+            more = !(w->flags & kEnd);
+            if (more) {
+                const uint32_t dst = raw_s + fetched % N * kSlot;
 #pragma unroll
-        for (int x = 0; x < C::R; ++x) {
-            if (n > 0) {
-                if (!(ok = wait(&bars->p_full[x], p_turn[x]++, &bars->stop))) break;
-                tc_after();
-                if (lane == 0) {
-                    if (x == 0 || (was & kTwo)) {
-                        const uint32_t o = tmem + C::kO + x * C::D, p = tmem + x * 128;
-                        const bool fresh = was & (kFirst | kFlush);
-#pragma unroll
-                        for (int k = 0; k < C::TOK / 16; ++k)
-                            mma_ts(o, p + k * 8, operand(v_at + pst * C::kTile + k * 2048, C::TOK * 128), kP,
-                                   !(fresh && k == 0));
-                        if (was & kLast) commit(smem_of(&bars->o_done[x]));
-                    }
-                    if (x == C::R - 1) commit(smem_of(&bars->v_free[pst]));
+                for (int i = 0; i < C::ITERS; ++i) {
+                    const int u = i * 4 + wp, b = u / C::PARTS >> 1, at = place(u);
+                    const int64_t off = w->off[b];
+                    const int64_t from = (off < 0 ? 0 : off) + (at - b * (kBlock * D));
+                    const int bytes = off < 0 ? 0 : 16;  // (0: zeros)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + at), "l"(codes + from),
+                                 "r"(bytes)
+                                 : "memory");
                 }
-                __syncwarp();
-            }
-            if (!(flags & kEnd)) {  // (a row tile without rows keeps step with the other)
-                const bool on = x == 0 || (flags & kTwo);
-                if (on && (flags & kFirst) && !(ok = wait(&bars->q_full[x], q_turn[x]++, &bars->stop))) break;
-                tc_after();
-                if (lane == 0) {
-                    if (on) {
-#pragma unroll
-                        for (int k = 0; k < C::D / 16; ++k)
-                            mma_ss(tmem + x * 128,
-                                   operand(q_at + x * C::kQ + (k / 4) * (128 * 128) + (k % 4) * 32, 16),
-                                   operand(k_at + st * C::kTile + (k / 4) * (C::TOK * 128) + (k % 4) * 32, 16), kS,
-                                   k > 0);
-                    }
-                    commit(smem_of(&bars->s_full[x]));
-                }
-                __syncwarp();
+                ++fetched;
             }
         }
-        if (!ok || (flags & kEnd)) break;
-        if (lane == 0) commit(smem_of(&bars->k_free[st]));
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = 0; i < N && ok; ++i) fetch();
+    for (int n = 0; ok && n < fetched; ++n) {
+        const Step* w = steps + n % C::M;
+        const int st = n & 1;
+        asm volatile("cp.async.wait_group %0;" ::"n"(N - 1) : "memory");
+        // K's stage is free behind the scores of step n - 2, V's behind its sums
+        if (n >= 2 && !(ok = wait(V ? &bars->pv[st] : &bars->s_full[C::R - 1][st], n / 2 - 1, &bars->stop))) break;
+        const uint32_t dst = stages_s + st * C::kTile, src = raw_s + n % N * kSlot;
+#pragma unroll
+        for (int i = 0; i < C::ITERS; ++i) {
+            const int u = i * 4 + wp, tg = u / C::PARTS, h = u % C::PARTS ^ odd, r = tg * 8 + r8;
+            uint32_t x[4], y[8];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                         : "r"(src + place(u))
+                         : "memory");
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                y[2 * k] = e4m3x2_to_f16x2(x[k]);
+                y[2 * k + 1] = e4m3x2_to_f16x2(x[k] >> 16);
+            }
+            if constexpr (V) {
+                const uint32_t f = w->f[tg >> 1];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y[k]) : "r"(f));
+                if (!(w->mask >> (tg >> 1) & 1)) {  // not of this step (a NaN code times 0 is not 0)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = 0u;
+                }
+            }
+            const uint32_t line = dst + h * (C::TOK * 128) + r * 128;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(line + (((2 * c4 + k) ^ (r & 7)) << 4)),
+                             "r"(y[4 * k]), "r"(y[4 * k + 1]), "r"(y[4 * k + 2]), "r"(y[4 * k + 3])
+                             : "memory");
+        }
+        fence_async();
         __syncwarp();
-        was = flags;
+        if (lane == 0) {
+            arrive(smem_of(V ? &bars->v_full[st] : &bars->k_full[st]));
+            arrive(smem_of(&bars->step_free[n % C::M]));
+        }
+        fetch();
     }
-    // nothing is in flight when the block leaves
-    if (lane == 0) commit(smem_of(&bars->last));
-    __syncwarp();
+    asm volatile("cp.async.wait_all;" ::: "memory");  // no copy outlives the block
+}
+
+// The two threads that issue the products, one the scores and one the sums.  The tensor
+// cores take a product in 65 cycles and have about four of them queued; a wait costs 100
+// cycles, a commit 60: with one thread, 1000 of a step's 3100 cycles were such gaps.
+// Operands' places are worked out for each product (kept, they fill the registers).
+template <class C, int X, bool FRESH>
+__device__ __forceinline__ void product_pv(uint32_t v_op, int st) {
+    v_op += st * (C::kTile >> 4);
+#pragma unroll
+    for (int k = 0; k < C::TOK / 16; ++k)
+        mma_ts<FRESH>(C::kO + X * C::D, (2 * X + st) * 64 + k * 8, v_op + (k * 2048 >> 4), product(C::D, true), k);
+}
+template <class C, int X>
+__device__ __forceinline__ void product_qk(uint32_t q_op, uint32_t k_op, int st) {
+    k_op += st * (C::kTile >> 4);
+#pragma unroll
+    for (int k = 0; k < C::D / 16; ++k)
+        mma_ss((2 * X + st) * 64, q_op + ((X * C::kQ + (k / 4) * (128 * 128) + (k % 4) * 32) >> 4),
+               k_op + (((k / 4) * (C::TOK * 128) + (k % 4) * 32) >> 4), product(C::TOK, false), k);
+}
+
+// Nothing of the thread's is in flight when it leaves.
+__device__ __forceinline__ void settle(uint64_t* bar) {
+    commit(smem_of(bar));
     const long long t0 = clock64();
-    while (!rmsn::mbar_try_wait(smem_of(&bars->last), 0) && clock64() - t0 < kWaitCycles) {
+    while (!rmsn::mbar_try_wait(smem_of(bar), 0) && clock64() - t0 < kWaitCycles) {
     }
+}
+
+template <class C>
+__device__ __forceinline__ void scores(unsigned char* smem, Bars* bars, const Step* steps) {
+    uint32_t q_op = operand(smem_of(smem), 16), k_op = operand(smem_of(smem) + C::R * C::kQ, 16);
+    uint32_t* stop = &bars->stop;
+    int turn[2] = {0, 0};
+    for (int n = 0;; ++n) {
+        const int st = n & 1;
+        asm volatile("" : "+r"(q_op), "+r"(k_op));
+        if (!wait_alone(&bars->step[n % C::M], n / C::M, stop)) break;
+        const uint32_t flags = steps[n % C::M].flags;
+        if (flags & kEnd) break;
+        // the scores' place is free behind the sums of step n - 2
+        if (n >= 2 && !wait_alone(&bars->pv[st], n / 2 - 1, stop)) break;
+        if (!wait_alone(&bars->k_full[st], n >> 1, stop)) break;
+        if (flags & kFirst) {
+            if (!wait_alone(&bars->q_full[0], turn[0]++, stop)) break;
+            if (C::R == 2 && (flags & kTwo) && !wait_alone(&bars->q_full[1], turn[1]++, stop)) break;
+        }
+        tc_after();
+        product_qk<C, 0>(q_op, k_op, st);
+        commit(smem_of(&bars->s_full[0][st]));
+        if constexpr (C::R == 2) {  // (a row tile without rows keeps step with the other)
+            if (flags & kTwo) product_qk<C, 1>(q_op, k_op, st);
+            commit(smem_of(&bars->s_full[1][st]));
+        }
+    }
+    settle(&bars->last[0]);
+}
+
+template <class C>
+__device__ __forceinline__ void sums(unsigned char* smem, Bars* bars, const Step* steps) {
+    uint32_t v_op = operand(smem_of(smem) + C::R * C::kQ + 2 * C::kTile, C::TOK * 128);
+    uint32_t* stop = &bars->stop;
+    for (int n = 0;; ++n) {
+        const int st = n & 1;
+        asm volatile("" : "+r"(v_op));
+        if (!wait_alone(&bars->step[n % C::M], n / C::M, stop)) break;
+        const uint32_t flags = steps[n % C::M].flags;
+        if (flags & kEnd) break;
+        arrive(smem_of(&bars->step_free[n % C::M]));
+        const bool fresh = flags & (kFirst | kFlush);
+        if (!wait_alone(&bars->v_full[st], n >> 1, stop) || !wait_alone(&bars->p_full[0][st], n >> 1, stop)) break;
+        tc_after();
+        if (fresh) product_pv<C, 0, true>(v_op, st);
+        else product_pv<C, 0, false>(v_op, st);
+        if constexpr (C::R == 2) {
+            if (!wait_alone(&bars->p_full[1][st], n >> 1, stop)) break;
+            tc_after();
+            if (flags & kTwo) {
+                if (fresh) product_pv<C, 1, true>(v_op, st);
+                else product_pv<C, 1, false>(v_op, st);
+            }
+        }
+        commit(smem_of(&bars->pv[st]));
+    }
+    settle(&bars->last[1]);
 }
 
 // The four warps of row tile x.
 template <class T, class C>
-__device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem, Bars* bars, const Step* steps, int x) {
+__device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem, Bars* bars, const Step* steps,
+                                       Way* way, int x) {
     constexpr int D = C::D, ROWS = 128 * C::R;
     const int wp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31, r = wp * 32 + lane;
     const uint32_t lanes = (uint32_t)(wp * 32) << 16;
-    const uint32_t s_at = bars->tmem + lanes + x * 128, o_at = bars->tmem + lanes + C::kO + x * D;
+    const uint32_t o_at = lanes + C::kO + x * D;
     unsigned char* q_rows = smem + x * C::kQ;
-    Walk walk;
-    walk.begin(a);
-    Piece p;
-    uint32_t s_turn = 0, o_turn = 0;
+    way->begin(a, lane);
     int n = 0;  // steps of the block so far
     float q_scale = 0.f, q_next = 0.f;
     int valid = 0, valid_next = 0;  // rows of this tile
     // the piece's queries, scaled to fp16 by a power of two as in attn_attend.cuh
     auto load_q = [&]() {
+        const Piece& p = way->p;
         const int cols = (p.g.s1 - p.g.s0) * a.n * a.group - p.tile * ROWS - x * 128;
         valid_next = cols < 0 ? 0 : cols;
         if (valid_next == 0) return;  // (x == 1 alone: the products leave it out)
@@ -564,14 +637,12 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
         __syncwarp();
         if (lane == 0) arrive(smem_of(&bars->q_full[x]));
     };
-    bool more = walk.next(a, &p);
-    if (more) load_q();
-    while (more) {
-        const Piece now = p;
+    if (way->more) load_q();
+    while (way->more) {
         q_scale = q_next;
         valid = valid_next;
         const bool busy = wp * 32 < valid;  // the warp has rows
-        float* part = a.parts + ((int64_t)blockIdx.x + now.item) * (ROWS * (int64_t)(D + 2)) + (x * 128 + r) * 8;
+        float* part = a.parts + ((int64_t)blockIdx.x + way->p.item) * (ROWS * (int64_t)(D + 2)) + (x * 128 + r) * 8;
         float ref = kNone, l = 0.f;
         float part_ref = 0.f;
         bool has_part = false;
@@ -584,7 +655,8 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
                 float o[32];
-                tmem_load(o, o_at + d);
+                tmem_begin(o, o_at + d);
+                tmem_loaded(o);
                 if (r < valid) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
@@ -605,106 +677,125 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
         if (valid > 0 || x == 0) {
             do {
                 const Step* w = steps + n % C::M;
-                if (!wait(&bars->step[n % C::M], (uint32_t)(n / C::M), &bars->stop)) return;
-                if (!wait(&bars->s_full[x], s_turn++, &bars->stop)) return;
+                const uint32_t s_at = lanes + (2 * x + (n & 1)) * 64;
+                if (!wait(&bars->step[n % C::M], n / C::M, &bars->stop)) return;
+                if (!wait(&bars->s_full[x][n & 1], n >> 1, &bars->stop)) return;
                 tc_after();
                 flags = w->flags;
                 if (busy) {
                     const uint32_t mask = w->mask;
-                    if (flags & kFlush) drain();
+                    if (flags & kFlush) {
+                        if (!wait(&bars->pv[(n - 1) & 1], (n - 1) >> 1, &bars->stop)) return;
+                        tc_after();
+                        drain();
+                    }
                     E = w->e;
-                    // the row's maximum
+                    // a row's scores stay in its thread's registers
+                    float s[C::TOK], kc[C::BLK];
+#pragma unroll
+                    for (int c = 0; c < C::TOK; c += 32) tmem_begin(s + c, s_at + c);
+#pragma unroll
+                    for (int b = 0; b < C::BLK; ++b) kc[b] = w->ks[b] * q_scale;  // not negative
+                    tmem_loaded(s);
                     float top = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < C::TOK; c += 32) {
-                        float s[32];
-                        tmem_load(s, s_at + c);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (!(mask >> (c / 16 + h) & 1)) continue;
-                            const float kc = w->ks[c / 16 + h] * q_scale;
-                            float m = -INFINITY;  // of the scores before the factor, which is not negative
+                    for (int b = 0; b < C::BLK; ++b) {
+                        float m0 = s[16 * b], m1 = s[16 * b + 1];
 #pragma unroll
-                            for (int i = 0; i < 16; i += 2) m = max3(m, s[16 * h + i], s[16 * h + i + 1]);
-                            top = fmaxf(top, __fmul_rn(m, kc));
+                        for (int i = 2; i < 16; i += 4) {
+                            m0 = max3(m0, s[16 * b + i], s[16 * b + i + 1]);
+                            if (i + 3 < 16) m1 = max3(m1, s[16 * b + i + 2], s[16 * b + i + 3]);
                         }
+                        const float m = __fmul_rn(fmaxf(m0, m1), kc[b]);
+                        if (mask >> b & 1) top = fmaxf(top, m);
                     }
                     if (__any_sync(0xFFFFFFFFu, top > ref + kSlack)) {
                         const float to = fmaxf(ref, top), keep = exp2a(ref - to);
                         ref = to;
                         l *= keep;
                         if (!(flags & (kFirst | kFlush))) {
+                            if (!wait(&bars->pv[(n - 1) & 1], (n - 1) >> 1, &bars->stop)) return;
+                            tc_after();
 #pragma unroll 1
-                            for (int d = 0; d < D; d += 32) {
-                                float o[32];
-                                tmem_load(o, o_at + d);
+                            for (int d = 0; d < D; d += 16) {
+                                float o[16];
+                                tmem_begin16(o, o_at + d);
+                                tmem_loaded(o);
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] *= keep;
-                                tmem_store32(o_at + d, o);
+                                for (int i = 0; i < 16; ++i) o[i] *= keep;
+                                tmem_store16(o_at + d, reinterpret_cast<const uint32_t(&)[16]>(o));
                             }
                             tmem_stored();
                         }
                     }
                     // the weights
-                    const bool wide = __any_sync(0xFFFFFFFFu, fabsf(ref) > kWide && ref != kNone);
-                    F2 sum = rmsn::f2(0.f, 0.f);
-                    const F2 less = rmsn::f2(-ref, -ref);
-#pragma unroll 1
+                    F2 sum[2] = {rmsn::f2(0.f, 0.f), rmsn::f2(0.f, 0.f)};
+                    if (__any_sync(0xFFFFFFFFu, fabsf(ref) > kWide && ref != kNone)) {
+#pragma unroll
+                        for (int j = 0; j < C::TOK; ++j)
+                            s[j] = exp2a(__fsub_rn(__fmul_rn(s[j], kc[j / 16]), ref));
+                    } else {
+                        const F2 less = rmsn::f2(-ref, -ref);
+#pragma unroll
+                        for (int j = 0; j < C::TOK; j += 2) {
+                            const F2 k2 = rmsn::f2(kc[j / 16], kc[j / 16]);
+                            float lo, hi;
+                            rmsn::f2split(rmsn::fma2(rmsn::f2(s[j], s[j + 1]), k2, less), lo, hi);
+                            s[j] = exp2a(lo);
+                            s[j + 1] = exp2a(hi);
+                        }
+                    }
+                    if (mask != (1u << C::BLK) - 1) {
+#pragma unroll
+                        for (int j = 0; j < C::TOK; ++j)
+                            if (!(mask >> (j / 16) & 1)) s[j] = 0.f;
+                    }
+#pragma unroll
                     for (int c = 0; c < C::TOK; c += 32) {
-                        float s[32];
                         uint32_t y[16];
-                        tmem_load(s, s_at + c);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (!(mask >> (c / 16 + h) & 1)) {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) y[8 * h + i] = 0u;
-                                continue;
-                            }
-                            const float kc = w->ks[c / 16 + h] * q_scale, vm = w->vm[c / 16 + h];
-                            const F2 kc2 = rmsn::f2(kc, kc), vm2 = rmsn::f2(vm, vm);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                float lo = s[16 * h + 2 * i], hi = s[16 * h + 2 * i + 1];
-                                if (wide) {
-                                    lo = __fsub_rn(__fmul_rn(lo, kc), ref);
-                                    hi = __fsub_rn(__fmul_rn(hi, kc), ref);
-                                } else {
-                                    rmsn::f2split(rmsn::fma2(rmsn::f2(lo, hi), kc2, less), lo, hi);
-                                }
-                                const F2 pp = rmsn::f2(exp2a(lo), exp2a(hi));
-                                sum = rmsn::add2(sum, pp);
-                                rmsn::f2split(rmsn::mul2(pp, vm2), lo, hi);
-                                y[8 * h + i] = rmsn::pack_f16x2(lo, hi);
-                            }
+                        for (int i = 0; i < 16; ++i) {
+                            const int j = c + 2 * i;
+                            const F2 pp = rmsn::f2(s[j], s[j + 1]);
+                            const float vm = w->vm[j / 16];
+                            float lo, hi;
+                            sum[i & 1] = rmsn::add2(sum[i & 1], pp);
+                            rmsn::f2split(rmsn::mul2(pp, rmsn::f2(vm, vm)), lo, hi);
+                            y[i] = rmsn::pack_f16x2(lo, hi);
                         }
                         tmem_store16(s_at + c / 2, y);
                     }
                     float lo, hi;
-                    rmsn::f2split(sum, lo, hi);
+                    rmsn::f2split(rmsn::add2(sum[0], sum[1]), lo, hi);
                     l += lo + hi;
                     tmem_stored();
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) arrive(smem_of(&bars->p_full[x]));
+                if (lane == 0) {
+                    arrive(smem_of(&bars->p_full[x][n & 1]));
+                    arrive(smem_of(&bars->step_free[n % C::M]));
+                }
                 ++n;
             } while (!(flags & kLast));
         } else {  // the other row tile's steps
             do {
-                if (!wait(&bars->step[n % C::M], (uint32_t)(n / C::M), &bars->stop)) return;
-                if (!wait(&bars->s_full[x], s_turn++, &bars->stop)) return;
+                if (!wait(&bars->step[n % C::M], n / C::M, &bars->stop)) return;
+                if (!wait(&bars->s_full[x][n & 1], n >> 1, &bars->stop)) return;
                 flags = steps[n % C::M].flags;
                 __syncwarp();
-                if (lane == 0) arrive(smem_of(&bars->p_full[x]));
+                if (lane == 0) {
+                    arrive(smem_of(&bars->p_full[x][n & 1]));
+                    arrive(smem_of(&bars->step_free[n % C::M]));
+                }
                 ++n;
             } while (!(flags & kLast));
         }
         // the next piece's queries while the last product runs: its scores are through
-        more = walk.next(a, &p);
-        if (more) load_q();
+        way->next_piece(a, lane);
+        if (way->more) load_q();
         if (valid > 0 || x == 0) {
-            if (!wait(&bars->o_done[x], o_turn++, &bars->stop)) return;
+            if (!wait(&bars->pv[(n - 1) & 1], (n - 1) >> 1, &bars->stop)) return;
             tc_after();
             if (busy) {
                 drain();
@@ -717,31 +808,34 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
 }
 
 template <class T, class C>
-__global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const PrefixArgs a) {
+__global__ void __launch_bounds__(C::kWarps * 32, 1) prefix_kernel(const PrefixArgs a) {
     extern __shared__ unsigned char raw[];
     __shared__ Bars bars;
     __shared__ Step steps[C::M];
+    __shared__ Way ways[4 * C::R];
     unsigned char* smem = raw + ((1024 - (smem_of(raw) & 1023)) & 1023);
     const int wp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::S; ++i) {
+        for (int i = 0; i < C::M; ++i) {
+            rmsn::mbar_init(smem_of(&bars.step[i]), 1);
+            rmsn::mbar_init(smem_of(&bars.step_free[i]), 4 * C::R + 9);
+        }
+        for (int i = 0; i < 2; ++i) {
             rmsn::mbar_init(smem_of(&bars.k_full[i]), 4);
             rmsn::mbar_init(smem_of(&bars.v_full[i]), 4);
-            rmsn::mbar_init(smem_of(&bars.k_free[i]), 1);
-            rmsn::mbar_init(smem_of(&bars.v_free[i]), 1);
-        }
-        for (int i = 0; i < C::M; ++i) rmsn::mbar_init(smem_of(&bars.step[i]), 1);
-        for (int i = 0; i < C::R; ++i) {
-            rmsn::mbar_init(smem_of(&bars.s_full[i]), 1);
-            rmsn::mbar_init(smem_of(&bars.p_full[i]), 4);
+            rmsn::mbar_init(smem_of(&bars.pv[i]), 1);
             rmsn::mbar_init(smem_of(&bars.q_full[i]), 4);
-            rmsn::mbar_init(smem_of(&bars.o_done[i]), 1);
+            for (int k = 0; k < 2; ++k) {
+                rmsn::mbar_init(smem_of(&bars.s_full[i][k]), 1);
+                rmsn::mbar_init(smem_of(&bars.p_full[i][k]), 4);
+            }
         }
-        rmsn::mbar_init(smem_of(&bars.last), 1);
+        rmsn::mbar_init(smem_of(&bars.last[0]), 1);
+        rmsn::mbar_init(smem_of(&bars.last[1]), 1);
         bars.stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (wp == 4 * C::R + 4) {
+    if (wp == 4 * C::R + 8) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_of(&bars.tmem)),
                      "n"(C::kCols)
                      : "memory");
@@ -750,22 +844,36 @@ __global__ void __launch_bounds__(C::kThreads, 1) prefix_kernel(const PrefixArgs
     tc_before();
     __syncthreads();
     tc_after();
+    // (all of TMEM is the block's, so it begins at 0, and places in it are constants)
+    if (threadIdx.x == 0 && bars.tmem != 0) bars.stop = 1;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (wp < 4 * C::R) soften<T, C>(a, smem, &bars, steps, wp >> 2);
-    else if (wp < 4 * C::R + 4) produce<C>(a, smem + C::R * C::kQ, &bars, steps, wp & 3);
-    else multiply<C>(smem, &bars, steps);
+    unsigned char* stages = smem + C::R * C::kQ;
+    unsigned char* codes = stages + 4 * C::kTile;
+    if (wp < 4 * C::R) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegsS));
+        soften<T, C>(a, smem, &bars, steps, &ways[wp], wp >> 2);
+    } else if (wp < 4 * C::R + 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsW));
+        if (wp < 4 * C::R + 4) widen<C, false>(a, stages, codes, &bars, steps, wp & 3);
+        else widen<C, true>(a, stages + 2 * C::kTile, codes + C::N * C::kRaw / 2, &bars, steps, wp & 3);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsM));
+        if (threadIdx.x == (4 * C::R + 8) * 32) scores<C>(smem, &bars, steps);
+        else if (threadIdx.x == (4 * C::R + 9) * 32) sums<C>(smem, &bars, steps);
+        else if (wp == 4 * C::R + 10) plan<C>(a, &bars, steps);
+    }
     tc_before();
     __syncthreads();
     tc_after();
-    if (wp == 4 * C::R + 4)
+    if (wp == 4 * C::R + 8)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(bars.tmem), "n"(C::kCols) : "memory");
     if (threadIdx.x == 0 && bars.stop) atomicOr(a.status, kWaitRanOut);
 }
 
 template <class C>
 PrefixEntry entry(int dt) {
-    return PrefixEntry{dt, C::D, C::R, C::TOK, C::kThreads, C::kSmem,
+    return PrefixEntry{dt, C::D, C::R, C::TOK, C::kWarps * 32, C::kSmem,
                        dt == 1 ? (const void*)&prefix_kernel<BF16, C> : (const void*)&prefix_kernel<F16, C>};
 }
 

@@ -205,7 +205,7 @@ int64_t rmsattn_kv_attention_workspace(int64_t n_seqs, int64_t n_queries, int64_
  * codes, which stay exact.
  *
  *   workspace   rmsattn_kv_prefix_attention_workspace(...) bytes on the device,
- *               16-byte aligned, used by this call alone until it has finished
+ *               32-byte aligned, used by this call alone until it has finished
  */
 int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* cache, const int32_t* block_table,
                                 int64_t table_stride, int64_t table_width, const int32_t* lengths,

@@ -576,62 +576,60 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
     int n = 0;  // steps of the block so far
     float q_scale = 0.f, q_next = 0.f;
     int valid = 0, valid_next = 0;  // rows of this tile
-    // the piece's queries, scaled to fp16 by a power of two as in attn_attend.cuh
+    // The piece's queries, scaled to fp16 by a power of two as in attn_attend.cuh: copied
+    // as they are (a warp its own rows), and rounded in place, a thread a row.
     auto load_q = [&]() {
         const Piece& p = way->p;
-        const int cols = (p.g.s1 - p.g.s0) * a.n * a.group - p.tile * ROWS - x * 128;
+        const int first = p.tile * ROWS + x * 128, cols = (p.g.s1 - p.g.s0) * a.n * a.group - first;
         valid_next = cols < 0 ? 0 : cols;
         if (valid_next == 0) return;  // (x == 1 alone: the products leave it out)
-        q_next = 0.f;
-        if (r >= valid_next) {  // rows of nothing: scores of 0
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint4*>(q_rows + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                    make_uint4(0, 0, 0, 0);
-        } else {
-            const int cc = p.tile * ROWS + x * 128 + r, token = cc / a.group;
+        // 16-byte chunk c of row i, swizzled
+        auto chunk = [&](int i, int c) {
+            return smem_of(q_rows) + (c >> 3) * (128 * 128) + i * 128 + (((c & 7) ^ (i & 7)) << 4);
+        };
+        constexpr int CH = D / 8;
+#pragma unroll 4
+        for (int k = 0; k < CH; ++k) {
+            const int e = k * 32 + lane, i = wp * 32 + e / CH, c = e % CH;
+            const bool on = i < valid_next;  // (rows of nothing: zeros, scores of 0)
+            const int cc = on ? first + i : first, token = cc / a.group;
             const uint16_t* src = static_cast<const uint16_t*>(a.q) + ((int64_t)p.g.s0 * a.n + token) * a.q_stride +
-                                  (int64_t)(p.hk * a.group + cc - token * a.group) * D;
-            constexpr int H = 64;  // dims held at once
-            uint4 v[H / 8];
-            float m = 0.f;
-#pragma unroll 1
-            for (int d0 = D - H; d0 >= 0; d0 -= H) {
+                                  (int64_t)(p.hk * a.group + cc - token * a.group) * D + c * 8;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(chunk(i, c)), "l"(src), "r"(on ? 16 : 0)
+                         : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        float m = 0.f;
+#pragma unroll 2
+        for (int c = 0; c < CH; ++c) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(chunk(r, c))
+                         : "memory");
 #pragma unroll
-                for (int i = 0; i < H / 8; ++i) v[i] = *reinterpret_cast<const uint4*>(src + d0 + i * 8);
+            for (int k = 0; k < 4; ++k)  // (a maximum leaves NaN out; its products find it)
+                m = rmsn::absmax3(m, rmsn::lo2<T>(w[k]), rmsn::hi2<T>(w[k]));
+        }
+        int e = (int)(__float_as_uint(m) >> 23) - 127 - 7;
+        e = e < -126 ? -126 : (e > 126 ? 126 : e);
+        const float down =
+            m > 3.402823466e38f ? __uint_as_float(0x7FFFFFFFu) : copysignf(pow2(-e), a.scale);
+        q_next = pow2(e) * (fabsf(a.scale) * kLog2e);
+#pragma unroll 2
+        for (int c = 0; c < CH; ++c) {
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(chunk(r, c))
+                         : "memory");
 #pragma unroll
-                for (int i = 0; i < H / 8; ++i) {
-                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        // (a maximum leaves NaN out; its products find it)
-                        m = rmsn::absmax3(m, rmsn::lo2<T>(w[k]), rmsn::hi2<T>(w[k]));
-                    }
-                }
-            }
-            int e = (int)(__float_as_uint(m) >> 23) - 127 - 7;
-            e = e < -126 ? -126 : (e > 126 ? 126 : e);
-            const float down = m > 3.402823466e38f ? __uint_as_float(0x7FFFFFFFu)
-                                                   : copysignf(pow2(-e), a.scale);
-            q_next = pow2(e) * (fabsf(a.scale) * kLog2e);
-#pragma unroll 1
-            for (int d0 = 0; d0 < D; d0 += H) {  // (the first are still there)
-                if (d0 > 0) {
-#pragma unroll
-                    for (int i = 0; i < H / 8; ++i) v[i] = *reinterpret_cast<const uint4*>(src + d0 + i * 8);
-                }
-#pragma unroll
-                for (int i = 0; i < H / 8; ++i) {
-                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                    uint32_t y[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        y[k] = rmsn::pack_f16x2(rmsn::lo2<T>(w[k]) * down, rmsn::hi2<T>(w[k]) * down);
-                    const int c = d0 / 8 + i;
-                    *reinterpret_cast<uint4*>(q_rows + (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                        make_uint4(y[0], y[1], y[2], y[3]);
-                }
-            }
+            for (int k = 0; k < 4; ++k)
+                w[k] = rmsn::pack_f16x2(rmsn::lo2<T>(w[k]) * down, rmsn::hi2<T>(w[k]) * down);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(chunk(r, c)), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                         "r"(w[3])
+                         : "memory");
         }
         fence_async();
         __syncwarp();
@@ -659,14 +657,21 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
                 tmem_loaded(o);
                 if (r < valid) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        float4* y = reinterpret_cast<float4*>(part + (d / 8 + i / 8) * (ROWS * 8) + (i & 4));
-                        float4 v = make_float4(o[i] * f0 * f1, o[i + 1] * f0 * f1, o[i + 2] * f0 * f1, o[i + 3] * f0 * f1);
-                        if (has_part) {
-                            const float4 w = *y;
-                            v = make_float4(v.x + w.x * keep, v.y + w.y * keep, v.z + w.z * keep, v.w + w.w * keep);
+                    for (int i = 0; i < 32; i += 8) {  // 32 bytes: a whole sector
+                        float* y = part + (d / 8 + i / 8) * (ROWS * 8);
+                        uint32_t u[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            o[i + k] *= f0;
+                            o[i + k] *= f1;
                         }
-                        *y = v;
+                        if (has_part) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) o[i + k] += y[k] * keep;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(o[i + k]);
+                        rmsn::st_stream32(y, u);
                     }
                 }
             }
@@ -731,19 +736,20 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
                     // the weights
                     F2 sum[2] = {rmsn::f2(0.f, 0.f), rmsn::f2(0.f, 0.f)};
                     if (__any_sync(0xFFFFFFFFu, fabsf(ref) > kWide && ref != kNone)) {
+                        // from the rounded products, as the reference was taken
 #pragma unroll
-                        for (int j = 0; j < C::TOK; ++j)
-                            s[j] = exp2a(__fsub_rn(__fmul_rn(s[j], kc[j / 16]), ref));
-                    } else {
-                        const F2 less = rmsn::f2(-ref, -ref);
+                        for (int j = 0; j < C::TOK; ++j) s[j] = __fmul_rn(s[j], kc[j / 16]);
 #pragma unroll
-                        for (int j = 0; j < C::TOK; j += 2) {
-                            const F2 k2 = rmsn::f2(kc[j / 16], kc[j / 16]);
-                            float lo, hi;
-                            rmsn::f2split(rmsn::fma2(rmsn::f2(s[j], s[j + 1]), k2, less), lo, hi);
-                            s[j] = exp2a(lo);
-                            s[j + 1] = exp2a(hi);
-                        }
+                        for (int b = 0; b < C::BLK; ++b) kc[b] = 1.f;
+                    }
+                    const F2 less = rmsn::f2(-ref, -ref);
+#pragma unroll
+                    for (int j = 0; j < C::TOK; j += 2) {
+                        const F2 k2 = rmsn::f2(kc[j / 16], kc[j / 16]);
+                        float lo, hi;
+                        rmsn::f2split(rmsn::fma2(rmsn::f2(s[j], s[j + 1]), k2, less), lo, hi);
+                        s[j] = exp2a(lo);
+                        s[j + 1] = exp2a(hi);
                     }
                     if (mask != (1u << C::BLK) - 1) {
 #pragma unroll

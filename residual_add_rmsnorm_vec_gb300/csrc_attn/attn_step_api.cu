@@ -254,7 +254,7 @@ RMSATTN_API int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* 
     if (!group_cu && n_groups > 1) return RMSN_EINVAL;
     if (n_seqs == 0) return RMSN_OK;
     if (!q || !out || !lengths || (n_groups && !prefix_lengths) || !workspace) return RMSN_EINVAL;
-    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(workspace, 16) ||
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lengths, 4) || !aligned(workspace, 32) ||
         !aligned(prefix_lengths, 4) || !aligned(group_cu, 4))
         return RMSN_EALIGN;
     DeviceInfo* d = device_info();

@@ -65,11 +65,11 @@ def test_norms_refusals(rn, kw, status):  # noqa: F811
     (dict(qs=255), EINVAL), (dict(os=252), EINVAL), (dict(ts=1), EINVAL), (dict(q=None), EINVAL),
     (dict(out=None), EINVAL), (dict(lengths=None), EINVAL), (dict(prefix=None), EINVAL), (dict(ws=None), EINVAL),
     (dict(q=24), EALIGN), (dict(out=8), EALIGN), (dict(lengths=18), EALIGN), (dict(prefix=18), EALIGN),
-    (dict(cu=18), EALIGN), (dict(ws=8), EALIGN), (dict(B=0, q=None, out=None, ws=None), OK),
+    (dict(cu=18), EALIGN), (dict(ws=16), EALIGN), (dict(B=0, q=None, out=None, ws=None), OK),
 ])
 def test_prefix_refusals(rn, kw, status):  # noqa: F811
     a = dict(q=16, cache=None, table=16, ts=2, width=2, lengths=16, prefix=16, cu=16, groups=2, out=16, qs=256, os=256,
-             B=3, n=1, hq=4, scale=0.125, ws=16, wsb=1 << 40, flags=BF16)
+             B=3, n=1, hq=4, scale=0.125, ws=32, wsb=1 << 40, flags=BF16)
     c = {k: kw[k] for k in kw if k not in a}
     a.update({k: kw[k] for k in kw if k in a})
     a["cache"] = ctypes.byref(cache_struct(rn, **c))

@@ -15,54 +15,71 @@ namespace rmsattn {
 
 namespace {
 
-// V consecutive elements of T as floats, from element e on.
+// V consecutive elements of T as they lie in memory.
+template <class T, int V>
+struct Raw {
+    uint32_t u[V * T::kBytes >= 4 ? V * T::kBytes / 4 : 1];
+};
 template <class T, int V, bool STREAM>
-__device__ __forceinline__ void load(const void* p, int64_t e, float (&y)[V]) {
+__device__ __forceinline__ Raw<T, V> load(const void* p, int64_t e) {
+    Raw<T, V> v;
     if constexpr (V == 1) {
-        y[0] = load1<T>(p, e);
+        if constexpr (T::kBytes == 4) v.u[0] = static_cast<const uint32_t*>(p)[e];
+        else v.u[0] = static_cast<const uint16_t*>(p)[e];
     } else if constexpr (T::kBytes == 4) {
         static_assert(V == 8, "");
-        const rmsn::V8 v = STREAM ? rmsn::ld_stream32(static_cast<const float*>(p) + e)
+        const rmsn::V8 w = STREAM ? rmsn::ld_stream32(static_cast<const float*>(p) + e)
                                   : rmsn::ld_keep32(static_cast<const float*>(p) + e);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = __uint_as_float(v.u[k]);
+        for (int k = 0; k < 8; ++k) v.u[k] = w.u[k];
     } else {
         const uint16_t* q = static_cast<const uint16_t*>(p) + e;
         const uint4 w = STREAM ? rmsn::ld_stream16(q) : rmsn::ld_keep16(q);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        v.u[0] = w.x;
+        v.u[1] = w.y;
+        v.u[2] = w.z;
+        v.u[3] = w.w;
+    }
+    return v;
+}
+template <class T, int V>
+__device__ __forceinline__ void widen(const Raw<T, V>& v, float (&y)[V]) {
+    if constexpr (T::kBytes == 4) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            y[2 * k] = rmsn::lo2<T>(u[k]);
-            y[2 * k + 1] = rmsn::hi2<T>(u[k]);
+        for (int k = 0; k < V; ++k) y[k] = __uint_as_float(v.u[k]);
+    } else if constexpr (V == 1) {
+        y[0] = rmsn::lo2<T>(v.u[0]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) {
+            y[2 * k] = rmsn::lo2<T>(v.u[k]);
+            y[2 * k + 1] = rmsn::hi2<T>(v.u[k]);
         }
     }
 }
-
-// Rounds to T, stores, and leaves the rounded values in y.
 template <class T, int V>
-__device__ __forceinline__ void store_rounded(void* p, int64_t e, float (&y)[V]) {
+__device__ __forceinline__ Raw<T, V> round_to(const float (&y)[V]) {
+    Raw<T, V> v;
     if constexpr (T::kBytes == 4) {
-        if constexpr (V == 1) {
-            static_cast<float*>(p)[e] = y[0];
-        } else {
-            uint32_t u[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) u[k] = __float_as_uint(y[k]);
-            rmsn::st_stream32(static_cast<float*>(p) + e, u);
-        }
+        for (int k = 0; k < V; ++k) v.u[k] = __float_as_uint(y[k]);
     } else if constexpr (V == 1) {
-        const uint32_t u = rmsn::pack2<T>(y[0], 0.f);
-        static_cast<uint16_t*>(p)[e] = (uint16_t)u;
-        y[0] = rmsn::lo2<T>(u);
+        v.u[0] = rmsn::pack2<T>(y[0], 0.f);
     } else {
-        uint32_t u[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            u[k] = rmsn::pack2<T>(y[2 * k], y[2 * k + 1]);
-            y[2 * k] = rmsn::lo2<T>(u[k]);
-            y[2 * k + 1] = rmsn::hi2<T>(u[k]);
-        }
-        rmsn::st_stream16(static_cast<uint16_t*>(p) + e, u);
+        for (int k = 0; k < V / 2; ++k) v.u[k] = rmsn::pack2<T>(y[2 * k], y[2 * k + 1]);
+    }
+    return v;
+}
+template <class T, int V>
+__device__ __forceinline__ void store(void* p, int64_t e, const Raw<T, V>& v) {
+    if constexpr (V == 1) {
+        if constexpr (T::kBytes == 4) static_cast<uint32_t*>(p)[e] = v.u[0];
+        else static_cast<uint16_t*>(p)[e] = (uint16_t)v.u[0];
+    } else if constexpr (T::kBytes == 4) {
+        rmsn::st_stream32(static_cast<float*>(p) + e, v.u);
+    } else {
+        rmsn::st_stream16(static_cast<uint16_t*>(p) + e, v.u);
     }
 }
 
@@ -95,72 +112,104 @@ __device__ __forceinline__ bool gate_row(const NormsArgs& a, int64_t t, int64_t*
     return i >= 0;
 }
 
-// y of a vector: from h and the weights.
+// y = (w + off) (h inv), in that order of roundings; w of ones (no weight) with off 0.
 template <class T, int V>
-__device__ __forceinline__ void norm(const void* w, int64_t j, float off, float inv, const float (&h)[V],
-                                     float (&y)[V]) {
+__device__ __forceinline__ void norm(const Raw<T, V>& w, float off, float inv, const float (&h)[V], float (&y)[V]) {
     float wv[V];
-    if (w) load<T, V, false>(w, j, wv);
+    widen<T, V>(w, wv);
+    if constexpr (V == 1) {
+        y[0] = __fmul_rn(__fmul_rn(h[0], inv), __fadd_rn(wv[0], off));
+    } else {  // two lanes an instruction, each rounded as above
+        const rmsn::F2 inv2 = rmsn::f2(inv, inv), off2 = rmsn::f2(off, off);
 #pragma unroll
-    for (int k = 0; k < V; ++k) y[k] = __fmul_rn(__fmul_rn(h[k], inv), w ? __fadd_rn(wv[k], off) : 1.f);
+        for (int k = 0; k < V; k += 2)
+            rmsn::f2split(rmsn::mul2(rmsn::mul2(rmsn::f2(h[k], h[k + 1]), inv2),
+                                     rmsn::add2(rmsn::f2(wv[k], wv[k + 1]), off2)),
+                          y[k], y[k + 1]);
+    }
+}
+template <class T, int V>
+__device__ __forceinline__ Raw<T, V> ones() {
+    Raw<T, V> v;
+#pragma unroll
+    for (uint32_t& u : v.u) u = rmsn::ones_word<T>();
+    return v;
 }
 
-// A row held in registers: CH vectors of V elements a thread.
+// A row held in registers: CH vectors of V elements a thread.  The row's loads are
+// issued at an address that is right for each (past the row's end: the row's begin),
+// not behind a branch, where they would be waited for.  The weights and gates, from L1
+// and L2, are loaded where they are used: 64 registers, 1024 threads an SM.
 template <class T, class R, int V, int CH, bool FP8>
-__global__ void __launch_bounds__(CH * V >= 32 ? 512 : 1024) norms_kernel(const NormsArgs a) {
+__global__ void __launch_bounds__(512, 2) norms_kernel(const NormsArgs a) {
     __shared__ float slot[3][32];
     rmsn::pdl_wait(a.pdl);
     rmsn::pdl_launch_dependents(a.pdl);
     const int64_t t = blockIdx.x, base = t * a.H;
-    const int step = blockDim.x * V;
     int64_t g0;
     if (!gate_row(a, t, &g0)) return;
-    float x[CH][V], r[CH][V];
+    Raw<T, V> x[CH];
+    Raw<R, V> r[CH];
+    int j[CH];
+    bool on[CH];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        j[c] = (threadIdx.x + c * blockDim.x) * V;
+        on[c] = j[c] < a.H;
+        if (!on[c]) j[c] = 0;
+        x[c] = load<T, V, true>(a.x, base + j[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) r[c] = load<R, V, true>(a.residual, base + j[c]);
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int j = threadIdx.x * V + c * step;
-        if (j < a.H) load<T, V, true>(a.x, base + j, x[c]);
-    }
+        float v[V];
+        widen<T, V>(x[c], v);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int j = threadIdx.x * V + c * step;
-        if (j < a.H) load<R, V, true>(a.residual, base + j, r[c]);
-    }
-#pragma unroll
-    for (int c = 0; c < CH; ++c)
-        if (threadIdx.x * V + c * step < a.H) {
-#pragma unroll
-            for (int k = 0; k < V; ++k) sum = __fmaf_rn(x[c][k], x[c][k], sum);
+        for (int k = 0; k < V; ++k) {
+            v[k] = on[c] ? v[k] : 0.f;
+            sum = __fmaf_rn(v[k], v[k], sum);
         }
+    }
     const float inv = rmsn::inv_rms(rmsn::block_allreduce<false>(sum, slot[0]), a.H, a.eps);
+    const float post_off = a.post_w ? a.w_off : 0.f, off = a.w ? a.w_off : 0.f;
     sum = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int j = threadIdx.x * V + c * step;
-        if (j >= a.H) continue;
-        float p[V], g[V];
-        norm<T, V>(a.post_w, j, a.w_off, inv, x[c], p);
-        if (a.gate) load<T, V, false>(a.gate, g0 + j, g);
+        float v[V], p[V], h[V];
+        widen<T, V>(x[c], v);
+        norm<T, V>(a.post_w ? load<T, V, false>(a.post_w, j[c]) : ones<T, V>(), post_off, inv, v, p);
+        if (a.gate) {
+            float g[V];
+            widen<T, V>(load<T, V, false>(a.gate, g0 + j[c]), g);
 #pragma unroll
-        for (int k = 0; k < V; ++k)
-            x[c][k] = __fmaf_rn(a.alpha, r[c][k], a.gate ? __fmul_rn(g[k], p[k]) : p[k]);
-        store_rounded<R, V>(a.residual_out, base + j, x[c]);
+            for (int k = 0; k < V; ++k) p[k] = __fmul_rn(g[k], p[k]);
+        }
+        widen<R, V>(r[c], h);
 #pragma unroll
-        for (int k = 0; k < V; ++k) sum = __fmaf_rn(x[c][k], x[c][k], sum);
+        for (int k = 0; k < V; ++k) h[k] = __fmaf_rn(a.alpha, h[k], p[k]);
+        r[c] = round_to<R, V>(h);
+        if (on[c]) store<R, V>(a.residual_out, base + j[c], r[c]);
+        widen<R, V>(r[c], h);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            h[k] = on[c] ? h[k] : 0.f;
+            sum = __fmaf_rn(h[k], h[k], sum);
+        }
     }
     const float inv2 = rmsn::inv_rms(rmsn::block_allreduce<false>(sum, slot[1]), a.H, a.eps);
     float top = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        const int j = threadIdx.x * V + c * step;
-        if (j >= a.H) continue;
-        norm<T, V>(a.w, j, a.w_off, inv2, x[c], x[c]);
+        float h[V], y[V];
+        widen<R, V>(r[c], h);
+        norm<T, V>(a.w ? load<T, V, false>(a.w, j[c]) : ones<T, V>(), off, inv2, h, y);
         if constexpr (FP8) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) top = fmaxf(top, fabsf(x[c][k]));
+            for (int k = 0; k < V; ++k) top = fmaxf(top, on[c] ? fabsf(y[k]) : 0.f);
         } else {
-            store_rounded<T, V>(a.out, base + j, x[c]);
+            if (on[c]) store<T, V>(a.out, base + j[c], round_to<T, V>(y));
         }
     }
     if constexpr (FP8) {
@@ -169,8 +218,10 @@ __global__ void __launch_bounds__(CH * V >= 32 ? 512 : 1024) norms_kernel(const 
         if (threadIdx.x == 0) a.out_scale[t] = __fdiv_rn(top, 448.f);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            const int j = threadIdx.x * V + c * step;
-            if (j < a.H) store_codes<V>(a.out, base + j, x[c], f);
+            float h[V], y[V];
+            widen<R, V>(r[c], h);
+            norm<T, V>(a.w ? load<T, V, false>(a.w, j[c]) : ones<T, V>(), off, inv2, h, y);
+            if (on[c]) store_codes<V>(a.out, base + j[c], y, f);
         }
     }
 }
@@ -185,49 +236,48 @@ __global__ void __launch_bounds__(1024) norms_long_kernel(const NormsArgs a) {
     const int64_t t = blockIdx.x, base = t * a.H;
     int64_t g0;
     if (!gate_row(a, t, &g0)) return;
-    float sum = 0.f, h[1], y[1], g[1];
+    auto weight = [](const void* w, int64_t e, float off) { return w ? __fadd_rn(load1<T>(w, e), off) : 1.f; };
+    float sum = 0.f;
     for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
-        load<T, 1, true>(a.x, base + j, h);
-        sum = __fmaf_rn(h[0], h[0], sum);
+        const float x = load1<T>(a.x, base + j);
+        sum = __fmaf_rn(x, x, sum);
     }
     const float inv = rmsn::inv_rms(rmsn::block_allreduce<false>(sum, slot[0]), a.H, a.eps);
     sum = 0.f;
     for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
-        load<T, 1, true>(a.x, base + j, h);
-        norm<T, 1>(a.post_w, j, a.w_off, inv, h, y);
-        load<R, 1, true>(a.residual, base + j, h);
-        if (a.gate) {
-            load<T, 1, false>(a.gate, g0 + j, g);
-            y[0] = __fmul_rn(g[0], y[0]);
-        }
-        h[0] = __fmaf_rn(a.alpha, h[0], y[0]);
-        store_rounded<R, 1>(a.residual_out, base + j, h);
+        float p = __fmul_rn(__fmul_rn(load1<T>(a.x, base + j), inv), weight(a.post_w, j, a.w_off));
+        if (a.gate) p = __fmul_rn(load1<T>(a.gate, g0 + j), p);
+        float h[1] = {__fmaf_rn(a.alpha, load1<R>(a.residual, base + j), p)};
+        const Raw<R, 1> kept = round_to<R, 1>(h);
+        store<R, 1>(a.residual_out, base + j, kept);
+        widen<R, 1>(kept, h);
         sum = __fmaf_rn(h[0], h[0], sum);
     }
     const float inv2 = rmsn::inv_rms(rmsn::block_allreduce<false>(sum, slot[1]), a.H, a.eps);
+    auto out = [&](int j) {
+        return __fmul_rn(__fmul_rn(load1<R>(a.residual_out, base + j), inv2), weight(a.w, j, a.w_off));
+    };
     float f = 1.f;
     if constexpr (FP8) {
         float top = 0.f;
-        for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
-            h[0] = load1<R>(a.residual_out, base + j);
-            norm<T, 1>(a.w, j, a.w_off, inv2, h, y);
-            top = fmaxf(top, fabsf(y[0]));
-        }
+        for (int j = threadIdx.x; j < a.H; j += blockDim.x) top = fmaxf(top, fabsf(out(j)));
         top = rmsn::block_allreduce<true>(top, slot[2]);
         f = top > 0.f ? __fdiv_rn(448.f, top) : 0.f;
         if (threadIdx.x == 0) a.out_scale[t] = __fdiv_rn(top, 448.f);
     }
     for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
-        h[0] = load1<R>(a.residual_out, base + j);
-        norm<T, 1>(a.w, j, a.w_off, inv2, h, y);
+        const float y[1] = {out(j)};
         if constexpr (FP8) store_codes<1>(a.out, base + j, y, f);
-        else store_rounded<T, 1>(a.out, base + j, y);
+        else store<T, 1>(a.out, base + j, round_to<T, 1>(y));
     }
 }
 
 template <class T, class R, bool FP8>
 const void* kernel(int v, int ch) {
-    if (v == 1) return ch == 0 ? (const void*)&norms_long_kernel<T, R, FP8> : (const void*)&norms_kernel<T, R, 1, 8, FP8>;
+    if (v == 1)
+        return ch == 0 ? (const void*)&norms_long_kernel<T, R, FP8>
+                       : (ch == 4 ? (const void*)&norms_kernel<T, R, 1, 4, FP8>
+                                  : (const void*)&norms_kernel<T, R, 1, 16, FP8>);
     return ch == 1 ? (const void*)&norms_kernel<T, R, 8, 1, FP8>
                    : (ch == 2 ? (const void*)&norms_kernel<T, R, 8, 2, FP8>
                               : (const void*)&norms_kernel<T, R, 8, 4, FP8>);

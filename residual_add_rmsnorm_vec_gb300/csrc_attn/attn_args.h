@@ -93,8 +93,8 @@ struct NormsArgs {
     float eps, alpha, w_off;
     uint32_t* status;
 };
-// v elements to a vector, ch vectors to a thread (v = 1, ch = 0: any row)
-const void* norms_kernel_of(int dt, bool r32, bool fp8, int v, int ch);
+// ch vectors of eight elements to a thread; 0: any row
+const void* norms_kernel_of(int dt, bool r32, bool fp8, bool ragged, int ch);
 
 // A group of sequences [s0, s1) that share their first `shared` tokens: `tiles`
 // tiles of `rows` columns (sequence x query token x head) for each key head,

@@ -83,6 +83,36 @@ __device__ __forceinline__ void store(void* p, int64_t e, const Raw<T, V>& v) {
     }
 }
 
+// The same at the ends of a row off the vectors' grid: of elements j to j + 7 those
+// within [0, H).
+template <class T, bool STREAM>
+__device__ __forceinline__ Raw<T, 8> load_row(const void* p, int64_t e, int j, int H, bool whole) {
+    if (whole) return load<T, 8, STREAM>(p, e);
+    Raw<T, 8> v;
+#pragma unroll
+    for (uint32_t& u : v.u) u = 0u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (j + k < 0 || j + k >= H) continue;
+        if constexpr (T::kBytes == 4) v.u[k] = static_cast<const uint32_t*>(p)[e + k];
+        else v.u[k / 2] |= (uint32_t) static_cast<const uint16_t*>(p)[e + k] << (k & 1) * 16;
+    }
+    return v;
+}
+template <class T>
+__device__ __forceinline__ void store_row(void* p, int64_t e, int j, int H, bool whole, const Raw<T, 8>& v) {
+    if (whole) {
+        store<T, 8>(p, e, v);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (j + k < 0 || j + k >= H) continue;
+        if constexpr (T::kBytes == 4) static_cast<uint32_t*>(p)[e + k] = v.u[k];
+        else static_cast<uint16_t*>(p)[e + k] = (uint16_t)(v.u[k / 2] >> (k & 1) * 16);
+    }
+}
+
 template <int V>
 __device__ __forceinline__ void store_codes(void* p, int64_t e, const float (&y)[V], float f) {
     uint8_t* q = static_cast<uint8_t*>(p) + e;
@@ -136,31 +166,49 @@ __device__ __forceinline__ Raw<T, V> ones() {
     return v;
 }
 
-// A row held in registers: CH vectors of V elements a thread.  The row's loads are
+// A row held in registers: CH vectors of eight elements a thread.  The row's loads are
 // issued at an address that is right for each (past the row's end: the row's begin),
 // not behind a branch, where they would be waited for.  The weights and gates, from L1
 // and L2, are loaded where they are used: 64 registers, 1024 threads an SM.
-template <class T, class R, int V, int CH, bool FP8>
+//
+// RAGGED: rows off the vectors' grid.  All of a token's rows begin at the same element
+// t H of their tensors, so that the vectors at multiples of eight of those lie on 16
+// bytes in each of them; the first and the last of a row go by elements, and so do the
+// weights, which are counted from the row's begin.
+template <class T, class R, int CH, bool FP8, bool RAGGED>
 __global__ void __launch_bounds__(512, 2) norms_kernel(const NormsArgs a) {
+    constexpr int V = 8;
     __shared__ float slot[3][32];
     rmsn::pdl_wait(a.pdl);
     rmsn::pdl_launch_dependents(a.pdl);
     const int64_t t = blockIdx.x, base = t * a.H;
     int64_t g0;
     if (!gate_row(a, t, &g0)) return;
+    const int shift = RAGGED ? (int)(base & 7) : 0;
     Raw<T, V> x[CH];
     Raw<R, V> r[CH];
     int j[CH];
-    bool on[CH];
+    bool on[CH], whole[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
-        j[c] = (threadIdx.x + c * blockDim.x) * V;
+        j[c] = (threadIdx.x + c * blockDim.x) * V - shift;
         on[c] = j[c] < a.H;
-        if (!on[c]) j[c] = 0;
-        x[c] = load<T, V, true>(a.x, base + j[c]);
+        whole[c] = !RAGGED || (j[c] >= 0 && j[c] + V <= a.H);
+        if (!on[c]) {
+            j[c] = 0;
+            whole[c] = !RAGGED;
+        }
+        x[c] = load_row<T, true>(a.x, base + j[c], j[c], on[c] ? a.H : 0, whole[c]);
     }
 #pragma unroll
-    for (int c = 0; c < CH; ++c) r[c] = load<R, V, true>(a.residual, base + j[c]);
+    for (int c = 0; c < CH; ++c) r[c] = load_row<R, true>(a.residual, base + j[c], j[c], on[c] ? a.H : 0, whole[c]);
+    auto weight = [&](const void* w, int c) {
+        if (!w) return ones<T, V>();
+        return load_row<T, false>(w, j[c], j[c], on[c] ? a.H : 0, !RAGGED);
+    };
+    // a gate's row for each token lies as the token's other rows do
+    const bool straight = !RAGGED || (((g0 - base) & 7) == 0 && (reinterpret_cast<uintptr_t>(a.gate) & (8 * T::kBytes - 1)) == 0);
+    auto inside = [&](int c, int k) { return on[c] && (!RAGGED || (j[c] + k >= 0 && j[c] + k < a.H)); };
     float sum = 0.f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -168,7 +216,7 @@ __global__ void __launch_bounds__(512, 2) norms_kernel(const NormsArgs a) {
         widen<T, V>(x[c], v);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            v[k] = on[c] ? v[k] : 0.f;
+            if (!RAGGED) v[k] = on[c] ? v[k] : 0.f;  // (ragged: zeros already)
             sum = __fmaf_rn(v[k], v[k], sum);
         }
     }
@@ -179,10 +227,10 @@ __global__ void __launch_bounds__(512, 2) norms_kernel(const NormsArgs a) {
     for (int c = 0; c < CH; ++c) {
         float v[V], p[V], h[V];
         widen<T, V>(x[c], v);
-        norm<T, V>(a.post_w ? load<T, V, false>(a.post_w, j[c]) : ones<T, V>(), post_off, inv, v, p);
+        norm<T, V>(weight(a.post_w, c), post_off, inv, v, p);
         if (a.gate) {
             float g[V];
-            widen<T, V>(load<T, V, false>(a.gate, g0 + j[c]), g);
+            widen<T, V>(load_row<T, false>(a.gate, g0 + j[c], j[c], on[c] ? a.H : 0, whole[c] && straight), g);
 #pragma unroll
             for (int k = 0; k < V; ++k) p[k] = __fmul_rn(g[k], p[k]);
         }
@@ -190,11 +238,11 @@ __global__ void __launch_bounds__(512, 2) norms_kernel(const NormsArgs a) {
 #pragma unroll
         for (int k = 0; k < V; ++k) h[k] = __fmaf_rn(a.alpha, h[k], p[k]);
         r[c] = round_to<R, V>(h);
-        if (on[c]) store<R, V>(a.residual_out, base + j[c], r[c]);
+        if (on[c]) store_row<R>(a.residual_out, base + j[c], j[c], a.H, whole[c], r[c]);
         widen<R, V>(r[c], h);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            h[k] = on[c] ? h[k] : 0.f;
+            h[k] = inside(c, k) ? h[k] : 0.f;
             sum = __fmaf_rn(h[k], h[k], sum);
         }
     }
@@ -204,12 +252,12 @@ __global__ void __launch_bounds__(512, 2) norms_kernel(const NormsArgs a) {
     for (int c = 0; c < CH; ++c) {
         float h[V], y[V];
         widen<R, V>(r[c], h);
-        norm<T, V>(a.w ? load<T, V, false>(a.w, j[c]) : ones<T, V>(), off, inv2, h, y);
+        norm<T, V>(weight(a.w, c), off, inv2, h, y);
         if constexpr (FP8) {
 #pragma unroll
-            for (int k = 0; k < V; ++k) top = fmaxf(top, on[c] ? fabsf(y[k]) : 0.f);
+            for (int k = 0; k < V; ++k) top = fmaxf(top, inside(c, k) ? fabsf(y[k]) : 0.f);
         } else {
-            if (on[c]) store<T, V>(a.out, base + j[c], round_to<T, V>(y));
+            if (on[c]) store_row<T>(a.out, base + j[c], j[c], a.H, whole[c], round_to<T, V>(y));
         }
     }
     if constexpr (FP8) {
@@ -220,8 +268,17 @@ __global__ void __launch_bounds__(512, 2) norms_kernel(const NormsArgs a) {
         for (int c = 0; c < CH; ++c) {
             float h[V], y[V];
             widen<R, V>(r[c], h);
-            norm<T, V>(a.w ? load<T, V, false>(a.w, j[c]) : ones<T, V>(), off, inv2, h, y);
-            if (on[c]) store_codes<V>(a.out, base + j[c], y, f);
+            norm<T, V>(weight(a.w, c), off, inv2, h, y);
+            if (!on[c]) continue;
+            if (whole[c]) {
+                store_codes<V>(a.out, base + j[c], y, f);
+            } else {
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const float one[1] = {y[k]};
+                    if (inside(c, k)) store_codes<1>(a.out, base + j[c] + k, one, f);
+                }
+            }
         }
     }
 }
@@ -273,26 +330,27 @@ __global__ void __launch_bounds__(1024) norms_long_kernel(const NormsArgs a) {
 }
 
 template <class T, class R, bool FP8>
-const void* kernel(int v, int ch) {
-    if (v == 1)
-        return ch == 0 ? (const void*)&norms_long_kernel<T, R, FP8>
-                       : (ch == 4 ? (const void*)&norms_kernel<T, R, 1, 4, FP8>
-                                  : (const void*)&norms_kernel<T, R, 1, 16, FP8>);
-    return ch == 1 ? (const void*)&norms_kernel<T, R, 8, 1, FP8>
-                   : (ch == 2 ? (const void*)&norms_kernel<T, R, 8, 2, FP8>
-                              : (const void*)&norms_kernel<T, R, 8, 4, FP8>);
+const void* kernel(bool ragged, int ch) {
+    if (ch == 0) return (const void*)&norms_long_kernel<T, R, FP8>;
+    if (ragged)
+        return ch == 1 ? (const void*)&norms_kernel<T, R, 1, FP8, true>
+                       : (ch == 2 ? (const void*)&norms_kernel<T, R, 2, FP8, true>
+                                  : (const void*)&norms_kernel<T, R, 4, FP8, true>);
+    return ch == 1 ? (const void*)&norms_kernel<T, R, 1, FP8, false>
+                   : (ch == 2 ? (const void*)&norms_kernel<T, R, 2, FP8, false>
+                              : (const void*)&norms_kernel<T, R, 4, FP8, false>);
 }
 
 }  // namespace
 
-const void* norms_kernel_of(int dt, bool r32, bool fp8, int v, int ch) {
-    if (dt == 0) return fp8 ? kernel<F32, F32, true>(v, ch) : kernel<F32, F32, false>(v, ch);
+const void* norms_kernel_of(int dt, bool r32, bool fp8, bool ragged, int ch) {
+    if (dt == 0) return fp8 ? kernel<F32, F32, true>(ragged, ch) : kernel<F32, F32, false>(ragged, ch);
     if (dt == 1) {
-        if (r32) return fp8 ? kernel<BF16, F32, true>(v, ch) : kernel<BF16, F32, false>(v, ch);
-        return fp8 ? kernel<BF16, BF16, true>(v, ch) : kernel<BF16, BF16, false>(v, ch);
+        if (r32) return fp8 ? kernel<BF16, F32, true>(ragged, ch) : kernel<BF16, F32, false>(ragged, ch);
+        return fp8 ? kernel<BF16, BF16, true>(ragged, ch) : kernel<BF16, BF16, false>(ragged, ch);
     }
-    if (r32) return fp8 ? kernel<F16, F32, true>(v, ch) : kernel<F16, F32, false>(v, ch);
-    return fp8 ? kernel<F16, F16, true>(v, ch) : kernel<F16, F16, false>(v, ch);
+    if (r32) return fp8 ? kernel<F16, F32, true>(ragged, ch) : kernel<F16, F32, false>(ragged, ch);
+    return fp8 ? kernel<F16, F16, true>(ragged, ch) : kernel<F16, F16, false>(ragged, ch);
 }
 
 }  // namespace rmsattn

@@ -137,24 +137,26 @@ RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const v
     a.alpha = residual_scale;
     a.w_off = weight_offset;
     a.status = d->status;
-    // vectors of eight elements where every row of every operand starts on one
-    bool vec = hidden % 8 == 0 && gate_stride % 8 == 0 && aligned(out, fp8 ? 8 : (uintptr_t)(8 * bytes)) &&
+    // Vectors of eight elements where the tensors of rows begin on one; where every row,
+    // and the weights' and gates', does too, no row has ends of its own.
+    bool vec = aligned(out, fp8 ? 8 : (uintptr_t)(8 * bytes)) && aligned(x, (uintptr_t)(8 * bytes)) &&
                aligned(residual, (uintptr_t)(8 * rbytes)) && aligned(residual_out, (uintptr_t)(8 * rbytes));
-    for (const void* p : same) vec = vec && aligned(p, (uintptr_t)(8 * bytes));
+    bool ragged = hidden % 8 != 0 || gate_stride % 8 != 0;
+    for (const void* p : same) ragged = ragged || !aligned(p, (uintptr_t)(8 * bytes));
     // Vectors of a thread: four put the most rows on an SM (16384 x 8192 bf16 162 us; two
     // 189 to 211); as few as hold the row where there are not rows enough for that, for
-    // the shorter chain (8 x 4096: see the kernel).  Rows off the grid by single elements.
+    // the shorter chain (8 x 4096: see the kernel).
     const bool few = n_tokens < 4 * (int64_t)d->num_sms;
-    const int v = vec ? 8 : 1;
-    int ch = vec ? 4 : (hidden <= 2048 ? 4 : 16);
-    if (vec && few) ch = hidden <= 4096 ? 1 : (hidden <= 8192 ? 2 : 4);
-    int64_t lanes = (hidden + v * ch - 1) / (v * ch);
-    if (lanes > 512) {
+    const int64_t vectors = (hidden + (ragged ? 14 : 7)) / 8;
+    int ch = 4;
+    if (few) ch = vectors <= 512 ? 1 : (vectors <= 1024 ? 2 : 4);
+    int64_t lanes = (vectors + ch - 1) / ch;
+    if (!vec || lanes > 512) {
         ch = 0;
-        lanes = 1024;
+        lanes = hidden < 1024 ? hidden : 1024;
     }
     const int threads = (int)((lanes + 31) / 32 * 32);
-    return launch(norms_kernel_of(dt, r32, fp8, ch ? v : 1, ch), dim3((unsigned)n_tokens), threads, 0, &a, a.pdl, stream);
+    return launch(norms_kernel_of(dt, r32, fp8, ragged, ch), dim3((unsigned)n_tokens), threads, 0, &a, a.pdl, stream);
 }
 
 // ---------------------------------------------------------------- shared prefix

@@ -2,6 +2,7 @@
 // kernels' units and the C-ABI layer.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace rmsattn {
@@ -145,6 +146,21 @@ struct PrefixEntry {
     const void* fn;
 };
 const void* prefix_plan_kernel();
+
+// The join of a sequence's own part with its group's.
+struct PrefixJoinArgs {
+    void* out;
+    int64_t out_stride, rows;  // rows: B n Hq
+    int32_t n, Hq, group, D;
+    int32_t item_rows;
+    const PrefixLine* line;
+    const PrefixGroup* groups;
+    const PrefixSeq* seqs;
+    const float* parts;
+    const float* own;
+    const float2* own_ml;
+};
+const void* prefix_join_kernel(int dt);
 const PrefixEntry* prefix_kernels_64(int* n);
 const PrefixEntry* prefix_kernels_128(int* n);
 const PrefixEntry* prefix_kernels_256(int* n);
@@ -173,12 +189,11 @@ struct AttendArgs {
     int64_t shares;     // of the line, one for each block
     int64_t min_chunk;  // steps of a share, at least
     char* ws;           // a Cut and two parts for every share
-    // behind a shared prefix: its parts
-    const PrefixLine* line;
-    const PrefixGroup* prefix;
+    // behind a shared prefix: where each sequence begins, and its own tokens' results
+    // [B, n, Hq, D] with each row's reference and weight
     const PrefixSeq* seqs;
-    const float* parts;
-    int32_t prefix_rows;  // columns of an item
+    float* own;
+    float2* own_ml;
 };
 
 constexpr int64_t kCutBytes = 32;

@@ -363,58 +363,19 @@ __device__ __forceinline__ void read8(float4 (&v)[2], const float* row, int d) {
     v[0] = *reinterpret_cast<const float4*>(row + unit_at(d));
     v[1] = *reinterpret_cast<const float4*>(row + unit_at(d + 4));
 }
-// Adds the shared prefix's parts to a column's: y its sums of dims d to d + 7
-// and l its weights' sum, both taken with reference mx.  The parts lie in the
-// order of the line's shares.
-__device__ __forceinline__ void add_prefix(const AttendArgs& a, int64_t b, int hk, const Col& c, int d,
-                                           float (&y)[8], float& l, float mx) {
-    const PrefixSeq sq = a.seqs[b];
-    if (sq.start == 0) return;
-    const PrefixGroup g = a.prefix[sq.group];
-    const uint32_t chunk = a.line->chunk;
-    const int cc = (((int)b - g.s0) * a.n + c.qi) * a.group + c.head - hk * a.group;
-    const int rows = a.prefix_rows, tile = cc / rows, row = cc - tile * rows, item = hk * g.tiles + tile;
-    const uint32_t at = (uint32_t)g.first + (uint32_t)item * (uint32_t)g.ns;
-    const int i0 = (int)(at / chunk), n = (int)((at + (uint32_t)g.ns - 1) / chunk) - i0 + 1;
-    const int64_t size = prefix_part(a.c.D, rows);
-    const float* p = a.parts + (i0 + g.item0 + item) * size;
-    const int at_y = d * rows + row * 8, at_ml = a.c.D * rows + row * 2;
-    constexpr int U = 4;
-    for (int k0 = 0; k0 < n; k0 += U) {
-        float2 ml[U];
-        float4 v[U][2];
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            ml[k] = make_float2(kNone, 0.f);
-            v[k][0] = v[k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k0 + k >= n) continue;
-            const float* q = p + (k0 + k) * size;
-            ml[k] = *reinterpret_cast<const float2*>(q + at_ml);
-            v[k][0] = *reinterpret_cast<const float4*>(q + at_y);
-            v[k][1] = *reinterpret_cast<const float4*>(q + at_y + 4);
-        }
-        float to = mx;
-#pragma unroll
-        for (int k = 0; k < U; ++k) to = fmaxf(to, ml[k].x);
-        const float keep = exp2a(mx - to);
-        mx = to;
-        l *= keep;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] *= keep;
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const float f = exp2a(ml[k].x - mx);
-            l += ml[k].y * f;
-            add8(y, v[k], f);
-        }
-    }
-}
-
-// Eight dims of a row's sums over its weights' sum; nothing seen gives 0.
+// Eight dims of a row's sums over its weights' sum; nothing seen gives 0.  PRE: the
+// sums as they are, with reference mx, for the join with the shared prefix's.
 template <class T, bool PRE>
-__device__ __forceinline__ void finish8(const AttendArgs& a, int64_t b, int hk, const Col& c, int d,
-                                        float (&y)[8], float l, float mx) {
-    if constexpr (PRE) add_prefix(a, b, hk, c, d, y, l, mx);
+__device__ __forceinline__ void finish8(const AttendArgs& a, int64_t b, const Col& c, int d, float (&y)[8],
+                                        float l, float mx) {
+    if constexpr (PRE) {
+        const int64_t row = (b * a.n + c.qi) * a.Hq + c.head;
+        float4* o = reinterpret_cast<float4*>(a.own + row * a.c.D + d);
+        o[0] = make_float4(y[0], y[1], y[2], y[3]);
+        o[1] = make_float4(y[4], y[5], y[6], y[7]);
+        if (d == 0) a.own_ml[row] = make_float2(mx, l);
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] = l == 0.f ? 0.f : y[k] / l;
     store8<T>(a, b, c, d, y);
@@ -1179,7 +1140,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                     add8(y, v, f);
                 }
                 if (whole) {
-                    finish8<T, PRE>(a, row_b, hk, col, d, y, lsum, mx);
+                    finish8<T, PRE>(a, row_b, col, d, y, lsum, mx);
                 } else if (a.split > 0) {
                     // to the block that finishes these dims, each sender its place
                     const int rank = (int)blockIdx.x & (a.split - 1);
@@ -1226,7 +1187,7 @@ __global__ void __launch_bounds__(C::W * 32, C::M) attend_kernel(const AttendArg
                     lsum += ml[r].y * f;
                     add8(y, from + 2 * r, f);
                 }
-                finish8<T, PRE>(a, row_b, hk, col, d, y, lsum, mx);
+                finish8<T, PRE>(a, row_b, col, d, y, lsum, mx);
             }
         }
         cur = seg_end;
@@ -1315,7 +1276,7 @@ __global__ void __launch_bounds__(512) attend_join_kernel(const AttendArgs a) {
         ls += total[k][oc] * f;
         add8(r, &sum[k][oc * (D / 4) + 2 * od], f);
     }
-    finish8<T, PRE>(a, cut.b, hk, col, od * 8, r, ls, mx);
+    finish8<T, PRE>(a, cut.b, col, od * 8, r, ls, mx);
 }
 
 template <class C, bool PRE = false>

@@ -1,5 +1,6 @@
 // Attention with a shared prefix: which sequences share how much, and the line of
-// the shared parts' steps (PrefixGroup).  One block; a warp to a group.
+// the shared parts' steps (PrefixGroup).  One block; a warp to a group.  A sequence
+// shares a prefix if each of its queries sees all of it.
 #include "attn_common.cuh"
 
 namespace rmsattn {
@@ -8,18 +9,12 @@ namespace {
 
 constexpr int kThreads = 512;
 
-// A sequence shares a prefix if each of its queries sees all of it.
-__device__ __forceinline__ bool shares(const PrefixArgs& a, int64_t b, int shared) {
-    return a.lengths[b] - a.n + 1 >= shared;
-}
-
 __global__ void __launch_bounds__(kThreads) prefix_plan(const PrefixArgs a) {
     __shared__ int64_t sums[2][kThreads / 32];
     rmsn::pdl_wait(a.pdl);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
     const PrefixSeq alone = {0, 0};
-    for (int64_t b = threadIdx.x; b < a.B; b += kThreads) a.seqs[b] = alone;
     // borders that are out of order, or of other sequences: nobody shares
     bool bad = false;
     if (a.cu) {
@@ -28,6 +23,11 @@ __global__ void __launch_bounds__(kThreads) prefix_plan(const PrefixArgs a) {
     }
     bad = __syncthreads_or(bad);
     if (bad && threadIdx.x == 0) atomicOr(a.status, kBadPage);
+    // sequences of no group (the groups lie one behind the other)
+    const bool none = bad || a.n_groups == 0;
+    const int64_t from = none ? a.B : (a.cu ? a.cu[0] : 0), to = none ? a.B : (a.cu ? a.cu[a.n_groups] : a.B);
+    for (int64_t b = threadIdx.x; b < a.B; b += kThreads)
+        if (b < from || b >= to) a.seqs[b] = alone;
     const int64_t room = a.table_width * a.c.page;
     for (int g = wp; g < a.n_groups; g += kThreads / 32) {
         PrefixGroup G = {0, 0, 0, -1, 0, 0, 0, 0};
@@ -39,21 +39,34 @@ __global__ void __launch_bounds__(kThreads) prefix_plan(const PrefixArgs a) {
             if (shared > room) shared = (int32_t)room;
             shared = shared < 0 ? 0 : shared & ~(kBlock - 1);
             int count = 0;
-            if (shared > 0)
-                for (int b0 = G.s0; b0 < G.s1; b0 += 32) {
-                    const bool on = b0 + lane < G.s1 && shares(a, b0 + lane, shared);
-                    const uint32_t who = __ballot_sync(0xFFFFFFFFu, on);
-                    if (G.seq < 0 && who) G.seq = b0 + __ffs(who) - 1;
-                    count += __popc(who);
+            constexpr int U = 8;  // lengths of a lane on their way at once
+            for (int b0 = G.s0; b0 < G.s1; b0 += 32 * U) {
+                uint32_t on = 0;
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const int b = b0 + 32 * k + lane;
+                    const bool in = b < G.s1;
+                    const int32_t len = a.lengths[in ? b : G.s0];
+                    on |= (uint32_t)(in && shared > 0 && len - (int64_t)a.n + 1 >= shared) << k;
                 }
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    const uint32_t who = __ballot_sync(0xFFFFFFFFu, on >> k & 1);
+                    if (G.seq < 0 && who) G.seq = b0 + 32 * k + __ffs(who) - 1;
+                    count += __popc(who);
+                    const int b = b0 + 32 * k + lane;
+                    if (b < G.s1) a.seqs[b] = on >> k & 1 ? PrefixSeq{shared, g} : alone;
+                }
+            }
             if (count > 1) {
                 G.shared = shared;
                 G.ns = (shared + a.tok - 1) / a.tok;
                 G.tiles = (int)(((int64_t)(G.s1 - G.s0) * a.n * a.group + a.rows - 1) / a.rows);
-                for (int b = G.s0 + lane; b < G.s1; b += 32)
-                    if (shares(a, b, shared)) a.seqs[b] = PrefixSeq{shared, g};
+            } else if (count == 1 && lane == 0) {
+                a.seqs[G.seq] = alone;  // (behind the warp's own stores: the same word)
             }
         }
+        __syncwarp();
         if (lane == 0) a.groups[g] = G;
     }
     __syncthreads();

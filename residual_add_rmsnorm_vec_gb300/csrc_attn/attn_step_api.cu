@@ -179,7 +179,7 @@ const PrefixEntry* prefix_entry_of(int dt, int64_t D, int64_t cols, int64_t n_gr
 // Where a call's workspace holds what.
 struct PrefixPlan {
     const PrefixEntry* e;
-    int64_t shares, groups, seqs, parts, own, total;  // offsets in bytes
+    int64_t shares, groups, seqs, parts, own, own_ml, behind_ws, total;  // offsets in bytes
     Plan behind;
 };
 
@@ -202,10 +202,14 @@ int plan_prefix(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
                                0, 0, &p->behind);
     if (st != RMSN_OK) return st;
     p->groups = round_up(sizeof(PrefixLine));
-    p->seqs = p->groups + round_up(n_groups * (int64_t)sizeof(PrefixGroup));
+    p->seqs = p->groups + round_up((n_groups + 1) * (int64_t)sizeof(PrefixGroup));
     p->parts = p->seqs + round_up(n_seqs * (int64_t)sizeof(PrefixSeq));
     p->own = p->parts + times(p->shares + items, prefix_part((int)head_dim, rows) * 4);
-    p->total = p->own + p->behind.workspace;
+    const int64_t out_rows = n_seqs * n_queries * n_q_heads;
+    p->own_ml = p->own + times(out_rows, head_dim * 4);
+    p->behind_ws = p->own_ml + round_up(out_rows * 8);
+    p->total = p->behind_ws + p->behind.workspace;
+    if (n_kv_heads * (head_dim / 8) > 65535) return RMSN_EUNSUPPORTED;  // the join's grid
     return too_big(p->total) ? RMSN_EUNSUPPORTED : RMSN_OK;
 }
 
@@ -290,7 +294,7 @@ RMSATTN_API int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* 
     a.scale = scale;
     a.status = d->status;
     a.pdl = 1;
-    a.ws = ws + p.own;
+    a.ws = ws + p.behind_ws;
     fill_attend(p.behind, n_queries, n_q_heads, &a);
 
     PrefixArgs f;
@@ -309,7 +313,7 @@ RMSATTN_API int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* 
     f.n = (int32_t)n_queries;
     f.group = a.group;
     f.tok = p.e->tok;
-    f.rows = a.prefix_rows = 128 * p.e->R;
+    f.rows = 128 * p.e->R;
     f.shares = (int32_t)p.shares;
     f.min_chunk = 1;
     f.pdl = (flags & RMSN_PDL) ? 1 : 0;
@@ -320,13 +324,32 @@ RMSATTN_API int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* 
     f.groups = reinterpret_cast<PrefixGroup*>(ws + p.groups);
     f.seqs = reinterpret_cast<PrefixSeq*>(ws + p.seqs);
     f.parts = reinterpret_cast<float*>(ws + p.parts);
-    a.line = f.line;
-    a.prefix = f.groups;
     a.seqs = f.seqs;
-    a.parts = f.parts;
+    a.own = reinterpret_cast<float*>(ws + p.own);
+    a.own_ml = reinterpret_cast<float2*>(ws + p.own_ml);
+    PrefixJoinArgs j;
+    memset(&j, 0, sizeof(j));
+    j.out = out;
+    j.out_stride = out_stride;
+    j.rows = n_seqs * n_queries * n_q_heads;
+    j.n = (int32_t)n_queries;
+    j.Hq = (int32_t)n_q_heads;
+    j.group = a.group;
+    j.D = a.c.D;
+    j.item_rows = f.rows;
+    j.line = f.line;
+    j.groups = f.groups;
+    j.seqs = f.seqs;
+    j.parts = f.parts;
+    j.own = a.own;
+    j.own_ml = a.own_ml;
     // each launch behind the one before: programmatic dependents of the call's own
     st = launch(prefix_plan_kernel(), dim3(1), 512, 0, &f, f.pdl, stream);
     if (st == RMSN_OK && n_groups)
         st = launch(p.e->fn, dim3((unsigned)p.shares), p.e->threads, (size_t)p.e->smem, &f, true, stream);
-    return st == RMSN_OK ? launch_attend(p.behind, &a, true, stream) : st;
+    if (st == RMSN_OK) st = launch_attend(p.behind, &a, true, stream);
+    if (st != RMSN_OK) return st;
+    const int64_t cols = n_seqs * n_queries * a.group;
+    return launch(prefix_join_kernel(dt), dim3((unsigned)((cols + 63) / 64), (unsigned)(a.c.H * (a.c.D / 8))), 256, 0,
+                  &j, true, stream);
 }

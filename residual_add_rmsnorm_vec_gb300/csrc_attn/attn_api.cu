@@ -391,10 +391,11 @@ void fill_attend(const Plan& p, int64_t n_queries, int64_t n_q_heads, AttendArgs
     a->min_chunk = p.min_chunk;
 }
 
-int launch_attend(const Plan& p, AttendArgs* a, bool pdl, cudaStream_t stream) {
-    const int st = launch(p.e->fn, dim3((unsigned)p.blocks), p.e->threads, (size_t)p.e->smem, a, pdl,
-                          stream, p.split > 1 ? p.split : 1);
-    if (st != RMSN_OK || p.split > 0 || p.blocks == 1) return st;
+int launch_attend(const Plan& p, AttendArgs* a, bool pdl, cudaStream_t stream, int which) {
+    const int st = which & 1 ? launch(p.e->fn, dim3((unsigned)p.blocks), p.e->threads, (size_t)p.e->smem, a,
+                                      pdl, stream, p.split > 1 ? p.split : 1)
+                             : RMSN_OK;
+    if (st != RMSN_OK || !(which & 2) || p.split > 0 || p.blocks == 1) return st;
     // always behind the stream's own kernel: a programmatic dependent of it
     const int used = a->cols < 8 * p.e->NT ? a->cols : 8 * p.e->NT;
     return launch(p.e->join, dim3((unsigned)(p.blocks - 1), (unsigned)(used + 3) / 4), p.join, 0, a, true,

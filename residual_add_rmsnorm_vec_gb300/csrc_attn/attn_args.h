@@ -160,7 +160,7 @@ struct PrefixJoinArgs {
     const float* own;
     const float2* own_ml;
 };
-const void* prefix_join_kernel(int dt);
+const void* prefix_join_kernel(int dt, int ways);  // 1 or 4
 const PrefixEntry* prefix_kernels_64(int* n);
 const PrefixEntry* prefix_kernels_128(int* n);
 const PrefixEntry* prefix_kernels_256(int* n);

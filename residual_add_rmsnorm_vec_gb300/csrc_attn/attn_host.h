@@ -84,6 +84,7 @@ int plan_attend(DeviceInfo* d, bool behind, int dt, int64_t n_seqs, int64_t n_qu
 
 // The attention's and its join's launches, once every pointer is in `a`.
 void fill_attend(const Plan& p, int64_t n_queries, int64_t n_q_heads, AttendArgs* a);
-int launch_attend(const Plan& p, AttendArgs* a, bool pdl, cudaStream_t stream);
+// (which: 1 the attention alone, 2 its join, 3 both)
+int launch_attend(const Plan& p, AttendArgs* a, bool pdl, cudaStream_t stream, int which = 3);
 
 }  // namespace rmsattn

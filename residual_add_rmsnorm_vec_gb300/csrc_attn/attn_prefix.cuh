@@ -852,7 +852,9 @@ __global__ void __launch_bounds__(C::kWarps * 32, 1) prefix_kernel(const PrefixA
     tc_after();
     // (all of TMEM is the block's, so it begins at 0, and places in it are constants)
     if (threadIdx.x == 0 && bars.tmem != 0) bars.stop = 1;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The plan's launch is over and its results are there: the launch between, whose
+    // programmatic dependent this is, has waited for it in each of its blocks before it
+    // let this one begin.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     unsigned char* stages = smem + C::R * C::kQ;
     unsigned char* codes = stages + 4 * C::kTile;
@@ -875,6 +877,8 @@ __global__ void __launch_bounds__(C::kWarps * 32, 1) prefix_kernel(const PrefixA
     if (wp == 4 * C::R + 8)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(bars.tmem), "n"(C::kCols) : "memory");
     if (threadIdx.x == 0 && bars.stop) atomicOr(a.status, kWaitRanOut);
+    // what waits for this launch has then waited for the one between, too
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <class C>

@@ -4,8 +4,9 @@
 //   out = sum_i O_i 2^(m_i - m) / sum_i l_i 2^(m_i - m),  m = max m_i
 //
 // What bounds it: the chain of loads (sequence, group, parts) and the parts' bytes from
-// L2.  A thread has eight dims of a row and every fourth part, up to eight of them on
-// their way at once; lanes run along a key head's columns, as those lie in the parts (32
+// L2.  A thread has eight dims of a row and every fourth part where there are many (else
+// all of them: 256 sequences with 6 parts 10 against 16 us), up to eight of them on their
+// way at once; lanes run along a key head's columns, as those lie in the parts (32
 // bytes each).  With the dims along the lanes and one thread to all parts, 64 sequences
 // of 32 / 8 heads x 128 with 19 parts took 17 us.
 #include "attn_common.cuh"
@@ -29,10 +30,10 @@ __device__ __forceinline__ void add(float4& y, const float4& v, float f) {
     y.w += v.w * f;
 }
 
-constexpr int kCols = 64, kWays = 4;
-
-template <class T>
-__global__ void __launch_bounds__(kCols* kWays) prefix_join(const PrefixJoinArgs a) {
+// kWays threads to a row's parts.
+template <class T, int kWays>
+__global__ void __launch_bounds__(256) prefix_join(const PrefixJoinArgs a) {
+    constexpr int kCols = 256 / kWays;
     __shared__ float4 sum[kWays][2][kCols];
     __shared__ float2 ref[kWays][kCols];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -128,8 +129,9 @@ __global__ void __launch_bounds__(kCols* kWays) prefix_join(const PrefixJoinArgs
 
 }  // namespace
 
-const void* prefix_join_kernel(int dt) {
-    return dt == 1 ? (const void*)&prefix_join<BF16> : (const void*)&prefix_join<F16>;
+const void* prefix_join_kernel(int dt, int ways) {
+    if (ways == 1) return dt == 1 ? (const void*)&prefix_join<BF16, 1> : (const void*)&prefix_join<F16, 1>;
+    return dt == 1 ? (const void*)&prefix_join<BF16, 4> : (const void*)&prefix_join<F16, 4>;
 }
 
 }  // namespace rmsattn

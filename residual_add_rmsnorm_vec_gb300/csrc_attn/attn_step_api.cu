@@ -343,13 +343,19 @@ RMSATTN_API int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* 
     j.parts = f.parts;
     j.own = a.own;
     j.own_ml = a.own_ml;
-    // each launch behind the one before: programmatic dependents of the call's own
+    // Each launch is a programmatic dependent of the one before.  The shared part needs the
+    // plan alone, not the own tokens' kernel: it starts beside that one, on the SMs that it
+    // leaves or does not take, and waits for it in the end, so that what comes behind finds
+    // both done.
     st = launch(prefix_plan_kernel(), dim3(1), 512, 0, &f, f.pdl, stream);
+    if (st == RMSN_OK) st = launch_attend(p.behind, &a, true, stream, 1);
     if (st == RMSN_OK && n_groups)
         st = launch(p.e->fn, dim3((unsigned)p.shares), p.e->threads, (size_t)p.e->smem, &f, true, stream);
-    if (st == RMSN_OK) st = launch_attend(p.behind, &a, true, stream);
+    if (st == RMSN_OK) st = launch_attend(p.behind, &a, true, stream, 2);
     if (st != RMSN_OK) return st;
-    const int64_t cols = n_seqs * n_queries * a.group;
-    return launch(prefix_join_kernel(dt), dim3((unsigned)((cols + 63) / 64), (unsigned)(a.c.H * (a.c.D / 8))), 256, 0,
-                  &j, true, stream);
+    // four threads to a row's parts where an item has many
+    const int64_t cols = n_seqs * n_queries * a.group, items = (cols + f.rows - 1) / f.rows * a.c.H;
+    const int ways = items * 8 >= p.shares ? 1 : 4;
+    return launch(prefix_join_kernel(dt, ways), dim3((unsigned)((cols * ways + 255) / 256), (unsigned)(a.c.H * (a.c.D / 8))),
+                  256, 0, &j, true, stream);
 }

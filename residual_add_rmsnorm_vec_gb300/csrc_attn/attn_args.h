@@ -101,13 +101,13 @@ const void* norms_kernel_of(int dt, bool r32, bool fp8, bool ragged, int ch);
 // tiles of `rows` columns (sequence x query token x head) for each key head,
 // an item each, from item0 on; an item is ns steps, the group's items lie
 // one behind the other on the line of all steps from `first` on.
-struct PrefixGroup {
+struct __align__(16) PrefixGroup {
     int32_t s0, s1, shared;
     int32_t seq;  // the sequence whose table row names the shared pages
     int32_t ns, first, item0, tiles;
 };
 // The line of the shared parts: total steps, and the steps of a share.
-struct PrefixLine {
+struct __align__(16) PrefixLine {
     int32_t total, chunk, pad[2];
 };
 // A sequence's shared tokens (0: it does not share) and its group.

@@ -247,16 +247,16 @@ struct Piece {
 struct Walk {
     int at, stop, g;
     __device__ __forceinline__ void begin(const PrefixArgs& a) {
-        const PrefixLine line = *a.line;
-        const int64_t from = (int64_t)blockIdx.x * line.chunk, to = from + line.chunk;
-        at = (int)(from < line.total ? from : line.total);
-        stop = (int)(to < line.total ? to : line.total);
+        const int4 line = __ldcg(reinterpret_cast<const int4*>(a.line));  // total, chunk
+        const int64_t from = (int64_t)blockIdx.x * line.y, to = from + line.y;
+        at = (int)(from < line.x ? from : line.x);
+        stop = (int)(to < line.x ? to : line.x);
         g = 0;
         if (at < stop) {  // the last group that begins at `at` or before; groups without steps begin where the next does
             int hi = a.n_groups;
             while (hi - g > 1) {
                 const int mid = (g + hi) >> 1;
-                if (a.groups[mid].first <= at) g = mid;
+                if (__ldcg(&a.groups[mid].first) <= at) g = mid;
                 else hi = mid;
             }
         }
@@ -264,7 +264,9 @@ struct Walk {
     __device__ __forceinline__ bool next(const PrefixArgs& a, Piece* p) {
         if (at >= stop) return false;
         for (;;) {
-            p->g = a.groups[g];
+            const int4* from = reinterpret_cast<const int4*>(a.groups + g);
+            const int4 u = __ldcg(from), v = __ldcg(from + 1);
+            p->g = PrefixGroup{u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
             if (p->g.ns > 0 && at < p->g.first + p->g.ns * p->g.tiles * a.c.H) break;
             ++g;
         }

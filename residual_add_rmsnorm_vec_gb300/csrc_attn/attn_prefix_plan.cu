@@ -62,8 +62,9 @@ __global__ void __launch_bounds__(kThreads) prefix_plan(const PrefixArgs a) {
                 G.shared = shared;
                 G.ns = (shared + a.tok - 1) / a.tok;
                 G.tiles = (int)(((int64_t)(G.s1 - G.s0) * a.n * a.group + a.rows - 1) / a.rows);
-            } else if (count == 1 && lane == 0) {
-                a.seqs[G.seq] = alone;  // (behind the warp's own stores: the same word)
+            } else if (count == 1) {  // nobody to share with
+                __syncwarp();
+                if (lane == 0) a.seqs[G.seq] = alone;
             }
         }
         __syncwarp();

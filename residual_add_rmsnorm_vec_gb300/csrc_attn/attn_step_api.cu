@@ -209,7 +209,8 @@ int plan_prefix(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
     p->own_ml = p->own + times(out_rows, head_dim * 4);
     p->behind_ws = p->own_ml + round_up(out_rows * 8);
     p->total = p->behind_ws + p->behind.workspace;
-    if (n_kv_heads * (head_dim / 8) > 65535) return RMSN_EUNSUPPORTED;  // the join's grid
+    // the join's grid; columns are counted in 31 bits
+    if (n_kv_heads * (head_dim / 8) > 65535 || cols >= (int64_t(1) << 31)) return RMSN_EUNSUPPORTED;
     return too_big(p->total) ? RMSN_EUNSUPPORTED : RMSN_OK;
 }
 

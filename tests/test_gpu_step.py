@@ -50,7 +50,7 @@ def pages_state(rng, B, page, width, spare, done=0.2, absent=0.1, shared=0, new=
         take = max(0, own - shared)
         table.append(prefix[:min(shared, own)] + order[:take] + [-1] * (width - own))
         order = order[take:]
-        table[-1] = table[-1][:width]
+        table[-1] = (table[-1] + [-1] * width)[:width]  # (a pool that ran out leaves rows short)
         kind = rng.random()
         more.append(-1 if kind < done else rng.choice([0, new, rng.randint(0, 2 * new)]))
         lengths.append(-1 if kind > 1 - absent else L)
@@ -698,3 +698,73 @@ def test_a_serving_step(rn):
             lengths[1] = 32
     assert seen == sum(max(a, 0) for p in plans for a in p)
     assert int(n_free) == B * width - 2 - sum(-(-int(L) // page) - 2 for L in lengths)
+
+
+# ---------------------------------------------------------------- drawn cases
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_prefix_drawn(rn, seed):
+    rng = random.Random(1000 + seed)
+    D, Hk, n = rng.choice([64, 128, 256]), rng.choice([1, 2, 3]), rng.choice([1, 1, 2, 5])
+    G, page = rng.choice([1, 3, 4, 8]), rng.choice([16, 32, 48, 128])
+    groups = [(rng.randint(1, rng.choice([2, 9, 40])), rng.randint(0, rng.choice([6, 40])) * page)
+              for _ in range(rng.choice([1, 1, 2, 5]))]
+    t, table, lengths, P, cu = prefix_state(groups, owns(groups, n, seed, rng.choice([n + 1, 60, 300])), Hk, page, D,
+                                            seed=seed, spread=rng.random() < 0.3, n=n)
+    for s in range(lengths.shape[0]):
+        if rng.random() < 0.1:
+            lengths[s] = rng.choice([0, -1, 1, int(lengths[s]) // 2])
+    dt = rng.choice([torch.bfloat16, torch.float16])
+    q = rand((lengths.shape[0], n, Hk * G, D), seed, dt).cuda()
+    if rng.random() < 0.3:  # lengths that are shorter than what is shared in earnest
+        P = (P.double() * rng.random()).to(torch.int32)
+    want, bound = ref.attend(q, t, table, lengths, float(torch.tensor(0.09)), 0, 0)
+    within(run_prefix(rn, q, t, table, lengths, P, cu, n, scale=0.09), want, bound)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_norms_drawn(rn, seed):
+    rng = random.Random(2000 + seed)
+    T, H = rng.choice([1, 3, 50, 700]), rng.choice([rng.randint(1, 300), rng.randint(300, 5000), 8 * rng.randint(1, 2100)])
+    dtype, gate, offset = rng.choice(["bf16", "f16", "f32"]), rng.choice(["none", "layer", "token", "sequence"]), rng.choice([0.0, 1.0])
+    stream, fp8 = ("same" if dtype == "f32" else rng.choice(["same", "f32"])), rng.random() < 0.4
+    x, r, pw, w, g, index = norms_inputs(T, H, dtype, stream, gate, offset, seed)
+    if rng.random() < 0.2:
+        pw = None
+    if rng.random() < 0.2:
+        w = None
+    if gate == "sequence" and rng.random() < 0.5:  # rows of a wider tensor, off the grid
+        wide = torch.zeros((3, 2 * H + 1), dtype=g.dtype, device="cuda")
+        wide[:, 1:H + 1] = g
+        g = wide[:, 1:H + 1]
+    done = rn.fused_block_norms(x, r, pw, w, eps=1e-5, gate=g, gate_index=index, residual_scale=-0.5, weight_offset=offset,
+                                out_dtype="fp8" if fp8 else None)
+    check_norms(done, x, r, pw, w, g, index, fp8, -0.5, offset, 1e-5)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_pages_drawn(rn, seed):
+    rng = random.Random(3000 + seed)
+    B, page, width = rng.randint(1, rng.choice([5, 60, 900])), rng.choice([16, 48, 256]), rng.randint(1, 20)
+    free, n_free, table, lengths, more, keep = pages_state(rng, B, page, width, rng.randint(0, 4), done=rng.choice([0.0, 0.3]),
+                                                           shared=rng.choice([0, 0, 1]), new=rng.choice([1, 30]),
+                                                           most=rng.randint(1, width + 1))
+    n_free = min(n_free, rng.choice([n_free, B // 2, 0]))
+    rows = sum(m for m, L in zip(more, lengths) if m > 0 and L >= 0)
+    step = check_pages(rn, free, n_free, table, lengths, more, keep, page, max(0, rows + rng.choice([0, 0, 3, -2])))
+    # a pool that ran out leaves entries of -1 inside of the sequences
+    bad = any(p < 0 for s, m in enumerate(more) if m < 0 <= lengths[s] for p in table[s][keep[s]:-(-lengths[s] // page)])
+    bad = bad or any(row >= 0 and slot < 0 and step.before[row] >= 0 for row, slot in zip(step.rows.tolist(), step.slots.tolist()))
+    assert rn.rmsattn_read_status(clear=True) == (rn.RMSATTN_BAD_PAGE if bad else 0)
+
+
+def test_a_window_of_no_rows_and_one_column(rn):
+    # the smallest of everything: one head, one sequence of a group of one, one token
+    t = ref.random_cache(2, 1, 16, 64, 7, "cuda", spread=False)
+    q = rand((1, 1, 1, 64), 3, torch.bfloat16).cuda()
+    table, lengths = i32([[1]]), i32([1])
+    for P in (0, 1, 16):
+        within(run_prefix(rn, q, t, table, lengths, i32([P]), None, 1), *ref.attend(q, t, table, lengths, 0.125, 0, 0))
+    empty = rn.kv_cache_prefix_attention(q[:0, 0], make_cache(rn, t), table[:0], lengths[:0], i32([16]))
+    assert tuple(empty.shape) == (0, 1, 64)

@@ -285,7 +285,7 @@ int64_t rmsattn_pages_workspace(int64_t n_seqs);
  *                or NULL (1, without the offset)
  *   residual     [n_tokens, hidden] of x's type, or fp32 with RMSN_RESIDUAL_F32
  *                (bf16 / fp16 x); residual_out the same, may be residual itself
- *   out          of x's type (may be x itself), or bytes
+ *   out          of x's type (may be x itself, not residual_out), or bytes
  *   gate         NULL (1); or rows of x's type gate_stride elements apart:
  *                gate_stride 0, n_gates 1: one row for all; n_gates == n_tokens: a
  *                row each; with gate_index [n_tokens], token t takes row
@@ -309,9 +309,11 @@ int rmsattn_block_norms(const void* x, const void* residual, const void* post_we
 
 /* Status word of this library's kernels on the current device: bit 2 (value
  * 4) is set when a block table named a page outside the cache or a token lay
- * past the table (and by what the plan and the norms say above).  Reads synchronously, behind the legacy default stream's work:
- * synchronise with streams made non-blocking (PyTorch's own) first.  `clear` !=
- * 0 resets the word. */
+ * past the table (and by what the plan and the norms say above); bit 0 (value 1)
+ * when a wait inside rmsattn_kv_prefix_attention ran out after about a second
+ * (its result is then not to be used; a defect, no input leads there).  Reads
+ * synchronously, behind the legacy default stream's work: synchronise with
+ * streams made non-blocking (PyTorch's own) first.  `clear` != 0 resets the word. */
 int rmsattn_read_status(uint32_t* status, int clear);
 
 #ifdef __cplusplus

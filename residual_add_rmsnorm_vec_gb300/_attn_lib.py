@@ -17,7 +17,8 @@ RMSATTN_POS_I64 = 0x4000
 RMSATTN_OUT_FP8 = 0x8000
 RMSATTN_BLOCK = 16
 RMSATTN_MAX_QUERIES = 32
-RMSATTN_BAD_PAGE = 4  # bit of the status word
+RMSATTN_BAD_PAGE = 4  # bits of the status word
+RMSATTN_WAIT_RAN_OUT = 1
 
 EXPORTED_ATTN = ("rmsattn_qk_rope_fwd", "rmsattn_kv_append", "rmsattn_kv_attention",
                  "rmsattn_kv_attention_workspace", "rmsattn_read_status", "rmsattn_kv_prefix_attention",
@@ -105,8 +106,8 @@ def load_fast():
 
 
 def rmsattn_read_status(clear: bool = False) -> int:
-    """Status word of the attention-path kernels on the current device (0, or
-    ``RMSATTN_BAD_PAGE``)."""
+    """Status word of the attention-path kernels on the current device (0, or the
+    bits ``RMSATTN_BAD_PAGE`` and ``RMSATTN_WAIT_RAN_OUT``)."""
     v = ctypes.c_uint32(0)
     st = load_attn().rmsattn_read_status(ctypes.byref(v), int(bool(clear)))
     if st != _lib.RMSN_OK:

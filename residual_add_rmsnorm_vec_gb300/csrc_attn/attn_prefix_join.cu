@@ -5,7 +5,7 @@
 //
 // What bounds it: the chain of loads (sequence, group, parts) and the parts' bytes from
 // L2.  A thread has eight dims of a row and every fourth part where there are many (else
-// all of them: 256 sequences with 6 parts 10 against 16 us), up to eight of them on their
+// all of them), up to eight of them on their
 // way at once; lanes run along a key head's columns, as those lie in the parts (32
 // bytes each).  With the dims along the lanes and one thread to all parts, 64 sequences
 // of 32 / 8 heads x 128 with 19 parts took 17 us.

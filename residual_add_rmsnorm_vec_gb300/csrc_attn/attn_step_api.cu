@@ -68,9 +68,12 @@ RMSATTN_API int rmsattn_pages_step(int32_t* free_pages, int64_t n_pages, const i
     a.slots = slots;
     a.ws = static_cast<int32_t*>(workspace);
     a.status = d->status;
-    // up to four rows to a thread; a warp to a sequence (one that returns pages has a row of
-    // them to read: with 32 sequences to a warp, 1024 x 1 token took 21 us)
-    const int threads = n_seqs <= 128 && n_rows <= 512 ? 128 : 512;
+    // Up to four rows to a thread; a warp to a sequence (one that returns pages has a row of
+    // them to read: with 32 sequences to a warp, 1024 x 1 token took 21 us).  Small blocks
+    // while their scan of all sequences is short and there are SMs for them: 8 x 1 token 4.8
+    // against 5.5 us, 64 x 200 6.6 against 7.4, but 1024 x 1 8.3 against 7.3, 64 x 2000
+    // 8.2 against 7.9.
+    const int threads = n_seqs <= 256 && n_rows <= 512 * (int64_t)d->num_sms ? 128 : 512;
     int64_t blocks = (n_rows + 4 * threads - 1) / (4 * threads);
     const int64_t by_seqs = (n_seqs * 32 + threads - 1) / threads;
     if (blocks < by_seqs) blocks = by_seqs;
@@ -116,6 +119,7 @@ RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const v
     if (!aligned(residual, (uintptr_t)rbytes) || !aligned(residual_out, (uintptr_t)rbytes) ||
         !aligned(out, fp8 ? 1 : (uintptr_t)bytes) || !aligned(out_scale, 4) || !aligned(gate_index, 4))
         return RMSN_EALIGN;
+    if (out == residual_out) return RMSN_EINVAL;
     DeviceInfo* d = device_info();
     if (!d) return RMSN_ECUDA;
     NormsArgs a;
@@ -144,28 +148,31 @@ RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const v
                aligned(residual, (uintptr_t)(8 * rbytes)) && aligned(residual_out, (uintptr_t)(8 * rbytes));
     bool ragged = hidden % 8 != 0 || gate_stride % 8 != 0;
     for (const void* p : same) ragged = ragged || !aligned(p, (uintptr_t)(8 * bytes));
-    // Vectors of a thread: four put the most rows on an SM (16384 x 8192 bf16 162 us; two
-    // 189 to 211); as few as hold the row where there are not rows enough for that, for
-    // the shorter chain (8 x 4096: see the kernel).
-    const bool few = n_tokens < 4 * (int64_t)d->num_sms;
+    // Vectors of a thread: as few as put all rows on the SMs at once, for the shorter chain
+    // (8 x 4096 bf16 3.5 us with one and 3.9 with four, 900 x 1024 3.5 and 4.2); four
+    // otherwise, which put the most rows on an SM (600 x 4096 6.3 us with one and 5.2 with
+    // four, 2000 x 4096 19 and 12, 16384 x 8192 200 with two and 160 with four).
     const int64_t vectors = (hidden + (ragged ? 14 : 7)) / 8;
-    int ch = 4;
-    if (few) ch = vectors <= 512 ? 1 : (vectors <= 1024 ? 2 : 4);
+    int64_t ch = 1;
+    while (ch < 4 && ((vectors + ch - 1) / ch > 512 || n_tokens * ((vectors + ch - 1) / ch) > 1024 * (int64_t)d->num_sms))
+        ch *= 2;
     int64_t lanes = (vectors + ch - 1) / ch;
     if (!vec || lanes > 512) {
         ch = 0;
         lanes = hidden < 1024 ? hidden : 1024;
     }
     const int threads = (int)((lanes + 31) / 32 * 32);
-    return launch(norms_kernel_of(dt, r32, fp8, ragged, ch), dim3((unsigned)n_tokens), threads, 0, &a, a.pdl, stream);
+    return launch(norms_kernel_of(dt, r32, fp8, ragged, (int)ch), dim3((unsigned)n_tokens), threads, 0, &a, a.pdl, stream);
 }
 
 // ---------------------------------------------------------------- shared prefix
 
 namespace {
 
-// Two row tiles where the groups have more than 128 columns on average (they share
-// the widening of each key and value), else one.
+// Two row tiles where the groups have more than 128 columns on average: they share the
+// widening of each key and value (4 heads x 128, 256 sequences x 8192 tokens 116 against
+// 123 us with one; 33 sequences 44 against 46).  One otherwise (32 sequences 40 against 42,
+// 8 groups of 32 sequences x 4096 99 against 101).
 const PrefixEntry* prefix_entry_of(int dt, int64_t D, int64_t cols, int64_t n_groups) {
     int n = 0;
     const PrefixEntry* t = D == 64 ? prefix_kernels_64(&n)
@@ -209,15 +216,17 @@ int plan_prefix(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
     p->own_ml = p->own + times(out_rows, head_dim * 4);
     p->behind_ws = p->own_ml + round_up(out_rows * 8);
     p->total = p->behind_ws + p->behind.workspace;
-    // the join's grid; columns are counted in 31 bits
-    if (n_kv_heads * (head_dim / 8) > 65535 || cols >= (int64_t(1) << 31)) return RMSN_EUNSUPPORTED;
     return too_big(p->total) ? RMSN_EUNSUPPORTED : RMSN_OK;
 }
 
 int check_prefix(int64_t n_seqs, int64_t n_queries, int64_t n_q_heads, int64_t n_kv_heads,
                  int64_t head_dim, int64_t n_groups) {
     if (n_groups < 0 || n_groups > (1 << 24)) return RMSN_EINVAL;
-    return check_attend(n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim);
+    const int st = check_attend(n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim);
+    if (st != RMSN_OK) return st;
+    // columns are counted in 31 bits; the join's grid
+    if (times(n_seqs * n_queries, n_q_heads / n_kv_heads) >= (int64_t(1) << 31)) return RMSN_EUNSUPPORTED;
+    return n_kv_heads * (head_dim / 8) > 65535 ? RMSN_EUNSUPPORTED : RMSN_OK;
 }
 
 }  // namespace
@@ -354,7 +363,9 @@ RMSATTN_API int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* 
         st = launch(p.e->fn, dim3((unsigned)p.shares), p.e->threads, (size_t)p.e->smem, &f, true, stream);
     if (st == RMSN_OK) st = launch_attend(p.behind, &a, true, stream, 2);
     if (st != RMSN_OK) return st;
-    // four threads to a row's parts where an item has many
+    // Four threads to a row's parts where an item has many, for there are few items: 8
+    // sequences x 2048 tokens 25.0 against 28.5 us, 64 x 8192 50 against 55; one else: 256 x
+    // 8192 115 against 118, 512 x 4096 169 against 178.
     const int64_t cols = n_seqs * n_queries * a.group, items = (cols + f.rows - 1) / f.rows * a.c.H;
     const int ways = items * 8 >= p.shares ? 1 : 4;
     return launch(prefix_join_kernel(dt, ways), dim3((unsigned)((cols * ways + 255) / 256), (unsigned)(a.c.H * (a.c.D / 8))),

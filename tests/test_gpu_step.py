@@ -768,3 +768,53 @@ def test_a_window_of_no_rows_and_one_column(rn):
         within(run_prefix(rn, q, t, table, lengths, i32([P]), None, 1), *ref.attend(q, t, table, lengths, 0.125, 0, 0))
     empty = rn.kv_cache_prefix_attention(q[:0, 0], make_cache(rn, t), table[:0], lengths[:0], i32([16]))
     assert tuple(empty.shape) == (0, 1, 64)
+
+
+# ---------------------------------------------------------------- far and empty
+
+
+def test_prefix_pages_past_32_bits(rn):
+    # the same pages at the begin of a cache and behind 2^32 bytes of it
+    Hk, page, D, groups = 8, 64, 128, [(9, 640), (3, 128)]
+    t, table, lengths, P, cu = prefix_state(groups, owns(groups, 1), Hk, page, D)
+    n, size = t["k"].shape[0], Hk * page * D
+    far = 2 ** 32 // size + 5
+    big = {}
+    for name, v in t.items():
+        big[name] = torch.empty((far + n,) + v.shape[1:], dtype=v.dtype, device="cuda")
+        big[name][far:] = v
+    q = rand((12, 1, 32, D), 3, torch.bfloat16).cuda()
+    got = run_prefix(rn, q, big, table + far, lengths, P, cu, 1)
+    within(got, *ref.attend(q, t, table, lengths, 1 / math.sqrt(D), 0, 0))
+    assert torch.equal(got, run_prefix(rn, q, t, table, lengths, P, cu, 1))
+
+
+def test_prefix_of_no_groups(rn):
+    t, table, lengths, _, _ = prefix_state([(5, 64)], owns([(5, 64)], 1), 2, 16, 64)
+    q = rand((5, 1, 4, 64), 3, torch.bfloat16).cuda()
+    got = run_prefix(rn, q, t, table, lengths, i32([]), i32([0]), 1)
+    within(got, *ref.attend(q, t, table, lengths, 0.125, 0, 0))
+
+
+def test_pages_slots_past_32_bits(rn):
+    page, n = 65536, 40000
+    free, n_free = rn.kv_free_pages(n)
+    free = free.flip(0).contiguous()  # the last page first
+    table = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    step = rn.kv_pages_step_(free, n_free, table, i32([0, 0, 0]), i32([70000, 5, 1]), page_size=page, n_rows=70010)
+    assert table[:, 0].tolist() == [n - 1, n - 3, n - 4] and int(table[0, 1]) == n - 2
+    want = [(n - 1) * page + i for i in range(page)] + [(n - 2) * page + i for i in range(70000 - page)]
+    want += [(n - 3) * page + i for i in range(5)] + [(n - 4) * page] + [-1] * 4
+    assert step.slots.tolist() == want and step.n_free.tolist() == [n - 4]
+
+
+@pytest.mark.parametrize("H", [8192, 8191])
+def test_norms_of_elements_past_31_bits(rn, H):
+    T = 2 ** 31 // H + 3
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((T, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    gate = torch.randn((T, H), generator=g, device="cuda", dtype=torch.bfloat16)
+    y, h, _ = rn.fused_block_norms(x, x, eps=1e-6, gate=gate, residual_scale=0.5)
+    rows = slice(T - 4, T)
+    check_norms((y[rows], h[rows], None), x[rows], x[rows], None, None, gate[rows], None, False, 0.5, 0.0)
+    check_norms((y[:2], h[:2], None), x[:2], x[:2], None, None, gate[:2], None, False, 0.5, 0.0)

@@ -140,3 +140,20 @@ def test_prefix_tensors_refused(rn, change):  # noqa: F811
     a.update(change)
     with pytest.raises((ValueError, TypeError)):
         rn.kv_cache_prefix_attention(**a)
+
+
+def test_norms_outputs_lie_apart(rn):  # noqa: F811
+    for flags, out, ro in ((BF16, 32, 32), (F32, 32, 32), (BF16 | FP8, 64, 64)):
+        assert rn.load_attn().rmsattn_block_norms(
+            32, 64, None, None, None, 0, None, 0, out, ro, 16 if flags & FP8 else None, 4, 64, 1e-6, 1.0, 0.0, flags,
+            None) == EINVAL
+
+
+def test_status_bits(rn):  # noqa: F811
+    assert (rn.RMSATTN_WAIT_RAN_OUT, rn.RMSATTN_BAD_PAGE) == (1, 4)
+
+
+def test_prefix_of_more_columns_than_are_counted(rn):  # noqa: F811
+    # sequences x query tokens x heads of a key head past 31 bits
+    lib = rn.load_attn()
+    assert lib.rmsattn_kv_prefix_attention_workspace(1 << 24, 32, 4, 1, 64, 64, 1) == EUNSUPPORTED

@@ -156,6 +156,9 @@ RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const v
     int64_t ch = 1;
     while (ch < 4 && ((vectors + ch - 1) / ch > 512 || n_tokens * ((vectors + ch - 1) / ch) > 1024 * (int64_t)d->num_sms))
         ch *= 2;
+    // three where that takes fewer turns of a warp (4099 x 2045: 3 x 86 lanes, or 4 x 65)
+    auto turns = [&](int64_t c) { return ((vectors + c - 1) / c + 31) / 32 * c; };
+    if (ch == 4 && (vectors + 2) / 3 <= 512 && turns(3) < turns(4)) ch = 3;
     int64_t lanes = (vectors + ch - 1) / ch;
     if (!vec || lanes > 512) {
         ch = 0;

@@ -36,6 +36,16 @@ Tensor make(at::IntArrayRef sizes, at::ScalarType type, int64_t index) {
     return at::empty(sizes, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)index));
 }
 
+// [size] of a type, at a byte of another tensor's memory.
+Tensor part(const Tensor& whole, int64_t at, int64_t size, at::ScalarType type) {
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(whole.storage()),
+                                                     c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                     c10::scalarTypeToTypeMeta(type));
+    impl->set_storage_offset(at / (int64_t)c10::elementSize(type));
+    impl->set_sizes_contiguous({size});
+    return Tensor(std::move(impl));
+}
+
 cudaStream_t stream_of(int64_t index) {
     return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index).stream();
 }
@@ -400,10 +410,15 @@ PyObject* pages_step(PyObject*, PyObject* const* a, Py_ssize_t count) {
         const int64_t need = rmsattn_pages_workspace(n);
         // (a size that the library refuses is not allocated for)
         if (need < 0 || T > (int64_t(1) << 29)) return leave();
-        Tensor out[7] = {make({n + 1}, at::kInt, index), make({T}, at::kInt, index), make({T}, at::kLong, index),
-                         make({T}, at::kInt, index),     make({n}, at::kInt, index), make({n}, at::kInt, index),
-                         make({1}, at::kInt, index)};
-        Tensor ws;
+        // the results lie in one allocation, each at a multiple of 16 bytes: with seven of their
+        // own a step of 8 sequences took 12.5 us, not 9.3 (its kernel 4.6)
+        const int64_t size[7] = {n + 1, T, T, T, n, n, 1};
+        const at::ScalarType type[7] = {at::kInt, at::kInt, at::kLong, at::kInt, at::kInt, at::kInt, at::kInt};
+        int64_t at[8] = {0};
+        for (int i = 0; i < 7; ++i) at[i + 1] = (at[i] + size[i] * (int64_t)c10::elementSize(type[i]) + 15) / 16 * 16;
+        const Tensor whole = make({at[7]}, at::kByte, index);
+        Tensor out[7], ws;
+        for (int i = 0; i < 7; ++i) out[i] = part(whole, at[i], size[i], type[i]);
         if (need > 0) ws = make({need}, at::kByte, index);
         auto to = [&](int i) { return static_cast<int32_t*>(out[i].mutable_data_ptr()); };
         const int st = rmsattn_pages_step(

@@ -8,6 +8,15 @@
 // products: 4 D flops for each pair of a row and a token against 2 D + 1/2 bytes a
 // token.  From about 150 rows on the tensor cores bound it, below that DRAM.
 //
+// Measured, 32 / 8 heads x 128: 64 sequences x 8192 shared tokens 24 us, of which 7 are a
+// block's start (TMEM, barriers, plan, queries, first pages); 256 x 16384 85 us, 808 TFLOP/s
+// (0.42 of the library's matrix product).  A step of 64 tokens and 256 rows takes 2000 cycles.
+// What bounds it there: a product of 128 rows and 16 of the inner dimension takes 65
+// cycles with 64 columns as with 128, for its A operand comes from shared memory, so S = Q
+// K^T runs at half its rate, and shared memory carries the codes, their widened copies and
+// Q beside it.  Steps of 128 tokens, whose scores fill TMEM once, took 104 us: products and
+// softmax in turn.
+//
 // A block holds R tiles of 128 rows (R = 2 where a group has more than 128 rows)
 // and walks over its share of the line of all steps, 64 tokens of an item (group x key
 // head x R tiles) each.  Its warps have fixed parts:

@@ -1,6 +1,9 @@
 // Attention with a shared prefix: which sequences share how much, and the line of
 // the shared parts' steps (PrefixGroup).  One block; a warp to a group.  A sequence
 // shares a prefix if each of its queries sees all of it.
+//
+// What bounds it: latency, 3 to 4 us with the launch (lengths, then the groups' places).  It
+// stands before both parts, which wait for nothing else.
 #include "attn_common.cuh"
 
 namespace rmsattn {

@@ -24,7 +24,8 @@ class KVStep(NamedTuple):
     ``kv_cache_append_``, ``positions`` to ``qk_norm_rope``, ``after`` to the
     attention (and into the next step as its lengths), ``rows`` to
     ``fused_block_norms`` (a gate row for each sequence), ``slots`` are the rows'
-    places in the cache, ``n_free`` the next step's free pages."""
+    places in the cache, ``n_free`` the next step's free pages.  They may share one
+    allocation."""
     cu_seqlens: torch.Tensor
     positions: torch.Tensor
     slots: torch.Tensor

@@ -10,6 +10,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -32,8 +33,10 @@ int dtype_flag(at::ScalarType t) {
     return t == at::kBFloat16 ? RMSN_IN_BF16 : (t == at::kHalf ? RMSN_IN_F16 : (t == at::kFloat ? RMSN_IN_F32 : -1));
 }
 
+// (at::empty by way of the dispatcher takes 0.4 us more: fused_block_norms of 8 x 4096, with
+// two results, 6.1 us a call and 7.0)
 Tensor make(at::IntArrayRef sizes, at::ScalarType type, int64_t index) {
-    return at::empty(sizes, at::TensorOptions().dtype(type).device(at::kCUDA, (c10::DeviceIndex)index));
+    return at::detail::empty_cuda(sizes, type, c10::Device(c10::kCUDA, (c10::DeviceIndex)index), std::nullopt);
 }
 
 // [size] of a type, at a byte of another tensor's memory.
@@ -411,7 +414,7 @@ PyObject* pages_step(PyObject*, PyObject* const* a, Py_ssize_t count) {
         // (a size that the library refuses is not allocated for)
         if (need < 0 || T > (int64_t(1) << 29)) return leave();
         // the results lie in one allocation, each at a multiple of 16 bytes: with seven of their
-        // own a step of 8 sequences took 12.5 us, not 9.3 (its kernel 4.6)
+        // own a step of 8 sequences took 12.5 us, not 8 (its kernel 4.6)
         const int64_t size[7] = {n + 1, T, T, T, n, n, 1};
         const at::ScalarType type[7] = {at::kInt, at::kInt, at::kLong, at::kInt, at::kInt, at::kInt, at::kInt};
         int64_t at[8] = {0};

@@ -96,8 +96,8 @@ def kv_pages_step_(free_pages: torch.Tensor, n_free: torch.Tensor, block_table: 
         raise ValueError("block_table rows must be contiguous")
     if page_size < _al.RMSATTN_BLOCK or page_size % _al.RMSATTN_BLOCK:
         raise ValueError(f"page_size must be a multiple of {_al.RMSATTN_BLOCK}, got {page_size}")
-    if n_rows < 0:
-        raise ValueError("n_rows must not be negative")
+    if not 0 <= n_rows <= 1 << 29:
+        raise ValueError(f"n_rows must be within [0, 2^29], got {n_rows}")
     if stream is not None or free_pages.get_device() != torch._C._cuda_getDevice():
         def call():
             step = kv_pages_step_(free_pages, n_free, block_table, lengths, new_tokens, shared_pages,

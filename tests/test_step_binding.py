@@ -95,7 +95,7 @@ def ints(*shape):
 @pytest.mark.parametrize("change", [
     dict(free_pages=ints(2, 4)), dict(free_pages=ints(8).long()), dict(n_free=ints(2)), dict(block_table=ints(4, 2)),
     dict(block_table=ints(3, 2).long()), dict(block_table=ints(3)), dict(lengths=ints(2)), dict(lengths=ints(1, 3)),
-    dict(new_tokens=ints(3).float()), dict(shared_pages=ints(4)), dict(page_size=8), dict(page_size=40), dict(n_rows=-1),
+    dict(new_tokens=ints(3).float()), dict(shared_pages=ints(4)), dict(page_size=8), dict(page_size=40), dict(n_rows=-1), dict(n_rows=(1 << 29) + 1),
     dict(lengths=ints(6)[::2]), dict(block_table=ints(2, 3).t()),
     dict(),  # all of it right, but on the CPU
 ])

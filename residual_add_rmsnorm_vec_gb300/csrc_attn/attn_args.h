@@ -127,7 +127,7 @@ struct PrefixArgs {
     int64_t B;
     int32_t n_groups, n, group;  // group: query heads of a key head
     int32_t tok, rows;           // tokens of a step, columns of an item
-    int32_t shares, min_chunk;
+    int32_t shares;
     int32_t pdl;
     float scale;
     uint64_t page_rcp;  // ceil(2^37 / (page / 16))

@@ -26,14 +26,10 @@ template <class T, int V>
 struct Raw {
     uint32_t u[V * T::kBytes >= 4 ? V * T::kBytes / 4 : 1];
 };
-template <class T, int V, bool STREAM>
-__device__ __forceinline__ Raw<T, V> load(const void* p, int64_t e) {
-    Raw<T, V> v;
-    if constexpr (V == 1) {
-        if constexpr (T::kBytes == 4) v.u[0] = static_cast<const uint32_t*>(p)[e];
-        else v.u[0] = static_cast<const uint16_t*>(p)[e];
-    } else if constexpr (T::kBytes == 4) {
-        static_assert(V == 8, "");
+template <class T, bool STREAM>
+__device__ __forceinline__ Raw<T, 8> load(const void* p, int64_t e) {
+    Raw<T, 8> v;
+    if constexpr (T::kBytes == 4) {
         const rmsn::V8 w = STREAM ? rmsn::ld_stream32(static_cast<const float*>(p) + e)
                                   : rmsn::ld_keep32(static_cast<const float*>(p) + e);
 #pragma unroll
@@ -93,7 +89,7 @@ __device__ __forceinline__ void store(void* p, int64_t e, const Raw<T, V>& v) {
 // within [0, H).
 template <class T, bool STREAM>
 __device__ __forceinline__ Raw<T, 8> load_row(const void* p, int64_t e, int j, int H, bool whole) {
-    if (whole) return load<T, 8, STREAM>(p, e);
+    if (whole) return load<T, STREAM>(p, e);
     Raw<T, 8> v;
 #pragma unroll
     for (uint32_t& u : v.u) u = 0u;
@@ -204,9 +200,9 @@ __device__ __forceinline__ void norm(const Raw<T, 8>& w, float off, float inv, c
 #pragma unroll
     for (int k = 0; k < 4; ++k) y[k] = rmsn::mul2(rmsn::mul2(h[k], inv2), rmsn::add2(wv[k], off2));
 }
-template <class T, int V>
-__device__ __forceinline__ Raw<T, V> ones() {
-    Raw<T, V> v;
+template <class T>
+__device__ __forceinline__ Raw<T, 8> ones() {
+    Raw<T, 8> v;
 #pragma unroll
     for (uint32_t& u : v.u) u = rmsn::ones_word<T>();
     return v;
@@ -249,10 +245,10 @@ __global__ void __launch_bounds__(512, 2) norms_kernel(const NormsArgs a) {
 #pragma unroll
     for (int c = 0; c < CH; ++c) r[c] = load_row<R, true>(a.residual, base + j[c], j[c], on[c] ? a.H : 0, whole[c]);
     auto from = [&](const void* row, int c) {
-        if constexpr (!RAGGED) return load<T, V, false>(row, j[c]);
+        if constexpr (!RAGGED) return load<T, false>(row, j[c]);
         else return on[c] ? load_any<T>(row, j[c], a.H) : Raw<T, V>{};
     };
-    auto weight = [&](const void* w, int c) { return w ? from(w, c) : ones<T, V>(); };
+    auto weight = [&](const void* w, int c) { return w ? from(w, c) : ones<T>(); };
     const char* gate = a.gate ? static_cast<const char*>(a.gate) + g0 * T::kBytes : nullptr;
     // what lies outside of the row counts as zero
     auto clear = [&](int c, float (&v)[V]) {

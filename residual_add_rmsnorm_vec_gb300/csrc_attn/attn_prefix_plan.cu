@@ -14,6 +14,7 @@ constexpr int kThreads = 512;
 
 __global__ void __launch_bounds__(kThreads) prefix_plan(const PrefixArgs a) {
     __shared__ int64_t sums[2][kThreads / 32];
+    __shared__ int2 sizes[kThreads];  // tiles and steps of the first groups
     rmsn::pdl_wait(a.pdl);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
@@ -71,7 +72,10 @@ __global__ void __launch_bounds__(kThreads) prefix_plan(const PrefixArgs a) {
             }
         }
         __syncwarp();
-        if (lane == 0) a.groups[g] = G;
+        if (lane == 0) {
+            a.groups[g] = G;
+            if (g < kThreads) sizes[g] = make_int2(G.tiles, G.ns);
+        }
     }
     __syncthreads();
     // the groups' places on the line, and of their items
@@ -80,8 +84,9 @@ __global__ void __launch_bounds__(kThreads) prefix_plan(const PrefixArgs a) {
         const int g = g0 + threadIdx.x;
         int64_t it = 0, st = 0;
         if (g < a.n_groups) {
-            it = (int64_t)a.groups[g].tiles * a.c.H;
-            st = it * a.groups[g].ns;
+            const int2 n = g < kThreads ? sizes[g] : make_int2(a.groups[g].tiles, a.groups[g].ns);
+            it = (int64_t)n.x * a.c.H;
+            st = it * n.y;
         }
         int64_t i1 = it, s1 = st;
 #pragma unroll
@@ -114,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) prefix_plan(const PrefixArgs a) {
     }
     if (threadIdx.x == 0) {
         int64_t chunk = (steps + a.shares - 1) / a.shares;
-        if (chunk < a.min_chunk) chunk = a.min_chunk;
+        if (chunk < 1) chunk = 1;
         *a.line = PrefixLine{(int32_t)steps, (int32_t)chunk, {0, 0}};
     }
 }

@@ -173,7 +173,7 @@ RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const v
 namespace {
 
 // Two row tiles where the groups have more than 128 columns on average: they share the
-// widening of each key and value (4 heads x 128, 256 sequences x 8192 tokens 116 against
+// widening of each key and value (4 heads x 128 to a key head, 300 own tokens: 256 sequences x 8192 tokens 116 against
 // 123 us with one; 33 sequences 44 against 46).  One otherwise (32 sequences 40 against 42,
 // 8 groups of 32 sequences x 4096 99 against 101).
 const PrefixEntry* prefix_entry_of(int dt, int64_t D, int64_t cols, int64_t n_groups) {
@@ -328,7 +328,6 @@ RMSATTN_API int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* 
     f.tok = p.e->tok;
     f.rows = 128 * p.e->R;
     f.shares = (int32_t)p.shares;
-    f.min_chunk = 1;
     f.pdl = (flags & RMSN_PDL) ? 1 : 0;
     f.scale = scale;
     f.page_rcp = a.page_rcp;

@@ -818,3 +818,10 @@ def test_norms_of_elements_past_31_bits(rn, H):
     rows = slice(T - 4, T)
     check_norms((y[rows], h[rows], None), x[rows], x[rows], None, None, gate[rows], None, False, 0.5, 0.0)
     check_norms((y[:2], h[:2], None), x[:2], x[:2], None, None, gate[:2], None, False, 0.5, 0.0)
+
+
+def test_prefix_of_more_groups_than_a_block_has_threads(rn):
+    groups = [(2, 32 * (g % 3)) for g in range(700)]
+    t, table, lengths, P, cu = prefix_state(groups, owns(groups, 1, most=20), 1, 16, 64)
+    q = rand((1400, 1, 2, 64), 3, torch.bfloat16).cuda()
+    within(run_prefix(rn, q, t, table, lengths, P, cu, 1), *ref.attend(q, t, table, lengths, 0.125, 0, 0))

@@ -292,7 +292,8 @@ int64_t rmsattn_pages_workspace(int64_t n_seqs);
  *                gate_index[t] of n_gates, and one with a negative index (a row
  *                behind the last sequence) is left out, out and residual_out
  *                untouched.  An index >= n_gates is left out too, and sets bit 2
- *                (value 4) of the status word.
+ *                (value 4) of the status word.  Where n_tokens or n_gates is 0, the
+ *                pointers of what is empty may be NULL.
  *
  * Sums of squares are fp32: rows need sum(x^2), sum(h^2) < FLT_MAX.  Rows, gates
  * and weights are contiguous; 16-byte vectors are used where every operand's rows

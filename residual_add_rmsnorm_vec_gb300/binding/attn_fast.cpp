@@ -493,7 +493,6 @@ PyObject* block_norms(PyObject*, PyObject* const* a, Py_ssize_t count) {
                 if (stride < H || (a[6] == Py_None ? n_gates != T : !ints(a[6], T, index))) return leave();
                 gates = g->const_data_ptr();
             }
-            if (!gates) return leave();
         }
         Tensor out[3];
         for (int i = 0; i < 3; ++i) {

@@ -104,13 +104,16 @@ RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const v
     if (too_big(times(n_tokens, hidden * 4))) return RMSN_EINVAL;
     if (!(eps >= 0.f) || !isfinite(eps) || !isfinite(residual_scale) || !isfinite(weight_offset))
         return RMSN_EINVAL;
-    if (gate ? (gate_stride < 0 || (gate_stride > 0 && gate_stride < hidden) || n_gates < 0 ||
-                too_big(times(n_gates, gate_stride * 4)))
-             : (gate_stride != 0 || gate_index != nullptr || n_gates != 0))
+    if (gate_stride < 0 || (gate_stride > 0 && gate_stride < hidden) || n_gates < 0 ||
+        too_big(times(n_gates, times(gate_stride, 4))))
         return RMSN_EINVAL;
-    if (gate && (gate_index ? n_gates > INT32_MAX : n_gates != (gate_stride ? n_tokens : 1))) return RMSN_EINVAL;
     if (fp8 ? (n_tokens && !out_scale) : out_scale != nullptr) return RMSN_EINVAL;
     if (n_tokens == 0) return RMSN_OK;
+    // From here on the pointers say what the gate is.  (An empty tensor's may be NULL: without
+    // tokens those of the index and of each token's gate, and of gates that are none at all,
+    // to which no index leads.)
+    if (!gate && (n_gates != 0 || (gate_stride != 0) != (gate_index != nullptr))) return RMSN_EINVAL;
+    if (gate_index ? n_gates > INT32_MAX : gate && n_gates != (gate_stride ? n_tokens : 1)) return RMSN_EINVAL;
     if (!x || !residual || !out || !residual_out) return RMSN_EINVAL;
     const int64_t rbytes = r32 ? 4 : bytes;
     const void* same[] = {x, post_weight, weight, gate};

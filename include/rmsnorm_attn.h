@@ -290,9 +290,11 @@ int64_t rmsattn_pages_workspace(int64_t n_seqs);
  *                gate_stride 0, n_gates 1: one row for all; n_gates == n_tokens: a
  *                row each; with gate_index [n_tokens], token t takes row
  *                gate_index[t] of n_gates, and one with a negative index (a row
- *                behind the last sequence) is left out, out and residual_out
- *                untouched.  An index >= n_gates is left out too, and sets bit 2
- *                (value 4) of the status word.  Where n_tokens or n_gates is 0, the
+ *                behind the last sequence) is left out, out, residual_out and
+ *                out_scale untouched, or zeros there with RMSATTN_ZERO_OUT,
+ *                RMSATTN_ZERO_RESIDUAL and RMSATTN_ZERO_SCALE (outputs that nothing
+ *                was written to before).  An index >= n_gates is left out too, and sets
+ *                bit 2 (value 4) of the status word.  Where n_tokens or n_gates is 0, the
  *                pointers of what is empty may be NULL.
  *
  * Sums of squares are fp32: rows need sum(x^2), sum(h^2) < FLT_MAX.  Rows, gates
@@ -300,6 +302,9 @@ int64_t rmsattn_pages_workspace(int64_t n_seqs);
  * allow it (hidden a multiple of 8).
  */
 #define RMSATTN_OUT_FP8 0x8000u
+#define RMSATTN_ZERO_OUT 0x10000u
+#define RMSATTN_ZERO_RESIDUAL 0x20000u
+#define RMSATTN_ZERO_SCALE 0x40000u
 
 int rmsattn_block_norms(const void* x, const void* residual, const void* post_weight,
                         const void* weight, const void* gate, int64_t gate_stride,

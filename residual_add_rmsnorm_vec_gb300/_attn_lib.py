@@ -15,6 +15,7 @@ RMSATTN_NORM = 0x1000
 RMSATTN_INTERLEAVED = 0x2000
 RMSATTN_POS_I64 = 0x4000
 RMSATTN_OUT_FP8 = 0x8000
+RMSATTN_ZERO_OUT, RMSATTN_ZERO_RESIDUAL, RMSATTN_ZERO_SCALE = 0x10000, 0x20000, 0x40000
 RMSATTN_BLOCK = 16
 RMSATTN_MAX_QUERIES = 32
 RMSATTN_BAD_PAGE = 4  # bits of the status word

@@ -507,6 +507,11 @@ PyObject* block_norms(PyObject*, PyObject* const* a, Py_ssize_t count) {
         if (rtype != type) flags |= RMSN_RESIDUAL_F32;
         if (fp8) flags |= RMSATTN_OUT_FP8;
         if (a[13] == Py_True) flags |= RMSN_PDL;
+        if (a[6] != Py_None) {  // rows that are left out of new outputs
+            if (!out[0].defined()) flags |= RMSATTN_ZERO_OUT;
+            if (!out[1].defined()) flags |= RMSATTN_ZERO_RESIDUAL;
+            if (fp8 && !out[2].defined()) flags |= RMSATTN_ZERO_SCALE;
+        }
         if (!out[0].defined()) out[0] = make({T, H}, otype, index);
         if (!out[1].defined()) out[1] = make({T, H}, rtype, index);
         if (fp8 && !out[2].defined()) out[2] = make({T}, at::kFloat, index);

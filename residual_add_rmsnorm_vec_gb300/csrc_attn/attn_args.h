@@ -92,6 +92,7 @@ struct NormsArgs {
     int64_t T, gate_stride, n_gates;
     int32_t H, pdl;
     float eps, alpha, w_off;
+    bool zero_out, zero_residual, zero_scale;  // of a row that is left out (else as it was)
     uint32_t* status;
 };
 // ch vectors of eight elements to a thread; 0: any row

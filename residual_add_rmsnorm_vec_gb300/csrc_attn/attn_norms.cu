@@ -178,7 +178,7 @@ __device__ __forceinline__ Raw<T, 8> load_any(const void* row, int j, int H) {
 }
 
 // The gate's row for row t (NULL: no gate), or false: the row belongs to no
-// sequence and is left as it is.
+// sequence and is left out.
 __device__ __forceinline__ bool gate_row(const NormsArgs& a, int64_t t, int64_t* at) {
     *at = t * a.gate_stride;
     if (!a.index) return true;
@@ -189,6 +189,20 @@ __device__ __forceinline__ bool gate_row(const NormsArgs& a, int64_t t, int64_t*
     }
     *at = i * a.gate_stride;
     return i >= 0;
+}
+
+// A row that is left out: zeros where the outputs are new, else as it was.
+template <class T, class R, bool FP8>
+__device__ __forceinline__ void leave_out(const NormsArgs& a, int64_t t) {
+    const int64_t base = t * a.H;
+    for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
+        if (a.zero_out) {
+            if constexpr (FP8) static_cast<uint8_t*>(a.out)[base + j] = 0;
+            else store1<T>(a.out, base + j, 0.f);
+        }
+        if (a.zero_residual) store1<R>(a.residual_out, base + j, 0.f);
+    }
+    if (FP8 && a.zero_scale && threadIdx.x == 0) a.out_scale[t] = 0.f;
 }
 
 // y = (w + off) (h inv), in that order of roundings.
@@ -225,7 +239,10 @@ __global__ void __launch_bounds__(512, 2) norms_kernel(const NormsArgs a) {
     rmsn::pdl_launch_dependents(a.pdl);
     const int64_t t = blockIdx.x, base = t * a.H;
     int64_t g0;
-    if (!gate_row(a, t, &g0)) return;
+    if (!gate_row(a, t, &g0)) {
+        leave_out<T, R, FP8>(a, t);
+        return;
+    }
     const int shift = RAGGED ? (int)(base & 7) : 0;
     Raw<T, V> x[CH];
     Raw<R, V> r[CH];
@@ -351,7 +368,10 @@ __global__ void __launch_bounds__(1024) norms_long_kernel(const NormsArgs a) {
     rmsn::pdl_launch_dependents(a.pdl);
     const int64_t t = blockIdx.x, base = t * a.H;
     int64_t g0;
-    if (!gate_row(a, t, &g0)) return;
+    if (!gate_row(a, t, &g0)) {
+        leave_out<T, R, FP8>(a, t);
+        return;
+    }
     auto weight = [](const void* w, int64_t e, float off) { return w ? __fadd_rn(load1<T>(w, e), off) : 1.f; };
     float sum = 0.f;
     for (int j = threadIdx.x; j < a.H; j += blockDim.x) {

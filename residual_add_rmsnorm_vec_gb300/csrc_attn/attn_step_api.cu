@@ -94,7 +94,9 @@ RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const v
                                     void* residual_out, float* out_scale, int64_t n_tokens,
                                     int64_t hidden, float eps, float residual_scale, float weight_offset,
                                     uint32_t flags, cudaStream_t stream) {
-    if (flags & ~(RMSN_IN_MASK | RMSN_RESIDUAL_F32 | RMSATTN_OUT_FP8 | RMSN_PDL)) return RMSN_EINVAL;
+    if (flags & ~(RMSN_IN_MASK | RMSN_RESIDUAL_F32 | RMSATTN_OUT_FP8 | RMSN_PDL | RMSATTN_ZERO_OUT |
+                  RMSATTN_ZERO_RESIDUAL | RMSATTN_ZERO_SCALE))
+        return RMSN_EINVAL;
     int64_t bytes = 0;
     const int dt = dtype_of(flags, &bytes);
     if (dt < 0) return RMSN_EINVAL;
@@ -108,6 +110,7 @@ RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const v
         too_big(times(n_gates, times(gate_stride, 4))))
         return RMSN_EINVAL;
     if (fp8 ? (n_tokens && !out_scale) : out_scale != nullptr) return RMSN_EINVAL;
+    if (!fp8 && (flags & RMSATTN_ZERO_SCALE)) return RMSN_EINVAL;
     if (n_tokens == 0) return RMSN_OK;
     // From here on the pointers say what the gate is.  (An empty tensor's may be NULL: without
     // tokens those of the index and of each token's gate, and of gates that are none at all,
@@ -144,6 +147,9 @@ RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const v
     a.eps = eps;
     a.alpha = residual_scale;
     a.w_off = weight_offset;
+    a.zero_out = (flags & RMSATTN_ZERO_OUT) != 0;
+    a.zero_residual = (flags & RMSATTN_ZERO_RESIDUAL) != 0;
+    a.zero_scale = (flags & RMSATTN_ZERO_SCALE) != 0;
     a.status = d->status;
     // Vectors of eight elements where the tensors of rows begin on one; where every row,
     // and the weights' and gates', does too, no row has ends of its own.

@@ -220,8 +220,9 @@ def fused_block_norms(x: torch.Tensor, residual: torch.Tensor, post_weight: torc
     [H] of x's dtype (None: 1), both plus ``weight_offset``.  ``gate``: None (1),
     [H], or rows [T, H]; with ``gate_index`` (int32 [T]) rows [n, H] of which
     token t takes row gate_index[t], and a token with a negative index is left
-    out (its rows of out and residual_out stay as they are).  ``out_dtype``:
-    x's, or "fp8" (E4M3 codes as uint8 with a scale for each token).  Returns
+    out: its row stays as it is in an ``out``, ``residual_out`` or ``out_scale`` that
+    is given, and is zeros in one that the call makes.  ``out_dtype``: x's, or
+    "fp8" (E4M3 codes as uint8 with a scale for each token).  Returns
     ``(out, residual_out, out_scale)``, out_scale None without fp8.
     """
     if stream is None:
@@ -287,6 +288,10 @@ def fused_block_norms(x: torch.Tensor, residual: torch.Tensor, post_weight: torc
             given = (out, residual_out, out_scale)
             return [t for t, g in zip(done, given) if t is not None and g is None], done
         return _other_call(device, stream, call)
+    if gate_index is not None:  # rows that are left out of new outputs
+        flags |= _al.RMSATTN_ZERO_OUT if out is None else 0
+        flags |= _al.RMSATTN_ZERO_RESIDUAL if residual_out is None else 0
+        flags |= _al.RMSATTN_ZERO_SCALE if fp8 and out_scale is None else 0
     if out is None:
         out = torch.empty((T, H), dtype=torch.uint8 if fp8 else dt, device=device)
     if residual_out is None:

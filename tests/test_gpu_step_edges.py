@@ -34,3 +34,35 @@ def test_norms_of_no_gates(rn, eps):  # noqa: F811
         torch.cuda.synchronize()
         assert rn.rmsattn_read_status(clear=True) == status
         assert (out == 7).all() and (ro == 5).all()
+
+
+@pytest.mark.parametrize("eps", [1e-6, 1])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,stream", [(64, "same"), (257, "f32"), (4096, "same"), (20000, "f32")])
+def test_norms_rows_left_out_of_new_outputs_are_zeros(rn, eps, fp8, H, stream):  # noqa: F811
+    T = 7
+    x, r, pw, w, g, _ = norms_inputs(T, H, "bf16", stream, "sequence", 0.0)
+    index = i32([0, -1, 2, -1, -5, 1, -1])
+    off = (index < 0).cpu()
+    kw = dict(eps=eps, gate=g, gate_index=index, out_dtype="fp8" if fp8 else None)
+    size = T * H * (1 if fp8 else 2)
+
+    def dirty():  # what the allocator hands out next is not zeros
+        junk = [torch.full((n,), 0x7F, dtype=torch.uint8, device="cuda")
+                for n in (size, T * H * r.element_size(), 4 * T) for _ in range(8)]
+        del junk
+
+    full = rn.fused_block_norms(x, r, pw, w, **{**kw, "gate_index": index.clamp(min=0)})
+    dirty()
+    out, ro, scale = rn.fused_block_norms(x, r, pw, w, **kw)
+    assert not out[off].any() and not ro[off].any() and (scale is None or not scale[off].any())
+    for a, b in zip((out, ro, scale), full):
+        assert a is None or torch.equal(a[~off], b[~off])
+    # a given output keeps its rows, beside new ones
+    mine = torch.full_like(ro, 5.0)
+    out, ro, scale = rn.fused_block_norms(x, r, pw, w, residual_out=mine, **kw)
+    assert (mine[off] == 5).all() and not out[off].any() and torch.equal(mine[~off], full[1][~off])
+    if fp8:
+        mine = torch.full((T,), 3.0, device="cuda")
+        out, ro, scale = rn.fused_block_norms(x, r, pw, w, out_scale=mine, **kw)
+        assert (mine[off] == 3).all() and not out[off].any() and not ro[off].any()

@@ -33,3 +33,8 @@ def test_norms_of_no_tokens(rn, flags, gate):  # noqa: F811
 ])
 def test_norms_of_no_tokens_still_refuse(rn, kw):  # noqa: F811
     assert norms(rn, **kw) == EINVAL
+
+
+@pytest.mark.parametrize("flags,status", [(0x70000 | FP8, OK), (0x30000, OK), (0x40000, EINVAL), (0x80000, EINVAL)])
+def test_norms_flags_of_rows_left_out(rn, flags, status):  # noqa: F811
+    assert norms(rn, flags=BF16 | flags) == status

@@ -329,13 +329,13 @@ __device__ __forceinline__ void plan(const PrefixArgs& a, Bars* bars, Step* step
             const int j = (p.step0 + t0) * C::TOK + lane * kBlock;
             const bool there = t0 + (lane >> 2) < p.steps && j < p.g.shared;
             const int slot = there ? (int)(((uint64_t)(uint32_t)(j >> 4) * a.page_rcp) >> 37) : 0;
-            const int32_t entry = row[slot];
+            const int32_t entry = __ldcg(row + slot);
             const bool have = there && (uint32_t)entry < (uint32_t)a.c.n_pages;
             if (there && !have) atomicOr(a.status, kBadPage);
             // (a block that is not there reads page 0's scale, and is left out)
             const int64_t page = have ? entry : 0;
             const int64_t block = have ? (int64_t)p.hk * (a.c.page >> 4) + ((j - slot * a.c.page) >> 4) : 0;
-            float ks = a.c.ks[page * a.c.scale_stride + block], vs = a.c.vs[page * a.c.scale_stride + block];
+            float ks = __ldcg(a.c.ks + page * a.c.scale_stride + block), vs = __ldcg(a.c.vs + page * a.c.scale_stride + block);
             if (!have) ks = vs = 0.f;
             const int64_t off = page * a.c.page_stride + block * (kBlock * C::D);
             const uint32_t valid = __ballot_sync(0xFFFFFFFFu, have);
@@ -863,9 +863,11 @@ __global__ void __launch_bounds__(C::kWarps * 32, 1) prefix_kernel(const PrefixA
     tc_after();
     // (all of TMEM is the block's, so it begins at 0, and places in it are constants)
     if (threadIdx.x == 0 && bars.tmem != 0) bars.stop = 1;
-    // The plan's launch is over and its results are there: the launch between, whose
-    // programmatic dependent this is, has waited for it in each of its blocks before it
-    // let this one begin.
+    // The plan's launch, and with it all that the stream wrote before this call, is over and
+    // its results are in L2: the launch between, whose programmatic dependent this is, has
+    // waited for it in each of its blocks before it let this one begin.  This one does not
+    // wait itself before its end, so whatever it reads goes past L1 (plan, table entries,
+    // scales by __ldcg, codes and queries by cp.async.cg).
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     unsigned char* stages = smem + C::R * C::kQ;
     unsigned char* codes = stages + 4 * C::kTile;

@@ -3,7 +3,8 @@ sequences that are left out, shared memory between arguments, many small groups.
 import pytest
 import torch
 
-from test_gpu_step import i32, norms_inputs, rn  # noqa: F401  (rn: a fixture)
+from test_gpu_attn import make_cache, rand
+from test_gpu_step import i32, norms_inputs, owns, prefix_state, rn  # noqa: F401  (rn: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +67,47 @@ def test_norms_rows_left_out_of_new_outputs_are_zeros(rn, eps, fp8, H, stream): 
         mine = torch.full((T,), 3.0, device="cuda")
         out, ro, scale = rn.fused_block_norms(x, r, pw, w, out_scale=mine, **kw)
         assert (mine[off] == 3).all() and not out[off].any() and not ro[off].any()
+
+
+# ---------------------------------------------------------------- shared prefix
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_prefix_follows_tables_scales_and_queries_written_just_before(rn, D):  # noqa: F811
+    # the shared part does not wait for the launch before it: what the stream wrote up to the call
+    # (table, scales, codes, queries, lengths) is read, never what lay there at the call before
+    groups, Hk, page = [(12, 640), (9, 320)], 2, 16
+    t, table, lengths, P, cu = prefix_state(groups, owns(groups, 1), Hk, page, D)
+    B, pages = lengths.shape[0], t["k"].shape[0]
+    states = []
+    for i in range(6):
+        order = torch.randperm(pages, generator=torch.Generator().manual_seed(i)).cuda()
+        back = torch.argsort(order)  # the same tokens in other pages, under other scales
+        moved = {n: v[order].contiguous() for n, v in t.items()}
+        moved["k_scale"] *= 0.5 + 0.1 * i
+        moved["v_scale"] *= 2.0 ** (i - 3)
+        states.append((rand((B, 8, D), i, torch.bfloat16).cuda(), moved, back[table.long()].to(torch.int32), lengths - i % 3))
+    live = [states[0][0].clone(), {n: v.clone() for n, v in t.items()}, table.clone(), lengths.clone()]
+    cache = make_cache(rn, live[1])
+
+    def one(state):
+        live[0].copy_(state[0])
+        for n, v in state[1].items():
+            live[1][n].copy_(v)
+        live[2].copy_(state[2])
+        live[3].copy_(state[3])
+        return rn.kv_cache_prefix_attention(live[0], cache, live[2], live[3], P, cu, pdl=True)
+
+    want = [rn.kv_cache_prefix_attention(q, make_cache(rn, c), tab, lens, P, cu) for q, c, tab, lens in states]
+    assert len({w.float().sum().item() for w in want}) == len(want)
+    one(states[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = [one(s) for s in states]
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        graph.replay()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert all(torch.equal(one(s), w) for s, w in zip(states, want))

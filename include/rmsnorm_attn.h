@@ -248,9 +248,11 @@ int64_t rmsattn_kv_prefix_attention_workspace(int64_t n_seqs, int64_t n_queries,
  *                            for a finished sequence, lengths[s] for one left out
  *   n_free_out [1]           free pages behind the step, F - taken
  * and in place block_table (the new entries alone) and free_pages (the returned
- * pages among its first n_free_out entries).  lengths and n_free are not changed
- * (the outputs may not be those arrays), so the same call gives the same results
- * again; a program goes on with `after` and n_free_out.
+ * pages among its first n_free_out entries).  lengths and n_free are not changed,
+ * so the same call gives the same results again; a program goes on with `after` and
+ * n_free_out.  What is written (results, workspace, free_pages, block_table) shares no
+ * byte with each other or with lengths, new_tokens, shared_pages and n_free: such a
+ * call is refused.
  *
  * free_pages holds n_pages entries, of which the first n_free (kept within
  * [0, n_pages]) count; page numbers outside [0, n_pages) and more returned pages

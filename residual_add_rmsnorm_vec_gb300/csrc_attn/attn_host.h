@@ -56,6 +56,23 @@ int launch(const void* fn, dim3 grid, int threads, size_t smem, void* args, bool
 // The cache's shape and pointers; fills the kernels' form of it.
 int check_cache(const rmsattn_cache* c, Cache* out);
 
+// Bytes that a call reads or writes: `rows` pieces of `bytes`, `stride` bytes apart.
+struct Bytes {
+    uintptr_t at;
+    uint64_t bytes, rows = 1, stride = 0;
+};
+inline Bytes bytes_of(const void* p, int64_t n, int64_t rows = 1, int64_t stride = 0) {
+    return {reinterpret_cast<uintptr_t>(p), (uint64_t)n, (uint64_t)rows, (uint64_t)stride};
+}
+// Whether a piece [p, p + n) meets one of r's.
+inline bool meets(uintptr_t p, uint64_t n, const Bytes& r) {
+    if (n == 0 || r.bytes == 0 || r.rows == 0 || p + n <= r.at) return false;
+    const uint64_t from = p > r.at ? p - r.at : 0;  // of the piece, from r's first byte on
+    const uint64_t row = r.stride ? from / r.stride : 0;
+    if (row < r.rows && from - row * r.stride < r.bytes) return true;
+    return row + 1 < r.rows && p + n - r.at > (row + 1) * r.stride;
+}
+
 // Block table of n_seqs rows.
 int check_table(const int32_t* table, int64_t stride, int64_t width, int64_t n_seqs, int page);
 

@@ -37,11 +37,25 @@ RMSATTN_API int rmsattn_pages_step(int32_t* free_pages, int64_t n_pages, const i
         if (!aligned(p, 4)) return RMSN_EALIGN;
     if (!aligned(positions, 16) || !aligned(slots, 16) || !aligned(rows, 16) || !aligned(workspace, 16))
         return RMSN_EALIGN;
-    if (n_free_out == n_free || (n_seqs && (before == lengths || after == lengths || before == new_tokens ||
-                                            after == new_tokens)))
-        return RMSN_EINVAL;
     const int64_t need = rmsattn_pages_workspace(n_seqs);
     if (need && (!workspace || workspace_bytes < need)) return RMSN_EINVAL;
+    // Blocks read the inputs while others write: what is written lies apart from all else.
+    const Bytes written[] = {bytes_of(cu_seqlens, (n_seqs + 1) * 4), bytes_of(positions, n_rows * 4),
+                             bytes_of(slots, n_rows * 8), bytes_of(rows, n_rows * 4),
+                             bytes_of(before, n_seqs * 4), bytes_of(after, n_seqs * 4),
+                             bytes_of(n_free_out, 4), bytes_of(workspace, need), bytes_of(free_pages, n_pages * 4)};
+    const Bytes read[] = {bytes_of(block_table, table_width * 4, n_seqs, table_stride * 4),
+                          bytes_of(n_free, 4), bytes_of(lengths, n_seqs * 4), bytes_of(new_tokens, n_seqs * 4),
+                          bytes_of(shared_pages, shared_pages ? n_seqs * 4 : 0)};
+    constexpr int kWritten = sizeof(written) / sizeof(written[0]);
+    for (int i = 0; i < kWritten; ++i) {
+        for (int k = 0; k < i; ++k)
+            if (meets(written[i].at, written[i].bytes, written[k])) return RMSN_EINVAL;
+        for (const Bytes& r : read)
+            if (meets(written[i].at, written[i].bytes, r)) return RMSN_EINVAL;
+    }
+    for (const Bytes& r : read)  // (the table is written, too)
+        if (&r != read && meets(r.at, r.bytes, read[0])) return RMSN_EINVAL;
     DeviceInfo* d = device_info();
     if (!d) return RMSN_ECUDA;
     PagesArgs a;

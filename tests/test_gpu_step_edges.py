@@ -111,3 +111,25 @@ def test_prefix_follows_tables_scales_and_queries_written_just_before(rn, D):  #
         graph.replay()
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
     assert all(torch.equal(one(s), w) for s, w in zip(states, want))
+
+
+# ---------------------------------------------------------------- pages
+
+
+def test_pages_of_lengths_between_the_tables_rows(rn):  # noqa: F811
+    # one buffer: three rows of two entries, five apart, and the lengths in the gap behind the first row
+    room = torch.zeros(16, dtype=torch.int32, device="cuda")
+    table, lengths = room[:15].view(3, 5)[:, :2], room[2:5]
+    table.fill_(-1)
+    lengths.copy_(i32([0, 0, 0]))
+    free, n_free = rn.kv_free_pages(6)
+    for page in (16, 48):
+        step = rn.kv_pages_step_(free, n_free, table, lengths, i32([20, -1, page]), page_size=page, n_rows=96)
+        assert step.after.tolist() == [20, 0, page] and lengths.tolist() == [0, 0, 0]
+    # ... but not in a row
+    with pytest.raises(rn.RmsnError):
+        rn.kv_pages_step_(free, n_free, table, room[1:4], i32([1, 1, 1]), page_size=16, n_rows=96)
+    with pytest.raises(rn.RmsnError):
+        rn.kv_pages_step_(free, n_free, table, free[:3], i32([1, 1, 1]), page_size=16, n_rows=96)
+    with pytest.raises(rn.RmsnError):
+        rn.kv_pages_step_(free, free[5:], table, lengths, i32([1, 1, 1]), page_size=16, n_rows=96)

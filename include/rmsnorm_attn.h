@@ -286,8 +286,8 @@ int64_t rmsattn_pages_workspace(int64_t n_seqs);
  *   x            [n_tokens, hidden] bf16 / fp16 / fp32, weights [hidden] of its type
  *                or NULL (1, without the offset)
  *   residual     [n_tokens, hidden] of x's type, or fp32 with RMSN_RESIDUAL_F32
- *                (bf16 / fp16 x); residual_out the same, may be residual itself
- *   out          of x's type (may be x itself, not residual_out), or bytes
+ *                (bf16 / fp16 x); residual_out the same
+ *   out          of x's type, or bytes
  *   gate         NULL (1); or rows of x's type gate_stride elements apart:
  *                gate_stride 0, n_gates 1: one row for all; n_gates == n_tokens: a
  *                row each; with gate_index [n_tokens], token t takes row
@@ -298,6 +298,10 @@ int64_t rmsattn_pages_workspace(int64_t n_seqs);
  *                was written to before).  An index >= n_gates is left out too, and sets
  *                bit 2 (value 4) of the status word.  Where n_tokens or n_gates is 0, the
  *                pointers of what is empty may be NULL.
+ *
+ * An output may be x, residual, or a gate row for each token (gate_stride ==
+ * hidden), where that has the output's type; any other memory that an output shares
+ * with an input or with another output is refused.
  *
  * Sums of squares are fp32: rows need sum(x^2), sum(h^2) < FLT_MAX.  Rows, gates
  * and weights are contiguous; 16-byte vectors are used where every operand's rows

@@ -139,7 +139,29 @@ RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const v
     if (!aligned(residual, (uintptr_t)rbytes) || !aligned(residual_out, (uintptr_t)rbytes) ||
         !aligned(out, fp8 ? 1 : (uintptr_t)bytes) || !aligned(out_scale, 4) || !aligned(gate_index, 4))
         return RMSN_EALIGN;
-    if (out == residual_out) return RMSN_EINVAL;
+    // A block reads its row before it writes it, so an output may lie on an input row for
+    // row; else a block would write what another one reads.
+    const int64_t row = hidden * (fp8 ? 1 : bytes), row_r = hidden * rbytes, row_x = hidden * bytes;
+    const Bytes outs[] = {bytes_of(out, n_tokens * row), bytes_of(residual_out, n_tokens * row_r),
+                          bytes_of(out_scale, fp8 ? n_tokens * 4 : 0)};
+    const int64_t out_rows[] = {row, row_r, 0};
+    const struct {
+        Bytes b;
+        int64_t row;  // bytes from row to row, 0: not a row for each token
+    } ins[] = {{bytes_of(x, n_tokens * row_x), row_x},
+               {bytes_of(residual, n_tokens * row_r), row_r},
+               {bytes_of(gate, gate ? row_x : 0, n_gates, gate_stride * bytes), gate_index ? 0 : gate_stride * bytes},
+               {bytes_of(post_weight, post_weight ? row_x : 0), 0},
+               {bytes_of(weight, weight ? row_x : 0), 0},
+               {bytes_of(gate_index, gate_index ? n_tokens * 4 : 0), 0}};
+    for (int i = 0; i < 3; ++i) {
+        for (int k = 0; k < i; ++k)
+            if (meets(outs[i].at, outs[i].bytes, outs[k])) return RMSN_EINVAL;
+        for (const auto& in : ins)
+            if ((in.b.at != outs[i].at || in.row == 0 || in.row != out_rows[i]) &&
+                meets(outs[i].at, outs[i].bytes, in.b))
+                return RMSN_EINVAL;
+    }
     DeviceInfo* d = device_info();
     if (!d) return RMSN_ECUDA;
     NormsArgs a;

@@ -133,3 +133,19 @@ def test_pages_of_lengths_between_the_tables_rows(rn):  # noqa: F811
         rn.kv_pages_step_(free, n_free, table, free[:3], i32([1, 1, 1]), page_size=16, n_rows=96)
     with pytest.raises(rn.RmsnError):
         rn.kv_pages_step_(free, free[5:], table, lengths, i32([1, 1, 1]), page_size=16, n_rows=96)
+
+
+@pytest.mark.parametrize("H", [256, 251, 20000])
+def test_norms_outputs_on_inputs_row_for_row(rn, H):  # noqa: F811
+    x, r, pw, w, g, _ = norms_inputs(9, H, "bf16", "same", "token", 0.0)
+    want = rn.fused_block_norms(x, r, pw, w, eps=1e-6, gate=g)[:2]
+    for out, ro in (("x", "r"), ("r", "x"), ("g", "r"), ("x", "g"), (None, "x"), ("r", None)):
+        t = dict(x=x.clone(), r=r.clone(), g=g.clone())
+        got = rn.fused_block_norms(t["x"], t["r"], pw, w, eps=1e-6, gate=t["g"], out=t.get(out), residual_out=t.get(ro))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # bytes of codes on x's rows are another row's
+    codes = x.view(torch.uint8).flatten()[:9 * H].view(9, H)
+    with pytest.raises(rn.RmsnError):
+        rn.fused_block_norms(x, r, pw, w, eps=1e-6, out_dtype="fp8", out=codes)
+    with pytest.raises(rn.RmsnError):
+        rn.fused_block_norms(x, r, pw, w, eps=1e-6, gate=g, gate_index=i32([0] * 9), out=g)

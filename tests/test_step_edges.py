@@ -87,3 +87,19 @@ def test_pages_workspace_apart(rn):  # noqa: F811
                after=0x600000, ws=0x700000, wsb=1 << 20)
     for name in ("free", "n_free", "lengths", "new", "cu", "pos", "slots", "rows", "before", "after", "out", "table"):
         assert pages(rn, **{**big, name: 0x700000})[0] == EINVAL
+
+
+@pytest.mark.parametrize("kw", [
+    dict(flags=BF16 | FP8, scale=0xF000, out=0x1000), dict(flags=BF16 | FP8, scale=0xF000, out=0x11C0),  # bytes on x's rows
+    dict(flags=BF16 | R32, out=0x2000), dict(flags=BF16 | R32, ro=0x1000),  # rows of other sizes
+    dict(out=0x1010), dict(ro=0x2010), dict(out=0x0FF0), dict(ro=0x1E10),   # rows shifted
+    dict(out=0x3000), dict(ro=0x4040), dict(out=0x4070),                    # weights
+    dict(gate=0x5000, n_gates=1, out=0x5000), dict(gate=0x5000, gs=72, n_gates=4, out=0x5000),
+    dict(gate=0x5000, gs=64, n_gates=4, ro=0x5080), dict(gate=0x5000, gs=64, n_gates=9, index=0x6000, out=0x5000),
+    dict(gate=0x5000, gs=64, n_gates=9, index=0x6000, ro=0x6000), dict(gate=0x5000, gs=64, n_gates=9, index=0x81F0),
+    dict(flags=BF16 | FP8, scale=0x1000), dict(flags=BF16 | FP8, scale=0x8000), dict(flags=BF16 | FP8, scale=0x91FC),
+    dict(out=0x9000), dict(out=0x9100),
+])
+def test_norms_that_share_memory_are_refused(rn, kw):  # noqa: F811
+    a = dict(T=4, x=0x1000, residual=0x2000, post=0x3000, w=0x4000, out=0x8000, ro=0x9000)
+    assert norms(rn, **{**a, **kw}) == EINVAL

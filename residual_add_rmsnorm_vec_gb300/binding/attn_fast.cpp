@@ -425,7 +425,7 @@ PyObject* pages_step(PyObject*, PyObject* const* a, Py_ssize_t count) {
         if (need > 0) ws = make({need}, at::kByte, index);
         auto to = [&](int i) { return static_cast<int32_t*>(out[i].mutable_data_ptr()); };
         const int st = rmsattn_pages_step(
-            const_cast<int32_t*>(words(a[0])), pages, words(a[1]),
+            static_cast<int32_t*>(free_pages->mutable_data_ptr()), pages, words(a[1]),
             static_cast<int32_t*>(table->mutable_data_ptr()), stride, table->size(1), words(a[3]), words(a[4]),
             words(a[5]), n, page, T, to(0), to(1), static_cast<int64_t*>(out[2].mutable_data_ptr()), to(3), to(4),
             to(5), to(6), need > 0 ? ws.mutable_data_ptr() : nullptr, need, a[8] == Py_True ? RMSN_PDL : 0u,

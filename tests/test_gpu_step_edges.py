@@ -149,3 +149,16 @@ def test_norms_outputs_on_inputs_row_for_row(rn, H):  # noqa: F811
         rn.fused_block_norms(x, r, pw, w, eps=1e-6, out_dtype="fp8", out=codes)
     with pytest.raises(rn.RmsnError):
         rn.fused_block_norms(x, r, pw, w, eps=1e-6, gate=g, gate_index=i32([0] * 9), out=g)
+
+
+@pytest.mark.parametrize("pdl", [False, 0])  # (a number: the way that is not marshalled natively)
+def test_pages_of_lazy_copies(rn, pdl):  # noqa: F811
+    # a copy that shares its memory until it is written to gets its own then
+    free, n_free = rn.kv_free_pages(8)
+    table, lengths = i32([[0, 1], [2, -1]]), i32([32, 5])
+    n_free.fill_(5)
+    copies = [torch._lazy_clone(t) for t in (free, table)]
+    step = rn.kv_pages_step_(copies[0], n_free, copies[1], lengths, i32([-1, 20]), page_size=16, n_rows=20, pdl=pdl)
+    assert free.tolist() == list(range(7, -1, -1)) and table.tolist() == [[0, 1], [2, -1]]
+    assert copies[1].tolist() == [[0, 1], [2, 1]] and copies[0].tolist() == [7, 6, 5, 4, 3, 0, 1, 0]
+    assert step.n_free.tolist() == [6]

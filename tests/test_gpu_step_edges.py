@@ -2,6 +2,7 @@
 sequences that are left out, shared memory between arguments, many small groups."""
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 from test_gpu_attn import make_cache, rand
 from test_gpu_step import i32, norms_inputs, owns, prefix_state, rn  # noqa: F401  (rn: a fixture)
@@ -162,3 +163,49 @@ def test_pages_of_lazy_copies(rn, pdl):  # noqa: F811
     assert free.tolist() == list(range(7, -1, -1)) and table.tolist() == [[0, 1], [2, -1]]
     assert copies[1].tolist() == [[0, 1], [2, 1]] and copies[0].tolist() == [7, 6, 5, 4, 3, 0, 1, 0]
     assert step.n_free.tolist() == [6]
+
+
+# ---------------------------------------------------------------- the native binding
+
+
+class Seen(TorchDispatchMode):
+    """What a mode sees being made."""
+
+    def __init__(self):
+        super().__init__()
+        self.made = []
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        out = func(*args, **(kwargs or {}))
+        if func is torch.ops.aten.empty.memory_format:
+            self.made.append((tuple(out.shape), out.dtype, out.data_ptr()))
+        return out
+
+
+@pytest.mark.parametrize("eps", [1e-6, 1])
+def test_dispatch_modes_see_the_results(rn, eps):  # noqa: F811
+    groups, Hk, page, D = [(4, 64)], 2, 16, 64
+    t, table, lengths, P, cu = prefix_state(groups, owns(groups, 1), Hk, page, D)
+    cache = make_cache(rn, t)
+    q, k = rand((4, 4, D), 1, torch.bfloat16).cuda(), rand((4, Hk, D), 2, torch.bfloat16).cuda()
+    x, r, pw, w, _, _ = norms_inputs(3, 64, "bf16", "f32", "none", 0.0)
+    free, n_free = rn.kv_free_pages(8)
+    rope = rn.rope_table(D)
+    positions = i32([0, 1, 2, 3])
+    scale = None if eps != 1 else 1
+    calls = [
+        lambda: rn.qk_norm_rope(q, k, positions, rope, head_dim=D, eps=eps),
+        lambda: [rn.kv_cache_attention(q, cache, table, lengths, scale=scale)],
+        lambda: [rn.kv_cache_prefix_attention(q, cache, table, lengths, P, cu, scale=scale)],
+        lambda: rn.fused_block_norms(x, r, pw, w, eps=eps, out_dtype="fp8"),
+        lambda: rn.kv_pages_step_(free, n_free, i32([[-1, -1]]), i32([0]), i32([3]), page_size=16, n_rows=4),
+    ]
+    for call in calls:
+        with Seen() as seen:
+            made = call()
+        for m in made:
+            assert (tuple(m.shape), m.dtype, m.data_ptr()) in seen.made
+        free, n_free = rn.kv_free_pages(8)
+        for a, b in zip(made, call()):
+            assert torch.equal(a, b)
+        free, n_free = rn.kv_free_pages(8)

@@ -215,7 +215,9 @@ int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* cache, const
                                 int64_t workspace_bytes, uint32_t flags, cudaStream_t stream);
 
 /* Bytes of workspace for these sizes on the current device (>= 0), or a negative
- * rmsn_status.  max_tokens: table_width * page_size. */
+ * rmsn_status.  max_tokens: table_width * page_size.  It grows with the rows
+ * n_seqs * n_queries * n_q_heads, by about 8 * head_dim + 16 bytes each, and with the
+ * groups by up to 28 * n_kv_heads * (head_dim + 2) bytes each, over some 5 to 25 MB. */
 int64_t rmsattn_kv_prefix_attention_workspace(int64_t n_seqs, int64_t n_queries, int64_t n_q_heads,
                                               int64_t n_kv_heads, int64_t head_dim, int64_t max_tokens,
                                               int64_t n_groups);

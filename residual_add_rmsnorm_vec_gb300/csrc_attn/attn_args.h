@@ -100,12 +100,13 @@ const void* norms_kernel_of(int dt, bool r32, bool fp8, bool ragged, int ch);
 
 // A group of sequences [s0, s1) that share their first `shared` tokens: `tiles`
 // tiles of `rows` columns (sequence x query token x head) for each key head,
-// an item each, from item0 on; an item is ns steps, the group's items lie
-// one behind the other on the line of all steps from `first` on.
+// an item each; an item is ns steps, the group's items lie one behind the other
+// on the line of all steps from `first` on.  Their parts' rows, in eights and for
+// all key heads, are counted from row0 on.
 struct __align__(16) PrefixGroup {
     int32_t s0, s1, shared;
     int32_t seq;  // the sequence whose table row names the shared pages
-    int32_t ns, first, item0, tiles;
+    int32_t ns, first, row0, tiles;
 };
 // The line of the shared parts: total steps, and the steps of a share.
 struct __align__(16) PrefixLine {
@@ -138,8 +139,17 @@ struct PrefixArgs {
     PrefixSeq* seqs;
     float* parts;  // one for each pair of a share and an item that it meets
 };
-// Floats of a part: sums [D / 8][rows][8], then reference and weight of each row.
-__host__ __device__ constexpr int64_t prefix_part(int D, int rows) { return (int64_t)rows * (D + 2); }
+// A part's rows stand in eights: their sums [D / 8][8][8], then reference and weight of each,
+// 8 (D + 2) floats.  A group has its columns' eights for each key head, most / 8 in each of its
+// tiles but the last, so that small groups take no whole tiles.  Share s's part of an item whose
+// rows begin at eight e begins at eight s most / 8 + e: behind the share's part of the item
+// before, and behind the earlier share's part of the same item.  (Columns are counted in 31
+// bits, and so are the eights.)
+__host__ __device__ constexpr uint32_t prefix_eights(uint32_t columns) { return (columns + 7) / 8; }
+// First eight of an item.
+__host__ __device__ constexpr uint32_t prefix_eight(const PrefixGroup& g, int per_seq, int hk, int tile, int most) {
+    return g.row0 + hk * prefix_eights((uint32_t)(g.s1 - g.s0) * per_seq) + tile * (most / 8);
+}
 
 // One compiled kernel: R tiles of 128 rows.
 struct PrefixEntry {

@@ -248,7 +248,7 @@ __device__ __forceinline__ bool wait_alone(const uint64_t* bar, int phase, uint3
 
 // A block's piece of an item: `steps` of its steps from `step0` on.
 struct Piece {
-    int hk, tile, step0, steps, item;  // item: counted over all groups
+    int hk, tile, step0, steps;
     PrefixGroup g;
 };
 
@@ -285,7 +285,6 @@ struct Walk {
         p->steps = stop - at < left ? stop - at : left;
         p->hk = item / p->g.tiles;
         p->tile = item - p->hk * p->g.tiles;
-        p->item = p->g.item0 + item;
         at += p->steps;
         return true;
     }
@@ -651,7 +650,9 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
         q_scale = q_next;
         valid = valid_next;
         const bool busy = wp * 32 < valid;  // the warp has rows
-        float* part = a.parts + ((int64_t)blockIdx.x + way->p.item) * (ROWS * (int64_t)(D + 2)) + (x * 128 + r) * 8;
+        const uint32_t eight = blockIdx.x * (ROWS / 8) + x * 16 + (r >> 3) +
+                               prefix_eight(way->p.g, a.n * a.group, way->p.hk, way->p.tile, ROWS);
+        float* part = a.parts + (int64_t)eight * (8 * (D + 2)) + (r & 7) * 8;
         float ref = kNone, l = 0.f;
         float part_ref = 0.f;
         bool has_part = false;
@@ -669,7 +670,7 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
                 if (r < valid) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) {  // 32 bytes: a whole sector
-                        float* y = part + (d / 8 + i / 8) * (ROWS * 8);
+                        float* y = part + (d / 8 + i / 8) * 64;
                         uint32_t u[8];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
@@ -817,8 +818,7 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
             if (busy) {
                 drain();
                 if (r < valid)
-                    *reinterpret_cast<float2*>(part - (x * 128 + r) * 8 + ROWS * D + (x * 128 + r) * 2) =
-                        make_float2(ref, l);
+                    *reinterpret_cast<float2*>(part + D * 8 - (r & 7) * 6) = make_float2(ref, l);
             }
         }
     }

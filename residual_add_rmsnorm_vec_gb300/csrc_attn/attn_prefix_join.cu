@@ -30,9 +30,10 @@ __device__ __forceinline__ void add(float4& y, const float4& v, float f) {
     y.w += v.w * f;
 }
 
-// kWays threads to a row's parts.
+// kWays threads to a row's parts.  Four blocks of four ways to an SM, for 64 sequences x 8192
+// then join in one wave (512 blocks; at 70 registers, three to an SM, 55.8 us and not 52.8).
 template <class T, int kWays>
-__global__ void __launch_bounds__(256) prefix_join(const PrefixJoinArgs a) {
+__global__ void __launch_bounds__(256, kWays == 4 ? 4 : 3) prefix_join(const PrefixJoinArgs a) {
     constexpr int kCols = 256 / kWays;
     __shared__ float4 sum[kWays][2][kCols];
     __shared__ float2 ref[kWays][kCols];
@@ -66,9 +67,10 @@ __global__ void __launch_bounds__(256) prefix_join(const PrefixJoinArgs a) {
         const int tile = cc / a.item_rows, r = cc - tile * a.item_rows, item = hk * g.tiles + tile;
         const uint32_t at = (uint32_t)g.first + (uint32_t)item * (uint32_t)g.ns;
         const int first = (int)(at / chunk), n = (int)((at + (uint32_t)g.ns - 1) / chunk) - first + 1;
-        const int64_t size = prefix_part(a.D, a.item_rows);
-        const float* p = a.parts + (first + g.item0 + item) * size;
-        const int at_y = d * a.item_rows + r * 8, at_ml = a.D * a.item_rows + r * 2;
+        const uint32_t eight = first * (a.item_rows / 8) + (r >> 3) + prefix_eight(g, a.n * a.group, hk, tile, a.item_rows);
+        const int size = a.item_rows * (a.D + 2);  // from a share's part to the next one's
+        const float* p = a.parts + (int64_t)eight * (8 * (a.D + 2)) + d * 8 + (r & 7) * 8;
+        const int to_ml = (a.D - d) * 8 - (r & 7) * 6;
         constexpr int U = 8;
         for (int k0 = way; k0 < n; k0 += U * kWays) {
             float2 ml[U];
@@ -76,9 +78,9 @@ __global__ void __launch_bounds__(256) prefix_join(const PrefixJoinArgs a) {
 #pragma unroll
             for (int k = 0; k < U; ++k) {  // (past the last: the last again, not added)
                 const float* q = p + (k0 + k * kWays < n ? k0 + k * kWays : n - 1) * size;
-                ml[k] = *reinterpret_cast<const float2*>(q + at_ml);
-                v[k][0] = *reinterpret_cast<const float4*>(q + at_y);
-                v[k][1] = *reinterpret_cast<const float4*>(q + at_y + 4);
+                ml[k] = *reinterpret_cast<const float2*>(q + to_ml);
+                v[k][0] = *reinterpret_cast<const float4*>(q);
+                v[k][1] = *reinterpret_cast<const float4*>(q + 4);
             }
             float to = m;
 #pragma unroll

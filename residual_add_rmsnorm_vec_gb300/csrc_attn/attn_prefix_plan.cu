@@ -14,7 +14,7 @@ constexpr int kThreads = 512;
 
 __global__ void __launch_bounds__(kThreads) prefix_plan(const PrefixArgs a) {
     __shared__ int64_t sums[2][kThreads / 32];
-    __shared__ int2 sizes[kThreads];  // tiles and steps of the first groups
+    __shared__ int4 sizes[kThreads];  // tiles, steps and sequences of the first groups
     rmsn::pdl_wait(a.pdl);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
@@ -74,47 +74,49 @@ __global__ void __launch_bounds__(kThreads) prefix_plan(const PrefixArgs a) {
         __syncwarp();
         if (lane == 0) {
             a.groups[g] = G;
-            if (g < kThreads) sizes[g] = make_int2(G.tiles, G.ns);
+            if (g < kThreads) sizes[g] = make_int4(G.tiles, G.ns, G.s0, G.s1);
         }
     }
     __syncthreads();
-    // the groups' places on the line, and of their items
-    int64_t steps = 0, items = 0;
+    // the groups' places on the line, and those of their parts' rows, in eights
+    int64_t steps = 0, rows = 0;
     for (int g0 = 0; g0 < a.n_groups; g0 += kThreads) {
         const int g = g0 + threadIdx.x;
-        int64_t it = 0, st = 0;
+        int64_t ro = 0, st = 0;
         if (g < a.n_groups) {
-            const int2 n = g < kThreads ? sizes[g] : make_int2(a.groups[g].tiles, a.groups[g].ns);
-            it = (int64_t)n.x * a.c.H;
-            st = it * n.y;
+            int4 n;
+            if (g < kThreads) n = sizes[g];
+            else n = make_int4(a.groups[g].tiles, a.groups[g].ns, a.groups[g].s0, a.groups[g].s1);
+            if (n.x > 0) ro = (int64_t)prefix_eights((uint32_t)(n.w - n.z) * a.n * a.group) * a.c.H;
+            st = (int64_t)n.x * a.c.H * n.y;
         }
-        int64_t i1 = it, s1 = st;
+        int64_t r1 = ro, s1 = st;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, i1, o), v = __shfl_up_sync(0xFFFFFFFFu, s1, o);
+            const int64_t u = __shfl_up_sync(0xFFFFFFFFu, r1, o), v = __shfl_up_sync(0xFFFFFFFFu, s1, o);
             if (lane >= o) {
-                i1 += u;
+                r1 += u;
                 s1 += v;
             }
         }
         if (lane == 31) {
-            sums[0][wp] = i1;
+            sums[0][wp] = r1;
             sums[1][wp] = s1;
         }
         __syncthreads();
-        int64_t i0 = items + i1 - it, s0 = steps + s1 - st;
+        int64_t r0 = rows + r1 - ro, s0 = steps + s1 - st;
         for (int w = 0; w < kThreads / 32; ++w) {
             if (w < wp) {
-                i0 += sums[0][w];
+                r0 += sums[0][w];
                 s0 += sums[1][w];
             }
-            items += sums[0][w];
+            rows += sums[0][w];
             steps += sums[1][w];
         }
         __syncthreads();
         if (g < a.n_groups) {
             a.groups[g].first = (int32_t)s0;
-            a.groups[g].item0 = (int32_t)i0;
+            a.groups[g].row0 = (int32_t)r0;
         }
     }
     if (threadIdx.x == 0) {

@@ -253,13 +253,15 @@ int plan_prefix(DeviceInfo* d, int dt, int64_t n_seqs, int64_t n_queries, int64_
     const int64_t items = times(tiles, n_kv_heads);
     if (times(items, (max_tokens + p->e->tok - 1) / p->e->tok) + p->shares >= (int64_t(1) << 31))
         return RMSN_EUNSUPPORTED;  // steps are counted in 31 bits
+    const int64_t part_rows = times(cols + 7 * some, n_kv_heads);
+    if (part_rows / 8 >= (int64_t(1) << 31)) return RMSN_EUNSUPPORTED;  // and eights of rows
     const int st = plan_attend(d, true, dt, n_seqs, n_queries, n_q_heads, n_kv_heads, head_dim, max_tokens,
                                0, 0, &p->behind);
     if (st != RMSN_OK) return st;
     p->groups = round_up(sizeof(PrefixLine));
     p->seqs = p->groups + round_up((n_groups + 1) * (int64_t)sizeof(PrefixGroup));
     p->parts = p->seqs + round_up(n_seqs * (int64_t)sizeof(PrefixSeq));
-    p->own = p->parts + times(p->shares + items, prefix_part((int)head_dim, rows) * 4);
+    p->own = p->parts + round_up(times(p->shares * rows + part_rows, (head_dim + 2) * 4));
     const int64_t out_rows = n_seqs * n_queries * n_q_heads;
     p->own_ml = p->own + times(out_rows, head_dim * 4);
     p->behind_ws = p->own_ml + round_up(out_rows * 8);

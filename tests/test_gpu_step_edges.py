@@ -1,11 +1,14 @@
 """GPU tests of the serving step's operators at their edges: empty batches, rows and
 sequences that are left out, shared memory between arguments, many small groups."""
+import math
+
 import pytest
 import torch
 from torch.utils._python_dispatch import TorchDispatchMode
 
-from test_gpu_attn import make_cache, rand
-from test_gpu_step import i32, norms_inputs, owns, prefix_state, rn  # noqa: F401  (rn: a fixture)
+import attn_ref as ref
+from test_gpu_attn import DT, make_cache, rand, within
+from test_gpu_step import i32, norms_inputs, owns, prefix_state, rn, run_prefix  # noqa: F401  (rn: a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -209,3 +212,27 @@ def test_dispatch_modes_see_the_results(rn, eps):  # noqa: F811
         for a, b in zip(made, call()):
             assert torch.equal(a, b)
         free, n_free = rn.kv_free_pages(8)
+
+
+def test_prefix_workspace_goes_by_rows_not_by_groups(rn):  # noqa: F811
+    size = rn.load_attn().rmsattn_kv_prefix_attention_workspace
+    for B, n, Hq, Hk, D in ((4096, 1, 32, 8, 128), (4096, 1, 16, 2, 256), (3000, 2, 64, 8, 64)):
+        one, pairs = size(B, n, Hq, Hk, D, 4096, 1), size(B, n, Hq, Hk, D, 4096, B // 2)
+        rows = B * n * Hq
+        assert one < rows * (8 * D + 16) + 2 ** 28
+        # a group more: 32 bytes, and what fills its rows up to eights for each key head
+        assert pairs < one + B // 2 * (32 + 7 * Hk * (D + 2) * 4) + 2 ** 20
+
+
+@pytest.mark.parametrize("groups,n,Hq,Hk,D,page,dtype", [
+    ([(2, 32)] * 90 + [(3, 64)] * 5 + [(1, 48)] * 3, 1, 32, 8, 128, 16, "bf16"),
+    ([(65, 256), (2, 48), (33, 128), (7, 64), (129, 32), (2, 16)], 1, 16, 4, 128, 16, "f16"),
+    ([(70, 512), (3, 64), (64, 192), (2, 48)], 1, 32, 8, 64, 16, "bf16"), ([(21, 512), (3, 64), (2, 48)] * 3, 3, 12, 4, 64, 16, "f16"),
+    ([(2, 64), (40, 320), (2, 32), (17, 320)], 1, 14, 2, 256, 16, "bf16"), ([(2, 3200)] * 4, 1, 5, 1, 128, 32, "bf16"),
+    ([(600, 64), (2, 32)], 1, 9, 3, 64, 32, "bf16"), ([(300, 16)], 2, 7, 1, 128, 16, "bf16"),
+])
+def test_prefix_groups_of_any_size_side_by_side(rn, groups, n, Hq, Hk, D, page, dtype):  # noqa: F811
+    t, table, lengths, P, cu = prefix_state(groups, owns(groups, n, most=40), Hk, page, D, n=n)
+    q = rand((lengths.shape[0], n, Hq, D), 3, DT[dtype]).cuda()
+    want, bound = ref.attend(q, t, table, lengths, 1 / math.sqrt(D), 0, 0)
+    within(run_prefix(rn, q, t, table, lengths, P, cu, n), want, bound)

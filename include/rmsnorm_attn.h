@@ -330,6 +330,15 @@ int rmsattn_block_norms(const void* x, const void* residual, const void* post_we
  * streams made non-blocking (PyTorch's own) first.  `clear` != 0 resets the word. */
 int rmsattn_read_status(uint32_t* status, int clear);
 
+/* Testing hook for the bounded waits inside rmsattn_kv_prefix_attention (not needed in
+ * normal use).  Sets, for calls that follow on the current device, after how many SM
+ * clock cycles a wait gives up: its block then stops, waits for what it has in flight
+ * (with the default bound), and bit 0 of the status word is set; the call's result is not
+ * to be used.  0 restores the default (about one second); a negative value makes a wait
+ * give up as soon as its barrier has been tried, so that the give-up path runs on a
+ * healthy GPU. */
+int rmsattn_set_wait_limit(int64_t cycles);
+
 #ifdef __cplusplus
 }
 #endif

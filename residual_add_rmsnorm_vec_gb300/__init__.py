@@ -34,7 +34,7 @@ from .api import (block_format_configs, check_row_args, fused_add_rmsnorm, fused
 from ._attn_lib import (  # noqa: F401
     EXPORTED_ATTN, RMSATTN_BAD_PAGE, RMSATTN_BLOCK, RMSATTN_INTERLEAVED, RMSATTN_MAX_QUERIES,
     RMSATTN_NORM, RMSATTN_OUT_FP8, RMSATTN_POS_I64, RMSATTN_WAIT_RAN_OUT, attn_library_path, load_attn, load_fast as load_attn_binding,
-    rmsattn_read_status)
+    rmsattn_read_status, rmsattn_set_wait_limit)
 from .attn import (KVCache, RopeTable, kv_cache_append_, kv_cache_attention, qk_norm_rope,  # noqa: F401
                    rope_table)
 from .step import (KVStep, fused_block_norms, kv_cache_prefix_attention, kv_free_pages,  # noqa: F401

@@ -24,7 +24,7 @@ RMSATTN_WAIT_RAN_OUT = 1
 EXPORTED_ATTN = ("rmsattn_qk_rope_fwd", "rmsattn_kv_append", "rmsattn_kv_attention",
                  "rmsattn_kv_attention_workspace", "rmsattn_read_status", "rmsattn_kv_prefix_attention",
                  "rmsattn_kv_prefix_attention_workspace", "rmsattn_pages_step", "rmsattn_pages_workspace",
-                 "rmsattn_block_norms")
+                 "rmsattn_block_norms", "rmsattn_set_wait_limit")
 
 
 class RmsattnCache(ctypes.Structure):
@@ -80,6 +80,8 @@ def load_attn() -> ctypes.CDLL:
             lib.rmsattn_block_norms.restype = ctypes.c_int
             lib.rmsattn_block_norms.argtypes = [vp, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, i64, i64,
                                                 f32, f32, f32, u32, vp]
+            lib.rmsattn_set_wait_limit.restype = ctypes.c_int
+            lib.rmsattn_set_wait_limit.argtypes = [i64]
             lib.rmsattn_read_status.restype = ctypes.c_int
             lib.rmsattn_read_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
             _loaded = lib
@@ -114,3 +116,10 @@ def rmsattn_read_status(clear: bool = False) -> int:
     if st != _lib.RMSN_OK:
         raise _lib.RmsnError(st, "rmsattn_read_status")
     return int(v.value)
+
+
+def rmsattn_set_wait_limit(cycles: int) -> int:
+    """Testing hook: the bound of the waits inside ``kv_cache_prefix_attention``'s
+    kernel on the current device (0 = the default; negative = give up once
+    a barrier has been tried)."""
+    return int(load_attn().rmsattn_set_wait_limit(int(cycles)))

@@ -494,3 +494,10 @@ RMSATTN_API int rmsattn_read_status(uint32_t* status, int clear) {
         return RMSN_ECUDA;
     return RMSN_OK;
 }
+
+RMSATTN_API int rmsattn_set_wait_limit(int64_t cycles) {
+    DeviceInfo* d = device_info();
+    if (!d) return RMSN_ECUDA;
+    d->wait_cycles.store(cycles == 0 ? kWaitCycles : cycles, std::memory_order_relaxed);
+    return RMSN_OK;
+}

@@ -10,6 +10,7 @@ namespace rmsattn {
 constexpr int kBlock = 16;          // tokens that share a cache scale
 constexpr uint32_t kBadPage = 4u;   // status bit: a page or token outside the cache
 constexpr uint32_t kWaitRanOut = 1u;  // status bit: a kernel gave up a wait
+constexpr long long kWaitCycles = 2000000000LL;  // before it does: about a second
 
 // q / k: first element of token 0's first head; strides in elements.
 struct RopeArgs {
@@ -133,6 +134,7 @@ struct PrefixArgs {
     int32_t pdl;
     float scale;
     uint64_t page_rcp;  // ceil(2^37 / (page / 16))
+    long long wait_cycles;  // of each wait inside a block, at most
     uint32_t* status;
     PrefixLine* line;
     PrefixGroup* groups;

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "../../include/rmsnorm_attn.h"
@@ -22,6 +23,7 @@ struct DeviceInfo {
     int num_sms = 0;
     uint32_t* status = nullptr;
     cudaError_t err = cudaSuccess;
+    std::atomic<int64_t> wait_cycles{kWaitCycles};  // (tests may lower it)
     std::mutex mu;
     struct {
         const void* fn;

@@ -44,8 +44,9 @@
 //   the product before.  Weights are lifted by kLift: a lifted weight times a significand
 //   stays below 2^15 + 2^12, and fp16's subnormals end 2^-34 below the reference.
 // * Parts go to the workspace in the order of the line: nothing depends on timing.
-// * Every wait gives up after a second: the block then stops, waits for its products
-//   and copies in flight, gives TMEM back, and bit 0 of the status word is set.
+// * Every wait gives up after a second (or the limit that a test sets): the block then
+//   stops, waits for its products and copies in flight, gives TMEM back, and bit 0 of the
+//   status word is set.
 // * Code is kept small (loops over a tile's pieces are rolled): most calls run a few
 //   steps a block, and each instruction that runs once is fetched from L2 first.
 #pragma once
@@ -63,7 +64,6 @@ constexpr float kSlack = 5.f;
 constexpr int kLiftLog = 9;
 constexpr float kLift = 512.f;
 constexpr float kWide = 4194304.f;  // 2^22: up to it, a product's rounding error is 2^-3 at most
-constexpr long long kWaitCycles = 2000000000LL;
 
 // flags of a step
 constexpr uint32_t kFirst = 1u, kLast = 2u, kFlush = 4u, kEnd = 8u, kTwo = 16u;
@@ -215,15 +215,15 @@ struct Bars {
     uint32_t tmem, stop;
 };
 
-// All of a warp's lanes wait together, for a second at most; false: the block stops.
-__device__ __forceinline__ bool wait(const uint64_t* bar, int phase, uint32_t* stop) {
+// All of a warp's lanes wait together, for `limit` cycles at most; false: the block stops.
+__device__ __forceinline__ bool wait(const uint64_t* bar, int phase, uint32_t* stop, long long limit) {
     const uint32_t b = smem_of(bar);
     bool ok = rmsn::mbar_try_wait(b, phase & 1);
     if (!__all_sync(0xFFFFFFFFu, ok)) {
         const long long t0 = clock64();
         while (!__all_sync(0xFFFFFFFFu, ok)) {
             if (!ok) ok = rmsn::mbar_try_wait(b, phase & 1);
-            const bool out = *reinterpret_cast<volatile uint32_t*>(stop) != 0 || clock64() - t0 > kWaitCycles;
+            const bool out = *reinterpret_cast<volatile uint32_t*>(stop) != 0 || clock64() - t0 > limit;
             if (__any_sync(0xFFFFFFFFu, out && !ok)) {
                 *reinterpret_cast<volatile uint32_t*>(stop) = 1;
                 return false;
@@ -233,12 +233,12 @@ __device__ __forceinline__ bool wait(const uint64_t* bar, int phase, uint32_t* s
     return true;
 }
 // The same for one thread.
-__device__ __forceinline__ bool wait_alone(const uint64_t* bar, int phase, uint32_t* stop) {
+__device__ __forceinline__ bool wait_alone(const uint64_t* bar, int phase, uint32_t* stop, long long limit) {
     const uint32_t b = smem_of(bar);
     if (rmsn::mbar_try_wait(b, phase & 1)) return true;
     const long long t0 = clock64();
     while (!rmsn::mbar_try_wait(b, phase & 1)) {
-        if (*reinterpret_cast<volatile uint32_t*>(stop) != 0 || clock64() - t0 > kWaitCycles) {
+        if (*reinterpret_cast<volatile uint32_t*>(stop) != 0 || clock64() - t0 > limit) {
             *reinterpret_cast<volatile uint32_t*>(stop) = 1;
             return false;
         }
@@ -374,7 +374,7 @@ __device__ __forceinline__ void plan(const PrefixArgs& a, Bars* bars, Step* step
                     if (rem == 0 && last) flags |= kLast;
                     begin = false;
                     Step* w = steps + n % C::M;
-                    if (n >= C::M && !wait(&bars->step_free[n % C::M], n / C::M - 1, &bars->stop)) return;
+                    if (n >= C::M && !wait(&bars->step_free[n % C::M], n / C::M - 1, &bars->stop, a.wait_cycles)) return;
                     if (lane >> 2 == i) {
                         const int b = lane & 3, k7 = 7 + e - E;
                         const bool on = mask >> lane & 1;
@@ -397,7 +397,7 @@ __device__ __forceinline__ void plan(const PrefixArgs& a, Bars* bars, Step* step
         }
     }
     // one more step's word: there are none left
-    if (n >= C::M && !wait(&bars->step_free[n % C::M], n / C::M - 1, &bars->stop)) return;
+    if (n >= C::M && !wait(&bars->step_free[n % C::M], n / C::M - 1, &bars->stop, a.wait_cycles)) return;
     if (lane == 0) {
         steps[n % C::M].flags = kEnd;
         arrive(smem_of(&bars->step[n % C::M]));
@@ -425,7 +425,7 @@ __device__ __forceinline__ void widen(const PrefixArgs& a, unsigned char* stages
     int fetched = 0;
     auto fetch = [&]() {  // the next step's codes into its slot
         if (more) {
-            if (!(ok = wait(&bars->step[fetched % C::M], fetched / C::M, &bars->stop))) return;
+            if (!(ok = wait(&bars->step[fetched % C::M], fetched / C::M, &bars->stop, a.wait_cycles))) return;
             const Step* w = steps + fetched % C::M;
             more = !(w->flags & kEnd);
             if (more) {
@@ -451,7 +451,7 @@ __device__ __forceinline__ void widen(const PrefixArgs& a, unsigned char* stages
         const int st = n & 1;
         asm volatile("cp.async.wait_group %0;" ::"n"(N - 1) : "memory");
         // K's stage is free behind the scores of step n - 2, V's behind its sums
-        if (n >= 2 && !(ok = wait(V ? &bars->pv[st] : &bars->s_full[C::R - 1][st], n / 2 - 1, &bars->stop))) break;
+        if (n >= 2 && !(ok = wait(V ? &bars->pv[st] : &bars->s_full[C::R - 1][st], n / 2 - 1, &bars->stop, a.wait_cycles))) break;
         const uint32_t dst = stages_s + st * C::kTile, src = raw_s + n % N * kSlot;
 #pragma unroll
         for (int i = 0; i < C::ITERS; ++i) {
@@ -513,7 +513,7 @@ __device__ __forceinline__ void product_qk(uint32_t q_op, uint32_t k_op, int st)
                k_op + (((k / 4) * (C::TOK * 128) + (k % 4) * 32) >> 4), product(C::TOK, false), k);
 }
 
-// Nothing of the thread's is in flight when it leaves.
+// Nothing of the thread's is in flight when it leaves (the default limit, whatever the call's is).
 __device__ __forceinline__ void settle(uint64_t* bar) {
     commit(smem_of(bar));
     const long long t0 = clock64();
@@ -522,22 +522,22 @@ __device__ __forceinline__ void settle(uint64_t* bar) {
 }
 
 template <class C>
-__device__ __forceinline__ void scores(unsigned char* smem, Bars* bars, const Step* steps) {
+__device__ __forceinline__ void scores(const PrefixArgs& a, unsigned char* smem, Bars* bars, const Step* steps) {
     uint32_t q_op = operand(smem_of(smem), 16), k_op = operand(smem_of(smem) + C::R * C::kQ, 16);
     uint32_t* stop = &bars->stop;
     int turn[2] = {0, 0};
     for (int n = 0;; ++n) {
         const int st = n & 1;
         asm volatile("" : "+r"(q_op), "+r"(k_op));
-        if (!wait_alone(&bars->step[n % C::M], n / C::M, stop)) break;
+        if (!wait_alone(&bars->step[n % C::M], n / C::M, stop, a.wait_cycles)) break;
         const uint32_t flags = steps[n % C::M].flags;
         if (flags & kEnd) break;
         // the scores' place is free behind the sums of step n - 2
-        if (n >= 2 && !wait_alone(&bars->pv[st], n / 2 - 1, stop)) break;
-        if (!wait_alone(&bars->k_full[st], n >> 1, stop)) break;
+        if (n >= 2 && !wait_alone(&bars->pv[st], n / 2 - 1, stop, a.wait_cycles)) break;
+        if (!wait_alone(&bars->k_full[st], n >> 1, stop, a.wait_cycles)) break;
         if (flags & kFirst) {
-            if (!wait_alone(&bars->q_full[0], turn[0]++, stop)) break;
-            if (C::R == 2 && (flags & kTwo) && !wait_alone(&bars->q_full[1], turn[1]++, stop)) break;
+            if (!wait_alone(&bars->q_full[0], turn[0]++, stop, a.wait_cycles)) break;
+            if (C::R == 2 && (flags & kTwo) && !wait_alone(&bars->q_full[1], turn[1]++, stop, a.wait_cycles)) break;
         }
         tc_after();
         product_qk<C, 0>(q_op, k_op, st);
@@ -551,23 +551,23 @@ __device__ __forceinline__ void scores(unsigned char* smem, Bars* bars, const St
 }
 
 template <class C>
-__device__ __forceinline__ void sums(unsigned char* smem, Bars* bars, const Step* steps) {
+__device__ __forceinline__ void sums(const PrefixArgs& a, unsigned char* smem, Bars* bars, const Step* steps) {
     uint32_t v_op = operand(smem_of(smem) + C::R * C::kQ + 2 * C::kTile, C::TOK * 128);
     uint32_t* stop = &bars->stop;
     for (int n = 0;; ++n) {
         const int st = n & 1;
         asm volatile("" : "+r"(v_op));
-        if (!wait_alone(&bars->step[n % C::M], n / C::M, stop)) break;
+        if (!wait_alone(&bars->step[n % C::M], n / C::M, stop, a.wait_cycles)) break;
         const uint32_t flags = steps[n % C::M].flags;
         if (flags & kEnd) break;
         arrive(smem_of(&bars->step_free[n % C::M]));
         const bool fresh = flags & (kFirst | kFlush);
-        if (!wait_alone(&bars->v_full[st], n >> 1, stop) || !wait_alone(&bars->p_full[0][st], n >> 1, stop)) break;
+        if (!wait_alone(&bars->v_full[st], n >> 1, stop, a.wait_cycles) || !wait_alone(&bars->p_full[0][st], n >> 1, stop, a.wait_cycles)) break;
         tc_after();
         if (fresh) product_pv<C, 0, true>(v_op, st);
         else product_pv<C, 0, false>(v_op, st);
         if constexpr (C::R == 2) {
-            if (!wait_alone(&bars->p_full[1][st], n >> 1, stop)) break;
+            if (!wait_alone(&bars->p_full[1][st], n >> 1, stop, a.wait_cycles)) break;
             tc_after();
             if (flags & kTwo) {
                 if (fresh) product_pv<C, 1, true>(v_op, st);
@@ -701,14 +701,14 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
             do {
                 const Step* w = steps + n % C::M;
                 const uint32_t s_at = lanes + (2 * x + (n & 1)) * 64;
-                if (!wait(&bars->step[n % C::M], n / C::M, &bars->stop)) return;
-                if (!wait(&bars->s_full[x][n & 1], n >> 1, &bars->stop)) return;
+                if (!wait(&bars->step[n % C::M], n / C::M, &bars->stop, a.wait_cycles)) return;
+                if (!wait(&bars->s_full[x][n & 1], n >> 1, &bars->stop, a.wait_cycles)) return;
                 tc_after();
                 flags = w->flags;
                 if (busy) {
                     const uint32_t mask = w->mask;
                     if (flags & kFlush) {
-                        if (!wait(&bars->pv[(n - 1) & 1], (n - 1) >> 1, &bars->stop)) return;
+                        if (!wait(&bars->pv[(n - 1) & 1], (n - 1) >> 1, &bars->stop, a.wait_cycles)) return;
                         tc_after();
                         drain();
                     }
@@ -737,7 +737,7 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
                         ref = to;
                         l *= keep;
                         if (!(flags & (kFirst | kFlush))) {
-                            if (!wait(&bars->pv[(n - 1) & 1], (n - 1) >> 1, &bars->stop)) return;
+                            if (!wait(&bars->pv[(n - 1) & 1], (n - 1) >> 1, &bars->stop, a.wait_cycles)) return;
                             tc_after();
 #pragma unroll 1
                             for (int d = 0; d < D; d += 16) {
@@ -804,8 +804,8 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
             } while (!(flags & kLast));
         } else {  // the other row tile's steps
             do {
-                if (!wait(&bars->step[n % C::M], n / C::M, &bars->stop)) return;
-                if (!wait(&bars->s_full[x][n & 1], n >> 1, &bars->stop)) return;
+                if (!wait(&bars->step[n % C::M], n / C::M, &bars->stop, a.wait_cycles)) return;
+                if (!wait(&bars->s_full[x][n & 1], n >> 1, &bars->stop, a.wait_cycles)) return;
                 flags = steps[n % C::M].flags;
                 __syncwarp();
                 if (lane == 0) {
@@ -819,7 +819,7 @@ __device__ __forceinline__ void soften(const PrefixArgs& a, unsigned char* smem,
         way->next_piece(a, lane);
         if (way->more) load_q();
         if (valid > 0 || x == 0) {
-            if (!wait(&bars->pv[(n - 1) & 1], (n - 1) >> 1, &bars->stop)) return;
+            if (!wait(&bars->pv[(n - 1) & 1], (n - 1) >> 1, &bars->stop, a.wait_cycles)) return;
             tc_after();
             if (busy) {
                 drain();
@@ -886,8 +886,8 @@ __global__ void __launch_bounds__(C::kWarps * 32, 1) prefix_kernel(const PrefixA
         else widen<C, true>(a, stages + 2 * C::kTile, codes + C::N * C::kRaw / 2, &bars, steps, wp & 3);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegsM));
-        if (threadIdx.x == (4 * C::R + 8) * 32) scores<C>(smem, &bars, steps);
-        else if (threadIdx.x == (4 * C::R + 9) * 32) sums<C>(smem, &bars, steps);
+        if (threadIdx.x == (4 * C::R + 8) * 32) scores<C>(a, smem, &bars, steps);
+        else if (threadIdx.x == (4 * C::R + 9) * 32) sums<C>(a, smem, &bars, steps);
         else if (wp == 4 * C::R + 10) plan<C>(a, &bars, steps);
     }
     tc_before();

@@ -378,6 +378,7 @@ RMSATTN_API int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* 
     f.pdl = (flags & RMSN_PDL) ? 1 : 0;
     f.scale = scale;
     f.page_rcp = a.page_rcp;
+    f.wait_cycles = d->wait_cycles.load(std::memory_order_relaxed);
     f.status = d->status;
     f.line = reinterpret_cast<PrefixLine*>(ws);
     f.groups = reinterpret_cast<PrefixGroup*>(ws + p.groups);

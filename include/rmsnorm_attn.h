@@ -283,7 +283,8 @@ int64_t rmsattn_pages_workspace(int64_t n_seqs);
  *
  * in fp32, h rounded once to the residual's type, y (of the rounded h) once to
  * x's; with RMSATTN_OUT_FP8, out holds E4M3_RN_SATFINITE(y * (448 / max|y|)) and
- * out_scale max|y| / 448 (a row of zeros: codes and scale 0).
+ * out_scale max|y| / 448 (a row of zeros: codes and scale 0; where 448 / max|y| lies
+ * outside fp32's range, both factors are taken times a power of two first).
  *
  *   x            [n_tokens, hidden] bf16 / fp16 / fp32, weights [hidden] of its type
  *                or NULL (1, without the offset)

@@ -205,6 +205,10 @@ __device__ __forceinline__ void leave_out(const NormsArgs& a, int64_t t) {
     if (FP8 && a.zero_scale && threadIdx.x == 0) a.out_scale[t] = 0.f;
 }
 
+// 448 / top of an E4M3 row lies outside fp32's range for a row of less than 448 2^-128: y is
+// lifted by 2^64 first there (an exact product; rows of weights or residuals near zero).
+constexpr float kSmallRow = 0x1p-116f, kRowLift = 0x1p64f;
+
 // y = (w + off) (h inv), in that order of roundings.
 template <class T>
 __device__ __forceinline__ void norm(const Raw<T, 8>& w, float off, float inv, const rmsn::F2 (&h)[4], rmsn::F2 (&y)[4]) {
@@ -336,8 +340,15 @@ __global__ void __launch_bounds__(512, 2) norms_kernel(const NormsArgs a) {
             top = fmaxf(top, on[c] ? m : 0.f);
         }
         top = rmsn::block_allreduce<true>(top, slot[2]);
-        const float f = top > 0.f ? __fdiv_rn(448.f, top) : 0.f;
         if (threadIdx.x == 0) a.out_scale[t] = __fdiv_rn(top, 448.f);
+        if (top < kSmallRow) {
+            top *= kRowLift;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[c][k] = rmsn::mul2(y[c][k], rmsn::f2(kRowLift, kRowLift));
+        }
+        const float f = top > 0.f ? __fdiv_rn(448.f, top) : 0.f;
         const rmsn::F2 f2 = rmsn::f2(f, f);
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
@@ -393,17 +404,18 @@ __global__ void __launch_bounds__(1024) norms_long_kernel(const NormsArgs a) {
     auto out = [&](int j) {
         return __fmul_rn(__fmul_rn(load1<R>(a.residual_out, base + j), inv2), weight(a.w, j, a.w_off));
     };
-    float f = 1.f;
+    float f = 1.f, lift = 1.f;
     if constexpr (FP8) {
         float top = 0.f;
         for (int j = threadIdx.x; j < a.H; j += blockDim.x) top = fmaxf(top, fabsf(out(j)));
         top = rmsn::block_allreduce<true>(top, slot[2]);
-        f = top > 0.f ? __fdiv_rn(448.f, top) : 0.f;
         if (threadIdx.x == 0) a.out_scale[t] = __fdiv_rn(top, 448.f);
+        if (top < kSmallRow) lift = kRowLift;
+        f = top > 0.f ? __fdiv_rn(448.f, top * lift) : 0.f;
     }
     for (int j = threadIdx.x; j < a.H; j += blockDim.x) {
         const float y[1] = {out(j)};
-        if constexpr (FP8) static_cast<uint8_t*>(a.out)[base + j] = (uint8_t)pack_e4m3x2(__fmul_rn(y[0], f), 0.f);
+        if constexpr (FP8) static_cast<uint8_t*>(a.out)[base + j] = (uint8_t)pack_e4m3x2(__fmul_rn(y[0] * lift, f), 0.f);
         else store<T, 1>(a.out, base + j, round_to<T, 1>(y));
     }
 }

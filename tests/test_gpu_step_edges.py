@@ -7,6 +7,7 @@ import torch
 from torch.utils._python_dispatch import TorchDispatchMode
 
 import attn_ref as ref
+import step_ref
 from test_gpu_attn import DT, make_cache, rand, within
 from test_gpu_step import i32, norms_inputs, owns, prefix_state, rn, run_prefix  # noqa: F401  (rn: a fixture)
 
@@ -236,3 +237,33 @@ def test_prefix_groups_of_any_size_side_by_side(rn, groups, n, Hq, Hk, D, page, 
     q = rand((lengths.shape[0], n, Hq, D), 3, DT[dtype]).cuda()
     want, bound = ref.attend(q, t, table, lengths, 1 / math.sqrt(D), 0, 0)
     within(run_prefix(rn, q, t, table, lengths, P, cu, n), want, bound)
+
+
+@pytest.mark.parametrize("H", [64, 251, 4096, 20000])
+@pytest.mark.parametrize("stream", ["same", "f32"])
+def test_norms_codes_of_rows_near_zero(rn, H, stream):  # noqa: F811
+    # rows whose 448 / max|y| lies outside fp32's range: y = h / sqrt(eps), for h^2 is far below eps
+    T, eps = 8, 1e-6
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    g = torch.Generator().manual_seed(5)
+    whole = torch.randint(-64, 65, (T, H), generator=g).float()
+    whole[:, 0] = 64
+    whole[:, 1] = 0
+    size = [2.0 ** -133, 2.0 ** -136, 2.0 ** -130, 1.0, 0.0, 2.0 ** -127, 2.0 ** -124, 2.0 ** -100]  # (bf16 ends at 2^-133)
+    if stream == "same":
+        size[1] = 2.0 ** -132
+    r = (whole * torch.tensor(size)[:, None]).to(torch.float32 if stream == "f32" else torch.bfloat16)
+    y, h, scale = rn.fused_block_norms(x.cuda(), r.cuda(), eps=eps, out_dtype="fp8")
+    assert torch.equal(h.cpu(), r)
+    _, _, of = step_ref.norms(x, r, None, None, None, None, eps, 1.0, 0.0)
+    want, _, err = of(r)
+    # (y is rounded twice, to 2^-149 at the least; the scale once)
+    normal = (scale > 2.0 ** -126).cpu()
+    step_ref.check_codes(y.cpu()[normal], scale.cpu()[normal], want[normal], err[normal] + 2.0 ** -148)
+    assert bool(((scale.cpu().double() - want.abs().amax(-1) / 448).abs() <= (err.amax(-1) + 2.0 ** -140) / 448 + 2.0 ** -149).all())
+    codes = y.cpu().view(torch.float8_e4m3fn).double()
+    assert bool(codes.isfinite().all()) and not codes[4].any() and (codes[:, 1] == 0).all()
+    live = [i for i, s in enumerate(size) if s]
+    q = want[live] * 448 / want[live].abs().amax(-1, keepdim=True)
+    # half a step of the code, and y's roundings over the row's largest (2^-117 at the least)
+    assert bool(((codes[live] - q).abs() <= ref.half_step(q) * (1 + 2.0 ** -20) + 448 * (2.0 ** -30 + 2.0 ** -18)).all())

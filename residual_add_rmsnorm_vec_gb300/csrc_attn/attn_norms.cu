@@ -10,11 +10,16 @@
 // blocks of other rows on the SM stream while this one waits: a block per row,
 // the block scheduler brings in the next as soon as one retires.
 //
-// Measured: 16384 x 8192 bf16 156 us, 6.87 TB/s (1.01 of the copy peak); 4096 x 5120
-// bf16 to E4M3 with a gate for each sequence 31 us, 4.7 TB/s (27 without the gate: issue
-// slots and the chain of three row sums); 8 x 4096 3.2 us (a launch, two loads and two
-// sums); off the vectors' grid 4099 x 2045 31 us, 3.8 TB/s, 4096 x 8190 85 us, 3.2 TB/s
-// (issue slots: a weight is put together from two vectors).
+// Measured: 16384 x 8192 bf16 157 us, 6.84 TB/s (1.01 of the copy peak), with a gate for each
+// token 225, 5.96 TB/s, for each sequence 162, over an fp32 stream 233, 6.9 TB/s; fp32 8192 x
+// 8192 168, 6.4 TB/s.  4096 x 5120 bf16 to E4M3 with a gate for each sequence 31.5 us, 4.7 TB/s
+// (26 without the gate): the rows' loads are what its warps wait for first, at 27 warps an SM
+// (0.42), then the three row sums; issue slots are busy for 54 %.  8 x 4096 3.2 us (a launch,
+// two loads and two sums).  Off the vectors' grid 4099 x 2045 31 us, 3.8 TB/s, 4096 x 8190 85 us,
+// 3.2 TB/s (a weight is put together from two vectors; in fp32 from elements: 8192 x 8191 244).
+// Rows above 16384 elements, and tensors whose rows' first elements do not lie on the grid, go
+// element by element and meet memory again for each sum: 4096 x 20480 bf16 384 us (a floor of
+// 99), 16384 x 8192 that begin one element off 723.
 #include "attn_common.cuh"
 
 namespace rmsattn {
@@ -142,7 +147,7 @@ __device__ __forceinline__ float squares(const float (&e)[8]) {
 
 // Elements j to j + 7 of a row of H that begins anywhere; those outside of it are zero.
 // 16-bit ones come from the one or two vectors of memory that hold them, unless one of
-// those lies in the row in part.  By elements alone 4099 x 2045 took 40 us, not 31.
+// those lies in the row in part.  By elements alone 4099 x 2045 took 1.3 times as long.
 template <class T>
 __device__ __forceinline__ Raw<T, 8> load_any(const void* row, int j, int H) {
     if constexpr (T::kBytes == 2) {

@@ -2,12 +2,14 @@
 // block table, positions, slots.
 //
 // What bounds it: latency.  A step of 1024 sequences reads 12 KB and writes 30;
-// the chain is lengths -> two scans -> free list -> stores (8 sequences 4.6 us, 1024 x 1 token
-// 7.3, 9.3 with 5 % finished; 64 x 2000 tokens 7.6 and 8.9).  So one launch, and
+// the chain is lengths -> three block scans (rows, returned pages, taken pages) and a
+// maximum, eight barriers -> free list -> stores.  8 sequences x 1 token 4.8 us, 1024 x 1 7.0
+// (9.6 with 5 % finished), 64 x 2000 tokens 7.5 (9.0).  So one launch, and
 // no exchange between blocks: with up to kPagesOnce sequences every block scans
 // all of them for itself into shared memory (12 bytes a sequence from L2) and
 // then plans its own rows.  Larger batches scan once, in a first launch of one
-// block, into the workspace.
+// block, into the workspace; that block then bounds them (2048 x 1 8.2 us, 2049 x 1 11.5,
+// 4096 x 1 14.8, 16384 x 1 63).
 //
 // Nothing that a block writes is read by another one: the free list is read
 // below n_free and written from there on, the table's new entries are found from
@@ -286,8 +288,8 @@ __device__ __forceinline__ void plan_rows(const PagesArgs& a, const Scan& sc) {
         }
     }
     // rows: four to a thread (and whole vectors to write) where there are two or more, else
-    // one, whose chain of loads nothing lengthens (64 x 2000 tokens 7.9 us with four and 8.9
-    // with one; 1024 x 1 8.9 and 7.2)
+    // one, whose chain of loads nothing lengthens (64 x 2000 tokens take 0.89 of the time with
+    // four, 1024 x 1 1.23 of it)
     if (a.T >= 2 * threads) each_row<4>(a, sc, me, threads);
     else each_row<1>(a, sc, me, threads);
 }

@@ -8,7 +8,7 @@
 // products: 4 D flops for each pair of a row and a token against 2 D + 1/2 bytes a
 // token.  From about 150 rows on the tensor cores bound it, below that DRAM.
 //
-// Measured, 32 / 8 heads x 128: 64 sequences x 8192 shared tokens 24 us, of which 7 are a
+// Measured (this launch alone), 32 / 8 heads x 128: 64 sequences x 8192 shared tokens 24 us, of which 7 are a
 // block's start (TMEM, barriers, plan, queries, first pages); 256 x 16384 85 us, 808 TFLOP/s
 // (0.42 of the library's matrix product).  A step of 64 tokens and 256 rows takes 2000 cycles.
 // What bounds it there: a product of 128 rows and 16 of the inner dimension takes 65

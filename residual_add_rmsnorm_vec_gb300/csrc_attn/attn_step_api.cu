@@ -83,10 +83,9 @@ RMSATTN_API int rmsattn_pages_step(int32_t* free_pages, int64_t n_pages, const i
     a.ws = static_cast<int32_t*>(workspace);
     a.status = d->status;
     // Up to four rows to a thread; a warp to a sequence (one that returns pages has a row of
-    // them to read: with 32 sequences to a warp, 1024 x 1 token took 21 us).  Small blocks
-    // while their scan of all sequences is short and there are SMs for them: 8 x 1 token 4.8
-    // against 5.5 us, 64 x 200 6.6 against 7.4, but 1024 x 1 8.3 against 7.3, 64 x 2000
-    // 8.2 against 7.9.
+    // them to read: with 32 sequences to a warp, 1024 x 1 token took 2.3 times as long).  Small
+    // blocks while their scan of all sequences is short and there are SMs for them: 8 x 1 token
+    // take 0.87 of the large ones' time, 64 x 200 0.89, but 1024 x 1 1.14, 64 x 2000 1.04.
     const int threads = n_seqs <= 256 && n_rows <= 512 * (int64_t)d->num_sms ? 128 : 512;
     int64_t blocks = (n_rows + 4 * threads - 1) / (4 * threads);
     const int64_t by_seqs = (n_seqs * 32 + threads - 1) / threads;
@@ -194,9 +193,9 @@ RMSATTN_API int rmsattn_block_norms(const void* x, const void* residual, const v
     bool ragged = hidden % 8 != 0 || gate_stride % 8 != 0;
     for (const void* p : same) ragged = ragged || !aligned(p, (uintptr_t)(8 * bytes));
     // Vectors of a thread: as few as put all rows on the SMs at once, for the shorter chain
-    // (8 x 4096 bf16 3.5 us with one and 3.9 with four, 900 x 1024 3.5 and 4.2); four
-    // otherwise, which put the most rows on an SM (600 x 4096 6.3 us with one and 5.2 with
-    // four, 2000 x 4096 19 and 12, 16384 x 8192 200 with two and 160 with four).
+    // (8 x 4096 bf16 take 0.9 of the time with one as with four, 900 x 1024 0.82); four
+    // otherwise, which put the most rows on an SM (600 x 4096 take 0.84 of the time with four
+    // as with one, 2000 x 4096 0.61, 16384 x 8192 0.8 of the time with two).
     const int64_t vectors = (hidden + (ragged ? 14 : 7)) / 8;
     int64_t ch = 1;
     while (ch < 4 && ((vectors + ch - 1) / ch > 512 || n_tokens * ((vectors + ch - 1) / ch) > 1024 * (int64_t)d->num_sms))
@@ -413,9 +412,9 @@ RMSATTN_API int rmsattn_kv_prefix_attention(const void* q, const rmsattn_cache* 
         st = launch(p.e->fn, dim3((unsigned)p.shares), p.e->threads, (size_t)p.e->smem, &f, true, stream);
     if (st == RMSN_OK) st = launch_attend(p.behind, &a, true, stream, 2);
     if (st != RMSN_OK) return st;
-    // Four threads to a row's parts where an item has many, for there are few items: 8
-    // sequences x 2048 tokens 25.0 against 28.5 us, 64 x 8192 50 against 55; one else: 256 x
-    // 8192 115 against 118, 512 x 4096 169 against 178.
+    // Four threads to a row's parts where an item has many, for there are few items: the call of
+    // 8 sequences x 2048 tokens takes 0.88 of the time so, 64 x 8192 0.92; one else: with four
+    // 256 x 8192 take 1.03 of the time, 512 x 4096 1.05.
     const int64_t cols = n_seqs * n_queries * a.group, items = (cols + f.rows - 1) / f.rows * a.c.H;
     const int ways = items * 8 >= p.shares ? 1 : 4;
     return launch(prefix_join_kernel(dt, ways), dim3((unsigned)((cols * ways + 255) / 256), (unsigned)(a.c.H * (a.c.D / 8))),

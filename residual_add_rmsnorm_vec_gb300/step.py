@@ -138,6 +138,10 @@ def kv_cache_prefix_attention(q: torch.Tensor, cache: KVCache, block_table: torc
     one group of all), has the same first ``prefix_lengths[g]`` tokens, in the
     same pages.  ``lengths`` and the rows of ``block_table`` count those too.  A
     sequence that does not see all of the prefix reads its own row alone.
+
+    It takes some 25 us at the least: ``kv_cache_attention`` with the same arguments is
+    the faster one up to about 200 MB of keys and values over all sequences' lengths
+    (300 MB at head_dim 256).
     """
     if stream is None:
         done = (_al._fast or _al.load_fast()).kv_prefix_attention(
